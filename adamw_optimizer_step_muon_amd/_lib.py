@@ -29,9 +29,12 @@ EXPORTED = (
     "ma_newton_schulz_workspace_bytes", "ma_newton_schulz", "ma_muon_tune", "ma_muon_tune_reset",
     "ma_adamw_step_multi", "ma_muon_check_plan", "ma_muon_ns_time", "ma_muon_static_init",
     "ma_muon_step_static", "ma_muon_tune_configs", "ma_stream_probe", "ma_mfma_probe",
+    "ma_embedding_forward", "ma_embedding_workspace_bytes", "ma_embedding_backward",
+    "ma_adamw_step_embedding", "ma_layer_norm_forward", "ma_layer_norm_workspace_bytes",
+    "ma_layer_norm_backward", "ma_distill_forward", "ma_distill_backward", "ma_distill_loss_grad",
 )
 MA_STATIC_WORKSPACE_BYTES = 512 << 20
-ABI_VERSION = 4  # include/muon_adamw.h MA_ABI_VERSION
+ABI_VERSION = 5  # include/muon_adamw.h MA_ABI_VERSION
 
 
 class MuonAdamWError(RuntimeError):
@@ -177,6 +180,31 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                     ctypes.POINTER(_MuonHParams), ctypes.c_void_p,
                                     ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int32,
                                     ctypes.POINTER(ctypes.c_float)]
+    ptr, i32, i64, f32, size = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                                ctypes.c_size_t)
+    hp = ctypes.POINTER(_AdamWHParams)
+    for name, args in (
+            ("embedding_forward", [ptr, i64, i64, ptr, i32, i64, f32, ptr, i32, i64, ptr]),
+            ("embedding_backward", [ptr, i32, i64, ptr, i32, i64, f32, ptr, i64, i64, i32, ptr,
+                                    size, ptr]),
+            ("adamw_step_embedding", [ptr, ptr, ptr, i64, i64, ptr, i32, i64, ptr, i32, i64, f32,
+                                      hp, ptr, size, ptr]),
+            ("layer_norm_forward", [ptr, i32, i64, i64, i64, ptr, ptr, f32, ptr, i64, ptr, ptr,
+                                    ptr]),
+            ("layer_norm_backward", [ptr, i64, ptr, i64, i32, i64, i64, ptr, ptr, ptr, ptr, i64,
+                                     ptr, ptr, i32, ptr, size, ptr]),
+            ("distill_forward", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
+                                 ptr]),
+            ("distill_backward", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
+                                  ptr, i64, ptr]),
+            ("distill_loss_grad", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
+                                   ptr, i64, ptr])):
+        fn = getattr(lib, "ma_" + name)
+        fn.restype, fn.argtypes = ctypes.c_int, args
+    lib.ma_embedding_workspace_bytes.restype = size
+    lib.ma_embedding_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.ma_layer_norm_workspace_bytes.restype = size
+    lib.ma_layer_norm_workspace_bytes.argtypes = [i64, i64]
     _lib = lib
     return lib
 

@@ -561,6 +561,145 @@ ma_status adamw_const(const ma_adamw_hparams* hp, AdamWConst* c) {
   return MA_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Argument checks of the training operators
+// ---------------------------------------------------------------------------
+// One launch holds fewer than 2^32 threads.
+constexpr int64_t kMaxThreadsPerLaunch = (int64_t(1) << 32) - 65536;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 2;
+constexpr int64_t kMaxDim = int64_t(1) << 20;
+
+int64_t bytes_of(int type) { return type == MA_F32 ? 4 : 2; }
+
+ma_status check_type(int32_t type, const char* what) {
+  if (type != MA_F32 && type != MA_F16 && type != MA_BF16)
+    return fail(MA_ERR_INVALID_ARG, "%s type %d is not a ma_dtype", what, type);
+  return MA_OK;
+}
+ma_status check_bits(int32_t bits, const char* what) {
+  if (bits != 32 && bits != 64) return fail(MA_ERR_INVALID_ARG, "%s bits %d is not 32 or 64", what, bits);
+  return MA_OK;
+}
+ma_status check_pointer(const void* p, int64_t align, const char* what) {
+  if (!p) return fail(MA_ERR_INVALID_ARG, "%s is NULL", what);
+  if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(align))
+    return fail(MA_ERR_INVALID_ARG, "%s is not aligned to its elements", what);
+  return MA_OK;
+}
+// n rows of dim values, `stride` values apart.
+ma_status check_rows(const void* p, int32_t type, int64_t n, int64_t dim, int64_t stride,
+                     const char* what, Range* range) {
+  if (const ma_status st = check_type(type, what)) return st;
+  if (const ma_status st = check_pointer(p, bytes_of(type), what)) return st;
+  if (stride < dim)
+    return fail(MA_ERR_INVALID_ARG, "%s stride %lld below its %lld columns", what, (long long)stride,
+                (long long)dim);
+  if (stride > (int64_t(1) << 40) || ((n - 1) > (int64_t(1) << 56) / stride))
+    return fail(MA_ERR_UNSUPPORTED, "%s spans too many bytes", what);
+  *range = range_of(p, ((n - 1) * stride + dim) * bytes_of(type));
+  return MA_OK;
+}
+// Every written range (the first `writes`) against every other range; empty ranges (absent
+// buffers) meet nothing.
+ma_status check_disjoint(const Range* r, int count, int writes, const char* what) {
+  for (int i = 0; i < writes; ++i)
+    for (int j = i + 1; j < count; ++j)
+      if (r[i].lo < r[i].hi && r[j].lo < r[j].hi && overlap(r[i], r[j]))
+        return fail(MA_ERR_INVALID_ARG, "%s overlap", what);
+  return MA_OK;
+}
+ma_status check_workspace(const void* ws, size_t have, size_t need, Range* range) {
+  *range = Range{0, 0};
+  if (need == 0) return MA_OK;
+  if (!ws) return fail(MA_ERR_WORKSPACE, "workspace is NULL, %zu bytes needed", need);
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(MA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  if (have < need) return fail(MA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", have, need);
+  *range = range_of(ws, static_cast<int64_t>(need));
+  return MA_OK;
+}
+
+ma_status check_table(int64_t rows, int64_t dim, int64_t n) {
+  if (rows < 1 || dim < 1) return fail(MA_ERR_INVALID_ARG, "table of %lld x %lld", (long long)rows, (long long)dim);
+  if (n < 0) return fail(MA_ERR_INVALID_ARG, "n = %lld < 0", (long long)n);
+  if (rows > kMaxRows || dim > kMaxDim || n > kMaxTokens)
+    return fail(MA_ERR_UNSUPPORTED, "table of %lld x %lld with %lld tokens", (long long)rows, (long long)dim, (long long)n);
+  if (embedding_threads(rows, dim, n) > kMaxThreadsPerLaunch)
+    return fail(MA_ERR_UNSUPPORTED, "table of %lld x %lld with %lld tokens exceeds one launch", (long long)rows,
+                (long long)dim, (long long)n);
+  return MA_OK;
+}
+
+// Tokens, output gradients and workspace of a table gradient over `out` written ranges.
+ma_status check_table_grad(const void* tokens, int32_t token_bits, int64_t n, const void* dout,
+                           int32_t dout_type, int64_t dout_stride, float scale, int64_t rows,
+                           int64_t dim, const Range* out, int outs, void* ws, size_t ws_bytes,
+                           EmbeddingCall* e) {
+  if (!finite(scale)) return fail(MA_ERR_INVALID_ARG, "non-finite scale");
+  if (const ma_status st = check_bits(token_bits, "token")) return st;
+  if (const ma_status st = check_type(dout_type, "dout")) return st;
+  Range r[8] = {};
+  for (int i = 0; i < outs; ++i) r[i] = out[i];
+  Range* rest = r + outs;  // workspace, tokens, dout
+  const size_t need = static_cast<size_t>(plan_embedding(rows, dim, n).bytes);
+  if (n > 0) {
+    if (const ma_status st = check_pointer(tokens, token_bits / 8, "tokens")) return st;
+    if (const ma_status st = check_rows(dout, dout_type, n, dim, dout_stride, "dout", &rest[2])) return st;
+    rest[1] = range_of(tokens, n * (token_bits / 8));
+  }
+  if (const ma_status st = check_workspace(ws, ws_bytes, need, &rest[0])) return st;
+  if (const ma_status st = check_disjoint(r, outs + 3, outs + 1, "table, workspace, tokens or dout")) return st;
+  *e = EmbeddingCall{tokens, token_bits, n, rows, dim, dout, dout_type, dout_stride, scale, ws};
+  return MA_OK;
+}
+
+ma_status check_norm_size(int64_t n, int64_t dim) {
+  if (n < 0 || dim < 1) return fail(MA_ERR_INVALID_ARG, "%lld rows of %lld", (long long)n, (long long)dim);
+  if (dim > kMaxDim || n > kMaxThreadsPerLaunch / 1024)
+    return fail(MA_ERR_UNSUPPORTED, "%lld rows of %lld", (long long)n, (long long)dim);
+  return MA_OK;
+}
+
+// Everything of a distillation call but its outputs; ranges: logits, teacher, ids.
+ma_status check_distill(const DistillCall& c, Range* r) {
+  if (c.n < 0 || c.vocab < 1 || c.top < 0)
+    return fail(MA_ERR_INVALID_ARG, "%lld rows of %lld logits, %lld teacher entries", (long long)c.n,
+                (long long)c.vocab, (long long)c.top);
+  if (c.top > kMaxDistillTop)
+    return fail(MA_ERR_UNSUPPORTED, "%lld teacher entries, at most %d", (long long)c.top, kMaxDistillTop);
+  if (c.vocab > kMaxRows || c.n > kMaxThreadsPerLaunch / 1024)
+    return fail(MA_ERR_UNSUPPORTED, "%lld rows of %lld logits", (long long)c.n, (long long)c.vocab);
+  if (!finite(c.temperature) || !(c.temperature > 0.0f))
+    return fail(MA_ERR_INVALID_ARG, "temperature must be finite and above zero");
+  // exp2's argument is (z - m) log2(e) / tau, the loss's factor tau^2: both stay in range
+  if (c.temperature < 1e-6f || c.temperature > 1e6f)
+    return fail(MA_ERR_UNSUPPORTED, "temperature %g outside [1e-6, 1e6]", c.temperature);
+  if (const ma_status st = check_type(c.type, "logits")) return st;
+  if (const ma_status st = check_type(c.teacher_type, "teacher")) return st;
+  if (const ma_status st = check_bits(c.id_bits, "id")) return st;
+  if (c.n == 0) return MA_OK;
+  if (const ma_status st = check_rows(c.logits, c.type, c.n, c.vocab, c.stride, "logits", &r[0])) return st;
+  if (c.top > 0) {
+    if (const ma_status st = check_rows(c.teacher, c.teacher_type, c.n, c.top, c.top, "teacher", &r[1])) return st;
+    if (const ma_status st = check_pointer(c.ids, c.id_bits / 8, "ids")) return st;
+    r[2] = range_of(c.ids, c.n * c.top * (c.id_bits / 8));
+  }
+  return MA_OK;
+}
+ma_status check_floats(const void* p, int64_t n, const char* what, Range* r) {
+  if (const ma_status st = check_pointer(p, 4, what)) return st;
+  *r = range_of(p, n * 4);
+  return MA_OK;
+}
+// dlogits may be exactly the logits (same address and stride), and nothing else of the call.
+ma_status check_dlogits(const DistillCall& c, const Range* in, int ins, Range* d) {
+  if (const ma_status st = check_rows(c.dlogits, c.type, c.n, c.vocab, c.dlogits_stride, "dlogits", d)) return st;
+  const bool same = c.dlogits == c.logits && c.dlogits_stride == c.stride;
+  for (int i = same ? 1 : 0; i < ins; ++i)
+    if (in[i].lo < in[i].hi && overlap(*d, in[i])) return fail(MA_ERR_INVALID_ARG, "dlogits overlaps another buffer");
+  return MA_OK;
+}
+
 // Each device's copy of the static workspace (resolved once per device).
 constexpr int kMaxDevices = 64;
 std::mutex g_static_mu;
@@ -1556,6 +1695,191 @@ ma_status ma_adamw_step_multi(const ma_adamw_segment* segs, int32_t n_segs,
     t.nseg = k + 1;
   }
   return flush();
+}
+
+// ---------------------------------------------------------------------------
+// Training operators
+// ---------------------------------------------------------------------------
+ma_status ma_embedding_forward(const float* table, int64_t rows, int64_t dim, const void* tokens,
+                               int32_t token_bits, int64_t n, float scale, void* out,
+                               int32_t out_type, int64_t out_stride, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_table(rows, dim, n)) return st;
+  if (!finite(scale)) return fail(MA_ERR_INVALID_ARG, "non-finite scale");
+  if (const ma_status st = check_bits(token_bits, "token")) return st;
+  if (const ma_status st = check_type(out_type, "out")) return st;
+  if (n == 0) return MA_OK;
+  Range r[3];
+  if (const ma_status st = check_rows(out, out_type, n, dim, out_stride, "out", &r[0])) return st;
+  if (const ma_status st = check_floats(table, rows * dim, "table", &r[1])) return st;
+  if (const ma_status st = check_pointer(tokens, token_bits / 8, "tokens")) return st;
+  r[2] = range_of(tokens, n * (token_bits / 8));
+  if (const ma_status st = check_disjoint(r, 3, 1, "out, table or tokens")) return st;
+  const hipError_t e = launch_embedding_forward(table, rows, dim, tokens, token_bits, n, scale, out,
+                                                out_type, out_stride, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "embedding launch");
+  return MA_OK;
+}
+
+size_t ma_embedding_workspace_bytes(int64_t rows, int64_t dim, int64_t n) {
+  if (rows < 1 || dim < 1 || n < 1 || rows > kMaxRows || dim > kMaxDim || n > kMaxTokens) return 0;
+  return static_cast<size_t>(plan_embedding(rows, dim, n).bytes);
+}
+
+ma_status ma_embedding_backward(const void* tokens, int32_t token_bits, int64_t n, const void* dout,
+                                int32_t dout_type, int64_t dout_stride, float scale, float* grad,
+                                int64_t rows, int64_t dim, int32_t accumulate, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_table(rows, dim, n)) return st;
+  Range out;
+  if (const ma_status st = check_floats(grad, rows * dim, "grad", &out)) return st;
+  EmbeddingCall c;
+  if (const ma_status st = check_table_grad(tokens, token_bits, n, dout, dout_type, dout_stride, scale, rows,
+                                            dim, &out, 1, workspace, workspace_bytes, &c)) return st;
+  if (n == 0 && accumulate) return MA_OK;
+  const hipError_t e = launch_embedding_backward(c, grad, accumulate != 0, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "embedding gradient launch");
+  return MA_OK;
+}
+
+ma_status ma_adamw_step_embedding(float* param, float* exp_avg, float* exp_avg_sq, int64_t rows,
+                                  int64_t dim, const void* tokens, int32_t token_bits, int64_t n,
+                                  const void* dout, int32_t dout_type, int64_t dout_stride, float scale,
+                                  const ma_adamw_hparams* hp, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  g_last_error.clear();
+  AdamWConst k;
+  if (const ma_status st = adamw_const(hp, &k)) return st;
+  if (const ma_status st = check_table(rows, dim, n)) return st;
+  Range out[3];
+  if (const ma_status st = check_floats(param, rows * dim, "param", &out[0])) return st;
+  if (const ma_status st = check_floats(exp_avg, rows * dim, "exp_avg", &out[1])) return st;
+  if (const ma_status st = check_floats(exp_avg_sq, rows * dim, "exp_avg_sq", &out[2])) return st;
+  EmbeddingCall c;
+  if (const ma_status st = check_table_grad(tokens, token_bits, n, dout, dout_type, dout_stride, scale, rows,
+                                            dim, out, 3, workspace, workspace_bytes, &c)) return st;
+  const hipError_t e = launch_adamw_embedding(c, param, exp_avg, exp_avg_sq, k, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "embedding step launch");
+  return MA_OK;
+}
+
+ma_status ma_layer_norm_forward(const void* x, int32_t type, int64_t x_stride, int64_t n, int64_t dim,
+                                const float* weight, const float* bias, float eps, void* y,
+                                int64_t y_stride, float* mean, float* rstd, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_norm_size(n, dim)) return st;
+  if (const ma_status st = check_type(type, "x")) return st;
+  if (!finite(eps) || eps < 0.0f) return fail(MA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (n == 0) return MA_OK;
+  Range r[6] = {};
+  if (const ma_status st = check_rows(y, type, n, dim, y_stride, "y", &r[0])) return st;
+  if (const ma_status st = check_floats(mean, n, "mean", &r[1])) return st;
+  if (const ma_status st = check_floats(rstd, n, "rstd", &r[2])) return st;
+  if (const ma_status st = check_rows(x, type, n, dim, x_stride, "x", &r[3])) return st;
+  if (weight)
+    if (const ma_status st = check_floats(weight, dim, "weight", &r[4])) return st;
+  if (bias)
+    if (const ma_status st = check_floats(bias, dim, "bias", &r[5])) return st;
+  if (const ma_status st = check_disjoint(r, 6, 3, "y, mean, rstd, x, weight or bias")) return st;
+  const NormCall c{x, type, x_stride, n, dim, weight, bias, eps, y, y_stride, mean, rstd};
+  const hipError_t e = launch_layer_norm_forward(c, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "layer norm launch");
+  return MA_OK;
+}
+
+size_t ma_layer_norm_workspace_bytes(int64_t n, int64_t dim) {
+  if (n < 1 || dim < 1 || dim > kMaxDim || n > kMaxThreadsPerLaunch / 1024) return 0;
+  return layer_norm_workspace_bytes(n, dim);
+}
+
+ma_status ma_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                 int32_t type, int64_t n, int64_t dim, const float* weight,
+                                 const float* mean, const float* rstd, void* dx, int64_t dx_stride,
+                                 float* dweight, float* dbias, int32_t accumulate, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_norm_size(n, dim)) return st;
+  if (const ma_status st = check_type(type, "x")) return st;
+  Range r[9] = {};
+  if (dweight)
+    if (const ma_status st = check_floats(dweight, dim, "dweight", &r[0])) return st;
+  if (dbias)
+    if (const ma_status st = check_floats(dbias, dim, "dbias", &r[1])) return st;
+  if (n > 0) {
+    if (const ma_status st = check_rows(dx, type, n, dim, dx_stride, "dx", &r[2])) return st;
+    if (const ma_status st = check_rows(dy, type, n, dim, dy_stride, "dy", &r[4])) return st;
+    if (const ma_status st = check_rows(x, type, n, dim, x_stride, "x", &r[5])) return st;
+    if (const ma_status st = check_floats(mean, n, "mean", &r[6])) return st;
+    if (const ma_status st = check_floats(rstd, n, "rstd", &r[7])) return st;
+  }
+  if (weight)
+    if (const ma_status st = check_floats(weight, dim, "weight", &r[8])) return st;
+  const bool reduce = dweight || dbias;
+  if (const ma_status st = check_workspace(workspace, workspace_bytes,
+                                           reduce ? ma_layer_norm_workspace_bytes(n, dim) : 0, &r[3])) return st;
+  if (const ma_status st = check_disjoint(r, 9, 4, "gradients, workspace or inputs")) return st;
+  if (n == 0 && (accumulate || !reduce)) return MA_OK;
+  const NormGradCall c{dy, x, type, dy_stride, x_stride, n, dim, weight, mean, rstd, dx, dx_stride,
+                       dweight, dbias, accumulate != 0, static_cast<float*>(workspace)};
+  const hipError_t e = launch_layer_norm_backward(c, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "layer norm gradient launch");
+  return MA_OK;
+}
+
+ma_status ma_distill_forward(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,
+                             const void* teacher, int32_t teacher_type, const void* ids, int32_t id_bits,
+                             int64_t top, float temperature, float* loss, float* stats, void* stream) {
+  g_last_error.clear();
+  const DistillCall c{logits, type, stride, n, vocab, teacher, teacher_type, ids, id_bits, top,
+                      temperature, nullptr, loss, stats, nullptr, 0};
+  Range r[5] = {};
+  if (const ma_status st = check_distill(c, r + 2)) return st;
+  if (n == 0) return MA_OK;
+  if (const ma_status st = check_floats(loss, n, "loss", &r[0])) return st;
+  if (const ma_status st = check_floats(stats, 2 * n, "stats", &r[1])) return st;
+  if (const ma_status st = check_disjoint(r, 5, 2, "loss, stats or inputs")) return st;
+  const hipError_t e = launch_distill(c, kDistillForward, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "distillation launch");
+  return MA_OK;
+}
+
+ma_status ma_distill_backward(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,
+                              const void* teacher, int32_t teacher_type, const void* ids, int32_t id_bits,
+                              int64_t top, float temperature, const float* stats, const float* row_weight,
+                              void* dlogits, int64_t dlogits_stride, void* stream) {
+  g_last_error.clear();
+  const DistillCall c{logits, type, stride, n, vocab, teacher, teacher_type, ids, id_bits, top,
+                      temperature, row_weight, nullptr, const_cast<float*>(stats), dlogits, dlogits_stride};
+  Range r[5] = {}, d;
+  if (const ma_status st = check_distill(c, r)) return st;
+  if (n == 0) return MA_OK;
+  if (const ma_status st = check_floats(stats, 2 * n, "stats", &r[3])) return st;
+  if (const ma_status st = check_floats(row_weight, n, "row_weight", &r[4])) return st;
+  if (const ma_status st = check_dlogits(c, r, 5, &d)) return st;
+  const hipError_t e = launch_distill(c, kDistillBackward, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "distillation gradient launch");
+  return MA_OK;
+}
+
+ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,
+                               const void* teacher, int32_t teacher_type, const void* ids, int32_t id_bits,
+                               int64_t top, float temperature, const float* row_weight, float* loss,
+                               void* dlogits, int64_t dlogits_stride, void* stream) {
+  g_last_error.clear();
+  const DistillCall c{logits, type, stride, n, vocab, teacher, teacher_type, ids, id_bits, top,
+                      temperature, row_weight, loss, nullptr, dlogits, dlogits_stride};
+  Range r[5] = {}, d;
+  if (const ma_status st = check_distill(c, r)) return st;
+  if (n == 0) return MA_OK;
+  if (const ma_status st = check_floats(row_weight, n, "row_weight", &r[3])) return st;
+  if (const ma_status st = check_floats(loss, n, "loss", &r[4])) return st;
+  const Range lr[5] = {r[4], r[0], r[1], r[2], r[3]};
+  if (const ma_status st = check_disjoint(lr, 5, 1, "loss or inputs")) return st;
+  if (const ma_status st = check_dlogits(c, r, 5, &d)) return st;
+  const hipError_t e = launch_distill(c, kDistillBoth, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "distillation launch");
+  return MA_OK;
 }
 
 }  // extern "C"

@@ -401,4 +401,106 @@ hipError_t launch_adamw_multi(const AdamWSegTable& t, hipStream_t s);
 hipError_t launch_mfma_probe(const void* operands, int blocks, int iters, float* out,
                              unsigned long long* clocks, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// Training operators (embedding.hip, layer_norm.hip, distill.hip).  Activation types are
+// numbered as ma_dtype: 0 fp32, 1 fp16, 2 bf16.
+// ---------------------------------------------------------------------------
+// Workspace of a table gradient: byte offsets, the sort's shares and the segments' chunks.
+struct EmbeddingPlan {
+  int64_t keys[2], order[2], counts, start, end, partial, bytes;
+  int64_t share, chunk, chunks;
+  int blocks;
+};
+EmbeddingPlan plan_embedding(int64_t rows, int64_t dim, int64_t n);
+// Threads of the largest launch of a lookup or a table gradient.
+int64_t embedding_threads(int64_t rows, int64_t dim, int64_t n);
+
+struct SortArgs {
+  const void* tokens;
+  int64_t n, share;
+  uint32_t* counts;
+  uint32_t rows;
+  int token_bits;
+};
+struct RowArgs {
+  const uint32_t* keys;   // sorted rows of the n tokens, `rows` for padding
+  const uint32_t* order;  // their positions
+  uint32_t* start;        // per row; valid where the keys confirm it
+  uint32_t* end;
+  float* partial;         // 2 per chunk, dim values each
+  const void* dout;
+  int64_t dout_stride, n, dim, chunk;
+  uint32_t rows;
+  float scale;
+};
+// One table gradient's inputs (n >= 1, rows >= 1, dim >= 1).
+struct EmbeddingCall {
+  const void* tokens;
+  int token_bits;
+  int64_t n, rows, dim;
+  const void* dout;
+  int dout_type;
+  int64_t dout_stride;
+  float scale;
+  void* workspace;
+};
+hipError_t launch_embedding_forward(const float* table, int64_t rows, int64_t dim,
+                                    const void* tokens, int token_bits, int64_t n, float scale,
+                                    void* out, int out_type, int64_t out_stride, hipStream_t s);
+hipError_t launch_embedding_backward(const EmbeddingCall& e, float* grad, bool add, hipStream_t s);
+hipError_t launch_adamw_embedding(const EmbeddingCall& e, float* p, float* m, float* v,
+                                  const AdamWConst& c, hipStream_t s);
+
+struct NormCall {
+  const void* x;
+  int type;
+  int64_t x_stride, n, dim;
+  const float* weight;  // null: ones
+  const float* bias;    // null: zeros
+  float eps;
+  void* y;
+  int64_t y_stride;
+  float* mean;
+  float* rstd;
+};
+hipError_t launch_layer_norm_forward(const NormCall& c, hipStream_t s);
+struct NormGradCall {
+  const void* dy;
+  const void* x;
+  int type;
+  int64_t dy_stride, x_stride, n, dim;
+  const float* weight;  // null: ones
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  int64_t dx_stride;
+  float* dweight;  // may be null
+  float* dbias;    // may be null
+  bool add;
+  float* workspace;
+};
+size_t layer_norm_workspace_bytes(int64_t n, int64_t dim);
+hipError_t launch_layer_norm_backward(const NormGradCall& c, hipStream_t s);
+
+struct DistillCall {
+  const void* logits;
+  int type;
+  int64_t stride, n, vocab;
+  const void* teacher;
+  int teacher_type;
+  const void* ids;
+  int id_bits;
+  int64_t top;
+  float temperature;
+  const float* row_weight;  // gradients only
+  float* loss;              // null: no loss
+  float* stats;             // (n, 2): row maximum, sum of exponentials; read or written
+  void* dlogits;            // null: no gradient
+  int64_t dlogits_stride;
+};
+constexpr int kMaxDistillTop = 1024;
+// What the call computes: loss and stats, the gradient from given stats, or both at once.
+enum DistillMode { kDistillForward = 0, kDistillBackward = 1, kDistillBoth = 2 };
+hipError_t launch_distill(const DistillCall& c, DistillMode mode, hipStream_t s);
+
 }  // namespace ma

@@ -23,7 +23,9 @@ them so, and backward then accumulates into the buffer until ``zero_grad()`` dro
 them), and a single ma_muon_step runs all buckets, so buckets that share a GEMM
 configuration share its launches.  Parameters without a gradient are not stepped.
 State is fp32 and zero-initialised: ``momentum_buffer`` (4 bytes per Muon parameter),
-``exp_avg`` and ``exp_avg_sq`` (8 bytes per AdamW parameter).
+``exp_avg`` and ``exp_avg_sq`` (8 bytes per AdamW parameter).  An embedding table's gradient
+can come as tokens and output gradients (``add_token_gradient``, which ``embedding(...,
+optimizer=...)`` calls in its backward pass); its dense form is then never built.
 
 A Muon group's ``ns_mode`` (0 by default) selects the Newton-Schulz route: 1 runs the
 Gram-space iteration ("DMuon", section 2.2) on fp16 operands for the buckets whose long
@@ -101,6 +103,8 @@ class MuonAdamW:
         self.state: Dict[int, Dict] = {}
         self._workspace = None
         self._buckets: Dict[int, List[_Bucket]] = {}
+        # id(parameter) -> [(tokens, dout, scale, versions)], see add_token_gradient
+        self._token_grads: Dict[int, List] = {}
         for g in param_groups:
             kind = g.get("kind", "muon")
             if kind not in ("muon", "adamw"):
@@ -172,20 +176,68 @@ class MuonAdamW:
             self._workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return self._workspace
 
+    def add_token_gradient(self, param, tokens, dout, scale: float = 1.0) -> None:
+        """Adds to the gradient of an embedding table (a 2-D parameter of an "adamw" group)
+        scale * dout[t] on row tokens[t] for every t, without building it: the next step()
+        applies tokens and output gradients directly (adamw_step_embedding: no dense
+        gradient is written or read).  Several additions, or one next to a dense
+        ``param.grad``, are summed into ``param.grad`` at step() instead.  tokens (int32 or
+        int64) and dout (tokens.shape + (dim,)) are kept, not copied, until zero_grad() and
+        must not be modified before step().  What reads ``param.grad`` between backward and
+        step (clipping by a global norm, say) does not see this gradient; ``scale`` can
+        carry a clipping factor."""
+        if not any(q is param for g in self.param_groups if g["kind"] == "adamw"
+                   for q in g["params"]):
+            raise ValueError("token gradients are for parameters of an adamw group")
+        if param.dim() != 2 or dout.shape != tuple(tokens.shape) + (param.shape[1],):
+            raise ValueError("dout must be tokens.shape + (dim,) of a (rows, dim) parameter")
+        self._token_grads.setdefault(id(param), []).append(
+            (tokens, dout, float(scale), (tokens._version, dout._version)))
+
+    def _take_token_gradient(self, p):
+        """The token gradient to step p with directly, or None where p.grad holds it all."""
+        added = self._token_grads.get(id(p))
+        if not added:
+            return None
+        for tokens, dout, _, versions in added:
+            if (tokens._version, dout._version) != versions:
+                raise RuntimeError("the tokens or output gradients of a token gradient were "
+                                   "modified before step()")
+        if len(added) == 1 and p.grad is None:
+            return added[0]
+        from . import ops
+
+        for tokens, dout, scale, _ in added:
+            if p.grad is None:
+                p.grad = ops.embedding_backward(dout, tokens, p.shape[0], scale=scale)
+            else:
+                ops.embedding_backward(dout, tokens, p.shape[0], scale=scale, grad=p.grad,
+                                       accumulate=True)
+        del self._token_grads[id(p)]
+        return None
+
     def step(self) -> None:
         for gi, g in enumerate(self.param_groups):
             if g["kind"] == "adamw":
+                by_token = [(p, t) for p in g["params"]
+                            for t in [self._take_token_gradient(p)] if t is not None]
                 live = [p for p in g["params"] if p.grad is not None]
-                if not live:
+                if not live and not by_token:
                     continue
                 g["step"] += 1
-                # the group's tensors in one fused pass (one launch per 48 tensors)
                 b1, b2 = g["betas"]
+                hp = dict(step=g["step"], lr=g["lr"], beta1=b1, beta2=b2, eps=g["eps"],
+                          weight_decay=g["weight_decay"], decoupled=g["decoupled"],
+                          cautious_wd=g["cautious_wd"])
+                for p, (tokens, dout, scale, _) in by_token:
+                    from . import ops
+
+                    ops.adamw_step_embedding(p.data, tokens, dout, self.state[id(p)]["exp_avg"],
+                                             self.state[id(p)]["exp_avg_sq"], scale=scale, **hp)
+                # the group's tensors in one fused pass (one launch per 48 tensors)
                 segs = [(p.data, p.grad, self.state[id(p)]["exp_avg"],
                          self.state[id(p)]["exp_avg_sq"]) for p in live]
-                _lib.adamw_step_multi(segs, step=g["step"], lr=g["lr"], beta1=b1, beta2=b2,
-                                      eps=g["eps"], weight_decay=g["weight_decay"],
-                                      decoupled=g["decoupled"], cautious_wd=g["cautious_wd"])
+                _lib.adamw_step_multi(segs, **hp)
                 continue
             # Muon: every bucket with gradients in one call
             stacks = [st for b in self._buckets[gi] for st in b.live_stacks()]
@@ -201,6 +253,7 @@ class MuonAdamW:
                            ns_mode=g["ns_mode"], workspace=ws)
 
     def zero_grad(self, set_to_none: bool = True) -> None:
+        self._token_grads.clear()
         for g in self.param_groups:
             for p in g["params"]:
                 if p.grad is None:

@@ -10,6 +10,11 @@
  *   ma_adamw_step  the fused elementwise AdamW step over one flat fp32 range
  *                  (embeddings, LM head, normalisation gains, biases).
  *
+ * and the training operators that produce the gradients of those AdamW parameters, or
+ * spare them: ma_embedding_forward / _backward, ma_adamw_step_embedding (AdamW on a table
+ * straight from its tokens), ma_layer_norm_forward / _backward and ma_distill_forward /
+ * _backward / _loss_grad.
+ *
  * Sources, by page title:
  *   [HB] "Optimizers: AdamW, Muon and the distributed optimizer" (AI infra handbook):
  *        section "AdamW: decoupled weight decay" and section "Muon: orthogonalising
@@ -48,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MA_ABI_VERSION 4
+#define MA_ABI_VERSION 5
 
 typedef enum {
   MA_OK = 0,
@@ -380,6 +385,110 @@ ma_status ma_muon_check_plan(const ma_muon_bucket* buckets, int32_t n_buckets,
 ma_status ma_muon_ns_time(const ma_muon_bucket* buckets, int32_t n_buckets,
                           const ma_muon_hparams* hp, void* workspace, size_t workspace_bytes,
                           void* stream, int32_t reps, float* phase_ms);
+
+/* ------------------------------------------------------------------------------------
+ * Training operators: the first layer, the normalisations and the loss around the AdamW
+ * parameters.  Parameters and their gradients are fp32, as everywhere in this library;
+ * activations are fp32, fp16 or bf16 (rounded once, to nearest even, after fp32
+ * arithmetic).  Rows of activations are contiguous, `stride` values apart (>= their
+ * length); no alignment beyond an element's is needed, and results do not depend on
+ * strides or alignment.  Sums run in a fixed order without floating-point atomics: the
+ * same inputs give the same bits on every call.  Written buffers must not overlap any
+ * other buffer of the call unless stated.  All calls can be captured into a graph; none
+ * allocates, clears with a memset or synchronises.  Errors: MA_ERR_INVALID_ARG (NULL or
+ * misaligned pointers, sizes, types, overlap, non-finite scalars), MA_ERR_UNSUPPORTED
+ * (sizes above the stated limits or one launch), MA_ERR_WORKSPACE, MA_ERR_HIP.
+ * ------------------------------------------------------------------------------------ */
+typedef enum { MA_F32 = 0, MA_F16 = 1, MA_BF16 = 2 } ma_dtype;
+
+/* Lookup with scaling: out[t] = scale * table[token t], for n tokens (token_bits 32 or 64,
+ * signed).  A token outside [0, rows) marks padding: nothing is read, out[t] = 0.
+ * table: (rows, dim) fp32, rows < 2^31 - 1, dim <= 2^20; n <= 2^30 (0: no-op). */
+ma_status ma_embedding_forward(const float* table, int64_t rows, int64_t dim, const void* tokens,
+                               int32_t token_bits, int64_t n, float scale, void* out,
+                               int32_t out_type, int64_t out_stride, void* stream);
+
+/* Host only: workspace bytes of ma_embedding_backward and ma_adamw_step_embedding for n
+ * tokens (0 for n = 0 and for invalid sizes, which the calls then report). */
+size_t ma_embedding_workspace_bytes(int64_t rows, int64_t dim, int64_t n);
+
+/* The table's gradient by sorted tokens:
+ *   accumulate = 0: grad[v]  = scale * sum over t with token t = v of dout[t], all rows
+ *   accumulate = 1: grad[v] += the same, on the rows that occur; the others are untouched
+ * grad: (rows, dim) fp32, e.g. the table's part of the range ma_adamw_step reads.  Padding
+ * tokens (outside [0, rows)) contribute nothing and their dout is not read.  n = 0 clears
+ * grad or, with accumulate, does nothing.
+ * workspace: 256-byte aligned, ma_embedding_workspace_bytes; scratch. */
+ma_status ma_embedding_backward(const void* tokens, int32_t token_bits, int64_t n, const void* dout,
+                                int32_t dout_type, int64_t dout_stride, float scale, float* grad,
+                                int64_t rows, int64_t dim, int32_t accumulate, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* ma_adamw_step on a (rows, dim) table with the gradient of ma_embedding_backward
+ * (accumulate 0), which is neither written nor read back: 24 instead of 32 bytes of traffic
+ * per table element, and no gradient buffer.  Every row is stepped (rows that do not
+ * occur with a zero gradient).  The result is bitwise that of the two calls. */
+ma_status ma_adamw_step_embedding(float* param, float* exp_avg, float* exp_avg_sq, int64_t rows,
+                                  int64_t dim, const void* tokens, int32_t token_bits, int64_t n,
+                                  const void* dout, int32_t dout_type, int64_t dout_stride, float scale,
+                                  const ma_adamw_hparams* hp, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Layer norm of n rows of dim values (dim <= 2^20, n < 2^22):
+ *   mean = sum x / dim,  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
+ *   y = (x - mean) rstd weight + bias
+ * weight, bias: dim fp32 values, NULL for ones / zeros.  x and y have type `type`.  mean and
+ * rstd (n fp32 each) are what the backward pass needs. */
+ma_status ma_layer_norm_forward(const void* x, int32_t type, int64_t x_stride, int64_t n, int64_t dim,
+                                const float* weight, const float* bias, float eps, void* y,
+                                int64_t y_stride, float* mean, float* rstd, void* stream);
+
+/* Host only: workspace bytes of ma_layer_norm_backward (needed when dweight or dbias is
+ * given). */
+size_t ma_layer_norm_workspace_bytes(int64_t n, int64_t dim);
+
+/* Its gradients, for h = (x - mean) rstd and u = dy weight:
+ *   dx = rstd (u - sum u / dim - h sum (u h) / dim)
+ *   dweight (+)= sum over rows of dy h,  dbias (+)= sum over rows of dy
+ * dweight and dbias (dim fp32 each) may be NULL; accumulate = 1 adds to them.  n = 0 clears
+ * them or, with accumulate, does nothing. */
+ma_status ma_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                 int32_t type, int64_t n, int64_t dim, const float* weight,
+                                 const float* mean, const float* rstd, void* dx, int64_t dx_stride,
+                                 float* dweight, float* dbias, int32_t accumulate, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits.  Per row: `vocab` student logits z (type `type`,
+ * rows `stride` apart), `top` teacher logits a (teacher_type, rows contiguous) with their
+ * vocabulary ids (id_bits 32 or 64, signed), temperature tau in [1e-6, 1e6]:
+ *   p = softmax(a / tau) over the live entries: id in [0, vocab) and a above -inf
+ *   q = softmax(z / tau) over the vocabulary
+ *   loss = tau^2 sum p (log p - log q)          (Kullback-Leibler divergence)
+ * A row without a live entry has loss 0.  Repeated ids add up in q's target.  top = 1 is the
+ * cross entropy of a label (tau = 1).  0 <= top <= 1024, vocab < 2^31 - 1, n < 2^22.
+ * A student logit of -inf has q = 0 (loss inf where p > 0); a row of NaN, of +inf or of -inf
+ * alone has loss NaN.
+ * loss: n fp32.  stats: (n, 2) fp32, max z and sum exp((z - max z) / tau) of each row, for
+ * the backward call. */
+ma_status ma_distill_forward(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,
+                             const void* teacher, int32_t teacher_type, const void* ids, int32_t id_bits,
+                             int64_t top, float temperature, float* loss, float* stats, void* stream);
+
+/* The gradient of sum row_weight[r] loss[r] by the logits (row_weight: n fp32):
+ *   dlogits_j = row_weight tau (q_j - sum of p with id = j)
+ * zero for a row without a live entry or of weight 0, whatever its logits hold.  dlogits has
+ * the logits' type; it may be the logits themselves (same address and stride). */
+ma_status ma_distill_backward(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,
+                              const void* teacher, int32_t teacher_type, const void* ids, int32_t id_bits,
+                              int64_t top, float temperature, const float* stats, const float* row_weight,
+                              void* dlogits, int64_t dlogits_stride, void* stream);
+
+/* Both in one pass, for callers that know row_weight beforehand: the same loss and dlogits as
+ * the two calls. */
+ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,
+                               const void* teacher, int32_t teacher_type, const void* ids, int32_t id_bits,
+                               int64_t top, float temperature, const float* row_weight, float* loss,
+                               void* dlogits, int64_t dlogits_stride, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,280 @@
+"""The training operators as they are used together: a small model's training steps with
+MuonAdamW, graph capture, other streams and concurrent calls."""
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+ma = pytest.importorskip("adamw_optimizer_step_muon_amd")
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+V, D, T, K, EPS = 97, 32, 40, 6, 1e-5
+TAU, SCALE = 2.0, D ** 0.5
+
+
+def _model(seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    return {"table": 0.2 * r(V, D), "g0": 1 + 0.1 * r(D), "b0": 0.1 * r(D), "hidden": 0.2 * r(D, D),
+            "g1": 1 + 0.1 * r(D), "head": 0.2 * r(V, D)}
+
+
+def _batch(seed):
+    g = torch.Generator(device=DEV).manual_seed(1000 + seed)
+    tokens = torch.randint(0, V, (4, T // 4), generator=g, device=DEV)
+    tokens[2, 7:] = -1  # padded sequence
+    ids = torch.randint(0, V, (4, T // 4, K), generator=g, device=DEV)
+    ids[2, 7:] = -1
+    return tokens, torch.randn(4, T // 4, K, generator=g, device=DEV), ids
+
+
+def _loss(p, batch, optimizer=None):
+    tokens, teacher, ids = batch
+    x = ma.embedding(tokens, p["table"], scale=SCALE, optimizer=optimizer)
+    h = ma.layer_norm(x, p["g0"], p["b0"], eps=EPS)
+    x = x + torch.tanh((h.view(-1, D) @ p["hidden"]).view(x.shape))
+    y = ma.layer_norm(x, p["g1"], eps=EPS)
+    logits = (y.view(-1, D) @ p["head"].t()).view(*tokens.shape, V)
+    return ma.distill_loss(logits, teacher, ids, temperature=TAU).mean()
+
+
+def _plain_loss(p, batch):
+    """The same model in fp64 torch operations."""
+    tokens, teacher, ids = batch
+
+    def norm(x, w, b=0.0):
+        c = x - x.mean(-1, keepdim=True)
+        return c / torch.sqrt((c * c).mean(-1, keepdim=True) + EPS) * w + b
+
+    live = tokens >= 0
+    x = torch.where(live[..., None], p["table"][tokens.clamp(min=0)] * SCALE, 0.0)
+    x = x + torch.tanh((norm(x, p["g0"], p["b0"]).view(-1, D) @ p["hidden"]).view(x.shape))
+    logits = (norm(x, p["g1"]).view(-1, D) @ p["head"].t()).view(*tokens.shape, V)
+    log_q = torch.log_softmax(logits / TAU, -1)
+    log_p = torch.log_softmax(teacher.double() / TAU, -1)
+    kl = (log_p.exp() * (log_p - log_q.gather(-1, ids.clamp(min=0)))).sum(-1)
+    return TAU ** 2 * torch.where(live, kl, 0.0).mean()
+
+
+def _leaves(p):
+    return {k: t.clone().requires_grad_(True) for k, t in p.items()}
+
+
+def test_gradients_of_a_model():
+    """Every parameter's gradient against torch's fp64 one.  Ten stages of at most 130
+    roundings each (sums of 32, 40 or 97 terms): 1300 * 2^-24 = 8e-5 of the terms."""
+    p, batch = _model(1), _batch(1)
+    own, plain = _leaves(p), {k: t.double().requires_grad_(True) for k, t in p.items()}
+    a, b = _loss(own, batch), _plain_loss(plain, batch)
+    a.backward(), b.backward()
+    assert abs(float(a.detach()) - float(b.detach())) <= 8e-5 * abs(float(b.detach()))
+    for k in p:
+        d = (own[k].grad.double() - plain[k].grad).norm() / plain[k].grad.norm()
+        assert d <= 8e-5, (k, float(d))
+    assert own["table"].grad[batch[0].unique()[1:]].any()
+
+
+def _optimizer(p):
+    return ma.MuonAdamW([{"kind": "muon", "params": [p["hidden"]], "lr": 0.02},
+                         {"kind": "adamw", "params": [p[k] for k in ("table", "g0", "b0", "g1", "head")],
+                          "lr": 1e-2, "weight_decay": 0.1}])
+
+
+@pytest.mark.parametrize("micro", [1, 2])
+def test_steps_with_token_gradients_are_bitwise_the_dense_ones(micro):
+    """Three steps of `micro` batches each; two batches add up in a dense gradient, one is
+    stepped from the tokens."""
+    runs = []
+    for by_token in (False, True):
+        p = _leaves(_model(2))
+        opt = _optimizer(p)
+        for step in range(3):
+            for i in range(micro):
+                _loss(p, _batch(10 * step + i), opt if by_token else None).backward()
+            assert (p["table"].grad is None) == by_token
+            opt.step()
+            opt.zero_grad()
+            assert p["table"].grad is None
+        runs.append((p, opt.state_dict()["state"]))
+    for k in runs[0][0]:
+        # the two batches' dense gradients are added elementwise by autograd, and by the
+        # accumulating kernel: the same one rounding
+        assert torch.equal(runs[0][0][k], runs[1][0][k]), k
+    for i, st in runs[0][1].items():
+        for k in st:
+            assert torch.equal(st[k], runs[1][1][i][k])
+
+
+def test_tied_table_adds_token_and_dense_gradients():
+    p = _leaves(_model(3))
+    opt = _optimizer(p)
+    tokens, dout = torch.tensor([3, 3, 5], device=DEV), torch.randn(3, D, device=DEV)
+    dense = torch.randn(V, D, device=DEV)
+    p["table"].grad = dense.clone()
+    opt.add_token_gradient(p["table"], tokens, dout, 2.0)
+    before = p["table"].detach().clone()
+    opt.step()
+    want = dense + ma.embedding_backward(dout, tokens, V, scale=2.0)
+    assert torch.equal(p["table"].grad, want)
+    q = [before, want, torch.zeros_like(want), torch.zeros_like(want)]
+    ma.adamw_step(*q, step=1, lr=1e-2, weight_decay=0.1)
+    assert torch.equal(p["table"], q[0])
+
+
+def _calls(s):
+    """One training step's calls on static buffers."""
+    x = ma.embedding_forward(s["table"], s["tokens"], scale=SCALE, out_dtype=torch.bfloat16)
+    y, mean, rstd = ma.layer_norm_forward(x, s["g"], s["b"])
+    logits = y @ s["head"]
+    loss, dlogits = ma.distill_loss_grad(logits, s["teacher"], s["ids"], s["w"], temperature=TAU)
+    stats = ma.distill_forward(logits, s["teacher"], s["ids"], temperature=TAU)[1]
+    dlogits2 = ma.distill_backward(logits, s["teacher"], s["ids"], stats, s["w"], temperature=TAU)
+    dy = dlogits @ s["head_t"]
+    dx, dg, db = ma.layer_norm_backward(dy, x, mean, rstd, s["g"])
+    grad = ma.embedding_backward(dx, s["tokens"], s["table"].shape[0], scale=SCALE)
+    ma.adamw_step_embedding(s["p"], s["tokens"], dx, s["m"], s["v"], scale=SCALE, step=2, lr=1e-2)
+    return [y, loss, dlogits, dlogits2, dx, dg, db, grad]
+
+
+def _static(seed, n=700, rows=1500, dim=64, vocab=2050):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    s = {"table": r(rows, dim), "tokens": torch.randint(-1, 60, (n,), generator=g, device=DEV), "g": r(dim),
+         "b": r(dim), "head": r(dim, vocab).bfloat16(), "teacher": r(n, 9), "w": r(n).abs(),
+         "ids": torch.randint(0, vocab, (n, 9), generator=g, device=DEV), "p": r(rows, dim), "m": r(rows, dim),
+         "v": r(rows, dim).abs()}
+    s["head_t"] = s["head"].t().contiguous()
+    return s
+
+
+def test_captured_calls_replay_like_eager_ones():
+    """Two graphs of the same calls, replayed in turn on new inputs with eager work between."""
+    graphs = []
+    for seed in (1, 2):
+        s = _static(seed)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            _calls(s)  # library handles of the two products
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = _calls(s)
+        graphs.append((g, s, out))
+    for turn in range(3):
+        for k, (g, s, out) in enumerate(graphs):
+            new = _static(10 + 2 * turn + k)
+            for name in s:
+                s[name].copy_(new[name])
+            g.replay()
+            want = _calls(new)
+            torch.cuda.synchronize()
+            for a, b in zip(out + [s["p"], s["m"], s["v"]], want + [new["p"], new["m"], new["v"]]):
+                assert torch.equal(a, b)
+
+
+def test_captured_backward_pass_replays():
+    """loss.backward() through the autograd functions, captured: the parameters' gradients are
+    the graph's own buffers (no eager graph of these leaves exists)."""
+    p, batch = _leaves(_model(4)), _batch(4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _loss(p, batch).backward()
+        for t in p.values():
+            t.grad = None
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _loss(p, batch).backward()
+    for seed in (5, 6, 7):
+        for a, b in zip(batch, _batch(seed)):
+            a.copy_(b)
+        g.replay()
+        fresh = {k: t.detach().clone().requires_grad_(True) for k, t in p.items()}
+        _loss(fresh, _batch(seed)).backward()
+        torch.cuda.synchronize()
+        for k in p:
+            assert torch.equal(p[k].grad, fresh[k].grad), k
+
+
+def test_calls_on_another_stream():
+    s, t = _static(3), _static(3)
+    side = torch.cuda.Stream()
+    want = _calls(t)
+    side.wait_stream(torch.cuda.current_stream())
+    x = ma.embedding_forward(s["table"], s["tokens"], scale=SCALE, out_dtype=torch.bfloat16, stream=side)
+    y, mean, rstd = ma.layer_norm_forward(x, s["g"], s["b"], stream=side)
+    with torch.cuda.stream(side):
+        logits = y @ s["head"]
+    loss, dlogits = ma.distill_loss_grad(logits, s["teacher"], s["ids"], s["w"], temperature=TAU, stream=side)
+    with torch.cuda.stream(side):
+        dy = dlogits @ s["head_t"]
+    dx, dg, db = ma.layer_norm_backward(dy, x, mean, rstd, s["g"], stream=side)
+    grad = ma.embedding_backward(dx, s["tokens"], s["table"].shape[0], scale=SCALE, stream=side)
+    ma.adamw_step_embedding(s["p"], s["tokens"], dx, s["m"], s["v"], scale=SCALE, step=2, lr=1e-2, stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip([y, loss, dlogits, dx, dg, db, grad, s["p"], s["m"], s["v"]],
+                    [want[i] for i in (0, 1, 2, 4, 5, 6, 7)] + [t["p"], t["m"], t["v"]]):
+        assert torch.equal(a, b)
+
+
+def test_two_threads_at_once():
+    """Calls from two threads on their own streams, workspaces allocated per call."""
+    inputs, want = [_static(20), _static(21)], []
+    for seed in (20, 21):
+        t = _static(seed)
+        want.append(_calls(t) + [t["p"], t["m"], t["v"]])
+    torch.cuda.synchronize()
+    got, failed = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                out = _calls(inputs[i])
+                torch.cuda.current_stream().synchronize()
+                got[i] = out + [inputs[i][k] for k in "pmv"]
+        except Exception as e:  # pragma: no cover
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for a, b in zip(got, want):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_binding_checks_shapes():
+    x = torch.zeros(6, 8, device=DEV)
+    i = torch.zeros(6, dtype=torch.int64, device=DEV)
+    f = torch.zeros(6, device=DEV)
+    for bad in (lambda: ma.embedding_forward(x, i.float()), lambda: ma.embedding_forward(x.double(), i),
+                lambda: ma.embedding_forward(x, i, out=x[:, :4]), lambda: ma.embedding_forward(f, i),
+                lambda: ma.embedding_forward(x, i, out_dtype=torch.float64),
+                lambda: ma.embedding_backward(x[:5], i, 9), lambda: ma.embedding_backward(x, i.cpu(), 9),
+                lambda: ma.embedding_backward(x.t(), torch.zeros(8, dtype=torch.int64, device=DEV), 9),
+                lambda: ma.embedding_backward(x[:1].expand(6, 8), i, 9),
+                lambda: ma.embedding_backward(x, i, 9, grad=x),
+                lambda: ma.adamw_step_embedding(x, i, x.clone(), x[:5], x, step=1, lr=1.0),
+                lambda: ma.layer_norm_forward(x, f), lambda: ma.layer_norm_forward(x.double()),
+                lambda: ma.layer_norm_forward(x, out=x.bfloat16()),
+                lambda: ma.layer_norm_backward(x, x, f[:3], f), lambda: ma.layer_norm_backward(x.half(), x, f, f),
+                lambda: ma.layer_norm_backward(x, x.clone(), f, f.clone(), accumulate=True),
+                lambda: ma.layer_norm_backward(x, x, f, f, weight_grad=False, dweight=f),
+                lambda: ma.distill_forward(x, x, i[:, None]), lambda: ma.distill_forward(x, x[:, :2], i.view(6, 1)),
+                lambda: ma.distill_loss_grad(x, f[:, None], i[:, None], f[:2])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(ma.MuonAdamWError):
+        ma.embedding_forward(x, i, out=x)  # over its own table
+    with pytest.raises(ma.MuonAdamWError):
+        ma.layer_norm_forward(x, out=x)
+    with pytest.raises(ma.MuonAdamWError):
+        ma.distill_forward(x, f[:, None], i[:, None], temperature=0.0)
