@@ -569,6 +569,7 @@ constexpr int64_t kMaxThreadsPerLaunch = (int64_t(1) << 32) - 65536;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 2;
 constexpr int64_t kMaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxVocab = int64_t(1) << 30;  // room for a batch behind it in int
 
 int64_t bytes_of(int type) { return type == MA_F32 ? 4 : 2; }
 
@@ -667,7 +668,7 @@ ma_status check_distill(const DistillCall& c, Range* r) {
                 (long long)c.vocab, (long long)c.top);
   if (c.top > kMaxDistillTop)
     return fail(MA_ERR_UNSUPPORTED, "%lld teacher entries, at most %d", (long long)c.top, kMaxDistillTop);
-  if (c.vocab > kMaxRows || c.n > kMaxThreadsPerLaunch / 1024)
+  if (c.vocab > kMaxVocab || c.n > kMaxThreadsPerLaunch / 1024)
     return fail(MA_ERR_UNSUPPORTED, "%lld rows of %lld logits", (long long)c.n, (long long)c.vocab);
   if (!finite(c.temperature) || !(c.temperature > 0.0f))
     return fail(MA_ERR_INVALID_ARG, "temperature must be finite and above zero");

@@ -17,28 +17,38 @@
 namespace ma {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e38f;
 
-__device__ __forceinline__ float block_sum(float v, float* shared) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.0f;
-  for (int w = 0; w < kWaves; ++w) v += shared[w];
-  return v;
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Sums of exponentials in powers of two.  A set of values v has a maximum m, and s is the sum
+// of 2^(v scale - r) for the reference r = m scale, rounded (reference below; never fused
+// with what it is used in, so that everybody has the same r).  v scale - r is one fused
+// multiply-add: it rounds by its own size only, and a large m loses nothing.  Values beyond
+// kFar, whose products can overflow (rows filled with a type's lowest value), take the slower
+// (v - m) scale, where r = 0 stands for the difference already taken.
+constexpr float kFar = 1e30f;  // times the largest scale, log2(e) 1e6, still finite
+struct Soft {
+  float m, s;
+};
+__device__ __forceinline__ float reference(float m, float scale) {
+#pragma clang fp contract(off)
+  return m * scale;
 }
-__device__ __forceinline__ float block_max(float v, float* shared) {
-  v = wave_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = shared[0];
-  for (int w = 1; w < kWaves; ++w) v = fmaxf(v, shared[w]);
-  return v;
+template <bool kIsFar>
+__device__ __forceinline__ float exponent(float v, float scale, float m, float r) {
+  return kIsFar ? (v - m) * scale : __builtin_fmaf(v, scale, -r);
+}
+template <bool kIsFar>
+__device__ __forceinline__ float between(float from, float to, float scale) {
+  return kIsFar ? (from - to) * scale : reference(from, scale) - reference(to, scale);
+}
+// The lanes' sets joined; every lane gets the result.
+template <bool kIsFar>
+__device__ __forceinline__ Soft wave_join(Soft v, float scale) {
+  const float m = wave_max(v.m);
+  return Soft{m, wave_sum(v.s * exp2_(between<kIsFar>(v.m, m, scale)))};
 }
 
 __device__ __forceinline__ float teacher_at(const DistillCall& c, int64_t i) {
@@ -49,102 +59,241 @@ __device__ __forceinline__ float teacher_at(const DistillCall& c, int64_t i) {
   }
 }
 
-// One block per row.
-template <int T, int kMode>
+// A thread reads the row in batches of kU vectors of 16 bytes, all loaded before the first is
+// used.
+constexpr int kU = 4;
+template <int T>
+constexpr int kVec = 16 / sizeof(typename Act<T>::S);
+
+// Maximum and sum of a row; the waves' results go to out.
+template <int T, int kThreads, bool kIsFar>
+__device__ Soft sweep(const typename Act<T>::S* z, int vocab, float scale, Soft* out) {
+  constexpr int N = kVec<T>;
+  const int tid = threadIdx.x;
+  Soft a{kIsFar ? kLowest : -kFar, 0.0f};  // finite, so that differences to it are defined
+  const auto take = [&](const float (&v)[kU][N]) {
+    float m = a.m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) m = fmaxf(m, v[u][e]);
+    const float r = reference(m, scale);
+    float s[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      s[u] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[u] += exp2_(exponent<kIsFar>(v[u][e], scale, m, r));
+    }
+    a = Soft{m, a.s * exp2_(between<kIsFar>(a.m, m, scale)) + ((s[0] + s[1]) + (s[2] + s[3]))};
+  };
+  const int whole = vocab / (kThreads * kU * N) * (kThreads * kU * N);
+  for (int at = tid * N; at < whole; at += kThreads * kU * N) {
+    float v[kU][N];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load_act<T, N>(z + at + u * kThreads * N, v[u]);
+    take(v);
+  }
+  if (whole < vocab) {  // the last batch: missing values count as -inf
+    float v[kU][N];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int at = whole + (u * kThreads + tid) * N;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[u][e] = -INFINITY;
+      if (at < vocab) load_part<T, N>(z + at, vocab - at, -INFINITY, v[u]);
+    }
+    take(v);
+  }
+  a = wave_join<kIsFar>(a, scale);
+  if ((tid & 63) == 0) out[tid >> 6] = a;
+  return a;
+}
+
+// The waves' results joined, one a lane.
+template <int kThreads, bool kIsFar>
+__device__ Soft block_join(const Soft* of, float scale) {
+  const int lane = threadIdx.x & 63;
+  return wave_join<kIsFar>(lane < kThreads / 64 ? of[lane] : Soft{kIsFar ? kLowest : -kFar, 0.0f}, scale);
+}
+
+// dz = gq 2^exponent over the row, from its end to its beginning: what the first sweep read
+// last is still in the cache.
+template <int T, int kThreads, bool kIsFar>
+__device__ void spread(const typename Act<T>::S* z, typename Act<T>::S* dz, int vocab, float scale, float m,
+                       float r, float gq) {
+  constexpr int N = kVec<T>;
+  const int tid = threadIdx.x;
+  const auto give = [&](int at, const float (&v)[N]) {
+    float d[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) d[e] = gq * exp2_(exponent<kIsFar>(v[e], scale, m, r));
+    store_part<T, N>(dz + at, vocab - at, d);
+  };
+  const int whole = vocab / (kThreads * kU * N) * (kThreads * kU * N);
+  float v[kU][N];
+  if (whole < vocab) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int at = whole + (u * kThreads + tid) * N;
+      if (at < vocab) load_part<T, N>(z + at, vocab - at, 0.0f, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int at = whole + (u * kThreads + tid) * N;
+      if (at < vocab) give(at, v[u]);
+    }
+  }
+  for (int at = whole - (kThreads * kU - tid) * N; at >= 0; at -= kThreads * kU * N) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load_act<T, N>(z + at + u * kThreads * N, v[u]);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) give(at + u * kThreads * N, v[u]);
+  }
+}
+
+// One block per row: a sweep for maximum and sum (forward, both), a sweep for the gradient
+// (backward, both).
+template <int T, int kMode, int kThreads>
 __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   typedef typename Act<T>::S S;
+  constexpr int N = kVec<T>, kWaves = kThreads / 64;
+  constexpr int kPer = kMaxDistillTop / kThreads;  // teacher entries a thread holds
   constexpr bool kLoss = kMode != kDistillBackward, kGrad = kMode != kDistillForward;
-  __shared__ float shared[kWaves];
+  __shared__ Soft joined[2][kWaves];
+  __shared__ float terms[kWaves];
+  __shared__ float counts[kWaves];
   __shared__ float prob[kMaxDistillTop];
   __shared__ int32_t id[kMaxDistillTop];
   const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, top = static_cast<int>(c.top);
   const S* z = static_cast<const S*>(c.logits) + row * c.stride;
   S* dz = kGrad ? static_cast<S*>(c.dlogits) + row * c.dlogits_stride : nullptr;
   const float weight = kGrad ? c.row_weight[row] : 0.0f;
-  const float scale = kLog2e / c.temperature;  // exp((z - m) / tau) = 2^((z - m) scale)
+  const float scale = kLog2e / c.temperature;  // exp((v - m) / tau) = 2^((v - m) scale)
+  const int vocab = static_cast<int>(c.vocab);
 
-  // the teacher: thread i holds entry i (at most kThreads of them)
-  int32_t my_id = -1;
-  float a = -INFINITY, my_z = 0.0f;
-  if (tid < c.top) {
-    const int64_t at = row * c.top + tid;
+  // the teacher's entries and the logits at their places
+  int32_t my_id[kPer];
+  float a[kPer], my_z[kPer];
+  Soft ta{kLowest, 0.0f};
+  int live = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = k * kThreads + tid;
+    my_id[k] = -1;
+    my_z[k] = a[k] = 0.0f;
+    if (i >= top) continue;
+    const int64_t at = row * c.top + i;
     const int64_t j = c.id_bits == 64 ? static_cast<const int64_t*>(c.ids)[at]
                                       : static_cast<const int32_t*>(c.ids)[at];
-    a = teacher_at(c, at);
-    if (j >= 0 && j < c.vocab && a != -INFINITY) {
-      my_id = static_cast<int32_t>(j);
-      my_z = Act<T>::up(z[j]);
-    } else {
-      a = -INFINITY;
-    }
-  }
-  const bool live = my_id >= 0;
-  const float a_max = block_max(a, shared);
-  const float a_exp = live ? __builtin_amdgcn_exp2f((a - a_max) * scale) : 0.0f;
-  const float a_sum = block_sum(a_exp, shared);
-  const bool some = block_max(live ? 1.0f : 0.0f, shared) > 0.0f;
-  const float p = live ? a_exp / a_sum : 0.0f;
-  if (tid < c.top) {
-    prob[tid] = p;
-    id[tid] = my_id;
+    a[k] = teacher_at(c, at);
+    if (j < 0 || j >= c.vocab || a[k] == -INFINITY) continue;
+    my_id[k] = static_cast<int32_t>(j);
+    my_z[k] = Act<T>::up(z[j]);
+    ++live;
+    const float m = fmaxf(ta.m, a[k]);
+    ta = Soft{m, ta.s * exp2_(between<true>(ta.m, m, scale)) + exp2_(exponent<true>(a[k], scale, m, 0.0f))};
   }
 
-  float m, s;
+  Soft zs{0.0f, 0.0f};
+  if (kLoss) zs = sweep<T, kThreads, false>(z, vocab, scale, joined[0]);
+  ta = wave_join<true>(ta, scale);
+  const float lives = wave_sum(static_cast<float>(live));
+  if (lane == 0) {
+    joined[1][wave] = ta;
+    counts[wave] = lives;
+  }
+  __syncthreads();
   if (kLoss) {
-    // maximum and sum of exponentials in one sweep; a thread's start of -FLT_MAX keeps
-    // 2^(z - m) defined for rows of -inf, whose sum stays 0 and is reported as NaN below
-    float tm = -3.402823466e38f, ts = 0.0f;
-    for (int64_t i = tid; i < c.vocab; i += kThreads) {
-      const float v = Act<T>::up(z[i]);
-      const float nm = fmaxf(tm, v);
-      ts = ts * __builtin_amdgcn_exp2f((tm - nm) * scale) + __builtin_amdgcn_exp2f((v - nm) * scale);
-      tm = nm;
-    }
-    m = block_max(tm, shared);
-    s = block_sum(ts * __builtin_amdgcn_exp2f((tm - m) * scale), shared);
-    if (s == 0.0f) {
-      m = -INFINITY;
-      s = __builtin_nanf("");
-    }
-    float term = 0.0f;
-    if (p > 0.0f || a_sum != a_sum) {
-      const float log_p = ((a - a_max) * scale - __builtin_log2f(a_sum)) * kLn2;
-      const float log_q = ((my_z - m) * scale - __builtin_log2f(s)) * kLn2;
-      term = live ? p * (log_p - log_q) : 0.0f;
-    }
-    const float loss = block_sum(term, shared);
-    if (tid == 0) {
-      c.loss[row] = c.temperature * c.temperature * loss;
-      if (c.stats) {
-        c.stats[2 * row] = m;
-        c.stats[2 * row + 1] = s;
-      }
+    zs = block_join<kThreads, false>(joined[0], scale);
+    if (zs.s == 0.0f || zs.m > kFar) {  // every value below -kFar, or a reference that overflows
+      __syncthreads();
+      sweep<T, kThreads, true>(z, vocab, scale, joined[0]);
+      __syncthreads();
+      zs = block_join<kThreads, true>(joined[0], scale);
+      if (zs.s == 0.0f) zs = Soft{-INFINITY, __builtin_nanf("")};  // nothing above -inf
+    } else {
+      // from the rounded reference to the maximum itself
+      zs.s *= exp2_(-exponent<false>(zs.m, scale, zs.m, reference(zs.m, scale)));
     }
   } else {
-    m = c.stats[2 * row];
-    s = c.stats[2 * row + 1];
+    zs = Soft{c.stats[2 * row], c.stats[2 * row + 1]};
+  }
+  ta = block_join<kThreads, true>(joined[1], scale);
+  const bool some = wave_sum(lane < kWaves ? counts[lane] : 0.0f) > 0.0f;
+  // q = 2^(exponent(v) - zc) / zs.s, zc the maximum's own exponent
+  const bool far = fabsf(zs.m) > kFar;
+  const float zr = far ? 0.0f : reference(zs.m, scale);
+  const float zc = far ? 0.0f : exponent<false>(zs.m, scale, zs.m, zr);
+  const auto power_of = [&](float v) {
+    return far ? exponent<true>(v, scale, zs.m, zr) : exponent<false>(v, scale, zs.m, zr);
+  };
+
+  float p[kPer], term = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    p[k] = my_id[k] >= 0 ? exp2_(exponent<true>(a[k], scale, ta.m, 0.0f)) / ta.s : 0.0f;
+    if (kLoss && p[k] != 0.0f) {  // NaN included
+      const float log2_p = exponent<true>(a[k], scale, ta.m, 0.0f) - __builtin_log2f(ta.s);
+      const float log2_q = power_of(my_z[k]) - zc - __builtin_log2f(zs.s);
+      term += p[k] * (log2_p - log2_q);
+    }
+    const int i = k * kThreads + tid;
+    if (kGrad && i < top) {
+      prob[i] = p[k];
+      id[i] = my_id[k];
+    }
+  }
+  if (kLoss) {
+    term = wave_sum(term);
+    if (lane == 0) terms[wave] = term;
+  }
+  __syncthreads();
+  if (kLoss && tid == 0) {
+    float sum = 0.0f;
+    for (int w = 0; w < kWaves; ++w) sum += terms[w];
+    c.loss[row] = c.temperature * c.temperature / kLog2e * sum;
+    if (c.stats) {
+      c.stats[2 * row] = zs.m;
+      c.stats[2 * row + 1] = zs.s;
+    }
   }
   if (!kGrad) return;
-  const float g = weight * c.temperature;
-  const float gq = g / s;
-  const bool zero = weight == 0.0f || !some;
-  for (int64_t i = tid; i < c.vocab; i += kThreads) {
-    const float v = zero ? 0.0f : gq * __builtin_amdgcn_exp2f((Act<T>::up(z[i]) - m) * scale);
-    dz[i] = Act<T>::down(v);
+
+  const float g = weight * c.temperature, gq = g / zs.s * exp2_(-zc);
+  if (weight == 0.0f || !some) {
+    const float d[N] = {};
+    for (int at = tid * N; at < vocab; at += kThreads * N) store_part<T, N>(dz + at, vocab - at, d);
+    return;
   }
-  if (zero) return;
+  if (far) spread<T, kThreads, true>(z, dz, vocab, scale, zs.m, zr, gq);
+  else spread<T, kThreads, false>(z, dz, vocab, scale, zs.m, zr, gq);
+  // the teacher's entries again, from the logits read before: the first of equal ids writes,
+  // after the sweep's stores
   __syncthreads();
-  // the teacher's entries again, from the logits read before: the first of equal ids writes
-  if (live) {
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (my_id[k] < 0) continue;
+    const int mine = k * kThreads + tid;
     float sum = 0.0f;
     bool first = true;
-    for (int i = 0; i < c.top; ++i)
-      if (id[i] == my_id) {
-        if (i < tid) first = false;
+    for (int i = 0; i < top; ++i)
+      if (id[i] == my_id[k]) {
+        if (i < mine) first = false;
         sum += prob[i];
       }
-    if (first) dz[my_id] = Act<T>::down(gq * __builtin_amdgcn_exp2f((my_z - m) * scale) - g * sum);
+    if (first) dz[my_id[k]] = Act<T>::down(gq * exp2_(power_of(my_z[k])) - g * sum);
+  }
+}
+
+template <int T, int kThreads>
+void launch_rows(const DistillCall& c, DistillMode mode, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(c.n)), block(kThreads);
+  switch (mode) {
+    case kDistillForward: hipLaunchKernelGGL((distill_kernel<T, kDistillForward, kThreads>), grid, block, 0, s, c); break;
+    case kDistillBackward: hipLaunchKernelGGL((distill_kernel<T, kDistillBackward, kThreads>), grid, block, 0, s, c); break;
+    case kDistillBoth: hipLaunchKernelGGL((distill_kernel<T, kDistillBoth, kThreads>), grid, block, 0, s, c); break;
   }
 }
 
@@ -153,12 +302,9 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
 hipError_t launch_distill(const DistillCall& c, DistillMode mode, hipStream_t s) {
   return with_act(c.type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    const dim3 grid(static_cast<unsigned>(c.n)), block(kThreads);
-    switch (mode) {
-      case kDistillForward: hipLaunchKernelGGL((distill_kernel<T, kDistillForward>), grid, block, 0, s, c); break;
-      case kDistillBackward: hipLaunchKernelGGL((distill_kernel<T, kDistillBackward>), grid, block, 0, s, c); break;
-      case kDistillBoth: hipLaunchKernelGGL((distill_kernel<T, kDistillBoth>), grid, block, 0, s, c); break;
-    }
+    // 256 threads where a batch of theirs covers the row
+    if (c.vocab <= 256 * 4 * (T == kActF32 ? 4 : 8)) launch_rows<T, 256>(c, mode, s);
+    else launch_rows<T, 1024>(c, mode, s);
     return hipGetLastError();
   });
 }

@@ -99,16 +99,36 @@ inline hipError_t with_act(int type, F f) {
   return hipErrorInvalidValue;
 }
 
-// Sums over a wave; every lane gets the result.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+// Reductions over a wave by data-parallel moves within the vector unit: after quad, half-row
+// and row exchanges every lane has its row of 16, the two row broadcasts carry the rows'
+// results to lane 63, and every lane gets that lane's value.  Six dependent operations
+// without the shared memory's latency.  `fill` is the operation's neutral element.
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ float lane_move(float fill, float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, fill), __builtin_bit_cast(int, v),
+                                                               kCtrl, kRowMask, 0xf, false));
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+template <typename F>
+__device__ __forceinline__ float row16_reduce(float v, float fill, F f) {
+  v = f(v, lane_move<0xb1, 0xf>(fill, v));   // quads: lanes 1 0 3 2
+  v = f(v, lane_move<0x4e, 0xf>(fill, v));   // quads: lanes 2 3 0 1
+  v = f(v, lane_move<0x141, 0xf>(fill, v));  // halves of a row mirrored
+  return f(v, lane_move<0x140, 0xf>(fill, v));  // rows mirrored
 }
+template <typename F>
+__device__ __forceinline__ float wave_reduce(float v, float fill, F f) {
+  v = row16_reduce(v, fill, f);
+  v = f(v, lane_move<0x142, 0xa>(fill, v));  // lane 15 of rows 0 and 2 to rows 1 and 3
+  v = f(v, lane_move<0x143, 0xc>(fill, v));  // lane 31 to rows 2 and 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, 0.0f, Add()); }
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, -INFINITY, Max()); }
 
 }  // namespace ma

@@ -179,3 +179,34 @@ def test_no_rows():
     loss, stats = ma.distill_forward(z, a, ids)
     assert loss.shape == (0,) and stats.shape == (0, 2)
     assert ma.distill_loss_grad(z, a, ids, loss)[1].shape == (0, 40)
+
+
+@pytest.mark.parametrize("vocab", [50, 9000, 40001])
+@pytest.mark.parametrize("tau", [0.5, 4.0])
+def test_rows_far_from_zero(vocab, tau):
+    """Rows filled with the type's lowest or a huge value, and rows on a large offset: the
+    differences to the maximum are exact in fp32, so the loss is that of the differences."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    z = torch.randn(6, vocab, generator=g, device=DEV)
+    z[0], z[1] = low, high
+    z[2] = low
+    z[2, 3] = low / 2                    # one entry far above the others
+    z[3] = 4096.0 + (z[3] * 64).round() / 64   # exact sums
+    z[4] = -4096.0 + (z[4] * 64).round() / 64
+    z[5, ::2] = high
+    a, ids = torch.zeros(6, 2, device=DEV), torch.tensor([[3, 5]], device=DEV).repeat(6, 1)
+    ids[2] = torch.tensor([3, -1], device=DEV)
+    ids[5] = torch.tensor([4, 8], device=DEV)
+    w = torch.ones(6, device=DEV)
+    loss, grad = ma.distill_loss_grad(z, a, ids, w, temperature=tau)
+    own, stats = ma.distill_forward(z, a, ids, temperature=tau)
+    again = ma.distill_backward(z, a, ids, stats, w, temperature=tau)
+    ref, _, _ = training.distill(_np(z), _np(a), ids.cpu().numpy(), tau)
+    dz = training.distill_grad(_np(z), _np(a), ids.cpu().numpy(), np.ones(6), tau)
+    # |x| + sum q|x| <= 20 / tau, log s <= 11 (see the head of this file)
+    k = (vocab / 64 + 64) * E
+    assert (np.abs(_np(loss) - ref) <= tau ** 2 * (60 / tau * E + k + 48 * E + 4 * E * np.abs(ref))).all()
+    assert torch.equal(loss, own)
+    for got in (grad, again):
+        assert (np.abs(_np(got) - dz) <= tau * (60 / tau * E + k + 16 * E) + 2 * E).all()
