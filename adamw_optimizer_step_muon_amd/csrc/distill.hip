@@ -63,20 +63,40 @@ __device__ __forceinline__ float teacher_at(const DistillCall& c, int64_t i) {
 // used.
 constexpr int kU = 4;
 template <int T>
-constexpr int kVec = 16 / sizeof(typename Act<T>::S);
+constexpr int kVec = Vec<T>::kN;
+
+// What a first sweep keeps of its row for the second one: the last kKeep whole batches in the
+// block's shared memory (each thread reads back what it wrote itself) and the rest behind
+// them in registers.  Where kKeep is 0 nothing is kept.  Almost no second read hits the L2 (a
+// row of 128000 bf16 values is 256 KB, 32 CUs share 4 MB), so what is kept is traffic saved.
+// One batch of 64 KB lets two blocks of 1024 threads share a CU, one sweeping while the other
+// waits: loss and gradient of 4096 x 128000 bf16 took 467 us keeping nothing, 430 us (4.9
+// TB/s, the rate of a large copy) with one batch, and 489 us with two, which leave one block.
+constexpr int kKeepBatches = 1;
+template <int T, int kThreads, int kKeep>
+struct Kept {
+  typedef typename Vec<T>::P P;
+  P tail[kKeep > 0 ? kU : 1];
+  P* shared;  // kKeep batches, or null
+};
 
 // Maximum and sum of a row; the waves' results go to out.
-template <int T, int kThreads, bool kIsFar>
-__device__ Soft sweep(const typename Act<T>::S* z, int vocab, float scale, Soft* out) {
-  constexpr int N = kVec<T>;
+template <int T, int kThreads, bool kIsFar, int kKeep>
+__device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, Soft* out, Kept<T, kThreads, kKeep>& kept) {
+  typedef typename Kept<T, kThreads, kKeep>::P P;
+  constexpr int N = kVec<T>, kBatch = kThreads * kU * N;
   const int tid = threadIdx.x;
   Soft a{kIsFar ? kLowest : -kFar, 0.0f};  // finite, so that differences to it are defined
-  const auto take = [&](const float (&v)[kU][N]) {
-    float m = a.m;
+  const auto take = [&](const P (&x)[kU], int left) {  // values at and behind `left` count as -inf
+    float v[kU][N], m = a.m;
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int e = 0; e < N; ++e) m = fmaxf(m, v[u][e]);
+      for (int e = 0; e < N; ++e) {
+        v[u][e] = Act<T>::up(x[u][e]);
+        if (left < kBatch && (u * kThreads + tid) * N + e >= left) v[u][e] = -INFINITY;
+        m = fmaxf(m, v[u][e]);
+      }
     const float r = reference(m, scale);
     float s[kU];
 #pragma unroll
@@ -87,27 +107,30 @@ __device__ Soft sweep(const typename Act<T>::S* z, int vocab, float scale, Soft*
     }
     a = Soft{m, a.s * exp2_(between<kIsFar>(a.m, m, scale)) + ((s[0] + s[1]) + (s[2] + s[3]))};
   };
-  const int whole = vocab / (kThreads * kU * N) * (kThreads * kU * N);
-  for (int at = tid * N; at < whole; at += kThreads * kU * N) {
-    float v[kU][N];
+  const int whole = vocab / kBatch;
+  for (int b = 0; b < whole; ++b) {
+    P x[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) load_act<T, N>(z + at + u * kThreads * N, v[u]);
-    take(v);
+    for (int u = 0; u < kU; ++u) x[u] = *reinterpret_cast<const P*>(z + b * kBatch + (u * kThreads + tid) * N);
+    if (kKeep > 0 && b >= whole - kKeep) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) kept.shared[((whole - 1 - b) * kU + u) * kThreads + tid] = x[u];
+    }
+    take(x, kBatch);
   }
-  if (whole < vocab) {  // the last batch: missing values count as -inf
-    float v[kU][N];
+  const int left = vocab - whole * kBatch;
+  if (left > 0) {
+    P x[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int at = whole + (u * kThreads + tid) * N;
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[u][e] = -INFINITY;
-      if (at < vocab) load_part<T, N>(z + at, vocab - at, -INFINITY, v[u]);
+      const int at = (u * kThreads + tid) * N;
+      x[u] = load_raw<T>(z + whole * kBatch + at, left - at);
+      if (kKeep > 0) kept.tail[u] = x[u];
     }
-    take(v);
+    take(x, left);
   }
   a = wave_join<kIsFar>(a, scale);
   if ((tid & 63) == 0) out[tid >> 6] = a;
-  return a;
 }
 
 // The waves' results joined, one a lane.
@@ -117,44 +140,60 @@ __device__ Soft block_join(const Soft* of, float scale) {
   return wave_join<kIsFar>(lane < kThreads / 64 ? of[lane] : Soft{kIsFar ? kLowest : -kFar, 0.0f}, scale);
 }
 
-// dz = gq 2^exponent over the row, from its end to its beginning: what the first sweep read
-// last is still in the cache.
-template <int T, int kThreads, bool kIsFar>
+// dz = gq 2^exponent over the row, from its end to its beginning: what the first sweep kept,
+// or read last, comes first.  Non-temporal stores: dz is not read here, and what it leaves of
+// the cache is the logits' (500 -> 462 us for 4096 x 128000 bf16).
+template <int T, int kThreads, bool kIsFar, int kKeep>
 __device__ void spread(const typename Act<T>::S* z, typename Act<T>::S* dz, int vocab, float scale, float m,
-                       float r, float gq) {
-  constexpr int N = kVec<T>;
+                       float r, float gq, const Kept<T, kThreads, kKeep>& kept) {
+  typedef typename Kept<T, kThreads, kKeep>::P P;
+  constexpr int N = kVec<T>, kBatch = kThreads * kU * N;
   const int tid = threadIdx.x;
-  const auto give = [&](int at, const float (&v)[N]) {
-    float d[N];
+  const auto give = [&](int at, const P& x) {
+    P d;
 #pragma unroll
-    for (int e = 0; e < N; ++e) d[e] = gq * exp2_(exponent<kIsFar>(v[e], scale, m, r));
-    store_part<T, N>(dz + at, vocab - at, d);
+    for (int e = 0; e < N; ++e)
+      d[e] = Act<T>::down(gq * exp2_(exponent<kIsFar>(Act<T>::up(x[e]), scale, m, r)));
+    if (vocab - at >= N) {
+      __builtin_nontemporal_store(d, reinterpret_cast<P*>(dz + at));
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < vocab - at) dz[at + e] = d[e];
+    }
   };
-  const int whole = vocab / (kThreads * kU * N) * (kThreads * kU * N);
-  float v[kU][N];
-  if (whole < vocab) {
+  const int whole = vocab / kBatch;
+  const int left = vocab - whole * kBatch;
+  if (left > 0) {
+    P x[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int at = whole + (u * kThreads + tid) * N;
-      if (at < vocab) load_part<T, N>(z + at, vocab - at, 0.0f, v[u]);
+      const int at = (u * kThreads + tid) * N;
+      x[u] = kKeep > 0 ? kept.tail[kKeep > 0 ? u : 0] : load_raw<T>(z + whole * kBatch + at, left - at);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int at = whole + (u * kThreads + tid) * N;
-      if (at < vocab) give(at, v[u]);
+      const int at = (u * kThreads + tid) * N;
+      if (at < left) give(whole * kBatch + at, x[u]);
     }
   }
-  for (int at = whole - (kThreads * kU - tid) * N; at >= 0; at -= kThreads * kU * N) {
+  for (int b = whole - 1; b >= 0; --b) {
+    P x[kU];
+    if (kKeep > 0 && b >= whole - kKeep) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) load_act<T, N>(z + at + u * kThreads * N, v[u]);
+      for (int u = 0; u < kU; ++u) x[u] = kept.shared[((whole - 1 - b) * kU + u) * kThreads + tid];
+    } else {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) give(at + u * kThreads * N, v[u]);
+      for (int u = 0; u < kU; ++u) x[u] = *reinterpret_cast<const P*>(z + b * kBatch + (u * kThreads + tid) * N);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) give(b * kBatch + (u * kThreads + tid) * N, x[u]);
   }
 }
 
 // One block per row: a sweep for maximum and sum (forward, both), a sweep for the gradient
 // (backward, both).
-template <int T, int kMode, int kThreads>
+template <int T, int kMode, int kThreads, int kKeep>
 __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   typedef typename Act<T>::S S;
   constexpr int N = kVec<T>, kWaves = kThreads / 64;
@@ -196,8 +235,14 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
     ta = Soft{m, ta.s * exp2_(between<true>(ta.m, m, scale)) + exp2_(exponent<true>(a[k], scale, m, 0.0f))};
   }
 
+  Kept<T, kThreads, kKeep> kept;
+  kept.shared = nullptr;
+  if constexpr (kKeep > 0) {
+    __shared__ typename Kept<T, kThreads, kKeep>::P room[kKeep * kU * kThreads];
+    kept.shared = room;
+  }
   Soft zs{0.0f, 0.0f};
-  if (kLoss) zs = sweep<T, kThreads, false>(z, vocab, scale, joined[0]);
+  if (kLoss) sweep<T, kThreads, false, kKeep>(z, vocab, scale, joined[0], kept);
   ta = wave_join<true>(ta, scale);
   const float lives = wave_sum(static_cast<float>(live));
   if (lane == 0) {
@@ -209,7 +254,7 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
     zs = block_join<kThreads, false>(joined[0], scale);
     if (zs.s == 0.0f || zs.m > kFar) {  // every value below -kFar, or a reference that overflows
       __syncthreads();
-      sweep<T, kThreads, true>(z, vocab, scale, joined[0]);
+      sweep<T, kThreads, true, kKeep>(z, vocab, scale, joined[0], kept);
       __syncthreads();
       zs = block_join<kThreads, true>(joined[0], scale);
       if (zs.s == 0.0f) zs = Soft{-INFINITY, __builtin_nanf("")};  // nothing above -inf
@@ -267,8 +312,8 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
     for (int at = tid * N; at < vocab; at += kThreads * N) store_part<T, N>(dz + at, vocab - at, d);
     return;
   }
-  if (far) spread<T, kThreads, true>(z, dz, vocab, scale, zs.m, zr, gq);
-  else spread<T, kThreads, false>(z, dz, vocab, scale, zs.m, zr, gq);
+  if (far) spread<T, kThreads, true, kKeep>(z, dz, vocab, scale, zs.m, zr, gq, kept);
+  else spread<T, kThreads, false, kKeep>(z, dz, vocab, scale, zs.m, zr, gq, kept);
   // the teacher's entries again, from the logits read before: the first of equal ids writes,
   // after the sweep's stores
   __syncthreads();
@@ -291,9 +336,9 @@ template <int T, int kThreads>
 void launch_rows(const DistillCall& c, DistillMode mode, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(c.n)), block(kThreads);
   switch (mode) {
-    case kDistillForward: hipLaunchKernelGGL((distill_kernel<T, kDistillForward, kThreads>), grid, block, 0, s, c); break;
-    case kDistillBackward: hipLaunchKernelGGL((distill_kernel<T, kDistillBackward, kThreads>), grid, block, 0, s, c); break;
-    case kDistillBoth: hipLaunchKernelGGL((distill_kernel<T, kDistillBoth, kThreads>), grid, block, 0, s, c); break;
+    case kDistillForward: hipLaunchKernelGGL((distill_kernel<T, kDistillForward, kThreads, 0>), grid, block, 0, s, c); break;
+    case kDistillBackward: hipLaunchKernelGGL((distill_kernel<T, kDistillBackward, kThreads, 0>), grid, block, 0, s, c); break;
+    case kDistillBoth: hipLaunchKernelGGL((distill_kernel<T, kDistillBoth, kThreads, kThreads == 1024 ? kKeepBatches : 0>), grid, block, 0, s, c); break;
   }
 }
 

@@ -21,26 +21,6 @@ constexpr int kWaves = kThreads / 64;
 // once for mean, variance and output.  Blocks walk over rows (the next row's loads are
 // issued before this row's sums are joined) and keep the gains in registers.
 // ---------------------------------------------------------------------------
-template <int T>
-struct Vec {
-  typedef typename Act<T>::S S;
-  static constexpr int kN = 16 / sizeof(S);
-  typedef typename Pack<S, kN>::type P;
-};
-
-// The first cnt (any sign) of a vector's values; zeros behind them.
-template <int T>
-__device__ __forceinline__ typename Vec<T>::P load_raw(const typename Act<T>::S* p, int cnt) {
-  typedef typename Vec<T>::P P;
-  P x;
-  if (cnt >= Vec<T>::kN) {
-    x = *reinterpret_cast<const P*>(p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < Vec<T>::kN; ++e) x[e] = e < cnt ? p[e] : 0;
-  }
-  return x;
-}
 template <int N>
 __device__ __forceinline__ void load_floats(const float* p, int cnt, float fill, float (&v)[N]) {
   if (cnt >= N) {

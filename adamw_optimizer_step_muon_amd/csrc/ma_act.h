@@ -88,6 +88,27 @@ __device__ __forceinline__ void store_part(typename Act<T>::S* p, int n, const f
     if (e < n) p[e] = Act<T>::down(v[e]);
 }
 
+// Vectors of 16 bytes.
+template <int T>
+struct Vec {
+  typedef typename Act<T>::S S;
+  static constexpr int kN = 16 / sizeof(S);
+  typedef typename Pack<S, kN>::type P;
+};
+
+// The first cnt (any sign) of a vector's values; zeros behind them.
+template <int T>
+__device__ __forceinline__ typename Vec<T>::P load_raw(const typename Act<T>::S* p, int cnt) {
+  typedef typename Vec<T>::P P;
+  P x;
+  if (cnt >= Vec<T>::kN) {
+    x = *reinterpret_cast<const P*>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec<T>::kN; ++e) x[e] = e < cnt ? p[e] : 0;
+  }
+  return x;
+}
 // Calls f with the storage type as a compile-time constant.
 template <typename F>
 inline hipError_t with_act(int type, F f) {
