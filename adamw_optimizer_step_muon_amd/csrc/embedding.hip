@@ -10,14 +10,19 @@
 // outputs are summed in one fixed order by the threads that own the row: no atomics on
 // floats, the same bits on every run.  Three stages share one workspace:
 //   1. sort:     keys (row of each token, `rows` for padding) and the tokens' positions
-//   2. segments: [start, end) of each row that occurs; rows with more than kChunk tokens
+//   2. segments: [start, end) of each row that occurs; rows with more than a chunk of tokens
 //                get partial sums, one per chunk of sorted positions, so that a frequent
 //                token's row is summed by many blocks
 //   3. rows:     every element of the table: its row's sum, then the gradient's store or
 //                the AdamW update
-// Stage 2 writes start and end of the occurring rows only; stage 3 accepts a row's start
-// if the sorted keys confirm it (the key there is the row and the one before is not), so
-// nothing has to be cleared, whatever the workspace held.
+// start and end are written for the occurring rows only; stage 3 accepts a row's start if the
+// sorted keys confirm it (the key there is the row and the one before is not), so nothing
+// has to be cleared, whatever the workspace held.
+//
+// Threads take units of eight columns of a row: one 16-byte load of a 16-bit output row, two
+// of fp32 state.
+#include <algorithm>
+
 #include "adamw_elem.h"
 #include "ma_act.h"
 #include "ma_internal.h"
@@ -26,9 +31,12 @@ namespace ma {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSortThreads = 512;
+constexpr int kUnit = 8;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxBins = 512;  // 9 bits a pass: vocabularies up to 2^18 - 1 take two passes
+constexpr int kMaxBins = 512;      // 9 bits a pass: vocabularies up to 2^18 - 1 take two passes
+constexpr int kSmallSort = 4096;   // tokens sorted by one block in one launch
+static_assert(kSortThreads >= kMaxBins, "a thread per digit");
 
 __device__ __forceinline__ uint32_t key_of(const void* tokens, int bits, int64_t i,
                                            uint32_t rows) {
@@ -46,7 +54,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a, in
                                                                   const uint32_t* keys) {
   __shared__ uint32_t hist[kMaxBins];
   const int tid = threadIdx.x;
-  hist[tid] = 0;
+  if (tid < kMaxBins) hist[tid] = 0;
   __syncthreads();
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.share;
   const int64_t hi = lo + a.share < a.n ? lo + a.share : a.n;
@@ -58,37 +66,81 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a, in
   if (tid < bins) a.counts[static_cast<int64_t>(blockIdx.x) * bins + tid] = hist[tid];
 }
 
-// Stable scatter of each block's share to its digits' places.
-__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
-    SortArgs a, int shift, int bins, int first, const uint32_t* keys, const uint32_t* order,
-    uint32_t* keys_out, uint32_t* order_out) {
-  __shared__ uint32_t base[kMaxBins];
-  __shared__ uint32_t count[kSortWaves][kMaxBins];
-  __shared__ uint32_t wave_total[kSortWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // this block's first place for digit tid: all smaller digits, and this digit in earlier
-  // blocks
-  uint32_t before = 0, total = 0;
-  if (tid < bins)
-    for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-      const uint32_t c = a.counts[static_cast<int64_t>(b) * bins + tid];
-      if (b < static_cast<int>(blockIdx.x)) before += c;
-      total += c;
-    }
-  uint32_t scan = total;
+// What a block needs to give its keys their places.
+struct Places {
+  uint32_t base[kMaxBins];               // next place of each digit
+  uint32_t count[kSortWaves][kMaxBins];  // of a tile: each wave's first place of each digit
+  uint32_t wave_total[kSortWaves];
+};
+
+// Exclusive scan of one value per digit (thread) over the block.
+__device__ __forceinline__ uint32_t digit_scan(uint32_t v, Places& s) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t scan = v;
   for (int d = 1; d < 64; d <<= 1) {
     const uint32_t up = __shfl_up(scan, d, 64);
     if (lane >= d) scan += up;
   }
-  if (lane == 63) wave_total[wave] = scan;
+  if (lane == 63) s.wave_total[wave] = scan;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) scan += wave_total[w];
-  base[tid] = scan - total + before;
+  for (int w = 0; w < wave; ++w) scan += s.wave_total[w];
+  return scan - v;
+}
+
+// The place of this thread's key in a tile of kSortThreads keys (in: it has one), in the
+// order of threads within each digit.  Every thread of the block calls it.
+__device__ __forceinline__ uint32_t place_of(bool in, uint32_t digit, int bins, Places& s) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __syncthreads();  // the last tile's counts have been read
+  if (tid < bins) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) s.count[w][tid] = 0;
+  }
+  __syncthreads();
+  uint64_t same = __ballot(in);  // the lanes of this wave with the same digit
+  for (int bit = 1; bit < bins; bit <<= 1) {
+    const uint64_t with = __ballot((digit & bit) != 0);
+    same &= (digit & bit) ? with : ~with;
+  }
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  if (in && rank == 0) s.count[wave][digit] = static_cast<uint32_t>(__popcll(same));
+  __syncthreads();
+  if (tid < bins) {
+    uint32_t at = s.base[tid];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = s.count[w][tid];
+      s.count[w][tid] = at;
+      at += c;
+    }
+    s.base[tid] = at;
+  }
+  __syncthreads();
+  return in ? s.count[wave][digit] + rank : 0;
+}
+
+// Stable scatter of each block's share to its digits' places.
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
+    SortArgs a, int shift, int bins, int first, const uint32_t* keys, const uint32_t* order,
+    uint32_t* keys_out, uint32_t* order_out) {
+  __shared__ Places s;
+  const int tid = threadIdx.x;
+  // this block's first place for digit tid: all smaller digits, and this digit in earlier
+  // blocks
+  uint32_t before = 0, total = 0;
+  if (tid < bins) {
+#pragma unroll 8
+    for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+      const uint32_t c = a.counts[static_cast<int64_t>(b) * bins + tid];
+      before += b < static_cast<int>(blockIdx.x) ? c : 0;
+      total += c;
+    }
+  }
+  const uint32_t smaller = digit_scan(total, s);
+  if (tid < bins) s.base[tid] = smaller + before;
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.share;
   const int64_t hi = lo + a.share < a.n ? lo + a.share : a.n;
   for (int64_t t0 = lo; t0 < hi; t0 += kSortThreads) {
-    for (int w = 0; w < kSortWaves; ++w) count[w][tid] = 0;
-    __syncthreads();
     const int64_t i = t0 + tid;
     const bool in = i < hi;
     uint32_t k = 0, o = 0;
@@ -96,30 +148,55 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
       k = first ? key_of(a.tokens, a.token_bits, i, a.rows) : keys[i];
       o = first ? static_cast<uint32_t>(i) : order[i];
     }
-    const uint32_t d = (k >> shift) & (bins - 1);
-    // the lanes of this wave with the same digit
-    uint64_t same = __ballot(in);
-    for (int bit = 1; bit < bins; bit <<= 1) {
-      const uint64_t with = __ballot((d & bit) != 0);
-      same &= (d & bit) ? with : ~with;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    if (in && rank == 0) count[wave][d] = static_cast<uint32_t>(__popcll(same));
-    __syncthreads();
-    uint32_t at = base[tid];
-    for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = count[w][tid];
-      count[w][tid] = at;
-      at += c;
-    }
-    base[tid] = at;
-    __syncthreads();
+    const uint32_t at = place_of(in, (k >> shift) & (bins - 1), bins, s);
     if (in) {
-      const uint32_t place = count[wave][d] + rank;
-      keys_out[place] = k;
-      order_out[place] = o;
+      keys_out[at] = k;
+      order_out[at] = o;
+    }
+  }
+}
+
+// The whole sort of at most kSmallSort tokens in one block, and the rows' starts and ends.
+__global__ __launch_bounds__(kSortThreads) void sort_small_kernel(SortArgs a, int passes, int width,
+                                                                  uint32_t* keys_out, uint32_t* order_out,
+                                                                  uint32_t* start, uint32_t* end) {
+  __shared__ Places s;
+  __shared__ uint32_t keys[2][kSmallSort];
+  __shared__ uint16_t order[2][kSmallSort];
+  __shared__ uint32_t hist[kMaxBins];
+  const int tid = threadIdx.x, n = static_cast<int>(a.n), bins = 1 << width;
+  for (int i = tid; i < n; i += kSortThreads) {
+    keys[0][i] = key_of(a.tokens, a.token_bits, i, a.rows);
+    order[0][i] = static_cast<uint16_t>(i);
+  }
+  int from = 0;
+  for (int pass = 0; pass < passes; ++pass, from ^= 1) {
+    const int shift = pass * width;
+    if (tid < bins) hist[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kSortThreads) atomicAdd(&hist[(keys[from][i] >> shift) & (bins - 1)], 1u);
+    __syncthreads();
+    const uint32_t smaller = digit_scan(tid < bins ? hist[tid] : 0, s);
+    if (tid < bins) s.base[tid] = smaller;
+    for (int t0 = 0; t0 < n; t0 += kSortThreads) {
+      const int i = t0 + tid;
+      const bool in = i < n;
+      const uint32_t k = in ? keys[from][i] : 0;
+      const uint32_t at = place_of(in, (k >> shift) & (bins - 1), bins, s);
+      if (in) {
+        keys[from ^ 1][at] = k;
+        order[from ^ 1][at] = order[from][i];
+      }
     }
     __syncthreads();
+  }
+  for (int i = tid; i < n; i += kSortThreads) {
+    const uint32_t k = keys[from][i];
+    keys_out[i] = k;
+    order_out[i] = order[from][i];
+    if (k >= a.rows) continue;
+    if (i == 0 || keys[from][i - 1] != k) start[k] = i;
+    if (i == n - 1 || keys[from][i + 1] != k) end[k] = i + 1;
   }
 }
 
@@ -140,44 +217,70 @@ __device__ __forceinline__ int block_count(const uint32_t* keys, int64_t lo, int
   return c;
 }
 
+// acc += the output rows of the tokens at sorted positions [lo, hi), columns [c, c + cnt), in
+// order; kAhead rows are loaded before the first is added.
+constexpr int kAhead = 4;
 template <int T>
-__device__ void partial_sum(const RowArgs& a, int64_t lo, int64_t hi, int64_t slot, int64_t c) {
-  const typename Act<T>::S* dout = static_cast<const typename Act<T>::S*>(a.dout);
-  if (c >= a.dim) return;
-  float acc = 0.0f;
-  for (int64_t i = lo; i < hi; ++i) acc += Act<T>::up(dout[a.order[i] * a.dout_stride + c]);
-  a.partial[slot * a.dim + c] = acc;
+__device__ __forceinline__ void add_tokens(const RowArgs& a, int64_t lo, int64_t hi, int64_t c, int cnt,
+                                           float (&acc)[kUnit]) {
+  typedef typename Act<T>::S S;
+  const S* dout = static_cast<const S*>(a.dout) + c;
+  int64_t i = lo;
+  if (cnt >= kUnit) {
+    for (; i + kAhead <= hi; i += kAhead) {
+      float v[kAhead][kUnit];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) load_act<T, kUnit>(dout + a.order[i + k] * a.dout_stride, v[k]);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) acc[e] += v[k][e];
+    }
+  }
+  for (; i < hi; ++i) {
+    float v[kUnit];
+    load_part<T, kUnit>(dout + a.order[i] * a.dout_stride, cnt, 0.0f, v);
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e) acc[e] += v[e];
+  }
 }
 
 // Block (j, slice): sorted positions [j chunk, (j + 1) chunk).  Slice 0 writes the segments'
-// ends; every slice sums kThreads columns of the rows with more than `chunk` tokens.  At
-// most two of those meet a chunk: the one at its first position (partial 2 j) and the one
-// at its last (2 j + 1, where that is another row).
+// ends (ends: where the sort has not); every slice sums kThreads units of the rows with more
+// than `chunk` tokens.  At most two of those meet a chunk: the one at its first position
+// (partial 2 j) and the one at its last (2 j + 1, where that is another row).
 template <int T>
-__global__ __launch_bounds__(kThreads) void segments_kernel(RowArgs a) {
+__global__ __launch_bounds__(kThreads) void segments_kernel(RowArgs a, int ends) {
   __shared__ int shared[kThreads / 64];
   const int64_t n = a.n;
   const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
   const int64_t hi = lo + a.chunk < n ? lo + a.chunk : n;
-  if (blockIdx.y == 0)
+  if (ends && blockIdx.y == 0)
     for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
       const uint32_t k = a.keys[i];
       if (k >= a.rows) continue;
       if (i == 0 || a.keys[i - 1] != k) a.start[k] = static_cast<uint32_t>(i);
       if (i == n - 1 || a.keys[i + 1] != k) a.end[k] = static_cast<uint32_t>(i + 1);
     }
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
+  if (n <= a.chunk) return;
+  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * kUnit;
+  const int cnt = static_cast<int>(a.dim - c);
+  const auto sum = [&](int64_t from, int64_t to, int64_t slot) {
+    if (cnt <= 0) return;
+    float acc[kUnit] = {};
+    add_tokens<T>(a, from, to, c, cnt, acc);
+    store_part<kActF32, kUnit>(a.partial + slot * a.dim + c, cnt, acc);
+  };
+  const int64_t before = lo > a.chunk ? lo - a.chunk : 0, after = hi + a.chunk < n ? hi + a.chunk : n;
   const uint32_t k0 = a.keys[lo], k1 = a.keys[hi - 1];
   if (k0 < a.rows) {
-    const int back = block_count(a.keys, lo > a.chunk ? lo - a.chunk : 0, lo, k0, shared);
     const int in = block_count(a.keys, lo, hi, k0, shared);
-    const int fwd = block_count(a.keys, hi, hi + a.chunk < n ? hi + a.chunk : n, k0, shared);
-    if (back + in + fwd > a.chunk) partial_sum<T>(a, lo, lo + in, 2 * static_cast<int64_t>(blockIdx.x), c);
+    const int more = block_count(a.keys, before, lo, k0, shared) + block_count(a.keys, hi, after, k0, shared);
+    if (in + more > a.chunk) sum(lo, lo + in, 2 * static_cast<int64_t>(blockIdx.x));
   }
   if (k1 != k0 && k1 < a.rows) {
     const int in = block_count(a.keys, lo, hi, k1, shared);
-    const int fwd = block_count(a.keys, hi, hi + a.chunk < n ? hi + a.chunk : n, k1, shared);
-    if (in + fwd > a.chunk) partial_sum<T>(a, hi - in, hi, 2 * static_cast<int64_t>(blockIdx.x) + 1, c);
+    if (in + block_count(a.keys, hi, after, k1, shared) > a.chunk) sum(hi - in, hi, 2 * static_cast<int64_t>(blockIdx.x) + 1);
   }
 }
 
@@ -187,57 +290,100 @@ __global__ __launch_bounds__(kThreads) void segments_kernel(RowArgs a) {
 // Tokens of row v: their number, 0 if it does not occur; *s the first sorted position.
 __device__ __forceinline__ uint32_t segment_of(const RowArgs& a, uint32_t v, uint32_t* s) {
   if (a.n == 0) return 0;
-  const uint32_t b = a.start[v];
+  const uint32_t b = a.start[v], e = a.end[v];
   if (b >= a.n || a.keys[b] != v || (b > 0 && a.keys[b - 1] == v)) return 0;
   *s = b;
-  return a.end[v] - b;
+  return e - b;
 }
 
-// Column c of the sum over the m tokens at sorted position s.
+// scale times the sum over the m tokens from sorted position s on (zeros for none).
 template <int T>
-__device__ __forceinline__ float segment_sum(const RowArgs& a, uint32_t s, uint32_t m, int64_t c) {
-  float acc = 0.0f;
+__device__ __forceinline__ void row_gradient(const RowArgs& a, uint32_t s, uint32_t m, int64_t c, int cnt,
+                                             float (&g)[kUnit]) {
+#pragma clang fp contract(off)
+#pragma unroll
+  for (int e = 0; e < kUnit; ++e) g[e] = 0.0f;
+  if (m == 0) return;
   if (m <= static_cast<uint32_t>(a.chunk)) {
-    const typename Act<T>::S* dout = static_cast<const typename Act<T>::S*>(a.dout);
-    for (uint32_t i = s; i < s + m; ++i) acc += Act<T>::up(dout[a.order[i] * a.dout_stride + c]);
+    add_tokens<T>(a, s, static_cast<int64_t>(s) + m, c, cnt, g);
   } else {
     const int64_t j0 = s / a.chunk, j1 = (s + m - 1) / a.chunk;
-    acc = a.partial[(2 * j0 + (s % a.chunk != 0)) * a.dim + c];
-    for (int64_t j = j0 + 1; j <= j1; ++j) acc += a.partial[2 * j * a.dim + c];
+    load_part<kActF32, kUnit>(a.partial + (2 * j0 + (s % a.chunk != 0)) * a.dim + c, cnt, 0.0f, g);
+#pragma unroll 4
+    for (int64_t j = j0 + 1; j <= j1; ++j) {
+      float v[kUnit];
+      load_part<kActF32, kUnit>(a.partial + 2 * j * a.dim + c, cnt, 0.0f, v);
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) g[e] += v[e];
+    }
   }
-  return acc;
+#pragma unroll
+  for (int e = 0; e < kUnit; ++e) g[e] = a.scale * g[e];
 }
 
-// grad = s sum, or grad + s sum (kAdd, occurring rows only).  The product is rounded before
-// it is added, so adding gives the bits of a separate gradient's addition.
-template <int T, bool kAdd>
-__global__ __launch_bounds__(kThreads) void grad_rows_kernel(RowArgs a, float* grad) {
-#pragma clang fp contract(off)
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.rows) * a.dim) return;
-  const uint32_t v = static_cast<uint32_t>(i / a.dim);
-  uint32_t s = 0;
-  const uint32_t m = segment_of(a, v, &s);
-  if (kAdd && m == 0) return;
-  const float g = m ? a.scale * segment_sum<T>(a, s, m, i - v * a.dim) : 0.0f;
-  grad[i] = kAdd ? grad[i] + g : g;
+// Unit u of a table: row u / units, columns from (u % units) kUnit on.
+struct Unit {
+  uint32_t row;
+  int64_t c;
+  int cnt;
+};
+__device__ __forceinline__ Unit unit_of(uint32_t u, int64_t dim) {
+  const uint32_t units = static_cast<uint32_t>((dim + kUnit - 1) / kUnit);
+  const uint32_t row = u / units;
+  const int64_t c = static_cast<int64_t>(u - row * units) * kUnit;
+  return Unit{row, c, static_cast<int>(dim - c)};
+}
+
+// kStore: grad = s sum on every row.  kAddRows, kAddTokens: grad += s sum on the rows that
+// occur; a unit's row is a row of the table or that of a sorted position, whichever are
+// fewer.  The product is rounded before it is added, so adding gives the bits of a separate
+// gradient's addition.
+enum GradMode { kStore = 0, kAddRows = 1, kAddTokens = 2 };
+template <int T, int kMode>
+__global__ __launch_bounds__(kThreads) void grad_rows_kernel(RowArgs a, float* grad, uint32_t total) {
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
+  if (u >= total) return;
+  const Unit t = unit_of(u, a.dim);
+  uint32_t s = 0, m, v = t.row;
+  if (kMode == kAddTokens) {
+    s = t.row;
+    v = a.keys[s];
+    if (v >= a.rows || (s > 0 && a.keys[s - 1] == v)) return;
+    m = a.end[v] - s;
+  } else {
+    m = segment_of(a, v, &s);
+    if (kMode == kAddRows && m == 0) return;
+  }
+  float g[kUnit], old[kUnit];
+  float* to = grad + v * a.dim + t.c;
+  if (kMode != kStore) load_part<kActF32, kUnit>(to, t.cnt, 0.0f, old);
+  row_gradient<T>(a, s, m, t.c, t.cnt, g);
+  if (kMode != kStore) {
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e) g[e] = old[e] + g[e];
+  }
+  store_part<kActF32, kUnit>(to, t.cnt, g);
 }
 
 template <int T, int kMode>
 __global__ __launch_bounds__(kThreads) void step_rows_kernel(RowArgs a, float* p, float* m, float* v,
-                                                             AdamWConst c) {
-#pragma clang fp contract(off)
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= static_cast<int64_t>(a.rows) * a.dim) return;
-  const uint32_t r = static_cast<uint32_t>(i / a.dim);
+                                                             AdamWConst c, uint32_t total) {
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
+  if (u >= total) return;
+  const Unit t = unit_of(u, a.dim);
+  const int64_t at = t.row * a.dim + t.c;
+  float P[kUnit], M[kUnit], V[kUnit], g[kUnit];
+  load_part<kActF32, kUnit>(p + at, t.cnt, 0.0f, P);
+  load_part<kActF32, kUnit>(m + at, t.cnt, 0.0f, M);
+  load_part<kActF32, kUnit>(v + at, t.cnt, 0.0f, V);
   uint32_t s = 0;
-  const uint32_t cnt = segment_of(a, r, &s);
-  const float g = cnt ? a.scale * segment_sum<T>(a, s, cnt, i - r * a.dim) : 0.0f;
-  float P = p[i], M = m[i], V = v[i];
-  adamw_elem_t<kMode>(P, g, M, V, c);
-  p[i] = P;
-  m[i] = M;
-  v[i] = V;
+  const uint32_t count = segment_of(a, t.row, &s);
+  row_gradient<T>(a, s, count, t.c, t.cnt, g);
+#pragma unroll
+  for (int e = 0; e < kUnit; ++e) adamw_elem_t<kMode>(P[e], g[e], M[e], V[e], c);
+  store_part<kActF32, kUnit>(p + at, t.cnt, P);
+  store_part<kActF32, kUnit>(m + at, t.cnt, M);
+  store_part<kActF32, kUnit>(v + at, t.cnt, V);
 }
 
 // ---------------------------------------------------------------------------
@@ -246,14 +392,20 @@ __global__ __launch_bounds__(kThreads) void step_rows_kernel(RowArgs a, float* p
 template <int T>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(const float* table, uint32_t rows,
                                                           int64_t dim, const void* tokens,
-                                                          int token_bits, int64_t n, float scale,
+                                                          int token_bits, uint32_t total, float scale,
                                                           typename Act<T>::S* out,
                                                           int64_t out_stride) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= n * dim) return;
-  const int64_t t = i / dim, c = i - t * dim;
-  const uint32_t v = key_of(tokens, token_bits, t, rows);
-  out[t * out_stride + c] = Act<T>::down(v < rows ? scale * table[v * dim + c] : 0.0f);
+  const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
+  if (u >= total) return;
+  const Unit t = unit_of(u, dim);
+  const uint32_t v = key_of(tokens, token_bits, t.row, rows);
+  float x[kUnit] = {};
+  if (v < rows) {
+    load_part<kActF32, kUnit>(table + v * dim + t.c, t.cnt, 0.0f, x);
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e) x[e] *= scale;
+  }
+  store_part<T, kUnit>(out + t.row * out_stride + t.c, t.cnt, x);
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -271,12 +423,12 @@ static void sort_digits(uint32_t rows, int* passes, int* width) {
 EmbeddingPlan plan_embedding(int64_t rows, int64_t dim, int64_t n) {
   EmbeddingPlan p{};
   if (rows < 1 || dim < 1 || n < 1) return p;
-  // at most 128 shares, so that each scatter block can add up every block's counts
-  p.share = (n + 127) / 128;
-  p.share = (p.share + kSortThreads - 1) / kSortThreads * kSortThreads;
+  // shares of two tiles, and at most 128 of them: each scatter block adds up all their counts
+  p.share = 2 * kSortThreads;
+  while ((n + p.share - 1) / p.share > 128) p.share *= 2;
   p.blocks = static_cast<int>((n + p.share - 1) / p.share);
-  // at most 1024 partial sums to join for one row
-  p.chunk = 64;
+  // at most 1024 partial sums to join for one row, and none where they are not worth a launch
+  p.chunk = n <= 128 ? 128 : 64;
   while (n / p.chunk > 1024) p.chunk *= 2;
   p.chunks = (n + p.chunk - 1) / p.chunk;
   int64_t at = 0;
@@ -298,10 +450,11 @@ EmbeddingPlan plan_embedding(int64_t rows, int64_t dim, int64_t n) {
   return p;
 }
 
+static int64_t units_of(int64_t rows, int64_t dim) { return rows * ((dim + kUnit - 1) / kUnit); }
+
 int64_t embedding_threads(int64_t rows, int64_t dim, int64_t n) {
   const EmbeddingPlan p = plan_embedding(rows, dim, n);
-  const int64_t table = rows * dim, out = n * dim, parts = p.chunks * kThreads;
-  return (table > out ? (table > parts ? table : parts) : (out > parts ? out : parts)) + kThreads;
+  return std::max(std::max(units_of(rows, dim), units_of(n, dim)), p.chunks * kThreads) + kThreads;
 }
 
 // Sorts the tokens and finds the segments; fills the arguments of stage 3.
@@ -323,18 +476,28 @@ static hipError_t sort_tokens(const EmbeddingCall& e, RowArgs* out, hipStream_t 
   sa.counts = reinterpret_cast<uint32_t*>(ws + p.counts);
   int passes, width;
   sort_digits(sa.rows, &passes, &width);
-  const dim3 grid(static_cast<unsigned>(p.blocks)), block(kSortThreads);
-  for (int pass = 0; pass < passes; ++pass) {
-    const int from = (pass + 1) & 1, to = pass & 1;
-    hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0, keys[from]);
-    hipLaunchKernelGGL(sort_scatter_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0,
-                       keys[from], order[from], keys[to], order[to]);
+  uint32_t* start = reinterpret_cast<uint32_t*>(ws + p.start);
+  uint32_t* end = reinterpret_cast<uint32_t*>(ws + p.end);
+  const bool small = e.n <= kSmallSort;
+  int last = 0;
+  if (small) {
+    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, s, sa, passes, width, keys[0], order[0],
+                       start, end);
+  } else {
+    const dim3 grid(static_cast<unsigned>(p.blocks)), block(kSortThreads);
+    for (int pass = 0; pass < passes; ++pass) {
+      const int from = (pass + 1) & 1, to = pass & 1;
+      hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0, keys[from]);
+      hipLaunchKernelGGL(sort_scatter_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0,
+                         keys[from], order[from], keys[to], order[to]);
+    }
+    last = (passes - 1) & 1;
   }
   RowArgs a{};
-  a.keys = keys[(passes - 1) & 1];
-  a.order = order[(passes - 1) & 1];
-  a.start = reinterpret_cast<uint32_t*>(ws + p.start);
-  a.end = reinterpret_cast<uint32_t*>(ws + p.end);
+  a.keys = keys[last];
+  a.order = order[last];
+  a.start = start;
+  a.end = end;
   a.partial = reinterpret_cast<float*>(ws + p.partial);
   a.dout = e.dout;
   a.dout_stride = e.dout_stride;
@@ -344,26 +507,26 @@ static hipError_t sort_tokens(const EmbeddingCall& e, RowArgs* out, hipStream_t 
   a.chunk = p.chunk;
   a.scale = e.scale;
   *out = a;
+  if (small && e.n <= p.chunk) return hipGetLastError();
   return with_act(e.dout_type, [&](auto t) {
-    const dim3 g(static_cast<unsigned>(p.chunks),
-                 e.n > p.chunk ? static_cast<unsigned>((e.dim + kThreads - 1) / kThreads) : 1u);
-    hipLaunchKernelGGL((segments_kernel<decltype(t)::value>), g, dim3(kThreads), 0, s, a);
+    const int64_t slices = (units_of(1, e.dim) + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL((segments_kernel<decltype(t)::value>), dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(slices)),
+                       dim3(kThreads), 0, s, a, small ? 0 : 1);
     return hipGetLastError();
   });
 }
 
-static dim3 row_grid(const EmbeddingCall& e) {
-  return dim3(static_cast<unsigned>((e.rows * e.dim + kThreads - 1) / kThreads));
-}
+static dim3 unit_grid(int64_t units) { return dim3(static_cast<unsigned>((units + kThreads - 1) / kThreads)); }
 
 hipError_t launch_embedding_forward(const float* table, int64_t rows, int64_t dim,
                                     const void* tokens, int token_bits, int64_t n, float scale,
                                     void* out, int out_type, int64_t out_stride, hipStream_t s) {
   return with_act(out_type, [&](auto t) {
     typedef typename Act<decltype(t)::value>::S S;
-    hipLaunchKernelGGL((lookup_kernel<decltype(t)::value>), dim3(static_cast<unsigned>((n * dim + kThreads - 1) / kThreads)),
-                       dim3(kThreads), 0, s, table, static_cast<uint32_t>(rows), dim, tokens,
-                       token_bits, n, scale, static_cast<S*>(out), out_stride);
+    const int64_t units = units_of(n, dim);
+    hipLaunchKernelGGL((lookup_kernel<decltype(t)::value>), unit_grid(units), dim3(kThreads), 0, s, table,
+                       static_cast<uint32_t>(rows), dim, tokens, token_bits, static_cast<uint32_t>(units), scale,
+                       static_cast<S*>(out), out_stride);
     return hipGetLastError();
   });
 }
@@ -373,8 +536,13 @@ hipError_t launch_embedding_backward(const EmbeddingCall& e, float* grad, bool a
   const hipError_t st = sort_tokens(e, &a, s);
   if (st != hipSuccess) return st;
   return with_act(e.dout_type, [&](auto t) {
-    if (add) hipLaunchKernelGGL((grad_rows_kernel<decltype(t)::value, true>), row_grid(e), dim3(kThreads), 0, s, a, grad);
-    else hipLaunchKernelGGL((grad_rows_kernel<decltype(t)::value, false>), row_grid(e), dim3(kThreads), 0, s, a, grad);
+    constexpr int T = decltype(t)::value;
+    const bool by_token = add && e.n < e.rows;
+    const int64_t units = units_of(by_token ? e.n : e.rows, e.dim);
+    const uint32_t total = static_cast<uint32_t>(units);
+    if (by_token) hipLaunchKernelGGL((grad_rows_kernel<T, kAddTokens>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
+    else if (add) hipLaunchKernelGGL((grad_rows_kernel<T, kAddRows>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
+    else hipLaunchKernelGGL((grad_rows_kernel<T, kStore>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
     return hipGetLastError();
   });
 }
@@ -386,10 +554,13 @@ hipError_t launch_adamw_embedding(const EmbeddingCall& e, float* p, float* m, fl
   if (st != hipSuccess) return st;
   return with_act(e.dout_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
+    const int64_t units = units_of(e.rows, e.dim);
+    const dim3 grid = unit_grid(units), block(kThreads);
+    const uint32_t total = static_cast<uint32_t>(units);
     switch (decay_mode(c)) {
-      case kCoupled: hipLaunchKernelGGL((step_rows_kernel<T, kCoupled>), row_grid(e), dim3(kThreads), 0, s, a, p, m, v, c); break;
-      case kDecoupledCautious: hipLaunchKernelGGL((step_rows_kernel<T, kDecoupledCautious>), row_grid(e), dim3(kThreads), 0, s, a, p, m, v, c); break;
-      default: hipLaunchKernelGGL((step_rows_kernel<T, kDecoupled>), row_grid(e), dim3(kThreads), 0, s, a, p, m, v, c); break;
+      case kCoupled: hipLaunchKernelGGL((step_rows_kernel<T, kCoupled>), grid, block, 0, s, a, p, m, v, c, total); break;
+      case kDecoupledCautious: hipLaunchKernelGGL((step_rows_kernel<T, kDecoupledCautious>), grid, block, 0, s, a, p, m, v, c, total); break;
+      default: hipLaunchKernelGGL((step_rows_kernel<T, kDecoupled>), grid, block, 0, s, a, p, m, v, c, total); break;
     }
     return hipGetLastError();
   });
