@@ -19,8 +19,10 @@
 // sorted keys confirm it (the key there is the row and the one before is not), so nothing
 // has to be cleared, whatever the workspace held.
 //
-// Threads take units of eight columns of a row: one 16-byte load of a 16-bit output row, two
-// of fp32 state.
+// Threads take units of a few columns of a row.  Where fp32 rows are written (stage 3) a unit
+// is four columns, so that a wave's stores cover whole cache lines and can bypass the cache:
+// units of eight leave every store half a line, 1.2 times slower with non-temporal stores and
+// 1.1 times without.  Elsewhere it is eight, one 16-byte access of a 16-bit row.
 #include <algorithm>
 
 #include "adamw_elem.h"
@@ -31,7 +33,8 @@ namespace ma {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 8;
+constexpr int kWide = 8;    // columns of a unit: lookup, partial sums
+constexpr int kNarrow = 4;  // rows of the table
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxBins = 512;      // 9 bits a pass: vocabularies up to 2^18 - 1 take two passes
@@ -49,8 +52,7 @@ __device__ __forceinline__ uint32_t key_of(const void* tokens, int bits, int64_t
 // 1. sort
 // ---------------------------------------------------------------------------
 // Digit counts of each block's share [b * share, (b + 1) * share) of the n keys.
-__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a, int shift, int bins,
-                                                                  int first,
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a, int shift, int bins, int first,
                                                                   const uint32_t* keys) {
   __shared__ uint32_t hist[kMaxBins];
   const int tid = threadIdx.x;
@@ -125,6 +127,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
     uint32_t* keys_out, uint32_t* order_out) {
   __shared__ Places s;
   const int tid = threadIdx.x;
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.share;
+  const int64_t hi = lo + a.share < a.n ? lo + a.share : a.n;
   // this block's first place for digit tid: all smaller digits, and this digit in earlier
   // blocks
   uint32_t before = 0, total = 0;
@@ -138,8 +142,6 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
   }
   const uint32_t smaller = digit_scan(total, s);
   if (tid < bins) s.base[tid] = smaller + before;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.share;
-  const int64_t hi = lo + a.share < a.n ? lo + a.share : a.n;
   for (int64_t t0 = lo; t0 < hi; t0 += kSortThreads) {
     const int64_t i = t0 + tid;
     const bool in = i < hi;
@@ -203,39 +205,30 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(SortArgs a, in
 // ---------------------------------------------------------------------------
 // 2. segments
 // ---------------------------------------------------------------------------
-// How many of the keys at [lo, hi) equal k (every thread gets the count).
-__device__ __forceinline__ int block_count(const uint32_t* keys, int64_t lo, int64_t hi,
-                                           uint32_t k, int* shared) {
-  int c = 0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) c += keys[i] == k;
-  for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = c;
-  __syncthreads();
-  c = 0;
-  for (int w = 0; w < kThreads / 64; ++w) c += shared[w];
-  return c;
-}
-
 // acc += the output rows of the tokens at sorted positions [lo, hi), columns [c, c + cnt), in
 // order; kAhead rows are loaded before the first is added.
-constexpr int kAhead = 4;
-template <int T>
-__device__ __forceinline__ void add_tokens(const RowArgs& a, int64_t lo, int64_t hi, int64_t c, int cnt,
+constexpr int kAhead = 8;
+template <int T, int kUnit>
+__device__ __forceinline__ void add_tokens(const RowArgs& a, uint32_t lo, uint32_t hi, int64_t c, int cnt,
                                            float (&acc)[kUnit]) {
   typedef typename Act<T>::S S;
+  typedef typename Pack<S, kUnit>::type P;
   const S* dout = static_cast<const S*>(a.dout) + c;
-  int64_t i = lo;
+  uint32_t i = lo;
   if (cnt >= kUnit) {
-    for (; i + kAhead <= hi; i += kAhead) {
-      float v[kAhead][kUnit];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) load_act<T, kUnit>(dout + a.order[i + k] * a.dout_stride, v[k]);
+    for (; i < hi; i += kAhead) {
+      P v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
+        if (i + k < hi) v[k] = *reinterpret_cast<const P*>(dout + a.order[i + k] * a.dout_stride);
 #pragma unroll
-        for (int e = 0; e < kUnit; ++e) acc[e] += v[k][e];
+      for (int k = 0; k < kAhead; ++k)
+        if (i + k < hi) {
+#pragma unroll
+          for (int e = 0; e < kUnit; ++e) acc[e] += Act<T>::up(v[k][e]);
+        }
     }
+    return;
   }
   for (; i < hi; ++i) {
     float v[kUnit];
@@ -246,42 +239,62 @@ __device__ __forceinline__ void add_tokens(const RowArgs& a, int64_t lo, int64_t
 }
 
 // Block (j, slice): sorted positions [j chunk, (j + 1) chunk).  Slice 0 writes the segments'
-// ends (ends: where the sort has not); every slice sums kThreads units of the rows with more
-// than `chunk` tokens.  At most two of those meet a chunk: the one at its first position
-// (partial 2 j) and the one at its last (2 j + 1, where that is another row).
+// ends (ends: where the sort has not); every slice sums 64 units, one a lane, of the rows with
+// more than `chunk` tokens, each wave a quarter of the tokens, joined in order.  At most two
+// of those rows meet a chunk: the one at its first position (partial 2 j) and the one at its
+// last (2 j + 1, where that is another row).
 template <int T>
 __global__ __launch_bounds__(kThreads) void segments_kernel(RowArgs a, int ends) {
-  __shared__ int shared[kThreads / 64];
-  const int64_t n = a.n;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.chunk;
-  const int64_t hi = lo + a.chunk < n ? lo + a.chunk : n;
+  constexpr int kWaves = kThreads / 64;
+  __shared__ float join[kWaves][kWide][64];
+  const uint32_t n = static_cast<uint32_t>(a.n), chunk = static_cast<uint32_t>(a.chunk);
+  const uint32_t lo = blockIdx.x * chunk, hi = lo + chunk < n ? lo + chunk : n;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (ends && blockIdx.y == 0)
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += kThreads) {
       const uint32_t k = a.keys[i];
       if (k >= a.rows) continue;
-      if (i == 0 || a.keys[i - 1] != k) a.start[k] = static_cast<uint32_t>(i);
-      if (i == n - 1 || a.keys[i + 1] != k) a.end[k] = static_cast<uint32_t>(i + 1);
+      if (i == 0 || a.keys[i - 1] != k) a.start[k] = i;
+      if (i == n - 1 || a.keys[i + 1] != k) a.end[k] = i + 1;
     }
-  if (n <= a.chunk) return;
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * kUnit;
+  if (n <= chunk) return;
+  const int64_t c = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * kWide;
   const int cnt = static_cast<int>(a.dim - c);
-  const auto sum = [&](int64_t from, int64_t to, int64_t slot) {
-    if (cnt <= 0) return;
-    float acc[kUnit] = {};
-    add_tokens<T>(a, from, to, c, cnt, acc);
-    store_part<kActF32, kUnit>(a.partial + slot * a.dim + c, cnt, acc);
+  const auto sum = [&](uint32_t from, uint32_t to, int64_t slot) {
+    const uint32_t part = (to - from + kWaves - 1) / kWaves, at = from + wave * part;
+    float acc[kWide] = {};
+    if (cnt > 0 && at < to) add_tokens<T, kWide>(a, at, at + part < to ? at + part : to, c, cnt, acc);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kWide; ++e) join[wave][e][lane] = acc[e];
+    __syncthreads();
+    if (wave != 0 || cnt <= 0) return;
+#pragma unroll
+    for (int e = 0; e < kWide; ++e)
+      for (int w = 1; w < kWaves; ++w) acc[e] += join[w][e][lane];
+    store_part<kActF32, kWide>(a.partial + slot * a.dim + c, cnt, acc);
   };
-  const int64_t before = lo > a.chunk ? lo - a.chunk : 0, after = hi + a.chunk < n ? hi + a.chunk : n;
+  // each wave counts on its own: the keys before, in and behind the chunk that are its first
+  // or its last, a chunk at most on either side
   const uint32_t k0 = a.keys[lo], k1 = a.keys[hi - 1];
-  if (k0 < a.rows) {
-    const int in = block_count(a.keys, lo, hi, k0, shared);
-    const int more = block_count(a.keys, before, lo, k0, shared) + block_count(a.keys, hi, after, k0, shared);
-    if (in + more > a.chunk) sum(lo, lo + in, 2 * static_cast<int64_t>(blockIdx.x));
+  uint32_t in0 = 0, in1 = 0, more0 = 0, more1 = 0;
+  for (uint32_t i = lane; i < chunk; i += 64) {
+    const uint32_t here = lo + i < hi ? a.keys[lo + i] : a.rows;
+    const uint32_t after = hi + i < n ? a.keys[hi + i] : a.rows;
+    const uint32_t before = lo > i ? a.keys[lo - 1 - i] : a.rows;
+    in0 += here == k0;
+    in1 += here == k1;
+    more0 += (before == k0) + (after == k0);
+    more1 += after == k1;
   }
-  if (k1 != k0 && k1 < a.rows) {
-    const int in = block_count(a.keys, lo, hi, k1, shared);
-    if (in + block_count(a.keys, hi, after, k1, shared) > a.chunk) sum(hi - in, hi, 2 * static_cast<int64_t>(blockIdx.x) + 1);
+  for (int d = 32; d > 0; d >>= 1) {
+    in0 += __shfl_xor(in0, d, 64);
+    in1 += __shfl_xor(in1, d, 64);
+    more0 += __shfl_xor(more0, d, 64);
+    more1 += __shfl_xor(more1, d, 64);
   }
+  if (k0 < a.rows && in0 + more0 > chunk) sum(lo, lo + in0, 2 * static_cast<int64_t>(blockIdx.x));
+  if (k1 != k0 && k1 < a.rows && in1 + more1 > chunk) sum(hi - in1, hi, 2 * static_cast<int64_t>(blockIdx.x) + 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -299,39 +312,61 @@ __device__ __forceinline__ uint32_t segment_of(const RowArgs& a, uint32_t v, uin
 // scale times the sum over the m tokens from sorted position s on (zeros for none).
 template <int T>
 __device__ __forceinline__ void row_gradient(const RowArgs& a, uint32_t s, uint32_t m, int64_t c, int cnt,
-                                             float (&g)[kUnit]) {
+                                             float (&g)[kNarrow]) {
 #pragma clang fp contract(off)
 #pragma unroll
-  for (int e = 0; e < kUnit; ++e) g[e] = 0.0f;
+  for (int e = 0; e < kNarrow; ++e) g[e] = 0.0f;
   if (m == 0) return;
   if (m <= static_cast<uint32_t>(a.chunk)) {
-    add_tokens<T>(a, s, static_cast<int64_t>(s) + m, c, cnt, g);
+    add_tokens<T, kNarrow>(a, s, s + m, c, cnt, g);
   } else {
     const int64_t j0 = s / a.chunk, j1 = (s + m - 1) / a.chunk;
-    load_part<kActF32, kUnit>(a.partial + (2 * j0 + (s % a.chunk != 0)) * a.dim + c, cnt, 0.0f, g);
+    load_part<kActF32, kNarrow>(a.partial + (2 * j0 + (s % a.chunk != 0)) * a.dim + c, cnt, 0.0f, g);
 #pragma unroll 4
     for (int64_t j = j0 + 1; j <= j1; ++j) {
-      float v[kUnit];
-      load_part<kActF32, kUnit>(a.partial + 2 * j * a.dim + c, cnt, 0.0f, v);
+      float v[kNarrow];
+      load_part<kActF32, kNarrow>(a.partial + 2 * j * a.dim + c, cnt, 0.0f, v);
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e) g[e] += v[e];
+      for (int e = 0; e < kNarrow; ++e) g[e] += v[e];
     }
   }
 #pragma unroll
-  for (int e = 0; e < kUnit; ++e) g[e] = a.scale * g[e];
+  for (int e = 0; e < kNarrow; ++e) g[e] = a.scale * g[e];
 }
 
-// Unit u of a table: row u / units, columns from (u % units) kUnit on.
+// Unit u of a table: row u / units, columns from (u % units) N on.
+template <int N>
 struct Unit {
-  uint32_t row;
-  int64_t c;
-  int cnt;
+  uint32_t row, unit;
+  __device__ __forceinline__ Unit(uint32_t u, int64_t dim) {
+    const uint32_t units = static_cast<uint32_t>((dim + N - 1) / N);
+    row = u / units;
+    unit = u - row * units;
+  }
+  __device__ __forceinline__ int64_t column() const { return static_cast<int64_t>(unit) * N; }
 };
-__device__ __forceinline__ Unit unit_of(uint32_t u, int64_t dim) {
-  const uint32_t units = static_cast<uint32_t>((dim + kUnit - 1) / kUnit);
-  const uint32_t row = u / units;
-  const int64_t c = static_cast<int64_t>(u - row * units) * kUnit;
-  return Unit{row, c, static_cast<int>(dim - c)};
+
+// Streaming accesses of fp32 state: not read again before the caches are.
+__device__ __forceinline__ void stream_in(const float* p, int cnt, float (&v)[kNarrow]) {
+  typedef Pack<float, kNarrow>::type P;
+  if (cnt >= kNarrow) {
+    const P x = __builtin_nontemporal_load(reinterpret_cast<const P*>(p));
+#pragma unroll
+    for (int e = 0; e < kNarrow; ++e) v[e] = x[e];
+  } else {
+    load_part<kActF32, kNarrow>(p, cnt, 0.0f, v);
+  }
+}
+__device__ __forceinline__ void stream_out(float* p, int cnt, const float (&v)[kNarrow]) {
+  typedef Pack<float, kNarrow>::type P;
+  if (cnt >= kNarrow) {
+    P x;
+#pragma unroll
+    for (int e = 0; e < kNarrow; ++e) x[e] = v[e];
+    __builtin_nontemporal_store(x, reinterpret_cast<P*>(p));
+  } else {
+    store_part<kActF32, kNarrow>(p, cnt, v);
+  }
 }
 
 // kStore: grad = s sum on every row.  kAddRows, kAddTokens: grad += s sum on the rows that
@@ -343,7 +378,7 @@ template <int T, int kMode>
 __global__ __launch_bounds__(kThreads) void grad_rows_kernel(RowArgs a, float* grad, uint32_t total) {
   const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
   if (u >= total) return;
-  const Unit t = unit_of(u, a.dim);
+  const Unit<kNarrow> t(u, a.dim);
   uint32_t s = 0, m, v = t.row;
   if (kMode == kAddTokens) {
     s = t.row;
@@ -354,15 +389,17 @@ __global__ __launch_bounds__(kThreads) void grad_rows_kernel(RowArgs a, float* g
     m = segment_of(a, v, &s);
     if (kMode == kAddRows && m == 0) return;
   }
-  float g[kUnit], old[kUnit];
-  float* to = grad + v * a.dim + t.c;
-  if (kMode != kStore) load_part<kActF32, kUnit>(to, t.cnt, 0.0f, old);
-  row_gradient<T>(a, s, m, t.c, t.cnt, g);
+  const int64_t c = t.column();
+  const int cnt = static_cast<int>(a.dim - c);
+  float g[kNarrow], old[kNarrow];
+  float* to = grad + v * a.dim + c;
+  if (kMode != kStore) load_part<kActF32, kNarrow>(to, cnt, 0.0f, old);
+  row_gradient<T>(a, s, m, c, cnt, g);
   if (kMode != kStore) {
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e) g[e] = old[e] + g[e];
+    for (int e = 0; e < kNarrow; ++e) g[e] = old[e] + g[e];
   }
-  store_part<kActF32, kUnit>(to, t.cnt, g);
+  stream_out(to, cnt, g);
 }
 
 template <int T, int kMode>
@@ -370,20 +407,21 @@ __global__ __launch_bounds__(kThreads) void step_rows_kernel(RowArgs a, float* p
                                                              AdamWConst c, uint32_t total) {
   const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
   if (u >= total) return;
-  const Unit t = unit_of(u, a.dim);
-  const int64_t at = t.row * a.dim + t.c;
-  float P[kUnit], M[kUnit], V[kUnit], g[kUnit];
-  load_part<kActF32, kUnit>(p + at, t.cnt, 0.0f, P);
-  load_part<kActF32, kUnit>(m + at, t.cnt, 0.0f, M);
-  load_part<kActF32, kUnit>(v + at, t.cnt, 0.0f, V);
+  const Unit<kNarrow> t(u, a.dim);
+  const int64_t col = t.column(), at = t.row * a.dim + col;
+  const int cnt = static_cast<int>(a.dim - col);
+  float P[kNarrow], M[kNarrow], V[kNarrow], g[kNarrow];
+  stream_in(p + at, cnt, P);
+  stream_in(m + at, cnt, M);
+  stream_in(v + at, cnt, V);
   uint32_t s = 0;
   const uint32_t count = segment_of(a, t.row, &s);
-  row_gradient<T>(a, s, count, t.c, t.cnt, g);
+  row_gradient<T>(a, s, count, col, cnt, g);
 #pragma unroll
-  for (int e = 0; e < kUnit; ++e) adamw_elem_t<kMode>(P[e], g[e], M[e], V[e], c);
-  store_part<kActF32, kUnit>(p + at, t.cnt, P);
-  store_part<kActF32, kUnit>(m + at, t.cnt, M);
-  store_part<kActF32, kUnit>(v + at, t.cnt, V);
+  for (int e = 0; e < kNarrow; ++e) adamw_elem_t<kMode>(P[e], g[e], M[e], V[e], c);
+  stream_out(p + at, cnt, P);
+  stream_out(m + at, cnt, M);
+  stream_out(v + at, cnt, V);
 }
 
 // ---------------------------------------------------------------------------
@@ -397,15 +435,17 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const float* table, ui
                                                           int64_t out_stride) {
   const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
   if (u >= total) return;
-  const Unit t = unit_of(u, dim);
+  const Unit<kWide> t(u, dim);
+  const int64_t c = t.column();
+  const int cnt = static_cast<int>(dim - c);
   const uint32_t v = key_of(tokens, token_bits, t.row, rows);
-  float x[kUnit] = {};
+  float x[kWide] = {};
   if (v < rows) {
-    load_part<kActF32, kUnit>(table + v * dim + t.c, t.cnt, 0.0f, x);
+    load_part<kActF32, kWide>(table + v * dim + c, cnt, 0.0f, x);
 #pragma unroll
-    for (int e = 0; e < kUnit; ++e) x[e] *= scale;
+    for (int e = 0; e < kWide; ++e) x[e] *= scale;
   }
-  store_part<T, kUnit>(out + t.row * out_stride + t.c, t.cnt, x);
+  store_part<T, kWide>(out + t.row * out_stride + c, cnt, x);
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -428,7 +468,7 @@ EmbeddingPlan plan_embedding(int64_t rows, int64_t dim, int64_t n) {
   while ((n + p.share - 1) / p.share > 128) p.share *= 2;
   p.blocks = static_cast<int>((n + p.share - 1) / p.share);
   // at most 1024 partial sums to join for one row, and none where they are not worth a launch
-  p.chunk = n <= 128 ? 128 : 64;
+  p.chunk = n <= 128 ? 128 : 32;
   while (n / p.chunk > 1024) p.chunk *= 2;
   p.chunks = (n + p.chunk - 1) / p.chunk;
   int64_t at = 0;
@@ -450,11 +490,11 @@ EmbeddingPlan plan_embedding(int64_t rows, int64_t dim, int64_t n) {
   return p;
 }
 
-static int64_t units_of(int64_t rows, int64_t dim) { return rows * ((dim + kUnit - 1) / kUnit); }
+static int64_t units_of(int64_t rows, int64_t dim, int unit) { return rows * ((dim + unit - 1) / unit); }
 
 int64_t embedding_threads(int64_t rows, int64_t dim, int64_t n) {
   const EmbeddingPlan p = plan_embedding(rows, dim, n);
-  return std::max(std::max(units_of(rows, dim), units_of(n, dim)), p.chunks * kThreads) + kThreads;
+  return std::max(std::max(units_of(rows, dim, kNarrow), units_of(n, dim, kNarrow)), p.chunks * kThreads) + kThreads;
 }
 
 // Sorts the tokens and finds the segments; fills the arguments of stage 3.
@@ -488,8 +528,8 @@ static hipError_t sort_tokens(const EmbeddingCall& e, RowArgs* out, hipStream_t 
     for (int pass = 0; pass < passes; ++pass) {
       const int from = (pass + 1) & 1, to = pass & 1;
       hipLaunchKernelGGL(sort_count_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0, keys[from]);
-      hipLaunchKernelGGL(sort_scatter_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0,
-                         keys[from], order[from], keys[to], order[to]);
+      hipLaunchKernelGGL(sort_scatter_kernel, grid, block, 0, s, sa, pass * width, 1 << width, pass == 0, keys[from],
+                         order[from], keys[to], order[to]);
     }
     last = (passes - 1) & 1;
   }
@@ -509,7 +549,7 @@ static hipError_t sort_tokens(const EmbeddingCall& e, RowArgs* out, hipStream_t 
   *out = a;
   if (small && e.n <= p.chunk) return hipGetLastError();
   return with_act(e.dout_type, [&](auto t) {
-    const int64_t slices = (units_of(1, e.dim) + kThreads - 1) / kThreads;
+    const int64_t slices = (units_of(1, e.dim, kWide) + 63) / 64;
     hipLaunchKernelGGL((segments_kernel<decltype(t)::value>), dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(slices)),
                        dim3(kThreads), 0, s, a, small ? 0 : 1);
     return hipGetLastError();
@@ -523,7 +563,7 @@ hipError_t launch_embedding_forward(const float* table, int64_t rows, int64_t di
                                     void* out, int out_type, int64_t out_stride, hipStream_t s) {
   return with_act(out_type, [&](auto t) {
     typedef typename Act<decltype(t)::value>::S S;
-    const int64_t units = units_of(n, dim);
+    const int64_t units = units_of(n, dim, kWide);
     hipLaunchKernelGGL((lookup_kernel<decltype(t)::value>), unit_grid(units), dim3(kThreads), 0, s, table,
                        static_cast<uint32_t>(rows), dim, tokens, token_bits, static_cast<uint32_t>(units), scale,
                        static_cast<S*>(out), out_stride);
@@ -538,7 +578,7 @@ hipError_t launch_embedding_backward(const EmbeddingCall& e, float* grad, bool a
   return with_act(e.dout_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     const bool by_token = add && e.n < e.rows;
-    const int64_t units = units_of(by_token ? e.n : e.rows, e.dim);
+    const int64_t units = units_of(by_token ? e.n : e.rows, e.dim, kNarrow);
     const uint32_t total = static_cast<uint32_t>(units);
     if (by_token) hipLaunchKernelGGL((grad_rows_kernel<T, kAddTokens>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
     else if (add) hipLaunchKernelGGL((grad_rows_kernel<T, kAddRows>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
@@ -554,7 +594,7 @@ hipError_t launch_adamw_embedding(const EmbeddingCall& e, float* p, float* m, fl
   if (st != hipSuccess) return st;
   return with_act(e.dout_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    const int64_t units = units_of(e.rows, e.dim);
+    const int64_t units = units_of(e.rows, e.dim, kNarrow);
     const dim3 grid = unit_grid(units), block(kThreads);
     const uint32_t total = static_cast<uint32_t>(units);
     switch (decay_mode(c)) {
