@@ -15,52 +15,69 @@ captured gradients: no eager autograd graph of the same parameters may be alive 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
-from ._lib import (_AdamWHParams, _check, _ptr, _require_f32_cuda, _scratch, _stream_handle, load)
+from ._lib import _AdamWHParams, _check, _require_f32_cuda, _stream_handle, load
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _BITS = {torch.int32: 32, torch.int64: 64}
 
 
 # --------------------------------------------------------------------------
-# marshalling helpers
+# marshalling helpers.  Small calls are bound by this code, not by their kernels, so the
+# checks touch each tensor once and the current stream is asked for its handle directly.
 # --------------------------------------------------------------------------
-def _on(device):
-    """Launches go to the tensors' device, whichever device is current."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _empty(shape, dtype, device, stream):
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and stream != torch.cuda.current_stream(device):
+def _call(name, device, stream, *args):
+    """The C call `name` with the stream's handle, on the tensors' device, whichever device
+    is current."""
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = _stream_handle(stream, device)
+    fn = getattr(load(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status:
+        _check(status)
+
+
+def _empty(like, shape, dtype, stream):
+    """A tensor on the device of `like`.  Work on another stream than the current one is
+    recorded, so that the memory is not handed out again before that stream is done."""
+    t = like.new_empty(shape, dtype=dtype)
+    if stream is not None and stream != torch.cuda.current_stream(like.device):
         t.record_stream(stream)
     return t
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _tensor(name, t, device) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU (got {t.device})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _type(name, dtype) -> int:
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16 (got {dtype})")
-    return _DTYPES[dtype]
+    return code
 
 
-def _rows(name, t):
+def _rows(name, t, device=None):
     """(rows, columns, row stride in values) of an activation tensor (..., columns)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got {t.device})")
+    _tensor(name, t, device)
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     dim = t.shape[-1]
@@ -79,39 +96,61 @@ def _rows(name, t):
     return n, dim, stride
 
 
-def _ints(name, t) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must live on the GPU (got {t.device})")
-    if t.dtype not in _BITS:
+def _ints(name, t, device=None) -> int:
+    _tensor(name, t, device)
+    bits = _BITS.get(t.dtype)
+    if bits is None:
         raise ValueError(f"{name} must be int32 or int64 (got {t.dtype})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _BITS[t.dtype]
+    return bits
 
 
-def _vector(name, t, dim):
+def _floats(name, t, count, device=None) -> int:
+    """The address of an fp32 vector of `count` values; 0 for None."""
     if t is None:
-        return
-    _require_f32_cuda(name, t)
-    if t.numel() != dim:
-        raise ValueError(f"{name} must hold {dim} values (got {t.numel()})")
+        return 0
+    _tensor(name, t, device)
+    if t.dtype is not torch.float32 or not t.is_contiguous():
+        _require_f32_cuda(name, t)
+    if t.numel() != count:
+        raise ValueError(f"{name} must hold {count} values (got {t.numel()})")
+    return t.data_ptr()
 
 
-def _table(name, t):
-    _require_f32_cuda(name, t)
+def _table(name, t, device=None):
+    _tensor(name, t, device)
+    if t.dtype is not torch.float32 or not t.is_contiguous():
+        _require_f32_cuda(name, t)
     if t.dim() != 2:
         raise ValueError(f"{name} must be a (rows, dim) table")
     return t.shape
 
 
-def _workspace(workspace, need, device, stream):
-    """(tensor or None, bytes): the caller's workspace, or one allocated for the call."""
+def _workspace(workspace, need, like, stream):
+    """(the tensor to keep, address, bytes) of the caller's workspace, or of one allocated
+    for the call."""
     if workspace is None:
-        return (_scratch(need, device, stream), need) if need else (None, 0)
-    _same_device(device, workspace=workspace)
-    return workspace, workspace.numel() * workspace.element_size()
+        if not need:
+            return None, 0, 0
+        workspace = _empty(like, need, torch.uint8, stream)
+    else:
+        _tensor("workspace", workspace, like.device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=256)
+def embedding_workspace_bytes(rows: int, dim: int, n: int) -> int:
+    """Workspace of embedding_backward and adamw_step_embedding for n tokens."""
+    return int(load().ma_embedding_workspace_bytes(int(rows), int(dim), int(n)))
+
+
+@functools.lru_cache(maxsize=256)
+def layer_norm_workspace_bytes(n: int, dim: int) -> int:
+    """Workspace of layer_norm_backward for n rows."""
+    return int(load().ma_layer_norm_workspace_bytes(int(n), int(dim)))
 
 
 # --------------------------------------------------------------------------
@@ -122,29 +161,22 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     result tokens.shape + (dim,) in out_dtype (float32 when None) or written to `out`.  A
     token outside [0, rows) is padding: a zero row."""
     rows, dim = _table("table", table)
-    bits = _ints("tokens", tokens)
-    shape = tuple(tokens.shape) + (dim,)
+    device = table.device
+    bits = _ints("tokens", tokens, device)
+    shape = tokens.shape + (dim,)
     if out is None:
-        out = _empty(shape, out_dtype or torch.float32, table.device, stream)
-    elif tuple(out.shape) != shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be {shape} of {out_dtype or out.dtype}")
-    _same_device(table.device, tokens=tokens, out=out)
-    _, _, stride = _rows("out", out)
-    with _on(table.device):
-        _check(load().ma_embedding_forward(
-            _ptr(table), rows, dim, _ptr(tokens), bits, tokens.numel(), scale, _ptr(out),
-            _type("out", out.dtype), stride, _stream_handle(stream, table.device)))
+        out = _empty(table, shape, out_dtype or torch.float32, stream)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {tuple(shape)} of {out_dtype or out.dtype}")
+    _, _, stride = _rows("out", out, device)
+    _call("ma_embedding_forward", device, stream, table.data_ptr(), rows, dim, tokens.data_ptr(),
+          bits, tokens.numel(), scale, out.data_ptr(), _type("out", out.dtype), stride)
     return out
 
 
-def embedding_workspace_bytes(rows: int, dim: int, n: int) -> int:
-    """Workspace of embedding_backward and adamw_step_embedding for n tokens."""
-    return int(load().ma_embedding_workspace_bytes(int(rows), int(dim), int(n)))
-
-
-def _token_rows(tokens, dout, dim):
-    bits = _ints("tokens", tokens)
-    n, cols, stride = _rows("dout", dout)
+def _token_rows(tokens, dout, dim, device):
+    bits = _ints("tokens", tokens, device)
+    n, cols, stride = _rows("dout", dout, device)
     if cols != dim or n != tokens.numel():
         raise ValueError(f"dout {tuple(dout.shape)} does not match {tokens.numel()} tokens of {dim}")
     return bits, n, stride, _type("dout", dout.dtype)
@@ -156,21 +188,16 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
     (dim,), into `grad` (allocated when None) or, with accumulate, added to it."""
     if accumulate and grad is None:
         raise ValueError("accumulate needs a grad to add to")
-    rows, dim = int(rows), dout.shape[-1]
-    bits, n, stride, dtype = _token_rows(tokens, dout, dim)
-    device = dout.device
+    rows, dim, device = int(rows), dout.shape[-1], dout.device
+    bits, n, stride, dtype = _token_rows(tokens, dout, dim, device)
     if grad is None:
-        grad = _empty((rows, dim), torch.float32, device, stream)
-    elif tuple(_table("grad", grad)) != (rows, dim):
+        grad = _empty(dout, (rows, dim), torch.float32, stream)
+    elif tuple(_table("grad", grad, device)) != (rows, dim):
         raise ValueError(f"grad must be ({rows}, {dim})")
-    _same_device(device, tokens=tokens, grad=grad)
-    lib = load()
-    with _on(device):
-        ws, size = _workspace(workspace, lib.ma_embedding_workspace_bytes(rows, dim, n), device,
-                              stream)
-        _check(lib.ma_embedding_backward(
-            _ptr(tokens), bits, n, _ptr(dout), dtype, stride, scale, _ptr(grad), rows, dim,
-            int(bool(accumulate)), _ptr(ws), size, _stream_handle(stream, device)))
+    need = embedding_workspace_bytes(rows, dim, n)
+    _keep, ws, size = _workspace(workspace, need, dout, stream)
+    _call("ma_embedding_backward", device, stream, tokens.data_ptr(), bits, n, dout.data_ptr(),
+          dtype, stride, scale, grad.data_ptr(), rows, dim, int(bool(accumulate)), ws, size)
     return grad
 
 
@@ -182,23 +209,18 @@ def adamw_step_embedding(param, tokens, dout, exp_avg, exp_avg_sq, *, scale: flo
     embedding_backward(dout, tokens, rows, scale=scale), which is not materialised: bitwise
     adamw_step on that gradient."""
     rows, dim = _table("param", param)
-    for name, t in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
-        if tuple(_table(name, t)) != (rows, dim):
-            raise ValueError(f"{name} must be ({rows}, {dim})")
-    bits, n, stride, dtype = _token_rows(tokens, dout, dim)
     device = param.device
-    _same_device(device, tokens=tokens, dout=dout, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq)
-    hp = _AdamWHParams(lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
-                       step=int(step), decoupled=int(bool(decoupled)),
-                       cautious_wd=int(bool(cautious_wd)))
-    lib = load()
-    with _on(device):
-        ws, size = _workspace(workspace, lib.ma_embedding_workspace_bytes(rows, dim, n), device,
-                              stream)
-        _check(lib.ma_adamw_step_embedding(
-            _ptr(param), _ptr(exp_avg), _ptr(exp_avg_sq), rows, dim, _ptr(tokens), bits, n,
-            _ptr(dout), dtype, stride, scale, ctypes.byref(hp), _ptr(ws), size,
-            _stream_handle(stream, device)))
+    if _table("exp_avg", exp_avg, device) != param.shape or \
+            _table("exp_avg_sq", exp_avg_sq, device) != param.shape:
+        raise ValueError(f"exp_avg and exp_avg_sq must be ({rows}, {dim})")
+    bits, n, stride, dtype = _token_rows(tokens, dout, dim, device)
+    hp = _AdamWHParams(lr, beta1, beta2, eps, weight_decay, int(step), int(bool(decoupled)),
+                       int(bool(cautious_wd)))
+    need = embedding_workspace_bytes(rows, dim, n)
+    _keep, ws, size = _workspace(workspace, need, param, stream)
+    _call("ma_adamw_step_embedding", device, stream, param.data_ptr(), exp_avg.data_ptr(),
+          exp_avg_sq.data_ptr(), rows, dim, tokens.data_ptr(), bits, n, dout.data_ptr(), dtype,
+          stride, scale, ctypes.byref(hp), ws, size)
 
 
 # --------------------------------------------------------------------------
@@ -209,27 +231,19 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, out=None
     fp32 vectors or None; y has x's type; mean and rstd (x.shape[:-1], fp32) are the
     backward pass's inputs."""
     n, dim, stride = _rows("x", x)
-    _vector("weight", weight, dim)
-    _vector("bias", bias, dim)
     dtype, device = _type("x", x.dtype), x.device
+    w, b = _floats("weight", weight, dim, device), _floats("bias", bias, dim, device)
     if out is None:
-        out = _empty(x.shape, x.dtype, device, stream)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and type")
-    _, _, out_stride = _rows("out", out)
-    _same_device(device, weight=weight, bias=bias, out=out)
-    mean = _empty(x.shape[:-1], torch.float32, device, stream)
-    rstd = _empty(x.shape[:-1], torch.float32, device, stream)
-    with _on(device):
-        _check(load().ma_layer_norm_forward(
-            _ptr(x), dtype, stride, n, dim, _ptr(weight), _ptr(bias), eps, _ptr(out), out_stride,
-            _ptr(mean), _ptr(rstd), _stream_handle(stream, device)))
+        out, out_stride = _empty(x, x.shape, x.dtype, stream), max(dim, 1)
+    else:
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have x's shape and type")
+        _, _, out_stride = _rows("out", out, device)
+    mean = _empty(x, x.shape[:-1], torch.float32, stream)
+    rstd = _empty(x, x.shape[:-1], torch.float32, stream)
+    _call("ma_layer_norm_forward", device, stream, x.data_ptr(), dtype, stride, n, dim, w, b, eps,
+          out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
     return out, mean, rstd
-
-
-def layer_norm_workspace_bytes(n: int, dim: int) -> int:
-    """Workspace of layer_norm_backward for n rows."""
-    return int(load().ma_layer_norm_workspace_bytes(int(n), int(dim)))
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = True,
@@ -239,33 +253,26 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
     that one out (None).  dweight, dbias: fp32 vectors to write, or with accumulate to add to
     (allocated when None)."""
     n, dim, x_stride = _rows("x", x)
-    dn, ddim, dy_stride = _rows("dy", dy)
-    if (dn, ddim) != (n, dim) or dy.dtype != x.dtype:
-        raise ValueError("dy must have x's shape and type")
-    _vector("weight", weight, dim)
-    _vector("mean", mean, n)
-    _vector("rstd", rstd, n)
     device = x.device
-    for name, t, wanted in (("dweight", dweight, weight_grad), ("dbias", dbias, bias_grad)):
-        _vector(name, t, dim)
-        if t is not None and not wanted:
-            raise ValueError(f"{name} is given but not wanted")
-        if accumulate and wanted and t is None:
-            raise ValueError(f"accumulate needs a {name} to add to")
-    dx = _empty(x.shape, x.dtype, device, stream)
+    dn, ddim, dy_stride = _rows("dy", dy, device)
+    if dn != n or ddim != dim or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and type")
+    if (dweight is not None and not weight_grad) or (dbias is not None and not bias_grad):
+        raise ValueError("a gradient buffer is given for a gradient that is not wanted")
+    if accumulate and ((weight_grad and dweight is None) or (bias_grad and dbias is None)):
+        raise ValueError("accumulate needs the gradients to add to")
     if weight_grad and dweight is None:
-        dweight = _empty(dim, torch.float32, device, stream)
+        dweight = _empty(x, dim, torch.float32, stream)
     if bias_grad and dbias is None:
-        dbias = _empty(dim, torch.float32, device, stream)
-    _same_device(device, dy=dy, mean=mean, rstd=rstd, weight=weight, dweight=dweight, dbias=dbias)
-    lib = load()
-    with _on(device):
-        need = lib.ma_layer_norm_workspace_bytes(n, dim) if weight_grad or bias_grad else 0
-        ws, size = _workspace(workspace, need, device, stream)
-        _check(lib.ma_layer_norm_backward(
-            _ptr(dy), dy_stride, _ptr(x), x_stride, _type("x", x.dtype), n, dim, _ptr(weight),
-            _ptr(mean), _ptr(rstd), _ptr(dx), max(dim, 1), _ptr(dweight), _ptr(dbias),
-            int(bool(accumulate)), _ptr(ws), size, _stream_handle(stream, device)))
+        dbias = _empty(x, dim, torch.float32, stream)
+    dx = _empty(x, x.shape, x.dtype, stream)
+    need = layer_norm_workspace_bytes(n, dim) if weight_grad or bias_grad else 0
+    _keep, ws, size = _workspace(workspace, need, x, stream)
+    _call("ma_layer_norm_backward", device, stream, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride,
+          _type("x", x.dtype), n, dim, _floats("weight", weight, dim, device),
+          _floats("mean", mean, n, device), _floats("rstd", rstd, n, device), dx.data_ptr(),
+          max(dim, 1), _floats("dweight", dweight, dim, device),
+          _floats("dbias", dbias, dim, device), int(bool(accumulate)), ws, size)
     return dx, dweight, dbias
 
 
@@ -273,27 +280,26 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
 # distillation
 # --------------------------------------------------------------------------
 def _distill(logits, teacher, ids, temperature):
-    """The leading arguments shared by the three calls, and (rows, vocab)."""
+    """The leading arguments shared by the three calls, and the number of rows."""
     n, vocab, stride = _rows("logits", logits)
-    if not isinstance(teacher, torch.Tensor) or teacher.shape[:-1] != logits.shape[:-1] \
-            or not teacher.is_contiguous():
+    _tensor("teacher", teacher, logits.device)
+    if teacher.shape[:-1] != logits.shape[:-1] or not teacher.is_contiguous():
         raise ValueError("teacher must be contiguous with the logits' leading dimensions")
-    bits = _ints("ids", ids)
+    bits = _ints("ids", ids, logits.device)
     if ids.shape != teacher.shape:
         raise ValueError("ids must have the teacher's shape")
-    _same_device(logits.device, teacher=teacher, ids=ids)
-    return (_ptr(logits), _type("logits", logits.dtype), stride, n, vocab, _ptr(teacher),
-            _type("teacher", teacher.dtype), _ptr(ids), bits, teacher.shape[-1],
+    return (logits.data_ptr(), _type("logits", logits.dtype), stride, n, vocab, teacher.data_ptr(),
+            _type("teacher", teacher.dtype), ids.data_ptr(), bits, teacher.shape[-1],
             float(temperature)), n
 
 
 def _dlogits(logits, dlogits, stream):
+    """(dlogits, row stride)"""
     if dlogits is None:
-        return _empty(logits.shape, logits.dtype, logits.device, stream)
+        return _empty(logits, logits.shape, logits.dtype, stream), logits.shape[-1]
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError("dlogits must have the logits' shape and type")
-    _same_device(logits.device, dlogits=dlogits)
-    return dlogits
+    return dlogits, _rows("dlogits", dlogits, logits.device)[2]
 
 
 def distill_forward(logits, teacher, ids, *, temperature: float = 1.0, stream=None):
@@ -302,12 +308,9 @@ def distill_forward(logits, teacher, ids, *, temperature: float = 1.0, stream=No
     at the vocabulary places ids.  loss has the leading dimensions; stats (..., 2) is the
     backward pass's input."""
     args, _ = _distill(logits, teacher, ids, temperature)
-    device = logits.device
-    loss = _empty(logits.shape[:-1], torch.float32, device, stream)
-    stats = _empty(tuple(logits.shape[:-1]) + (2,), torch.float32, device, stream)
-    with _on(device):
-        _check(load().ma_distill_forward(*args, _ptr(loss), _ptr(stats),
-                                         _stream_handle(stream, device)))
+    loss = _empty(logits, logits.shape[:-1], torch.float32, stream)
+    stats = _empty(logits, logits.shape[:-1] + (2,), torch.float32, stream)
+    _call("ma_distill_forward", logits.device, stream, *args, loss.data_ptr(), stats.data_ptr())
     return loss, stats
 
 
@@ -317,14 +320,9 @@ def distill_backward(logits, teacher, ids, stats, row_weight, *, temperature: fl
     `dlogits` (allocated when None; may be `logits` itself)."""
     args, n = _distill(logits, teacher, ids, temperature)
     device = logits.device
-    _vector("stats", stats, 2 * n)
-    _vector("row_weight", row_weight, n)
-    _same_device(device, stats=stats, row_weight=row_weight)
-    dlogits = _dlogits(logits, dlogits, stream)
-    _, _, stride = _rows("dlogits", dlogits)
-    with _on(device):
-        _check(load().ma_distill_backward(*args, _ptr(stats), _ptr(row_weight), _ptr(dlogits),
-                                          stride, _stream_handle(stream, device)))
+    s, w = _floats("stats", stats, 2 * n, device), _floats("row_weight", row_weight, n, device)
+    dlogits, stride = _dlogits(logits, dlogits, stream)
+    _call("ma_distill_backward", device, stream, *args, s, w, dlogits.data_ptr(), stride)
     return dlogits
 
 
@@ -334,14 +332,11 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
     the values of distill_forward and distill_backward."""
     args, n = _distill(logits, teacher, ids, temperature)
     device = logits.device
-    _vector("row_weight", row_weight, n)
-    _same_device(device, row_weight=row_weight)
-    loss = _empty(logits.shape[:-1], torch.float32, device, stream)
-    dlogits = _dlogits(logits, dlogits, stream)
-    _, _, stride = _rows("dlogits", dlogits)
-    with _on(device):
-        _check(load().ma_distill_loss_grad(*args, _ptr(row_weight), _ptr(loss), _ptr(dlogits),
-                                           stride, _stream_handle(stream, device)))
+    w = _floats("row_weight", row_weight, n, device)
+    loss = _empty(logits, logits.shape[:-1], torch.float32, stream)
+    dlogits, stride = _dlogits(logits, dlogits, stream)
+    _call("ma_distill_loss_grad", device, stream, *args, w, loss.data_ptr(), dlogits.data_ptr(),
+          stride)
     return loss, dlogits
 
 
