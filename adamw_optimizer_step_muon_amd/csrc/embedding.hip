@@ -38,7 +38,10 @@ constexpr int kNarrow = 4;  // rows of the table
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxBins = 512;      // 9 bits a pass: vocabularies up to 2^18 - 1 take two passes
-constexpr int kSmallSort = 4096;   // tokens sorted by one block in one launch
+constexpr int kOneLaunch = 16384;  // tokens sorted in one launch: keys and two orders in 128 KB
+constexpr int kLocalBits = 6;      // digits of its passes
+constexpr int kLocalBins = 1 << kLocalBits;
+static_assert(kLocalBins == 64 && kOneLaunch <= 65536, "a digit a lane, 16-bit places");
 static_assert(kSortThreads >= kMaxBins, "a thread per digit");
 
 __device__ __forceinline__ uint32_t key_of(const void* tokens, int bits, int64_t i,
@@ -158,47 +161,115 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
   }
 }
 
-// The whole sort of at most kSmallSort tokens in one block, and the rows' starts and ends.
-__global__ __launch_bounds__(kSortThreads) void sort_small_kernel(SortArgs a, int passes, int width,
-                                                                  uint32_t* keys_out, uint32_t* order_out,
-                                                                  uint32_t* start, uint32_t* end) {
-  __shared__ Places s;
-  __shared__ uint32_t keys[2][kSmallSort];
-  __shared__ uint16_t order[2][kSmallSort];
-  __shared__ uint32_t hist[kMaxBins];
-  const int tid = threadIdx.x, n = static_cast<int>(a.n), bins = 1 << width;
-  for (int i = tid; i < n; i += kSortThreads) {
-    keys[0][i] = key_of(a.tokens, a.token_bits, i, a.rows);
-    order[0][i] = static_cast<uint16_t>(i);
+// The whole sort of at most kOneLaunch tokens in one launch, and the rows' starts and ends.  The
+// order of the rows is free, as long as a row's tokens stand together in their own order:
+// block b takes the rows with b in their low bits.  Every block reads all tokens (from the
+// L2), keeps its own in their order, sorts those by the other bits within its shared memory,
+// and knows its first place from the number of tokens of the blocks before it.  8191 tokens
+// take 11 us here and 25 us in the four launches of two counted passes, 16384 tokens 21 and 25 us.
+struct OneLaunch {
+  uint32_t keys[kOneLaunch];      // of all tokens
+  uint16_t order[2][kOneLaunch];  // of the block's own
+  uint32_t base[kLocalBins];
+  uint32_t count[kSortWaves][kLocalBins];
+  uint32_t own[kSortWaves], before[kSortWaves], wave_total[kSortWaves];
+};
+__global__ __launch_bounds__(kSortThreads) void sort_one_launch_kernel(SortArgs a, int block_bits, int key_bits,
+                                                                       uint32_t* keys_out, uint32_t* order_out,
+                                                                       uint32_t* start, uint32_t* end) {
+  __shared__ OneLaunch s;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = static_cast<int>(a.n);
+  const uint32_t mine = blockIdx.x, low = (1u << block_bits) - 1;
+  // a wave's share of the tokens: 64-token steps, in order
+  const int steps = (n + kSortThreads - 1) / kSortThreads;
+  uint32_t own = 0, before = 0;
+#pragma unroll 4
+  for (int k = 0; k < steps; ++k) {
+    const int i = (wave * steps + k) * 64 + lane;
+    if (i < n) {
+      const uint32_t key = key_of(a.tokens, a.token_bits, i, a.rows);
+      s.keys[i] = key;
+      own += (key & low) == mine;
+      before += (key & low) < mine;
+    }
+  }
+  for (int d = 32; d > 0; d >>= 1) {
+    own += __shfl_xor(own, d, 64);
+    before += __shfl_xor(before, d, 64);
+  }
+  if (lane == 0) {
+    s.own[wave] = own;
+    s.before[wave] = before;
+  }
+  __syncthreads();
+  uint32_t first = 0, m = 0, at = 0;  // the block's first place and tokens, the wave's first
+  for (int w = 0; w < kSortWaves; ++w) {
+    first += s.before[w];
+    if (w < wave) at += s.own[w];
+    m += s.own[w];
+  }
+  for (int k = 0; k < steps; ++k) {
+    const int i = (wave * steps + k) * 64 + lane;
+    const bool keep = i < n && (s.keys[i] & low) == mine;
+    const uint64_t kept = __ballot(keep);
+    if (keep) s.order[0][at + __popcll(kept & ((1ull << lane) - 1))] = static_cast<uint16_t>(i);
+    at += static_cast<uint32_t>(__popcll(kept));
   }
   int from = 0;
-  for (int pass = 0; pass < passes; ++pass, from ^= 1) {
-    const int shift = pass * width;
-    if (tid < bins) hist[tid] = 0;
+  for (int shift = block_bits; shift < key_bits; shift += kLocalBits, from ^= 1) {
+    // stable scatter by one digit, as sort_scatter_kernel's
+    if (tid < kLocalBins) s.base[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kSortThreads) atomicAdd(&hist[(keys[from][i] >> shift) & (bins - 1)], 1u);
+    for (uint32_t i = tid; i < m; i += kSortThreads)
+      atomicAdd(&s.base[(s.keys[s.order[from][i]] >> shift) & (kLocalBins - 1)], 1u);
     __syncthreads();
-    const uint32_t smaller = digit_scan(tid < bins ? hist[tid] : 0, s);
-    if (tid < bins) s.base[tid] = smaller;
-    for (int t0 = 0; t0 < n; t0 += kSortThreads) {
-      const int i = t0 + tid;
-      const bool in = i < n;
-      const uint32_t k = in ? keys[from][i] : 0;
-      const uint32_t at = place_of(in, (k >> shift) & (bins - 1), bins, s);
-      if (in) {
-        keys[from ^ 1][at] = k;
-        order[from ^ 1][at] = order[from][i];
+    if (wave == 0) {  // kLocalBins digits, one a lane
+      const uint32_t c = s.base[lane];
+      uint32_t scan = c;
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t up = __shfl_up(scan, d, 64);
+        if (lane >= d) scan += up;
       }
+      s.base[lane] = scan - c;
     }
-    __syncthreads();
+    for (uint32_t t0 = 0; t0 < m; t0 += kSortThreads) {
+      const uint32_t i = t0 + tid;
+      const bool in = i < m;
+      const uint16_t o = in ? s.order[from][i] : 0;
+      const uint32_t digit = in ? (s.keys[o] >> shift) & (kLocalBins - 1) : 0;
+      s.count[wave][lane] = 0;  // the wave's own row
+      uint64_t same = __ballot(in);
+      for (int bit = 1; bit < kLocalBins; bit <<= 1) {
+        const uint64_t with = __ballot((digit & bit) != 0);
+        same &= (digit & bit) ? with : ~with;
+      }
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      __builtin_amdgcn_wave_barrier();
+      if (in && rank == 0) s.count[wave][digit] = static_cast<uint32_t>(__popcll(same));
+      __syncthreads();
+      if (tid < kLocalBins) {
+        uint32_t next = s.base[tid];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+          const uint32_t c = s.count[w][tid];
+          s.count[w][tid] = next;
+          next += c;
+        }
+        s.base[tid] = next;
+      }
+      __syncthreads();
+      if (in) s.order[from ^ 1][s.count[wave][digit] + rank] = o;
+      __syncthreads();
+    }
   }
-  for (int i = tid; i < n; i += kSortThreads) {
-    const uint32_t k = keys[from][i];
-    keys_out[i] = k;
-    order_out[i] = order[from][i];
+  __syncthreads();
+  for (uint32_t i = tid; i < m; i += kSortThreads) {
+    const uint32_t o = s.order[from][i], k = s.keys[o];
+    keys_out[first + i] = k;
+    order_out[first + i] = o;
     if (k >= a.rows) continue;
-    if (i == 0 || keys[from][i - 1] != k) start[k] = i;
-    if (i == n - 1 || keys[from][i + 1] != k) end[k] = i + 1;
+    if (i == 0 || s.keys[s.order[from][i - 1]] != k) start[k] = first + i;
+    if (i == m - 1 || s.keys[s.order[from][i + 1]] != k) end[k] = first + i + 1;
   }
 }
 
@@ -374,32 +445,46 @@ __device__ __forceinline__ void stream_out(float* p, int cnt, const float (&v)[k
 // fewer.  The product is rounded before it is added, so adding gives the bits of a separate
 // gradient's addition.
 enum GradMode { kStore = 0, kAddRows = 1, kAddTokens = 2 };
+// The row of line `line` (a row, or in kAddTokens a sorted position), its first sorted position
+// and its number of tokens; false where the line has nothing to do.
+template <int kMode>
+__device__ __forceinline__ bool line_of(const RowArgs& a, uint32_t line, uint32_t* v, uint32_t* s, uint32_t* m) {
+  if (kMode == kAddTokens) {
+    *s = line;
+    *v = a.keys[line];
+    if (*v >= a.rows || (line > 0 && a.keys[line - 1] == *v)) return false;
+    *m = a.end[*v] - line;
+    return true;
+  }
+  *v = line;
+  *m = segment_of(a, line, s);
+  return kMode == kStore || *m > 0;
+}
+template <int kMode>
+__device__ __forceinline__ void put(float* to, int cnt, float (&g)[kNarrow]) {
+  if (kMode == kStore) {
+    stream_out(to, cnt, g);
+    return;
+  }
+  float old[kNarrow];
+  load_part<kActF32, kNarrow>(to, cnt, 0.0f, old);
+#pragma unroll
+  for (int e = 0; e < kNarrow; ++e) g[e] = old[e] + g[e];
+  store_part<kActF32, kNarrow>(to, cnt, g);
+}
+
 template <int T, int kMode>
 __global__ __launch_bounds__(kThreads) void grad_rows_kernel(RowArgs a, float* grad, uint32_t total) {
   const uint32_t u = blockIdx.x * kThreads + threadIdx.x;
   if (u >= total) return;
   const Unit<kNarrow> t(u, a.dim);
-  uint32_t s = 0, m, v = t.row;
-  if (kMode == kAddTokens) {
-    s = t.row;
-    v = a.keys[s];
-    if (v >= a.rows || (s > 0 && a.keys[s - 1] == v)) return;
-    m = a.end[v] - s;
-  } else {
-    m = segment_of(a, v, &s);
-    if (kMode == kAddRows && m == 0) return;
-  }
+  uint32_t s = 0, m, v;
+  if (!line_of<kMode>(a, t.row, &v, &s, &m)) return;
   const int64_t c = t.column();
   const int cnt = static_cast<int>(a.dim - c);
-  float g[kNarrow], old[kNarrow];
-  float* to = grad + v * a.dim + c;
-  if (kMode != kStore) load_part<kActF32, kNarrow>(to, cnt, 0.0f, old);
+  float g[kNarrow];
   row_gradient<T>(a, s, m, c, cnt, g);
-  if (kMode != kStore) {
-#pragma unroll
-    for (int e = 0; e < kNarrow; ++e) g[e] = old[e] + g[e];
-  }
-  stream_out(to, cnt, g);
+  put<kMode>(grad + v * a.dim + c, cnt, g);
 }
 
 // kStore where many rows of a wide table occur: a wave per tile of a row, so that the row's
@@ -583,11 +668,15 @@ static hipError_t sort_tokens(const EmbeddingCall& e, RowArgs* out, hipStream_t 
   sort_digits(sa.rows, &passes, &width);
   uint32_t* start = reinterpret_cast<uint32_t*>(ws + p.start);
   uint32_t* end = reinterpret_cast<uint32_t*>(ws + p.end);
-  const bool small = e.n <= kSmallSort;
+  const bool small = e.n <= kOneLaunch;
   int last = 0;
   if (small) {
-    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(kSortThreads), 0, s, sa, passes, width, keys[0], order[0],
-                       start, end);
+    // some 32 tokens a block, at most a block per CU (8191 tokens: 64 blocks 1.7 us slower)
+    int bits = 1, block_bits = 0;
+    while (bits < 32 && (sa.rows >> bits)) ++bits;
+    while (block_bits < 8 && block_bits < bits && e.n >> (5 + block_bits)) ++block_bits;
+    hipLaunchKernelGGL(sort_one_launch_kernel, dim3(1u << block_bits), dim3(kSortThreads), 0, s, sa,
+                       block_bits, bits, keys[0], order[0], start, end);
   } else {
     const dim3 grid(static_cast<unsigned>(p.blocks)), block(kSortThreads);
     for (int pass = 0; pass < passes; ++pass) {
@@ -642,16 +731,18 @@ hipError_t launch_embedding_backward(const EmbeddingCall& e, float* grad, bool a
   if (st != hipSuccess) return st;
   return with_act(e.dout_type, [&](auto t) {
     constexpr int T = decltype(t)::value;
+    if (!add && e.dim >= kTile && e.n * kTileRows >= e.rows * kTileTokens) {
+      const int64_t threads = e.rows * ((e.dim + kTile - 1) / kTile) * 64;
+      hipLaunchKernelGGL((grad_tiles_kernel<T>), dim3(static_cast<unsigned>((threads + kTileThreads - 1) / kTileThreads)),
+                         dim3(kTileThreads), 0, s, a, grad);
+      return hipGetLastError();
+    }
     const bool by_token = add && e.n < e.rows;
     const int64_t units = units_of(by_token ? e.n : e.rows, e.dim, kNarrow);
     const uint32_t total = static_cast<uint32_t>(units);
     if (by_token) hipLaunchKernelGGL((grad_rows_kernel<T, kAddTokens>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
     else if (add) hipLaunchKernelGGL((grad_rows_kernel<T, kAddRows>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
-    else if (e.dim >= kTile && e.n * kTileRows >= e.rows * kTileTokens) {
-      const int64_t threads = e.rows * ((e.dim + kTile - 1) / kTile) * 64;
-      hipLaunchKernelGGL((grad_tiles_kernel<T>), dim3(static_cast<unsigned>((threads + kTileThreads - 1) / kTileThreads)),
-                         dim3(kTileThreads), 0, s, a, grad);
-    } else hipLaunchKernelGGL((grad_rows_kernel<T, kStore>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
+    else hipLaunchKernelGGL((grad_rows_kernel<T, kStore>), unit_grid(units), dim3(kThreads), 0, s, a, grad, total);
     return hipGetLastError();
   });
 }
