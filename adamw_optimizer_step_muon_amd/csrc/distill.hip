@@ -67,16 +67,16 @@ constexpr int kVec = Vec<T>::kN;
 
 // What a first sweep keeps of its row for the second one: the last kKeep whole batches in the
 // block's shared memory (each thread reads back what it wrote itself) and the rest behind
-// them in registers.  Where kKeep is 0 nothing is kept.  Almost no second read hits the L2 (a
+// them in registers (kNothing: not even that).  Almost no second read hits the L2 (a
 // row of 128000 bf16 values is 256 KB, 32 CUs share 4 MB), so what is kept is traffic saved.
 // One batch of 64 KB lets two blocks of 1024 threads share a CU, one sweeping while the other
 // waits: loss and gradient of 4096 x 128000 bf16 took 467 us keeping nothing, 430 us (4.9
 // TB/s, the rate of a large copy) with one batch, and 489 us with two, which leave one block.
-constexpr int kKeepBatches = 1;
+constexpr int kKeepBatches = 1, kNothing = -1;
 template <int T, int kThreads, int kKeep>
 struct Kept {
   typedef typename Vec<T>::P P;
-  P tail[kKeep > 0 ? kU : 1];
+  P tail[kKeep >= 0 ? kU : 1];
   P* shared;  // kKeep batches, or null
 };
 
@@ -125,7 +125,7 @@ __device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, Soft*
     for (int u = 0; u < kU; ++u) {
       const int at = (u * kThreads + tid) * N;
       x[u] = load_raw<T>(z + whole * kBatch + at, left - at);
-      if (kKeep > 0) kept.tail[u] = x[u];
+      if constexpr (kKeep >= 0) kept.tail[u] = x[u];
     }
     take(x, left);
   }
@@ -169,7 +169,8 @@ __device__ void spread(const typename Act<T>::S* z, typename Act<T>::S* dz, int 
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int at = (u * kThreads + tid) * N;
-      x[u] = kKeep > 0 ? kept.tail[kKeep > 0 ? u : 0] : load_raw<T>(z + whole * kBatch + at, left - at);
+      if constexpr (kKeep >= 0) x[u] = kept.tail[u];
+      else x[u] = load_raw<T>(z + whole * kBatch + at, left - at);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -192,18 +193,17 @@ __device__ void spread(const typename Act<T>::S* z, typename Act<T>::S* dz, int 
 }
 
 // One block per row: a sweep for maximum and sum (forward, both), a sweep for the gradient
-// (backward, both).
-template <int T, int kMode, int kThreads, int kKeep>
+// (backward, both).  A thread holds up to kPer of the teacher's entries.
+template <int T, int kMode, int kThreads, int kPer, int kKeep>
 __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   typedef typename Act<T>::S S;
   constexpr int N = kVec<T>, kWaves = kThreads / 64;
-  constexpr int kPer = kMaxDistillTop / kThreads;  // teacher entries a thread holds
   constexpr bool kLoss = kMode != kDistillBackward, kGrad = kMode != kDistillForward;
   __shared__ Soft joined[2][kWaves];
   __shared__ float terms[kWaves];
   __shared__ float counts[kWaves];
-  __shared__ float prob[kMaxDistillTop];
-  __shared__ int32_t id[kMaxDistillTop];
+  __shared__ float prob[kThreads * kPer];
+  __shared__ int32_t id[kThreads * kPer];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, top = static_cast<int>(c.top);
   const S* z = static_cast<const S*>(c.logits) + row * c.stride;
@@ -332,13 +332,14 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   }
 }
 
-template <int T, int kThreads>
+template <int T, int kThreads, int kPer>
 void launch_rows(const DistillCall& c, DistillMode mode, hipStream_t s) {
+  constexpr int kKeep = kThreads == 1024 ? kKeepBatches : 0;
   const dim3 grid(static_cast<unsigned>(c.n)), block(kThreads);
   switch (mode) {
-    case kDistillForward: hipLaunchKernelGGL((distill_kernel<T, kDistillForward, kThreads, 0>), grid, block, 0, s, c); break;
-    case kDistillBackward: hipLaunchKernelGGL((distill_kernel<T, kDistillBackward, kThreads, 0>), grid, block, 0, s, c); break;
-    case kDistillBoth: hipLaunchKernelGGL((distill_kernel<T, kDistillBoth, kThreads, kThreads == 1024 ? kKeepBatches : 0>), grid, block, 0, s, c); break;
+    case kDistillForward: hipLaunchKernelGGL((distill_kernel<T, kDistillForward, kThreads, kPer, kNothing>), grid, block, 0, s, c); break;
+    case kDistillBackward: hipLaunchKernelGGL((distill_kernel<T, kDistillBackward, kThreads, kPer, kNothing>), grid, block, 0, s, c); break;
+    case kDistillBoth: hipLaunchKernelGGL((distill_kernel<T, kDistillBoth, kThreads, kPer, kKeep>), grid, block, 0, s, c); break;
   }
 }
 
@@ -347,9 +348,16 @@ void launch_rows(const DistillCall& c, DistillMode mode, hipStream_t s) {
 hipError_t launch_distill(const DistillCall& c, DistillMode mode, hipStream_t s) {
   return with_act(c.type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    // 256 threads where a batch of theirs covers the row
-    if (c.vocab <= 256 * 4 * (T == kActF32 ? 4 : 8)) launch_rows<T, 256>(c, mode, s);
-    else launch_rows<T, 1024>(c, mode, s);
+    // as few threads as read the row in one batch and hold the teacher's entries: short rows
+    // spend their time on the way between load, join and store, so more of them at once helps
+    // (16384 rows of 1000 bf16 logits, loss and gradient: 29 us with 64 threads a row, 79 us
+    // with 256; 16384 x 16000: 206 us with 512, 297 us with 1024)
+    const int64_t batch = kU * kVec<T>;  // a thread's
+    if (c.vocab <= 64 * batch && c.top <= 64) launch_rows<T, 64, 1>(c, mode, s);
+    else if (c.vocab <= 256 * batch && c.top <= 256) launch_rows<T, 256, 1>(c, mode, s);
+    else if (c.vocab <= 256 * batch) launch_rows<T, 256, kMaxDistillTop / 256>(c, mode, s);
+    else if (c.vocab <= 512 * batch) launch_rows<T, 512, kMaxDistillTop / 512>(c, mode, s);
+    else launch_rows<T, 1024, 1>(c, mode, s);
     return hipGetLastError();
   });
 }
