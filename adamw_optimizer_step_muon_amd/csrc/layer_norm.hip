@@ -17,7 +17,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
 // ---------------------------------------------------------------------------
-// Rows in registers: kTPR threads hold a row, kNV vectors of 16 bytes each, so x is read
+// Rows in registers: kTPR threads (16 to 1024) hold a row, kNV vectors of 16 bytes each, so x is read
 // once for mean, variance and output.  Blocks walk over rows (the next row's loads are
 // issued before this row's sums are joined) and keep the gains in registers.
 // ---------------------------------------------------------------------------
@@ -42,7 +42,14 @@ __device__ __forceinline__ void load_floats(const float* p, int cnt, float fill,
 template <int kTPR, int kCount>
 __device__ __forceinline__ void row_sums(float (&v)[kCount], float* shared) {
 #pragma unroll
-  for (int k = 0; k < kCount; ++k) v[k] = wave_sum(v[k]);
+  for (int k = 0; k < kCount; ++k) {
+    if constexpr (kTPR >= 64) {
+      v[k] = wave_sum(v[k]);
+    } else {
+      v[k] = row16_reduce(v[k], 0.0f, Add());
+      if (kTPR == 32) v[k] += __shfl_xor(v[k], 16, 64);
+    }
+  }
   if constexpr (kTPR > 64) {
     constexpr int kW = kTPR / 64;
     const int wave = threadIdx.x >> 6;
@@ -153,78 +160,98 @@ __global__ __launch_bounds__(kBlock) void norm_grad_rows_kernel(NormGradCall c) 
   const S* x0 = static_cast<const S*>(c.x) + t * N;
   const S* y0 = static_cast<const S*>(c.dy) + t * N;
   int cnt[kNV];
-  float w[kNV][N], dw[kNV][N], db[kNV][N];
-  P nx[kNV], ny[kNV];
+  float dw[kNV][N], db[kNV][N];
 #pragma unroll
   for (int v = 0; v < kNV; ++v) {
     cnt[v] = static_cast<int>(c.dim) - (v * kTPR + t) * N;
-    if (!kLean && base + sub < c.n) {
-      nx[v] = load_raw<T>(x0 + (base + sub) * c.x_stride + v * kTPR * N, cnt[v]);
-      ny[v] = load_raw<T>(y0 + (base + sub) * c.dy_stride + v * kTPR * N, cnt[v]);
+#pragma unroll
+    for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = 0.0f;
+  }
+  const auto load_rows = [&](int64_t row, P (&x)[kNV], P (&y)[kNV]) {
+#pragma unroll
+    for (int v = 0; v < kNV; ++v) {
+      x[v] = load_raw<T>(x0 + row * c.x_stride + v * kTPR * N, cnt[v]);
+      y[v] = load_raw<T>(y0 + row * c.dy_stride + v * kTPR * N, cnt[v]);
     }
+  };
+  const auto load_gains = [&](int v, float (&w)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = 1.0f;
+    if (c.weight) load_floats<N>(c.weight + (v * kTPR + t) * N, cnt[v], 0.0f, w);
+  };
+  const float dim = static_cast<float>(c.dim);
+  // the row's two sums, and its share of the columns'
+  const auto gather = [&](int v, const P& x, const P& y, const float (&w)[N], float mean, float rstd, float (&s)[2]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      w[v][e] = 1.0f;
-      dw[v][e] = db[v][e] = 0.0f;
+      // behind the row's end dy is zero, so nothing is added
+      const float g = Act<T>::up(y[e]), h = (Act<T>::up(x[e]) - mean) * rstd;
+      const float u = g * w[e];
+      s[0] += u;
+      s[1] += u * h;
+      dw[v][e] += g * h;
+      db[v][e] += g;
     }
-    if (c.weight && !kLean) load_floats<N>(c.weight + (v * kTPR + t) * N, cnt[v], 0.0f, w[v]);
-  }
-  const float dim = static_cast<float>(c.dim);
+  };
+  const auto give = [&](int v, const P& x, const P& y, const float (&w)[N], int64_t row, float mean, float rstd,
+                        const float (&s)[2]) {
+    const float m1 = s[0] / dim, m2 = s[1] / dim;
+    float d[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float h = (Act<T>::up(x[e]) - mean) * rstd;
+      d[e] = rstd * (Act<T>::up(y[e]) * w[e] - m1 - h * m2);
+    }
+    if (cnt[v] > 0)
+      store_part<T, N>(static_cast<S*>(c.dx) + row * c.dx_stride + (v * kTPR + t) * N, cnt[v], d);
+  };
   int turn = 0;
-  for (; base < c.n; base += step, turn ^= 1) {  // the same trips for every thread of the block
-    const int64_t row = base + sub;
-    const bool live = row < c.n;
-    P x[kNV], y[kNV];
-    if constexpr (kLean) {
-#pragma unroll
-      for (int v = 0; v < kNV; ++v)
-        if (live) {
-          nx[v] = load_raw<T>(x0 + row * c.x_stride + v * kTPR * N, cnt[v]);
-          ny[v] = load_raw<T>(y0 + row * c.dy_stride + v * kTPR * N, cnt[v]);
-          if (c.weight) load_floats<N>(c.weight + (v * kTPR + t) * N, cnt[v], 0.0f, w[v]);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < kNV; ++v) {
-      x[v] = nx[v];
-      y[v] = ny[v];
-    }
-    const float mean = live ? c.mean[row] : 0.0f, rstd = live ? c.rstd[row] : 0.0f;
-    if (!kLean && row + step < c.n) {
+  if constexpr (kLean) {
+    for (int64_t row = base; row < c.n; row += step, turn ^= 1) {  // one row a block
+      const float mean = c.mean[row], rstd = c.rstd[row];
+      P x[kNV], y[kNV];
+      load_rows(row, x, y);
+      float s[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int v = 0; v < kNV; ++v) {
-        nx[v] = load_raw<T>(x0 + (row + step) * c.x_stride + v * kTPR * N, cnt[v]);
-        ny[v] = load_raw<T>(y0 + (row + step) * c.dy_stride + v * kTPR * N, cnt[v]);
+        float w[N];
+        load_gains(v, w);
+        gather(v, x[v], y[v], w, mean, rstd, s);
+      }
+      row_sums<kTPR>(s, shared[turn]);
+#pragma unroll
+      for (int v = 0; v < kNV; ++v) {
+        float w[N];
+        load_gains(v, w);
+        give(v, x[v], y[v], w, row, mean, rstd, s);
       }
     }
-    float s[2] = {0.0f, 0.0f};
-    if (live) {
+  } else {
+    float w[kNV][N];
+    P nx[kNV], ny[kNV];
 #pragma unroll
-      for (int v = 0; v < kNV; ++v)
+    for (int v = 0; v < kNV; ++v) load_gains(v, w[v]);
+    if (base + sub < c.n) load_rows(base + sub, nx, ny);
+    for (; base < c.n; base += step, turn ^= 1) {  // the same trips for every thread of the block
+      const int64_t row = base + sub;
+      const bool live = row < c.n;
+      P x[kNV], y[kNV];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          // behind the row's end dy is zero, so nothing is added
-          const float g = Act<T>::up(y[v][e]), h = (Act<T>::up(x[v][e]) - mean) * rstd;
-          const float u = g * w[v][e];
-          s[0] += u;
-          s[1] += u * h;
-          dw[v][e] += g * h;
-          db[v][e] += g;
-        }
-    }
-    row_sums<kTPR>(s, shared[turn]);
-    if (!live) continue;
-    const float m1 = s[0] / dim, m2 = s[1] / dim;
-#pragma unroll
-    for (int v = 0; v < kNV; ++v) {
-      float d[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float h = (Act<T>::up(x[v][e]) - mean) * rstd;
-        d[e] = rstd * (Act<T>::up(y[v][e]) * w[v][e] - m1 - h * m2);
+      for (int v = 0; v < kNV; ++v) {
+        x[v] = nx[v];
+        y[v] = ny[v];
       }
-      if (cnt[v] > 0)
-        store_part<T, N>(static_cast<S*>(c.dx) + row * c.dx_stride + (v * kTPR + t) * N, cnt[v], d);
+      const float mean = live ? c.mean[row] : 0.0f, rstd = live ? c.rstd[row] : 0.0f;
+      if (row + step < c.n) load_rows(row + step, nx, ny);
+      float s[2] = {0.0f, 0.0f};
+      if (live) {
+#pragma unroll
+        for (int v = 0; v < kNV; ++v) gather(v, x[v], y[v], w[v], mean, rstd, s);
+      }
+      row_sums<kTPR>(s, shared[turn]);
+      if (!live) continue;
+#pragma unroll
+      for (int v = 0; v < kNV; ++v) give(v, x[v], y[v], w[v], row, mean, rstd, s);
     }
   }
   if (!c.dweight && !c.dbias) return;
@@ -376,7 +403,9 @@ namespace {
 template <int T, typename F>
 bool with_row(int64_t dim, F f) {
   const int64_t v = (dim + Vec<T>::kN - 1) / Vec<T>::kN;
-  if (v <= 64) f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
+  if (v <= 16) f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+  else if (v <= 32) f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+  else if (v <= 64) f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   else if (v <= 128) f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
   else if (v <= 256) f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
   else if (v <= 512) f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());

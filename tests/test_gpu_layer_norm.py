@@ -24,7 +24,7 @@ DEV = "cuda:0"
 TYPES = [torch.float32, torch.float16, torch.bfloat16]
 E = 2.0 ** -24
 TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
-SIZES = [(1, 1), (3, 2), (5, 33), (64, 64), (257, 100), (19, 768), (7, 1279), (6, 2048), (5, 2051),
+SIZES = [(1, 1), (3, 2), (5, 33), (64, 64), (257, 100), (77, 200), (19, 768), (7, 1279), (6, 2048), (5, 2051),
          (3, 4096), (4, 8192), (3, 8195), (2, 16391), (2, 40000)]
 
 
