@@ -14,6 +14,10 @@
 #include "ma_act.h"
 #include "ma_internal.h"
 
+// Every multiply-add here is written out: left to the compiler, the instances of one kernel
+// fused differently, and the one-pass call's loss was an ulp off the two calls'.
+#pragma clang fp contract(off)
+
 namespace ma {
 namespace {
 
@@ -32,10 +36,7 @@ constexpr float kFar = 1e30f;  // times the largest scale, log2(e) 1e6, still fi
 struct Soft {
   float m, s;
 };
-__device__ __forceinline__ float reference(float m, float scale) {
-#pragma clang fp contract(off)
-  return m * scale;
-}
+__device__ __forceinline__ float reference(float m, float scale) { return m * scale; }
 template <bool kIsFar>
 __device__ __forceinline__ float exponent(float v, float scale, float m, float r) {
   return kIsFar ? (v - m) * scale : __builtin_fmaf(v, scale, -r);

@@ -165,10 +165,11 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     bits = _ints("tokens", tokens, device)
     shape = tokens.shape + (dim,)
     if out is None:
-        out = _empty(table, shape, out_dtype or torch.float32, stream)
-    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be {tuple(shape)} of {out_dtype or out.dtype}")
-    _, _, stride = _rows("out", out, device)
+        out, stride = _empty(table, shape, out_dtype or torch.float32, stream), dim
+    else:
+        if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be {tuple(shape)} of {out_dtype or out.dtype}")
+        _, _, stride = _rows("out", out, device)
     _call("ma_embedding_forward", device, stream, table.data_ptr(), rows, dim, tokens.data_ptr(),
           bits, tokens.numel(), scale, out.data_ptr(), _type("out", out.dtype), stride)
     return out

@@ -210,3 +210,37 @@ def test_rows_far_from_zero(vocab, tau):
     assert torch.equal(loss, own)
     for got in (grad, again):
         assert (np.abs(_np(got) - dz) <= tau * (60 / tau * E + k + 16 * E) + 2 * E).all()
+
+
+def test_offsets_past_32_bits():
+    """The last rows of more than 2^31 logits are those of a small batch."""
+    n, vocab = 20_000, 128_000
+    z = torch.zeros(n, vocab, dtype=torch.bfloat16, device=DEV)
+    z[-3:] = (3 * torch.randn(3, vocab, device=DEV)).bfloat16()
+    a, ids = torch.randn(n, 5, device=DEV), torch.randint(0, vocab, (n, 5), device=DEV)
+    w = torch.rand(n, device=DEV) + 0.5
+    loss, stats = ma.distill_forward(z, a, ids)
+    few = (z[-3:], a[-3:], ids[-3:])
+    want, grad = ma.distill_loss_grad(*few, w[-3:])
+    assert torch.equal(loss[-3:], want) and torch.equal(stats[-3:], ma.distill_forward(*few)[1])
+    got = ma.distill_backward(z, a, ids, stats, w)
+    assert torch.equal(got[-3:], grad)
+    both, got = ma.distill_loss_grad(z, a, ids, w, dlogits=z)
+    assert got is z and torch.equal(both, loss) and torch.equal(z[-3:], grad)
+
+
+@pytest.mark.parametrize("vocab", [64, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193, 16384, 16385, 32768, 32769])
+@pytest.mark.parametrize("top", [1, 64, 65, 300])
+def test_borders_of_the_row_layouts(vocab, top):
+    """Vocabularies and teacher lists on both sides of the sizes at which a row takes more
+    threads or another batch, each type at its own."""
+    top = min(top, vocab)
+    for dtype in (torch.float32, torch.bfloat16):
+        z, a, ids, w = _inputs(3, vocab, top, dtype, vocab + top)
+        loss, grad = ma.distill_loss_grad(z, a, ids, w)
+        rl, rz, bl, bz = _bounds(_np(z), _np(a), ids.cpu().numpy(), _np(w), 1.0)
+        assert (np.abs(_np(loss) - rl) <= bl).all()
+        _check(grad, rz, bz, dtype)
+        own, stats = ma.distill_forward(z, a, ids)
+        assert torch.equal(own, loss)
+        assert torch.equal(ma.distill_backward(z, a, ids, stats, w), grad)

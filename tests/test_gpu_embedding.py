@@ -186,3 +186,82 @@ def test_infinite_and_nan_gradients_stay_in_their_rows():
     ok[2, 0] = ok[3, 1] = False
     want = torch.tensor([0.0, 2.0, 2.0, 1.0, 0.0], device=DEV)[:, None].expand(5, 4)
     assert torch.equal(g[ok], want[ok])
+
+
+def _check_gradient(tokens, dout, rows, scale=1.0):
+    grad = ma.embedding_backward(dout, tokens, rows, scale=scale)
+    ref, size, count = training.embedding_grad(dout.double().cpu().numpy(), tokens.cpu().numpy(), rows, scale)
+    assert (np.abs(grad.double().cpu().numpy() - ref) <= (count[:, None] + 1) * E * size).all()
+    assert not grad[torch.from_numpy(count == 0).to(DEV)].any()
+
+
+@pytest.mark.parametrize("rows,dim,n", [
+    (70000, 4, 20011),    # counted sort, two passes
+    (600000, 3, 16500),   # three passes
+    (300, 520, 16385),    # one pass, many rows of many tokens, in tiles
+    (9, 2, 40000),        # one pass of few digits
+    (262143, 1, 16384),   # the most tokens of the one-launch sort, 18 bits
+    (262144, 2, 16390),   # the first size of three passes
+])
+def test_sorts_of_many_tokens(rows, dim, n):
+    rng = np.random.default_rng(n)
+    _check_gradient(_tokens(rng, rows, n, torch.int64), torch.randn(n, dim, device=DEV), rows, 0.5)
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 65, 127, 128, 129, 160, 161, 257, 1000])
+@pytest.mark.parametrize("rows", [1, 3])
+def test_chunk_borders(n, rows):
+    """Rows whose tokens fill, straddle and just miss the chunks that are summed apart."""
+    rng = np.random.default_rng(n)
+    tokens = torch.from_numpy(np.sort(rng.integers(0, rows, n))).to(DEV)
+    dout = torch.randn(n, 6, device=DEV)
+    _check_gradient(tokens, dout, rows)
+    _check_gradient(tokens[torch.randperm(n, device=DEV)], dout, rows)
+    _check_gradient(torch.where(torch.arange(n, device=DEV) % 5 == 1, -1, tokens), dout, rows)
+
+
+def test_only_padding():
+    tokens = torch.full((300,), -1, device=DEV)
+    dout = torch.full((300, 7), float("nan"), device=DEV)
+    assert not ma.embedding_backward(dout, tokens, 40).any()
+    assert not ma.embedding_forward(torch.randn(40, 7, device=DEV), tokens).any()
+    keep = torch.randn(40, 7, device=DEV)
+    again = keep.clone()
+    ma.embedding_backward(dout, tokens, 40, grad=again, accumulate=True)
+    assert torch.equal(keep, again)
+
+
+def test_more_tokens_than_rows_add_up():
+    """Adding on a table with fewer rows than tokens takes the table's rows as lines."""
+    rng = np.random.default_rng(1)
+    tokens = _tokens(rng, 13, 500, torch.int32)
+    dout = torch.randn(500, 30, device=DEV).half()
+    base = torch.randn(13, 30, device=DEV)
+    got = ma.embedding_backward(dout, tokens, 13, grad=base.clone(), accumulate=True)
+    assert torch.equal(got, base + ma.embedding_backward(dout, tokens, 13))
+
+
+def test_offsets_past_32_bits():
+    """Tables and outputs of more than 2^32 values: the last rows are those of small ones."""
+    rows, dim = 2_200_000, 2048
+    table = torch.empty(rows, dim, device=DEV)
+    table[-3:] = torch.arange(3 * dim, device=DEV).view(3, dim)
+    t = torch.tensor([rows - 1, rows, rows - 3], device=DEV)
+    out = ma.embedding_forward(table, t)
+    assert torch.equal(out[0], table[-1]) and torch.equal(out[2], table[-3]) and not out[1].any()
+    dout = torch.randn(3, dim, device=DEV)
+    ma.embedding_backward(dout, t, rows, grad=table)  # the table's memory as the gradient
+    assert torch.equal(table[-1], dout[0]) and torch.equal(table[-3], dout[2])
+    assert not table[-2].any() and not table[rows // 2 - 5:rows // 2 + 5].any()
+    del table
+    n, dim = 1_100_000, 4096
+    wide = torch.empty(n, dim, dtype=torch.bfloat16, device=DEV)
+    few = torch.tensor([5, n // 2, n - 2, n - 1], device=DEV)
+    wide[few] = torch.randn(4, dim, device=DEV).bfloat16()
+    tokens = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    tokens[few] = torch.tensor([7, 3, 3, 0], dtype=torch.int32, device=DEV)
+    grad = ma.embedding_backward(wide, tokens, 9)
+    w = wide[few].float()
+    assert torch.equal(grad[7], w[0]) and torch.equal(grad[3], w[1] + w[2]) and torch.equal(grad[0], w[3])
+    ma.embedding_forward(grad, tokens, out=wide)
+    assert torch.equal(wide[few], grad[tokens[few].long()].bfloat16()) and not wide[n - 3].any()

@@ -142,3 +142,23 @@ def test_a_rows_nan_stays_in_its_row():
     y, _, _ = ma.layer_norm_forward(x)
     assert torch.isnan(y[7]).all()
     assert torch.isfinite(y[torch.arange(20, device=DEV) != 7]).all()
+
+
+def test_offsets_past_32_bits():
+    """The last rows of a batch of more than 2^31 values are those of a small one."""
+    n, dim = 300_000, 8192
+    x = torch.zeros(n, dim, dtype=torch.bfloat16, device=DEV)
+    dy = torch.zeros(n, dim, dtype=torch.bfloat16, device=DEV)
+    x[-4:], dy[-4:] = torch.randn(4, dim, device=DEV).bfloat16(), torch.randn(4, dim, device=DEV).bfloat16()
+    w = torch.randn(dim, device=DEV)
+    y, mean, rstd = ma.layer_norm_forward(x, w)
+    ys, ms, rs = ma.layer_norm_forward(x[-4:], w)
+    assert torch.equal(y[-4:], ys) and torch.equal(mean[-4:], ms) and torch.equal(rstd[-4:], rs)
+    del y
+    dx, dw, db = ma.layer_norm_backward(dy, x, mean, rstd, w)
+    dxs, dws, dbs = ma.layer_norm_backward(dy[-4:], x[-4:], ms, rs, w)
+    assert torch.equal(dx[-4:], dxs) and not dx[n // 2].any()
+    # the other rows add zeros; four terms in another order
+    for a, b, t in ((dw, dws, dy[-4:].float() * (x[-4:].float() - ms[:, None]) * rs[:, None]),
+                    (db, dbs, dy[-4:].float())):
+        assert ((a - b).abs() <= 8 * E * t.abs().sum(0)).all()
