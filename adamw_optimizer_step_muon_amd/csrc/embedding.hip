@@ -44,11 +44,13 @@ constexpr int kLocalBins = 1 << kLocalBits;
 static_assert(kLocalBins == 64 && kOneLaunch <= 65536, "a digit a lane, 16-bit places");
 static_assert(kSortThreads >= kMaxBins, "a thread per digit");
 
+__device__ __forceinline__ uint32_t key_of(int64_t token, uint32_t rows) {
+  return token >= 0 && token < static_cast<int64_t>(rows) ? static_cast<uint32_t>(token) : rows;
+}
 __device__ __forceinline__ uint32_t key_of(const void* tokens, int bits, int64_t i,
                                            uint32_t rows) {
-  const int64_t t = bits == 64 ? static_cast<const int64_t*>(tokens)[i]
-                               : static_cast<const int32_t*>(tokens)[i];
-  return t >= 0 && t < static_cast<int64_t>(rows) ? static_cast<uint32_t>(t) : rows;
+  return key_of(bits == 64 ? static_cast<const int64_t*>(tokens)[i]
+                           : static_cast<int64_t>(static_cast<const int32_t*>(tokens)[i]), rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -183,16 +185,29 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_launch_kernel(SortArgs 
   // a wave's share of the tokens: 64-token steps, in order
   const int steps = (n + kSortThreads - 1) / kSortThreads;
   uint32_t own = 0, before = 0;
-#pragma unroll 4
-  for (int k = 0; k < steps; ++k) {
-    const int i = (wave * steps + k) * 64 + lane;
-    if (i < n) {
-      const uint32_t key = key_of(a.tokens, a.token_bits, i, a.rows);
-      s.keys[i] = key;
-      own += (key & low) == mine;
-      before += (key & low) < mine;
+  const auto read = [&](const auto* tokens) {
+    constexpr int kBatch = 8;  // steps whose loads are issued together (clamped, not skipped)
+    for (int k0 = 0; k0 < steps; k0 += kBatch) {
+      int64_t t[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = (wave * steps + k0 + k) * 64 + lane;
+        t[k] = tokens[i < n ? i : n - 1];
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = (wave * steps + k0 + k) * 64 + lane;
+        if (k0 + k < steps && i < n) {
+          const uint32_t key = key_of(t[k], a.rows);
+          s.keys[i] = key;
+          own += (key & low) == mine;
+          before += (key & low) < mine;
+        }
+      }
     }
-  }
+  };
+  if (a.token_bits == 64) read(static_cast<const int64_t*>(a.tokens));
+  else read(static_cast<const int32_t*>(a.tokens));
   for (int d = 32; d > 0; d >>= 1) {
     own += __shfl_xor(own, d, 64);
     before += __shfl_xor(before, d, 64);
