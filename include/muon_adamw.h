@@ -409,7 +409,7 @@ ma_status ma_embedding_forward(const float* table, int64_t rows, int64_t dim, co
                                int32_t out_type, int64_t out_stride, void* stream);
 
 /* Host only: workspace bytes of ma_embedding_backward and ma_adamw_step_embedding for n
- * tokens (0 for up to 128 tokens, and for invalid sizes, which the calls then report). */
+ * tokens (0 for up to 256 tokens, and for invalid sizes, which the calls then report). */
 size_t ma_embedding_workspace_bytes(int64_t rows, int64_t dim, int64_t n);
 
 /* The table's gradient by sorted tokens:
