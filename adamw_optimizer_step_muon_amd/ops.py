@@ -414,6 +414,8 @@ def embedding(tokens, table, *, scale: float = 1.0, out_dtype=None, optimizer=No
     padding (zero row, no gradient).  With `optimizer` (the MuonAdamW that holds the table in
     an "adamw" group) the backward pass sets no table.grad: it hands the tokens and output
     gradients to optimizer.add_token_gradient, and the next step() applies them."""
+    if optimizer is not None:
+        optimizer.check_token_parameter(table)
     return _Embedding.apply(tokens, table, float(scale), out_dtype, optimizer)
 
 

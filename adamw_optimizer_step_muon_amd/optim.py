@@ -176,6 +176,14 @@ class MuonAdamW:
             self._workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return self._workspace
 
+    def check_token_parameter(self, param) -> None:
+        """Raises unless `param` can take token gradients (see add_token_gradient)."""
+        if not any(q is param for g in self.param_groups if g["kind"] == "adamw"
+                   for q in g["params"]):
+            raise ValueError("token gradients are for parameters of an adamw group")
+        if param.dim() != 2:
+            raise ValueError("token gradients are for (rows, dim) parameters")
+
     def add_token_gradient(self, param, tokens, dout, scale: float = 1.0) -> None:
         """Adds to the gradient of an embedding table (a 2-D parameter of an "adamw" group)
         scale * dout[t] on row tokens[t] for every t, without building it: the next step()
@@ -186,11 +194,16 @@ class MuonAdamW:
         must not be modified before step().  What reads ``param.grad`` between backward and
         step (clipping by a global norm, say) does not see this gradient; ``scale`` can
         carry a clipping factor."""
-        if not any(q is param for g in self.param_groups if g["kind"] == "adamw"
-                   for q in g["params"]):
-            raise ValueError("token gradients are for parameters of an adamw group")
-        if param.dim() != 2 or dout.shape != tuple(tokens.shape) + (param.shape[1],):
+        import torch
+
+        self.check_token_parameter(param)
+        if dout.shape != tokens.shape + (param.shape[1],):
             raise ValueError("dout must be tokens.shape + (dim,) of a (rows, dim) parameter")
+        if tokens.dtype not in (torch.int32, torch.int64) or \
+                dout.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+            raise ValueError("tokens must be int32 or int64, dout float32, float16 or bfloat16")
+        if tokens.device != param.device or dout.device != param.device:
+            raise ValueError("tokens and dout must be on the parameter's device")
         self._token_grads.setdefault(id(param), []).append(
             (tokens, dout, float(scale), (tokens._version, dout._version)))
 

@@ -155,6 +155,12 @@ def test_masked_logits_and_teachers():
     assert loss[4] == 0 and loss[5] == 0 and not grad[4:7].any()
     assert loss[7] == inf and torch.isfinite(grad[7]).all()
     assert abs(float(grad[7].double().sum())) < 1.5e-5
+    # a teacher's NaN in its row only, and not where its id is padding
+    a[1, 0] = a[2, 1] = float("nan")
+    ids[2, 1] = -1
+    loss, _ = ma.distill_forward(z, a, ids)
+    assert torch.isnan(loss[1]) and torch.isfinite(loss[[0, 2, 3]]).all()
+    a[1, 0] = a[2, 1] = 0.5
     # rows that have no softmax
     z[0], z[1, 5] = -inf, float("nan")
     ids[0] = torch.arange(4, device=DEV)

@@ -213,6 +213,12 @@ def test_token_gradients_are_checked_when_added():
         opt.add_token_gradient(other, tokens, torch.zeros(5, 4))
     with pytest.raises(ValueError, match="dout"):
         opt.add_token_gradient(table, tokens, torch.zeros(5, 3))
+    with pytest.raises(ValueError, match="int32"):
+        opt.add_token_gradient(table, tokens.float(), torch.zeros(5, 4))
+    with pytest.raises(ValueError, match="float32"):
+        opt.add_token_gradient(table, tokens, torch.zeros(5, 4).double())
+    with pytest.raises(ValueError, match="adamw group"):
+        ma.embedding(tokens, other, optimizer=opt)
     dout = torch.zeros(5, 4)
     opt.add_token_gradient(table, tokens, dout)
     dout.add_(1.0)
