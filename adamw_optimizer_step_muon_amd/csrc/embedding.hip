@@ -305,11 +305,17 @@ __device__ __forceinline__ void add_tokens(const RowArgs& a, uint32_t lo, uint32
   const S* dout = static_cast<const S*>(a.dout) + c;
   uint32_t i = lo;
   if (cnt >= kUnit) {
+    // the next batch's positions are on their way while this batch's rows are
+    uint32_t at[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) at[k] = i + k < hi ? a.order[i + k] : 0;
     for (; i < hi; i += kAhead) {
       P v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
-        if (i + k < hi) v[k] = *reinterpret_cast<const P*>(dout + a.order[i + k] * a.dout_stride);
+        if (i + k < hi) v[k] = *reinterpret_cast<const P*>(dout + at[k] * a.dout_stride);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) at[k] = i + kAhead + k < hi ? a.order[i + kAhead + k] : 0;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (i + k < hi) {
