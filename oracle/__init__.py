@@ -22,9 +22,12 @@ function:
                                          first-step closed form, pure decay)
 * adamw_step with cautious_wd            special cases only ("parity unpinned"
                                          for the mixed-sign case)
+* training (embedding, layer norm,       not on the pages: definitions, against
+  distillation)                          central differences and closed forms
 """
+from . import training
 from .adamw import AdamWResult, adamw_step
 from .muon import QUINTIC, MuonResult, Route, muon_step, muon_step_bucket, newton_schulz, route, update_scale
 
 __all__ = ["AdamWResult", "adamw_step", "QUINTIC", "MuonResult", "Route", "muon_step",
-           "muon_step_bucket", "newton_schulz", "route", "update_scale"]
+           "muon_step_bucket", "newton_schulz", "route", "training", "update_scale"]
