@@ -31,6 +31,7 @@ _BITS = {torch.int32: 32, torch.int64: 64}
 # checks touch each tensor once and the current stream is asked for its handle directly.
 # --------------------------------------------------------------------------
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_functions: dict = {}
 
 
 def _call(name, device, stream, *args):
@@ -40,7 +41,9 @@ def _call(name, device, stream, *args):
         handle = _raw_stream(device.index)
     else:
         handle = _stream_handle(stream, device)
-    fn = getattr(load(), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
     if device.index == torch.cuda.current_device():
         status = fn(*args, handle)
     else:
@@ -57,6 +60,13 @@ def _empty(like, shape, dtype, stream):
     if stream is not None and stream != torch.cuda.current_stream(like.device):
         t.record_stream(stream)
     return t
+
+
+def _like(t, stream):
+    """A contiguous tensor of t's shape and type (the cheapest allocation there is)."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(t, t.shape, t.dtype, stream)
 
 
 def _tensor(name, t, device) -> None:
@@ -235,13 +245,13 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, out=None
     dtype, device = _type("x", x.dtype), x.device
     w, b = _floats("weight", weight, dim, device), _floats("bias", bias, dim, device)
     if out is None:
-        out, out_stride = _empty(x, x.shape, x.dtype, stream), max(dim, 1)
+        out, out_stride = _like(x, stream), max(dim, 1)
     else:
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have x's shape and type")
         _, _, out_stride = _rows("out", out, device)
     mean = _empty(x, x.shape[:-1], torch.float32, stream)
-    rstd = _empty(x, x.shape[:-1], torch.float32, stream)
+    rstd = _like(mean, stream)
     _call("ma_layer_norm_forward", device, stream, x.data_ptr(), dtype, stride, n, dim, w, b, eps,
           out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
     return out, mean, rstd
@@ -265,8 +275,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
     if weight_grad and dweight is None:
         dweight = _empty(x, dim, torch.float32, stream)
     if bias_grad and dbias is None:
-        dbias = _empty(x, dim, torch.float32, stream)
-    dx = _empty(x, x.shape, x.dtype, stream)
+        dbias = _like(dweight, stream) if weight_grad else _empty(x, dim, torch.float32, stream)
+    dx = _like(x, stream)
     need = layer_norm_workspace_bytes(n, dim) if weight_grad or bias_grad else 0
     _keep, ws, size = _workspace(workspace, need, x, stream)
     _call("ma_layer_norm_backward", device, stream, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride,
@@ -297,7 +307,7 @@ def _distill(logits, teacher, ids, temperature):
 def _dlogits(logits, dlogits, stream):
     """(dlogits, row stride)"""
     if dlogits is None:
-        return _empty(logits, logits.shape, logits.dtype, stream), logits.shape[-1]
+        return _like(logits, stream), logits.shape[-1]
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError("dlogits must have the logits' shape and type")
     return dlogits, _rows("dlogits", dlogits, logits.device)[2]
