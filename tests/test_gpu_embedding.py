@@ -208,6 +208,16 @@ def test_sorts_of_many_tokens(rows, dim, n):
     _check_gradient(_tokens(rng, rows, n, torch.int64), torch.randn(n, dim, device=DEV), rows, 0.5)
 
 
+@pytest.mark.parametrize("rows", [70000, 1 << 20])
+@pytest.mark.parametrize("n,keep", [(9000, 1.0), (16384, 0.5), (30000, 0.5)])
+def test_rows_alike_in_their_low_bits(rows, n, keep):
+    """One block of the one-launch sort has all tokens; one digit of the counted one does."""
+    rng = np.random.default_rng(n)
+    t = 256 * rng.integers(0, rows // 256, n)
+    t[rng.random(n) > keep] = -1
+    _check_gradient(torch.from_numpy(t).to(DEV), torch.randn(n, 2, device=DEV), rows)
+
+
 @pytest.mark.parametrize("n", [31, 32, 33, 64, 65, 127, 128, 129, 160, 161, 257, 1000])
 @pytest.mark.parametrize("rows", [1, 3])
 def test_chunk_borders(n, rows):
