@@ -177,7 +177,7 @@ struct OneLaunch {
   uint16_t order[2][kOneLaunch];  // of the block's own
   uint32_t base[kLocalBins];
   uint32_t count[kSortWaves][kLocalBins];
-  uint32_t own[kSortWaves], before[kSortWaves], wave_total[kSortWaves];
+  uint32_t own[kSortWaves], before[kSortWaves];
 };
 __global__ __launch_bounds__(kSortThreads) void sort_one_launch_kernel(SortArgs a, int block_bits, int key_bits,
                                                                        uint32_t* keys_out, uint32_t* order_out,

@@ -239,7 +239,12 @@ __global__ __launch_bounds__(kBlock) void norm_grad_rows_kernel(NormGradCall c) 
     P nx[kNV], ny[kNV];
 #pragma unroll
     for (int v = 0; v < kNV; ++v) load_gains(v, w[v]);
-    if (base + sub < c.n) load_rows(base + sub, nx, ny);
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (base + sub < c.n) {
+      load_rows(base + sub, nx, ny);
+      next_mean = c.mean[base + sub];
+      next_rstd = c.rstd[base + sub];
+    }
     for (; base < c.n; base += step, turn ^= 1) {  // the same trips for every thread of the block
       const int64_t row = base + sub;
       const bool live = row < c.n;
@@ -249,8 +254,12 @@ __global__ __launch_bounds__(kBlock) void norm_grad_rows_kernel(NormGradCall c) 
         x[v] = nx[v];
         y[v] = ny[v];
       }
-      const float mean = live ? c.mean[row] : 0.0f, rstd = live ? c.rstd[row] : 0.0f;
-      if (row + step < c.n) load_rows(row + step, nx, ny);
+      const float mean = next_mean, rstd = next_rstd;
+      if (row + step < c.n) {
+        next_mean = c.mean[row + step];
+        next_rstd = c.rstd[row + step];
+        load_rows(row + step, nx, ny);
+      }
       float s[2] = {0.0f, 0.0f};
       if (live) {
 #pragma unroll

@@ -53,12 +53,25 @@ def _call(name, device, stream, *args):
         _check(status)
 
 
+def _record(stream, *tensors):
+    """Work on a given stream: the tensors' memory is not handed out again before that stream
+    is done with it, should the caller drop them."""
+    for t in tensors:
+        if t is not None and stream != torch.cuda.current_stream(t.device):
+            t.record_stream(stream)
+
+
+def record_use(*tensors):
+    """Records tensors on their devices' current streams (see _record)."""
+    for t in tensors:
+        t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def _empty(like, shape, dtype, stream):
-    """A tensor on the device of `like`.  Work on another stream than the current one is
-    recorded, so that the memory is not handed out again before that stream is done."""
+    """A tensor on the device of `like`, recorded on `stream`."""
     t = like.new_empty(shape, dtype=dtype)
-    if stream is not None and stream != torch.cuda.current_stream(like.device):
-        t.record_stream(stream)
+    if stream is not None:
+        _record(stream, t)
     return t
 
 
@@ -182,6 +195,8 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
         _, _, stride = _rows("out", out, device)
     _call("ma_embedding_forward", device, stream, table.data_ptr(), rows, dim, tokens.data_ptr(),
           bits, tokens.numel(), scale, out.data_ptr(), _type("out", out.dtype), stride)
+    if stream is not None:
+        _record(stream, table, tokens, out)
     return out
 
 
@@ -209,6 +224,8 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
     _keep, ws, size = _workspace(workspace, need, dout, stream)
     _call("ma_embedding_backward", device, stream, tokens.data_ptr(), bits, n, dout.data_ptr(),
           dtype, stride, scale, grad.data_ptr(), rows, dim, int(bool(accumulate)), ws, size)
+    if stream is not None:
+        _record(stream, tokens, dout, grad, _keep)
     return grad
 
 
@@ -232,6 +249,8 @@ def adamw_step_embedding(param, tokens, dout, exp_avg, exp_avg_sq, *, scale: flo
     _call("ma_adamw_step_embedding", device, stream, param.data_ptr(), exp_avg.data_ptr(),
           exp_avg_sq.data_ptr(), rows, dim, tokens.data_ptr(), bits, n, dout.data_ptr(), dtype,
           stride, scale, ctypes.byref(hp), ws, size)
+    if stream is not None:
+        _record(stream, param, exp_avg, exp_avg_sq, tokens, dout, _keep)
 
 
 # --------------------------------------------------------------------------
@@ -254,6 +273,8 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, out=None
     rstd = _like(mean, stream)
     _call("ma_layer_norm_forward", device, stream, x.data_ptr(), dtype, stride, n, dim, w, b, eps,
           out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
+    if stream is not None:
+        _record(stream, x, weight, bias, out)
     return out, mean, rstd
 
 
@@ -284,6 +305,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
           _floats("mean", mean, n, device), _floats("rstd", rstd, n, device), dx.data_ptr(),
           max(dim, 1), _floats("dweight", dweight, dim, device),
           _floats("dbias", dbias, dim, device), int(bool(accumulate)), ws, size)
+    if stream is not None:
+        _record(stream, dy, x, mean, rstd, weight, dweight, dbias, _keep)
     return dx, dweight, dbias
 
 
@@ -322,6 +345,8 @@ def distill_forward(logits, teacher, ids, *, temperature: float = 1.0, stream=No
     loss = _empty(logits, logits.shape[:-1], torch.float32, stream)
     stats = _empty(logits, logits.shape[:-1] + (2,), torch.float32, stream)
     _call("ma_distill_forward", logits.device, stream, *args, loss.data_ptr(), stats.data_ptr())
+    if stream is not None:
+        _record(stream, logits, teacher, ids)
     return loss, stats
 
 
@@ -334,6 +359,8 @@ def distill_backward(logits, teacher, ids, stats, row_weight, *, temperature: fl
     s, w = _floats("stats", stats, 2 * n, device), _floats("row_weight", row_weight, n, device)
     dlogits, stride = _dlogits(logits, dlogits, stream)
     _call("ma_distill_backward", device, stream, *args, s, w, dlogits.data_ptr(), stride)
+    if stream is not None:
+        _record(stream, logits, teacher, ids, stats, row_weight, dlogits)
     return dlogits
 
 
@@ -348,6 +375,8 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
     dlogits, stride = _dlogits(logits, dlogits, stream)
     _call("ma_distill_loss_grad", device, stream, *args, w, loss.data_ptr(), dlogits.data_ptr(),
           stride)
+    if stream is not None:
+        _record(stream, logits, teacher, ids, row_weight, dlogits)
     return loss, dlogits
 
 

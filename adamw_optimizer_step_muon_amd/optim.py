@@ -221,6 +221,7 @@ class MuonAdamW:
         from . import ops
 
         for tokens, dout, scale, _ in added:
+            ops.record_use(tokens, dout)
             if p.grad is None:
                 p.grad = ops.embedding_backward(dout, tokens, p.shape[0], scale=scale)
             else:
@@ -247,6 +248,9 @@ class MuonAdamW:
 
                     ops.adamw_step_embedding(p.data, tokens, dout, self.state[id(p)]["exp_avg"],
                                              self.state[id(p)]["exp_avg_sq"], scale=scale, **hp)
+                    # made by the backward pass, perhaps on another stream than this step's,
+                    # and dropped by zero_grad()
+                    ops.record_use(tokens, dout)
                 # the group's tensors in one fused pass (one launch per 48 tensors)
                 segs = [(p.data, p.grad, self.state[id(p)]["exp_avg"],
                          self.state[id(p)]["exp_avg_sq"]) for p in live]

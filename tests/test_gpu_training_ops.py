@@ -222,6 +222,36 @@ def test_calls_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_inputs_dropped_while_another_stream_uses_them():
+    """The caller's tensors are recorded on the stream that the work is given to: dropped right
+    after the call, their memory is not handed out before that stream is done."""
+    side = torch.cuda.Stream()
+    n, dim, rows = 4096, 2048, 5000
+    table = torch.randn(rows, dim, device=DEV)
+    want = []
+    for seed in range(3):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        t = torch.randint(0, rows, (n,), generator=g, device=DEV)
+        want.append((ma.embedding_backward(torch.randn(n, dim, generator=g, device=DEV), t, rows), table[t]))
+    torch.cuda.synchronize()
+    got = []
+    with torch.cuda.stream(side):
+        busy = torch.randn(4096, 4096, device=DEV)
+        for _ in range(20):
+            busy = torch.tanh(busy @ busy)
+    for seed in range(3):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        t = torch.randint(0, rows, (n,), generator=g, device=DEV)
+        dout = torch.randn(n, dim, generator=g, device=DEV)
+        side.wait_stream(torch.cuda.current_stream())
+        got.append((ma.embedding_backward(dout, t, rows, stream=side), ma.embedding_forward(table, t, stream=side)))
+        del t, dout
+        torch.full((n, dim), 1e30, device=DEV), torch.full((n,), rows - 1, device=DEV)  # the same sizes again
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_two_threads_at_once():
     """Calls from two threads on their own streams, workspaces allocated per call."""
     inputs, want = [_static(20), _static(21)], []
