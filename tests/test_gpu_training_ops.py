@@ -281,6 +281,24 @@ def test_two_threads_at_once():
             assert torch.equal(x, y)
 
 
+def test_single_rows_and_tokens():
+    """Vectors and zero-dimensional tokens are batches of one."""
+    v, table = torch.randn(64, device=DEV), torch.randn(50, 64, device=DEV)
+    y, mean, rstd = ma.layer_norm_forward(v)
+    rows = ma.layer_norm_forward(v[None])
+    assert y.shape == (64,) and mean.shape == rstd.shape == () and torch.equal(y, rows[0][0])
+    dx, dw, _ = ma.layer_norm_backward(y, v, mean, rstd)
+    assert dx.shape == dw.shape == (64,)
+    t = torch.tensor(3, device=DEV)
+    assert torch.equal(ma.embedding_forward(table, t), table[3])
+    grad = ma.embedding_backward(v, t, 50)
+    assert torch.equal(grad[3], v) and not grad[:3].any() and not grad[4:].any()
+    ids, one = torch.tensor([1, 5], device=DEV), torch.tensor(1.0, device=DEV)
+    loss, dz = ma.distill_loss_grad(v, table[0, :2].contiguous(), ids, one)
+    rows = ma.distill_loss_grad(v[None], table[:1, :2].contiguous(), ids[None], one[None])
+    assert loss.shape == () and torch.equal(loss, rows[0][0]) and torch.equal(dz, rows[1][0])
+
+
 def test_binding_checks_shapes():
     x = torch.zeros(6, 8, device=DEV)
     i = torch.zeros(6, dtype=torch.int64, device=DEV)
