@@ -672,7 +672,7 @@ ma_status check_distill(const DistillCall& c, Range* r) {
     return fail(MA_ERR_UNSUPPORTED, "%lld rows of %lld logits", (long long)c.n, (long long)c.vocab);
   if (!finite(c.temperature) || !(c.temperature > 0.0f))
     return fail(MA_ERR_INVALID_ARG, "temperature must be finite and above zero");
-  // exp2's argument is (z - m) log2(e) / tau, the loss's factor tau^2: both stay in range
+  // log2(e) / tau and tau^2 stay far from the ends of fp32
   if (c.temperature < 1e-6f || c.temperature > 1e6f)
     return fail(MA_ERR_UNSUPPORTED, "temperature %g outside [1e-6, 1e6]", c.temperature);
   if (const ma_status st = check_type(c.type, "logits")) return st;

@@ -29,10 +29,14 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // Sums of exponentials in powers of two.  A set of values v has a maximum m, and s is the sum
 // of 2^(v scale - r) for the reference r = m scale, rounded (reference below; never fused
 // with what it is used in, so that everybody has the same r).  v scale - r is one fused
-// multiply-add: it rounds by its own size only, and a large m loses nothing.  Values beyond
-// kFar, whose products can overflow (rows filled with a type's lowest value), take the slower
-// (v - m) scale, where r = 0 stands for the difference already taken.
-constexpr float kFar = 1e30f;  // times the largest scale, log2(e) 1e6, still finite
+// multiply-add: it rounds by its own size only.  The maximum's own exponent is what r was
+// rounded by, half a step of r: up to 1/2 while |r| < 2^24, and beyond what exp2 can hold from
+// some 2^31 on.  So rows whose maximum reaches far_from(scale) take the slower (v - m) scale,
+// where r = 0 stands for the difference already taken: rows filled with a mask's value, or
+// far above zero.  Other rows' smaller values are taken against -far_from(scale) at least, which
+// bounds their sums too.
+constexpr float kFarProduct = 16777216.0f;
+__device__ __forceinline__ float far_from(float scale) { return kFarProduct / scale; }
 struct Soft {
   float m, s;
 };
@@ -87,7 +91,7 @@ __device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, Soft*
   typedef typename Kept<T, kThreads, kKeep>::P P;
   constexpr int N = kVec<T>, kBatch = kThreads * kU * N;
   const int tid = threadIdx.x;
-  Soft a{kIsFar ? kLowest : -kFar, 0.0f};  // finite, so that differences to it are defined
+  Soft a{kIsFar ? kLowest : -far_from(scale), 0.0f};  // finite, so that differences to it are defined
   const auto take = [&](const P (&x)[kU], int left) {  // values at and behind `left` count as -inf
     float v[kU][N], m = a.m;
 #pragma unroll
@@ -138,7 +142,7 @@ __device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, Soft*
 template <int kThreads, bool kIsFar>
 __device__ Soft block_join(const Soft* of, float scale) {
   const int lane = threadIdx.x & 63;
-  return wave_join<kIsFar>(lane < kThreads / 64 ? of[lane] : Soft{kIsFar ? kLowest : -kFar, 0.0f}, scale);
+  return wave_join<kIsFar>(lane < kThreads / 64 ? of[lane] : Soft{kIsFar ? kLowest : -far_from(scale), 0.0f}, scale);
 }
 
 // dz = gq 2^exponent over the row, from its end to its beginning: what the first sweep kept,
@@ -253,7 +257,7 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   __syncthreads();
   if (kLoss) {
     zs = block_join<kThreads, false>(joined[0], scale);
-    if (zs.s == 0.0f || zs.m > kFar) {  // every value below -kFar, or a reference that overflows
+    if (fabsf(zs.m) >= far_from(scale)) {  // the same for every thread
       __syncthreads();
       sweep<T, kThreads, true, kKeep>(z, vocab, scale, joined[0], kept);
       __syncthreads();
@@ -269,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   ta = block_join<kThreads, true>(joined[1], scale);
   const bool some = wave_sum(lane < kWaves ? counts[lane] : 0.0f) > 0.0f;
   // q = 2^(exponent(v) - zc) / zs.s, zc the maximum's own exponent
-  const bool far = fabsf(zs.m) > kFar;
+  const bool far = fabsf(zs.m) >= far_from(scale);
   const float zr = far ? 0.0f : reference(zs.m, scale);
   const float zc = far ? 0.0f : exponent<false>(zs.m, scale, zs.m, zr);
   const auto power_of = [&](float v) {

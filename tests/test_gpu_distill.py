@@ -250,3 +250,48 @@ def test_borders_of_the_row_layouts(vocab, top):
         own, stats = ma.distill_forward(z, a, ids)
         assert torch.equal(own, loss)
         assert torch.equal(ma.distill_backward(z, a, ids, stats, w), grad)
+
+
+FILLS = [s * c for c in (1e7, 1e9, 5e9, 1e10, 1e12, 1e15, 1e20, 1e30) for s in (1.0, -1.0)]
+
+
+@pytest.mark.parametrize("vocab", [50, 9000, 40001])
+@pytest.mark.parametrize("dtype,tau,fills", [
+    (torch.float32, 1e-3, FILLS), (torch.float32, 0.05, FILLS), (torch.float32, 1.0, FILLS), (torch.float32, 4.0, FILLS),
+    (torch.bfloat16, 0.05, FILLS), (torch.bfloat16, 1.0, FILLS),
+    (torch.float16, 1e-6, [6e4, -6e4, 3e3, -3e3]), (torch.float16, 1e-2, [6e4, -6e4])])
+def test_rows_filled_with_a_masks_value(vocab, dtype, tau, fills):
+    """Finite fills of any size give what their differences give (the bounds at the head of this
+    file): whole rows of one value, rows of which only some entries are left (so that whole
+    threads see masked values alone), rows a few steps of the type below the fill."""
+    rng = np.random.default_rng(vocab)
+    tau = float(np.float32(tau))
+    n = 3 * len(fills)
+    z = torch.empty(n, vocab, dtype=dtype, device=DEV)
+    ids = torch.from_numpy(rng.integers(0, vocab, (n, 3))).to(DEV)
+    for i, c in enumerate(fills):
+        z[3 * i] = c
+        z[3 * i + 1] = -abs(c)
+        left = rng.choice(vocab, 10, replace=False)
+        z[3 * i + 1, left] = torch.from_numpy(rng.standard_normal(10)).to(dtype).to(DEV)
+        ids[3 * i + 1, :2] = torch.from_numpy(left[:2]).to(DEV)
+        steps = torch.from_numpy(rng.integers(0, 4, vocab)).to(DEV)
+        z[3 * i + 2] = (c * (1 - steps.double() * torch.finfo(dtype).eps)).to(dtype)
+    a = torch.from_numpy((tau * rng.standard_normal((n, 3))).astype(np.float32)).to(DEV)
+    w = torch.from_numpy(rng.random(n).astype(np.float32) + 0.1).to(DEV)
+    rl, rz, bl, bz = _bounds(_np(z), _np(a), ids.cpu().numpy(), _np(w), tau)
+    # _bounds takes log q from 1e-300 at least, so of a teacher's entry whose q is smaller it has
+    # the 3 e |x| of the exponent alone.  What follows it rounds by |x| as well: the two
+    # subtractions of log s and of the maximum's exponent, log p - log q, the product with p,
+    # p itself (softmax of 3, at least 12 e), the sum of 3 and the factor tau^2 / log2(e) (4 e),
+    # some 24 e; _bounds has (76 + 16) e for every entry that it does not cut off.
+    Z, I = _np(z), ids.cpu().numpy()
+    x = np.abs(np.take_along_axis(Z, I, 1) - Z.max(1, keepdims=True)) / tau
+    p = training.teacher_probabilities(_np(a), I, vocab, tau)
+    bl = bl + tau ** 2 * 24 * E * np.where(x > 690, p * x, 0.0).sum(1)
+    loss, grad = ma.distill_loss_grad(z, a, ids, w, temperature=tau)
+    own, stats = ma.distill_forward(z, a, ids, temperature=tau)
+    assert (np.abs(_np(loss) - rl) <= bl).all() and torch.equal(own, loss)
+    assert (_np(stats)[:, 0] == Z.max(1)).all()
+    _check(grad, rz, bz, dtype)
+    assert torch.equal(ma.distill_backward(z, a, ids, stats, w, temperature=tau), grad)
