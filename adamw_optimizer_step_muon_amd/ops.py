@@ -10,8 +10,11 @@ kernels; ``embedding`` can hand its table gradient to a MuonAdamW in token form,
 Parameters and their gradients are fp32; activations fp32, fp16 or bf16.  Activation tensors
 have contiguous rows (the last dimension) at any common row stride.  Work is enqueued on
 ``stream`` (the tensors' device's current stream when None); outputs and workspaces come from
-torch's allocator.  A backward pass that is captured into a graph obeys torch's rule for
-captured gradients: no eager autograd graph of the same parameters may be alive meanwhile.
+torch's allocator, from the memory of the stream that they are used on.  A call orders no
+streams: with ``stream`` given, the caller has that stream wait for what makes the inputs, and
+waits for it before using the outputs elsewhere.  A backward pass that is captured into a graph
+obeys torch's rule for captured gradients: no eager autograd graph of the same parameters may be
+alive meanwhile.
 """
 from __future__ import annotations
 
@@ -67,11 +70,20 @@ def record_use(*tensors):
         t.record_stream(torch.cuda.current_stream(t.device))
 
 
+def _allocate(like, shape, dtype, stream):
+    """A tensor on the device of `like` from the memory of `stream`: what the current stream has
+    dropped may still be in use by work queued there, which `stream` does not wait for."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _empty(like, shape, dtype, stream):
-    """A tensor on the device of `like`, recorded on `stream`."""
-    t = like.new_empty(shape, dtype=dtype)
+    """An output: allocated on `stream`, and for the caller to use on the current one."""
+    t = _allocate(like, shape, dtype, stream)
     if stream is not None:
-        _record(stream, t)
+        record_use(t)
     return t
 
 
@@ -156,7 +168,7 @@ def _workspace(workspace, need, like, stream):
     if workspace is None:
         if not need:
             return None, 0, 0
-        workspace = _empty(like, need, torch.uint8, stream)
+        workspace = _allocate(like, need, torch.uint8, stream)
     else:
         _tensor("workspace", workspace, like.device)
         if not workspace.is_contiguous():

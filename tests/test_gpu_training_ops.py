@@ -326,3 +326,67 @@ def test_binding_checks_shapes():
         ma.layer_norm_forward(x, out=x)
     with pytest.raises(ma.MuonAdamWError):
         ma.distill_forward(x, f[:, None], i[:, None], temperature=0.0)
+
+
+def _every_call(s, x, stats, mean, stream):
+    """Each entry point once, on tensors that are all there."""
+    w, rows = s["w"], s["table"].shape[0]
+    out = [ma.embedding_forward(s["table"], s["tokens"], scale=SCALE, stream=stream),
+           *ma.layer_norm_forward(x, s["g"], s["b"], stream=stream),
+           *ma.layer_norm_backward(x, x, mean, w, s["g"], stream=stream),
+           ma.embedding_backward(x, s["tokens"], rows, stream=stream),
+           *ma.distill_forward(x, s["teacher"], s["ids"], stream=stream),
+           ma.distill_backward(x, s["teacher"], s["ids"], stats, w, stream=stream),
+           *ma.distill_loss_grad(x, s["teacher"], s["ids"], w, stream=stream)]
+    ma.adamw_step_embedding(s["p"], s["tokens"], x, s["m"], s["v"], step=1, lr=1e-2, stream=stream)
+    return out + [s["p"].clone(), s["m"].clone(), s["v"].clone()] if stream is None else out
+
+
+def _ready(seed):
+    s = _static(seed, vocab=64)
+    x = torch.randn(s["tokens"].numel(), 64, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV)
+    stats = torch.stack([x.amax(1), torch.exp(x - x.amax(1, keepdim=True)).sum(1)], 1)
+    mean = x.mean(1)
+    torch.cuda.synchronize()
+    return s, x, stats, mean
+
+
+def test_outputs_and_workspaces_are_the_streams_own_memory(monkeypatch):
+    """What calls on the current stream have dropped is not handed to calls on another stream,
+    which do not wait for the current one."""
+    from adamw_optimizer_step_muon_amd import ops
+
+    s, *rest = _ready(5)
+    seen, call = [], ops._call
+    monkeypatch.setattr(ops, "_call", lambda name, device, stream, *args: (
+        seen.append((stream, {a for a in args if isinstance(a, int) and a > 1 << 32})),
+        call(name, device, stream, *args)))
+    inputs = {t.data_ptr() for t in [*s.values(), *rest]}
+    for stream in (None, torch.cuda.Stream()):
+        out = _every_call(s, *rest, stream)
+        torch.cuda.synchronize()
+        del out
+    here, there = ({a for st, args in seen for a in args if (st is None) == k} - inputs for k in (True, False))
+    assert len(seen) == 16 and len(here) > 10 and len(there) > 10
+    assert not here & there
+
+
+def test_a_call_beside_one_that_has_just_returned():
+    """Calls of the same sizes on the current stream and, without a wait between them, on
+    another: each has its own memory, and gives what it gives alone."""
+    first, second = _ready(6), _ready(7)
+    want = _every_call(*_ready(6), None), _every_call(*_ready(7), None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    big = torch.randn(2048, 2048, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big = torch.tanh(big @ big)  # the current stream has work to come first
+    a = _every_call(*first, None)
+    b = _every_call(*second, side)
+    torch.cuda.synchronize()
+    b += [second[0][k] for k in "pmv"]
+    for got, ref in ((a, want[0]), (b, want[1])):
+        assert len(got) == len(ref)
+        for p, q in zip(got, ref):
+            assert torch.equal(p, q)
