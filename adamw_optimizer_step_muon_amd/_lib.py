@@ -249,16 +249,13 @@ def _stream_handle(stream, device) -> int:
 
 
 def _scratch(nbytes: int, device, stream):
-    """A workspace allocated for one call.  It is freed when the call returns, so when
-    the kernels run on another stream than the current one it is recorded on that
-    stream: the caching allocator then does not hand the memory out again before that
-    stream's work is done."""
+    """A workspace allocated for one call, from the memory of the stream that the call's
+    kernels run on: freed when the call returns, it goes to later work of that stream, and
+    what it gets has not been dropped by another stream whose work may still use it."""
     import torch
 
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        ws.record_stream(stream)
-    return ws
+    with torch.cuda.stream(stream):  # the current one for None
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _muon_hparams(lr, momentum, weight_decay, nesterov, ns_steps, ns_coeffs, ns_eps,
