@@ -22,6 +22,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.graph import increment_version
 
 from ._lib import _AdamWHParams, _check, _require_f32_cuda, _stream_handle, load
 
@@ -68,6 +69,12 @@ def record_use(*tensors):
     """Records tensors on their devices' current streams (see _record)."""
     for t in tensors:
         t.record_stream(torch.cuda.current_stream(t.device))
+
+
+def _wrote(*tensors):
+    """The caller's tensors that a call has written, by their addresses: their versions advance,
+    so that autograd and MuonAdamW see that what they kept of them has changed."""
+    increment_version([t for t in tensors if t is not None])
 
 
 def _allocate(like, shape, dtype, stream):
@@ -198,7 +205,7 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     rows, dim = _table("table", table)
     device = table.device
     bits = _ints("tokens", tokens, device)
-    shape = tokens.shape + (dim,)
+    shape, given = tokens.shape + (dim,), out
     if out is None:
         out, stride = _empty(table, shape, out_dtype or torch.float32, stream), dim
     else:
@@ -207,6 +214,8 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
         _, _, stride = _rows("out", out, device)
     _call("ma_embedding_forward", device, stream, table.data_ptr(), rows, dim, tokens.data_ptr(),
           bits, tokens.numel(), scale, out.data_ptr(), _type("out", out.dtype), stride)
+    if given is not None:
+        _wrote(given)
     if stream is not None:
         _record(stream, table, tokens, out)
     return out
@@ -228,6 +237,7 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
         raise ValueError("accumulate needs a grad to add to")
     rows, dim, device = int(rows), dout.shape[-1], dout.device
     bits, n, stride, dtype = _token_rows(tokens, dout, dim, device)
+    given = grad
     if grad is None:
         grad = _empty(dout, (rows, dim), torch.float32, stream)
     elif tuple(_table("grad", grad, device)) != (rows, dim):
@@ -236,6 +246,8 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
     _keep, ws, size = _workspace(workspace, need, dout, stream)
     _call("ma_embedding_backward", device, stream, tokens.data_ptr(), bits, n, dout.data_ptr(),
           dtype, stride, scale, grad.data_ptr(), rows, dim, int(bool(accumulate)), ws, size)
+    if given is not None:
+        _wrote(given)
     if stream is not None:
         _record(stream, tokens, dout, grad, _keep)
     return grad
@@ -261,6 +273,7 @@ def adamw_step_embedding(param, tokens, dout, exp_avg, exp_avg_sq, *, scale: flo
     _call("ma_adamw_step_embedding", device, stream, param.data_ptr(), exp_avg.data_ptr(),
           exp_avg_sq.data_ptr(), rows, dim, tokens.data_ptr(), bits, n, dout.data_ptr(), dtype,
           stride, scale, ctypes.byref(hp), ws, size)
+    _wrote(param, exp_avg, exp_avg_sq)
     if stream is not None:
         _record(stream, param, exp_avg, exp_avg_sq, tokens, dout, _keep)
 
@@ -275,6 +288,7 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, out=None
     n, dim, stride = _rows("x", x)
     dtype, device = _type("x", x.dtype), x.device
     w, b = _floats("weight", weight, dim, device), _floats("bias", bias, dim, device)
+    given = out
     if out is None:
         out, out_stride = _like(x, stream), max(dim, 1)
     else:
@@ -285,6 +299,8 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, out=None
     rstd = _like(mean, stream)
     _call("ma_layer_norm_forward", device, stream, x.data_ptr(), dtype, stride, n, dim, w, b, eps,
           out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
+    if given is not None:
+        _wrote(given)
     if stream is not None:
         _record(stream, x, weight, bias, out)
     return out, mean, rstd
@@ -305,6 +321,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
         raise ValueError("a gradient buffer is given for a gradient that is not wanted")
     if accumulate and ((weight_grad and dweight is None) or (bias_grad and dbias is None)):
         raise ValueError("accumulate needs the gradients to add to")
+    given = (dweight, dbias)
     if weight_grad and dweight is None:
         dweight = _empty(x, dim, torch.float32, stream)
     if bias_grad and dbias is None:
@@ -317,6 +334,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
           _floats("mean", mean, n, device), _floats("rstd", rstd, n, device), dx.data_ptr(),
           max(dim, 1), _floats("dweight", dweight, dim, device),
           _floats("dbias", dbias, dim, device), int(bool(accumulate)), ws, size)
+    if given[0] is not None or given[1] is not None:
+        _wrote(*given)
     if stream is not None:
         _record(stream, dy, x, mean, rstd, weight, dweight, dbias, _keep)
     return dx, dweight, dbias
@@ -369,8 +388,11 @@ def distill_backward(logits, teacher, ids, stats, row_weight, *, temperature: fl
     args, n = _distill(logits, teacher, ids, temperature)
     device = logits.device
     s, w = _floats("stats", stats, 2 * n, device), _floats("row_weight", row_weight, n, device)
+    given = dlogits
     dlogits, stride = _dlogits(logits, dlogits, stream)
     _call("ma_distill_backward", device, stream, *args, s, w, dlogits.data_ptr(), stride)
+    if given is not None:
+        _wrote(given)
     if stream is not None:
         _record(stream, logits, teacher, ids, stats, row_weight, dlogits)
     return dlogits
@@ -384,9 +406,12 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
     device = logits.device
     w = _floats("row_weight", row_weight, n, device)
     loss = _empty(logits, logits.shape[:-1], torch.float32, stream)
+    given = dlogits
     dlogits, stride = _dlogits(logits, dlogits, stream)
     _call("ma_distill_loss_grad", device, stream, *args, w, loss.data_ptr(), dlogits.data_ptr(),
           stride)
+    if given is not None:
+        _wrote(given)
     if stream is not None:
         _record(stream, logits, teacher, ids, row_weight, dlogits)
     return loss, dlogits

@@ -390,3 +390,50 @@ def test_a_call_beside_one_that_has_just_returned():
         assert len(got) == len(ref)
         for p, q in zip(got, ref):
             assert torch.equal(p, q)
+
+
+def test_writes_into_the_callers_tensors_advance_their_versions():
+    """As torch's own in-place operations do, so that what autograd or the optimizer keeps of
+    such a tensor is not taken for unchanged."""
+    s, x, stats, mean = _ready(8)
+    rows, w = s["table"].shape[0], s["w"]
+    calls = {
+        "lookup": lambda t: ma.embedding_forward(s["table"], s["tokens"], out=t[0]),
+        "gradient": lambda t: ma.embedding_backward(x, s["tokens"], rows, grad=t[1]),
+        "added": lambda t: ma.embedding_backward(x, s["tokens"], rows, grad=t[1], accumulate=True),
+        "norm": lambda t: ma.layer_norm_forward(x, out=t[0]),
+        "gain": lambda t: ma.layer_norm_backward(x, x, mean, w, dweight=t[2], bias_grad=False),
+        "bias": lambda t: ma.layer_norm_backward(x, x, mean, w, dbias=t[2], weight_grad=False),
+        "distilled": lambda t: ma.distill_backward(x, s["teacher"], s["ids"], stats, w, dlogits=t[0]),
+        "both": lambda t: ma.distill_loss_grad(x, s["teacher"], s["ids"], w, dlogits=t[0])}
+    written = {"lookup": 0, "gradient": 1, "added": 1, "norm": 0, "gain": 2, "bias": 2, "distilled": 0, "both": 0}
+    for name, call in calls.items():
+        t = [torch.zeros_like(x), torch.zeros_like(s["p"]), torch.zeros(64, device=DEV)]
+        kept = [*t, x, stats, mean, *s.values()]
+        before = [k._version for k in kept]
+        call(t)
+        assert [k._version > b for k, b in zip(kept, before)] == [i == written[name] for i in range(len(kept))], name
+    state = [s["p"], s["m"], s["v"]]
+    before = [k._version for k in state]
+    ma.adamw_step_embedding(s["p"], s["tokens"], x, s["m"], s["v"], step=1, lr=1e-2)
+    assert all(k._version > b for k, b in zip(state, before))
+
+    # logits that a loss has kept for its backward pass
+    z = x.clone().requires_grad_(True)
+    logits = z * 1.0
+    loss = ma.distill_loss(logits, s["teacher"], s["ids"]).sum()
+    ma.distill_loss_grad(logits.detach(), s["teacher"], s["ids"], w, dlogits=logits.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # output gradients that the optimizer has kept
+    table = torch.nn.Parameter(s["table"].clone())
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table]}])
+    dout = x.clone()
+    opt.add_token_gradient(table, s["tokens"], dout)
+    ma.layer_norm_forward(x, out=dout)
+    with pytest.raises(RuntimeError, match="modified before step"):
+        opt.step()
+    # tensors without a version
+    with torch.inference_mode():
+        u = torch.empty_like(x)
+    assert ma.layer_norm_forward(x, out=u)[0] is u
