@@ -8,7 +8,8 @@ kernels; ``embedding`` can hand its table gradient to a MuonAdamW in token form,
 ``step()`` then applies without building the dense gradient.
 
 Parameters and their gradients are fp32; activations fp32, fp16 or bf16.  Activation tensors
-have contiguous rows (the last dimension) at any common row stride.  Work is enqueued on
+have contiguous rows (the last dimension) at any common row stride; tokens, ids and teacher
+lists any strides (they are copied where they are not contiguous).  Work is enqueued on
 ``stream`` (the tensors' device's current stream when None); outputs and workspaces come from
 torch's allocator, from the memory of the stream that they are used on.  A call orders no
 streams: with ``stream`` given, the caller has that stream wait for what makes the inputs, and
@@ -143,9 +144,15 @@ def _ints(name, t, device=None) -> int:
     bits = _BITS.get(t.dtype)
     if bits is None:
         raise ValueError(f"{name} must be int32 or int64 (got {t.dtype})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     return bits
+
+
+def _contiguous(t, stream):
+    """t itself, or a copy made on the call's stream (for the duration of the call)."""
+    if t.is_contiguous():
+        return t
+    with torch.cuda.stream(stream):
+        return t.contiguous()
 
 
 def _floats(name, t, count, device=None) -> int:
@@ -205,14 +212,14 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     rows, dim = _table("table", table)
     device = table.device
     bits = _ints("tokens", tokens, device)
-    shape, given = tokens.shape + (dim,), out
+    shape, given, at = tokens.shape + (dim,), out, _contiguous(tokens, stream)
     if out is None:
         out, stride = _empty(table, shape, out_dtype or torch.float32, stream), dim
     else:
         if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be {tuple(shape)} of {out_dtype or out.dtype}")
         _, _, stride = _rows("out", out, device)
-    _call("ma_embedding_forward", device, stream, table.data_ptr(), rows, dim, tokens.data_ptr(),
+    _call("ma_embedding_forward", device, stream, table.data_ptr(), rows, dim, at.data_ptr(),
           bits, tokens.numel(), scale, out.data_ptr(), _type("out", out.dtype), stride)
     if given is not None:
         _wrote(given)
@@ -244,7 +251,8 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
         raise ValueError(f"grad must be ({rows}, {dim})")
     need = embedding_workspace_bytes(rows, dim, n)
     _keep, ws, size = _workspace(workspace, need, dout, stream)
-    _call("ma_embedding_backward", device, stream, tokens.data_ptr(), bits, n, dout.data_ptr(),
+    at = _contiguous(tokens, stream)
+    _call("ma_embedding_backward", device, stream, at.data_ptr(), bits, n, dout.data_ptr(),
           dtype, stride, scale, grad.data_ptr(), rows, dim, int(bool(accumulate)), ws, size)
     if given is not None:
         _wrote(given)
@@ -270,8 +278,9 @@ def adamw_step_embedding(param, tokens, dout, exp_avg, exp_avg_sq, *, scale: flo
                        int(bool(cautious_wd)))
     need = embedding_workspace_bytes(rows, dim, n)
     _keep, ws, size = _workspace(workspace, need, param, stream)
+    at = _contiguous(tokens, stream)
     _call("ma_adamw_step_embedding", device, stream, param.data_ptr(), exp_avg.data_ptr(),
-          exp_avg_sq.data_ptr(), rows, dim, tokens.data_ptr(), bits, n, dout.data_ptr(), dtype,
+          exp_avg_sq.data_ptr(), rows, dim, at.data_ptr(), bits, n, dout.data_ptr(), dtype,
           stride, scale, ctypes.byref(hp), ws, size)
     _wrote(param, exp_avg, exp_avg_sq)
     if stream is not None:
@@ -344,18 +353,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
 # --------------------------------------------------------------------------
 # distillation
 # --------------------------------------------------------------------------
-def _distill(logits, teacher, ids, temperature):
-    """The leading arguments shared by the three calls, and the number of rows."""
+def _distill(logits, teacher, ids, temperature, stream):
+    """The leading arguments shared by the three calls, the number of rows, and what the
+    arguments' addresses need alive."""
     n, vocab, stride = _rows("logits", logits)
     _tensor("teacher", teacher, logits.device)
-    if teacher.shape[:-1] != logits.shape[:-1] or not teacher.is_contiguous():
-        raise ValueError("teacher must be contiguous with the logits' leading dimensions")
+    if teacher.dim() != logits.dim() or teacher.shape[:-1] != logits.shape[:-1]:
+        raise ValueError("teacher must have the logits' leading dimensions")
     bits = _ints("ids", ids, logits.device)
     if ids.shape != teacher.shape:
         raise ValueError("ids must have the teacher's shape")
+    keep = teacher, ids = _contiguous(teacher, stream), _contiguous(ids, stream)
     return (logits.data_ptr(), _type("logits", logits.dtype), stride, n, vocab, teacher.data_ptr(),
             _type("teacher", teacher.dtype), ids.data_ptr(), bits, teacher.shape[-1],
-            float(temperature)), n
+            float(temperature)), n, keep
 
 
 def _dlogits(logits, dlogits, stream):
@@ -371,8 +382,9 @@ def distill_forward(logits, teacher, ids, *, temperature: float = 1.0, stream=No
     """(loss, stats) of ma_distill_forward: the Kullback-Leibler divergence, times
     temperature^2, of each row of logits (..., vocab) from the teacher's top logits (..., top)
     at the vocabulary places ids.  loss has the leading dimensions; stats (..., 2) is the
-    backward pass's input."""
-    args, _ = _distill(logits, teacher, ids, temperature)
+    backward pass's input.  Positions without a target (the last ones of a batch of sequences)
+    take ids of -1 and their logits stay where they are: loss and gradient are zero."""
+    args, _, _keep = _distill(logits, teacher, ids, temperature, stream)
     loss = _empty(logits, logits.shape[:-1], torch.float32, stream)
     stats = _empty(logits, logits.shape[:-1] + (2,), torch.float32, stream)
     _call("ma_distill_forward", logits.device, stream, *args, loss.data_ptr(), stats.data_ptr())
@@ -385,7 +397,7 @@ def distill_backward(logits, teacher, ids, stats, row_weight, *, temperature: fl
                      dlogits=None, stream=None):
     """The gradient of sum row_weight * loss by the logits (ma_distill_backward), into
     `dlogits` (allocated when None; may be `logits` itself)."""
-    args, n = _distill(logits, teacher, ids, temperature)
+    args, n, _keep = _distill(logits, teacher, ids, temperature, stream)
     device = logits.device
     s, w = _floats("stats", stats, 2 * n, device), _floats("row_weight", row_weight, n, device)
     given = dlogits
@@ -402,7 +414,7 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
                       stream=None):
     """(loss, dlogits) in one pass (ma_distill_loss_grad), for a row_weight known beforehand:
     the values of distill_forward and distill_backward."""
-    args, n = _distill(logits, teacher, ids, temperature)
+    args, n, _keep = _distill(logits, teacher, ids, temperature, stream)
     device = logits.device
     w = _floats("row_weight", row_weight, n, device)
     loss = _empty(logits, logits.shape[:-1], torch.float32, stream)
@@ -433,6 +445,7 @@ def _rowed(t):
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, table, scale, out_dtype, optimizer):
+        tokens = tokens.contiguous()
         ctx.save_for_backward(tokens)
         ctx.rows, ctx.scale = table.shape[0], scale
         ctx.optimizer, ctx.table = optimizer, table if optimizer is not None else None
@@ -470,6 +483,7 @@ class _LayerNorm(torch.autograd.Function):
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, teacher, ids, temperature):
+        teacher, ids = teacher.contiguous(), ids.contiguous()
         loss, stats = distill_forward(logits, teacher, ids, temperature=temperature)
         ctx.save_for_backward(logits, teacher, ids, stats)
         ctx.temperature = temperature

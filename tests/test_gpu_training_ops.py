@@ -437,3 +437,39 @@ def test_writes_into_the_callers_tensors_advance_their_versions():
     with torch.inference_mode():
         u = torch.empty_like(x)
     assert ma.layer_norm_forward(x, out=u)[0] is u
+
+
+def test_tokens_and_teacher_lists_of_any_strides():
+    """Slices of a batch's tokens and of longer teacher lists give what their copies give,
+    on the current stream, on another, and through autograd."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    table = torch.randn(V, D, generator=g, device=DEV)
+    tokens = torch.randint(-1, V, (6, 90), generator=g, device=DEV)[:, :-1]
+    dout = torch.randn(6, 89, D, generator=g, device=DEV)
+    logits = torch.randn(6, 89, V, generator=g, device=DEV)
+    teacher = torch.randn(6, 89, 2 * K, generator=g, device=DEV)[..., :K]
+    ids = torch.randint(-1, V, (K, 89, 6), generator=g, device=DEV).permute(2, 1, 0)
+    w = torch.rand(6, 89, generator=g, device=DEV)
+    assert not tokens.is_contiguous() and not teacher.is_contiguous() and not ids.is_contiguous()
+    torch.cuda.synchronize()
+
+    def run(tokens, teacher, ids, stream):
+        p, m, v = table.clone(), torch.zeros_like(table), torch.zeros_like(table)
+        torch.cuda.synchronize()
+        loss, stats = ma.distill_forward(logits, teacher, ids, stream=stream)
+        if stream is not None:
+            stream.synchronize()
+        ma.adamw_step_embedding(p, tokens, dout, m, v, step=1, lr=1e-2, stream=stream)
+        out = [ma.embedding_forward(table, tokens, stream=stream), ma.embedding_backward(dout, tokens, V, stream=stream),
+               loss, ma.distill_backward(logits, teacher, ids, stats, w, stream=stream),
+               *ma.distill_loss_grad(logits, teacher, ids, w, stream=stream), p, m, v]
+        torch.cuda.synchronize()
+        a, b = table.clone().requires_grad_(True), logits.clone().requires_grad_(True)
+        (ma.embedding(tokens, a) * dout).sum().backward()
+        (ma.distill_loss(b, teacher, ids) * w).sum().backward()
+        return out + [a.grad, b.grad]
+
+    want = run(tokens.contiguous(), teacher.contiguous(), ids.contiguous(), None)
+    for stream in (None, torch.cuda.Stream()):
+        for a, b in zip(run(tokens, teacher, ids, stream), want):
+            assert torch.equal(a, b)
