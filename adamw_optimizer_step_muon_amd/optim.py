@@ -43,6 +43,11 @@ ADAMW_DEFAULTS = dict(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
                       decoupled=True, cautious_wd=False)
 
 
+def _version(t):
+    """t's version, None for the tensors of inference mode, which have none."""
+    return None if t.is_inference() else t._version
+
+
 class _Bucket:
     """K same-shape Muon parameters stored as one (K, A, B) buffer."""
 
@@ -205,7 +210,7 @@ class MuonAdamW:
         if tokens.device != param.device or dout.device != param.device:
             raise ValueError("tokens and dout must be on the parameter's device")
         self._token_grads.setdefault(id(param), []).append(
-            (tokens, dout, float(scale), (tokens._version, dout._version)))
+            (tokens, dout, float(scale), (_version(tokens), _version(dout))))
 
     def _take_token_gradient(self, p):
         """The token gradient to step p with directly, or None where p.grad holds it all."""
@@ -213,7 +218,7 @@ class MuonAdamW:
         if not added:
             return None
         for tokens, dout, _, versions in added:
-            if (tokens._version, dout._version) != versions:
+            if (_version(tokens), _version(dout)) != versions:
                 raise RuntimeError("the tokens or output gradients of a token gradient were "
                                    "modified before step()")
         if len(added) == 1 and p.grad is None:

@@ -226,3 +226,14 @@ def test_token_gradients_are_checked_when_added():
         opt.step()
     opt.zero_grad()
     opt.step()  # nothing left to step
+
+
+def test_token_gradients_of_inference_mode():
+    """Its tensors have no version to check."""
+    table = torch.zeros(10, 4)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table]}])
+    with torch.inference_mode():
+        tokens, dout = torch.zeros(5, dtype=torch.int64), torch.zeros(5, 4)
+    opt.add_token_gradient(table, tokens, dout)
+    with pytest.raises(ValueError, match="GPU"):  # and no complaint about versions
+        opt.step()
