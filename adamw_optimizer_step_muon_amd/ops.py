@@ -121,6 +121,11 @@ def _type(name, dtype) -> int:
 def _rows(name, t, device=None):
     """(rows, columns, row stride in values) of an activation tensor (..., columns)."""
     _tensor(name, t, device)
+    return layout(name, t)
+
+
+def layout(name, t):
+    """_rows' result, wherever the tensor lives."""
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     dim = t.shape[-1]

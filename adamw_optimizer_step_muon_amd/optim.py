@@ -43,6 +43,9 @@ ADAMW_DEFAULTS = dict(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
                       decoupled=True, cautious_wd=False)
 
 
+_F32_MAX = 3.4028234663852886e38
+
+
 def _version(t):
     """t's version, None for the tensors of inference mode, which have none."""
     return None if t.is_inference() else t._version
@@ -186,7 +189,7 @@ class MuonAdamW:
         if not any(q is param for g in self.param_groups if g["kind"] == "adamw"
                    for q in g["params"]):
             raise ValueError("token gradients are for parameters of an adamw group")
-        if param.dim() != 2:
+        if param.dim() != 2 or param.numel() == 0:
             raise ValueError("token gradients are for (rows, dim) parameters")
 
     def add_token_gradient(self, param, tokens, dout, scale: float = 1.0) -> None:
@@ -209,8 +212,14 @@ class MuonAdamW:
             raise ValueError("tokens must be int32 or int64, dout float32, float16 or bfloat16")
         if tokens.device != param.device or dout.device != param.device:
             raise ValueError("tokens and dout must be on the parameter's device")
+        scale = float(scale)
+        if not abs(scale) <= _F32_MAX:
+            raise ValueError("scale must be finite in fp32")
+        from . import ops
+
+        ops.layout("dout", dout)
         self._token_grads.setdefault(id(param), []).append(
-            (tokens, dout, float(scale), (_version(tokens), _version(dout))))
+            (tokens, dout, scale, (_version(tokens), _version(dout))))
 
     def _take_token_gradient(self, p):
         """The token gradient to step p with directly, or None where p.grad holds it all."""

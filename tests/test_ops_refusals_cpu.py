@@ -237,3 +237,21 @@ def test_token_gradients_of_inference_mode():
     opt.add_token_gradient(table, tokens, dout)
     with pytest.raises(ValueError, match="GPU"):  # and no complaint about versions
         opt.step()
+
+
+def test_token_gradients_that_a_step_would_refuse_are_refused_when_added():
+    table, empty = torch.zeros(10, 4), torch.zeros(0, 4)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table, empty]}])
+    tokens, dout = torch.zeros(6, dtype=torch.int64), torch.zeros(6, 4)
+    for bad in (dout[:1].expand(6, 4), torch.zeros(4, 6).t()):
+        with pytest.raises(ValueError, match="rows"):
+            opt.add_token_gradient(table, tokens, bad)
+    with pytest.raises(ValueError, match="common stride"):
+        opt.add_token_gradient(table, tokens.view(2, 3), torch.zeros(2, 4, 4)[:, :3])
+    for scale in (NAN, float("inf"), 1e39):
+        with pytest.raises(ValueError, match="scale"):
+            opt.add_token_gradient(table, tokens, dout, scale)
+    with pytest.raises(ValueError, match="parameters"):
+        opt.add_token_gradient(empty, tokens, dout)
+    opt.step()  # nothing was added
+    assert opt.param_groups[0]["step"] == 0
