@@ -221,30 +221,43 @@ class MuonAdamW:
         self._token_grads.setdefault(id(param), []).append(
             (tokens, dout, scale, (_version(tokens), _version(dout))))
 
+    def _check_token_gradients(self) -> None:
+        """Raises what step() would find wrong with a token gradient, before it changes
+        anything."""
+        if not self._token_grads:
+            return
+        for g in self.param_groups:
+            for p in g["params"]:
+                for tokens, dout, _, versions in self._token_grads.get(id(p), ()):
+                    if (_version(tokens), _version(dout)) != versions:
+                        raise RuntimeError("the tokens or output gradients of a token gradient "
+                                           "were modified before step()")
+                    if p.grad is not None:
+                        _lib._require_f32_cuda("the grad that token gradients add to", p.grad)
+
     def _take_token_gradient(self, p):
         """The token gradient to step p with directly, or None where p.grad holds it all."""
         added = self._token_grads.get(id(p))
         if not added:
             return None
-        for tokens, dout, _, versions in added:
-            if (_version(tokens), _version(dout)) != versions:
-                raise RuntimeError("the tokens or output gradients of a token gradient were "
-                                   "modified before step()")
         if len(added) == 1 and p.grad is None:
             return added[0]
         from . import ops
 
-        for tokens, dout, scale, _ in added:
+        while added:  # what p.grad holds is no longer in the list
+            tokens, dout, scale, _ = added[0]
             ops.record_use(tokens, dout)
             if p.grad is None:
                 p.grad = ops.embedding_backward(dout, tokens, p.shape[0], scale=scale)
             else:
                 ops.embedding_backward(dout, tokens, p.shape[0], scale=scale, grad=p.grad,
                                        accumulate=True)
+            del added[0]
         del self._token_grads[id(p)]
         return None
 
     def step(self) -> None:
+        self._check_token_gradients()
         for gi, g in enumerate(self.param_groups):
             if g["kind"] == "adamw":
                 by_token = [(p, t) for p in g["params"]
@@ -252,11 +265,14 @@ class MuonAdamW:
                 live = [p for p in g["params"] if p.grad is not None]
                 if not live and not by_token:
                     continue
-                g["step"] += 1
                 b1, b2 = g["betas"]
-                hp = dict(step=g["step"], lr=g["lr"], beta1=b1, beta2=b2, eps=g["eps"],
+                hp = dict(step=g["step"] + 1, lr=g["lr"], beta1=b1, beta2=b2, eps=g["eps"],
                           weight_decay=g["weight_decay"], decoupled=g["decoupled"],
                           cautious_wd=g["cautious_wd"])
+                # the group's tensors in one fused pass (one launch per 48 tensors)
+                segs = [(p.data, p.grad, self.state[id(p)]["exp_avg"],
+                         self.state[id(p)]["exp_avg_sq"]) for p in live]
+                _lib.adamw_step_multi(segs, **hp)
                 for p, (tokens, dout, scale, _) in by_token:
                     from . import ops
 
@@ -265,10 +281,7 @@ class MuonAdamW:
                     # made by the backward pass, perhaps on another stream than this step's,
                     # and dropped by zero_grad()
                     ops.record_use(tokens, dout)
-                # the group's tensors in one fused pass (one launch per 48 tensors)
-                segs = [(p.data, p.grad, self.state[id(p)]["exp_avg"],
-                         self.state[id(p)]["exp_avg_sq"]) for p in live]
-                _lib.adamw_step_multi(segs, **hp)
+                g["step"] += 1
                 continue
             # Muon: every bucket with gradients in one call
             stacks = [st for b in self._buckets[gi] for st in b.live_stacks()]

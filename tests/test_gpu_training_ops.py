@@ -473,3 +473,56 @@ def test_tokens_and_teacher_lists_of_any_strides():
     for stream in (None, torch.cuda.Stream()):
         for a, b in zip(run(tokens, teacher, ids, stream), want):
             assert torch.equal(a, b)
+
+
+def _two_groups(seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    gain, table = torch.randn(D, generator=g, device=DEV), torch.randn(V, D, generator=g, device=DEV)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [gain], "lr": 1e-2}, {"kind": "adamw", "params": [table], "lr": 1e-2}])
+    gain.grad = torch.randn(D, generator=g, device=DEV)
+    pairs = [(torch.randint(0, V, (9,), generator=g, device=DEV), torch.randn(9, D, generator=g, device=DEV))
+             for _ in range(2)]
+    for tokens, dout in pairs:
+        opt.add_token_gradient(table, tokens, dout)
+    return opt, gain, table, pairs
+
+
+def test_a_step_repeated_after_a_refusal_counts_everything_once(monkeypatch):
+    """A step that fails, while it checks or while it adds up, and is called again."""
+    from adamw_optimizer_step_muon_amd import ops
+
+    opt, gain, table, pairs = _two_groups(1)
+    want = _two_groups(1)
+    dense = torch.randn(D, V, device=DEV).t()
+    want[2].grad = dense.contiguous()
+    want[0].step()
+    table.grad = dense  # refused: not contiguous
+    kept = [t.clone() for t in (gain, table)]
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step()
+    assert torch.equal(gain, kept[0]) and torch.equal(table, kept[1])
+    assert [g["step"] for g in opt.param_groups] == [0, 0]
+    table.grad = dense.contiguous()
+    opt.step()
+    for a, b in zip((gain, table, table.grad), (want[1], want[2], want[2].grad)):
+        assert torch.equal(a, b)
+
+    # the second of two additions fails once
+    opt, gain, table, pairs = _two_groups(2)
+    backward, calls = ops.embedding_backward, []
+
+    def fails_once(*args, **kw):
+        calls.append(1)
+        if len(calls) == 2:
+            raise MemoryError
+        return backward(*args, **kw)
+
+    monkeypatch.setattr(ops, "embedding_backward", fails_once)
+    gain.grad = None
+    with pytest.raises(MemoryError):
+        opt.step()
+    opt.step()
+    monkeypatch.undo()
+    ref = backward(pairs[0][1], pairs[0][0], V)
+    backward(pairs[1][1], pairs[1][0], V, grad=ref, accumulate=True)
+    assert torch.equal(table.grad, ref) and opt.param_groups[1]["step"] == 1

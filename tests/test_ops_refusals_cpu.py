@@ -228,17 +228,6 @@ def test_token_gradients_are_checked_when_added():
     opt.step()  # nothing left to step
 
 
-def test_token_gradients_of_inference_mode():
-    """Its tensors have no version to check."""
-    table = torch.zeros(10, 4)
-    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table]}])
-    with torch.inference_mode():
-        tokens, dout = torch.zeros(5, dtype=torch.int64), torch.zeros(5, 4)
-    opt.add_token_gradient(table, tokens, dout)
-    with pytest.raises(ValueError, match="GPU"):  # and no complaint about versions
-        opt.step()
-
-
 def test_token_gradients_that_a_step_would_refuse_are_refused_when_added():
     table, empty = torch.zeros(10, 4), torch.zeros(0, 4)
     opt = ma.MuonAdamW([{"kind": "adamw", "params": [table, empty]}])
@@ -255,3 +244,27 @@ def test_token_gradients_that_a_step_would_refuse_are_refused_when_added():
         opt.add_token_gradient(empty, tokens, dout)
     opt.step()  # nothing was added
     assert opt.param_groups[0]["step"] == 0
+
+
+def test_a_step_that_refuses_a_token_gradient_changes_nothing():
+    first, table = torch.zeros(3), torch.zeros(10, 4)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [first]}, {"kind": "adamw", "params": [table]}])
+    tokens, dout = torch.zeros(5, dtype=torch.int64), torch.zeros(5, 4)
+    first.grad = torch.zeros(3)
+    opt.add_token_gradient(table, tokens, dout)
+    opt.add_token_gradient(table, tokens, dout.clone())
+    dout.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified"):
+        opt.step()
+    assert table.grad is None and [g["step"] for g in opt.param_groups] == [0, 0]
+
+
+def test_token_gradients_of_inference_mode():
+    """Its tensors have no version to check."""
+    table = torch.zeros(10, 4)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table]}])
+    with torch.inference_mode():
+        tokens, dout = torch.zeros(5, dtype=torch.int64), torch.zeros(5, 4)
+    opt.add_token_gradient(table, tokens, dout)
+    with pytest.raises(ValueError, match="GPU"):  # and no complaint about versions
+        opt.step()
