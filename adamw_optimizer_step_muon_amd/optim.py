@@ -51,6 +51,29 @@ def _version(t):
     return None if t.is_inference() else t._version
 
 
+def _stream_of(t):
+    """(the current stream of t's device, whether a graph is being captured on it)."""
+    import torch
+
+    if not t.is_cuda:
+        return None
+    with torch.cuda.device(t.device):
+        return torch.cuda.current_stream(), torch.cuda.is_current_stream_capturing()
+
+
+def _order_behind(made_on, t) -> None:
+    """The current stream waits for what a token gradient was made on, if that is another: a
+    backward pass runs on its forward pass's stream, and torch orders its caller's stream
+    behind the gradients that it sets itself.  Between a captured part and an eager one there is
+    nothing to record: captures begin on an idle device, and replays are the caller's to order."""
+    if made_on is None:  # no GPU tensors: refused by the call that follows
+        return
+    here, capturing = _stream_of(t)
+    stream, captured = made_on
+    if stream != here and captured == capturing:
+        here.wait_stream(stream)
+
+
 class _Bucket:
     """K same-shape Muon parameters stored as one (K, A, B) buffer."""
 
@@ -111,7 +134,7 @@ class MuonAdamW:
         self.state: Dict[int, Dict] = {}
         self._workspace = None
         self._buckets: Dict[int, List[_Bucket]] = {}
-        # id(parameter) -> [(tokens, dout, scale, versions)], see add_token_gradient
+        # id(parameter) -> [(tokens, dout, scale, versions, stream)], see add_token_gradient
         self._token_grads: Dict[int, List] = {}
         for g in param_groups:
             kind = g.get("kind", "muon")
@@ -199,7 +222,8 @@ class MuonAdamW:
         gradient is written or read).  Several additions, or one next to a dense
         ``param.grad``, are summed into ``param.grad`` at step() instead.  tokens (int32 or
         int64) and dout (tokens.shape + (dim,)) are kept, not copied, until zero_grad() and
-        must not be modified before step().  What reads ``param.grad`` between backward and
+        must not be modified before step(), which waits for the stream that is current here
+        where its own is another.  What reads ``param.grad`` between backward and
         step (clipping by a global norm, say) does not see this gradient; ``scale`` can
         carry a clipping factor."""
         import torch
@@ -219,7 +243,7 @@ class MuonAdamW:
 
         ops.layout("dout", dout)
         self._token_grads.setdefault(id(param), []).append(
-            (tokens, dout, scale, (_version(tokens), _version(dout))))
+            (tokens, dout, scale, (_version(tokens), _version(dout)), _stream_of(param)))
 
     def _check_token_gradients(self) -> None:
         """Raises what step() would find wrong with a token gradient, before it changes
@@ -228,7 +252,7 @@ class MuonAdamW:
             return
         for g in self.param_groups:
             for p in g["params"]:
-                for tokens, dout, _, versions in self._token_grads.get(id(p), ()):
+                for tokens, dout, _, versions, _ in self._token_grads.get(id(p), ()):
                     if (_version(tokens), _version(dout)) != versions:
                         raise RuntimeError("the tokens or output gradients of a token gradient "
                                            "were modified before step()")
@@ -245,7 +269,8 @@ class MuonAdamW:
         from . import ops
 
         while added:  # what p.grad holds is no longer in the list
-            tokens, dout, scale, _ = added[0]
+            tokens, dout, scale, _, made_on = added[0]
+            _order_behind(made_on, p)
             ops.record_use(tokens, dout)
             if p.grad is None:
                 p.grad = ops.embedding_backward(dout, tokens, p.shape[0], scale=scale)
@@ -273,13 +298,13 @@ class MuonAdamW:
                 segs = [(p.data, p.grad, self.state[id(p)]["exp_avg"],
                          self.state[id(p)]["exp_avg_sq"]) for p in live]
                 _lib.adamw_step_multi(segs, **hp)
-                for p, (tokens, dout, scale, _) in by_token:
+                for p, (tokens, dout, scale, _, made_on) in by_token:
                     from . import ops
 
+                    _order_behind(made_on, p)
                     ops.adamw_step_embedding(p.data, tokens, dout, self.state[id(p)]["exp_avg"],
                                              self.state[id(p)]["exp_avg_sq"], scale=scale, **hp)
-                    # made by the backward pass, perhaps on another stream than this step's,
-                    # and dropped by zero_grad()
+                    # perhaps another stream's memory, and dropped by zero_grad()
                     ops.record_use(tokens, dout)
                 g["step"] += 1
                 continue

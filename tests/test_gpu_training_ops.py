@@ -526,3 +526,78 @@ def test_a_step_repeated_after_a_refusal_counts_everything_once(monkeypatch):
     ref = backward(pairs[0][1], pairs[0][0], V)
     backward(pairs[1][1], pairs[1][0], V, grad=ref, accumulate=True)
     assert torch.equal(table.grad, ref) and opt.param_groups[1]["step"] == 1
+
+
+@pytest.mark.parametrize("additions", [1, 2])
+def test_a_step_waits_for_the_stream_that_made_a_token_gradient(additions):
+    """Output gradients that another stream is still computing when step() is called."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    rows, dim, n = 3000, 512, 2048
+    values, a = torch.randn(rows, dim, generator=g, device=DEV), torch.randn(n, dim, generator=g, device=DEV)
+    turn = torch.randn(dim, dim, generator=g, device=DEV) / dim ** 0.5
+    tokens = torch.randint(0, rows, (n,), generator=g, device=DEV)
+
+    def made():
+        x = a
+        for _ in range(200):
+            x = torch.tanh(x @ turn)
+        return x
+
+    def run(stream):
+        table = values.clone()
+        opt = ma.MuonAdamW([{"kind": "adamw", "params": [table], "lr": 1e-2}])
+        torch.cuda.synchronize()
+        for _ in range(additions):
+            with torch.cuda.stream(stream):
+                opt.add_token_gradient(table, tokens, made())
+        opt.step()
+        torch.cuda.synchronize()
+        return table
+
+    want = run(torch.cuda.current_stream())
+    assert torch.equal(run(torch.cuda.Stream()), want)
+
+
+def test_a_captured_step_on_tokens_replays():
+    """Forward, backward and step by token gradients in one graph, with the embedding's forward
+    pass (so its backward) on another stream of the capture; every replay against eager steps."""
+    p, batch = _leaves(_model(11)), _batch(11)
+    start = {k: t.detach().clone() for k, t in p.items()}
+    warm = _leaves(_model(11))
+    o = _optimizer(warm)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _loss(warm, _batch(11), o).backward()
+        o.step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    del warm, o
+    opt = _optimizer(p)
+    leaves = {k: p[k].data for k in p}
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            loss = _loss(p, batch, opt)
+        loss.backward()  # on the forward pass's stream; torch orders this one behind its gradients
+        opt.step()
+        del loss
+        here.wait_stream(other)
+    assert p["table"].grad is None
+    q = _leaves(_model(11))
+    eager = _optimizer(q)
+    for seed in (12, 13, 14):
+        for a, b in zip(batch, _batch(seed)):
+            a.copy_(b)
+        graph.replay()
+        for g in eager.param_groups:
+            g["step"] = 0  # the captured step's count
+        _loss(q, _batch(seed), eager).backward()
+        eager.step()
+        eager.zero_grad()
+        torch.cuda.synchronize()
+        for k in p:
+            assert torch.equal(leaves[k], q[k].data), k
+    assert not torch.equal(leaves["table"], start["table"])
