@@ -64,14 +64,22 @@ def _stream_of(t):
 def _order_behind(made_on, t) -> None:
     """The current stream waits for what a token gradient was made on, if that is another: a
     backward pass runs on its forward pass's stream, and torch orders its caller's stream
-    behind the gradients that it sets itself.  Between a captured part and an eager one there is
-    nothing to record: captures begin on an idle device, and replays are the caller's to order."""
+    behind the gradients that it sets itself.  Between a captured part and an eager one, or two
+    captures, there is nothing to record: captures begin on an idle device, and replays are the
+    caller's to order."""
+    import torch
+
     if made_on is None:  # no GPU tensors: refused by the call that follows
         return
     here, capturing = _stream_of(t)
     stream, captured = made_on
-    if stream != here and captured == capturing:
-        here.wait_stream(stream)
+    if stream == here or captured != capturing:
+        return
+    if captured:
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                return
+    here.wait_stream(stream)
 
 
 class _Bucket:

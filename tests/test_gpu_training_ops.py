@@ -601,3 +601,25 @@ def test_a_captured_step_on_tokens_replays():
         for k in p:
             assert torch.equal(leaves[k], q[k].data), k
     assert not torch.equal(leaves["table"], start["table"])
+
+
+def test_a_backward_pass_and_a_step_captured_apart():
+    """Output gradients made in one graph and stepped by another, on their own streams; the
+    replays follow each other on one stream."""
+    table = torch.randn(V, D, device=DEV)
+    tokens, a = torch.randint(0, V, (30,), device=DEV), torch.randn(30, D, device=DEV)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table], "lr": 1e-2}])
+    torch.cuda.synchronize()
+    first, second = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(first, stream=torch.cuda.Stream()):
+        opt.add_token_gradient(table, tokens, torch.tanh(a))
+    with torch.cuda.graph(second, stream=torch.cuda.Stream()):
+        opt.step()
+    q = [table.clone(), torch.zeros_like(table), torch.zeros_like(table)]
+    for _ in range(3):
+        a.add_(0.5)
+        first.replay()
+        second.replay()
+        ma.adamw_step_embedding(q[0], tokens, torch.tanh(a), q[1], q[2], step=1, lr=1e-2)
+        torch.cuda.synchronize()
+        assert torch.equal(table, q[0])
