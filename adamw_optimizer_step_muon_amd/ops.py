@@ -473,6 +473,7 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps=eps)
         ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.shapes = [t if t is None else t.shape for t in (weight, bias)]
         return y
 
     @staticmethod
@@ -482,6 +483,7 @@ class _LayerNorm(torch.autograd.Function):
         dx, dw, db = layer_norm_backward(_rowed(dy), x, mean, rstd, weight,
                                          weight_grad=ctx.needs_input_grad[1],
                                          bias_grad=ctx.needs_input_grad[2])
+        dw, db = (t if t is None else t.view(shape) for t, shape in zip((dw, db), ctx.shapes))
         return dx, dw, db, None
 
 

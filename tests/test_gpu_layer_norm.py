@@ -162,3 +162,15 @@ def test_offsets_past_32_bits():
     for a, b, t in ((dw, dws, dy[-4:].float() * (x[-4:].float() - ms[:, None]) * rs[:, None]),
                     (db, dbs, dy[-4:].float())):
         assert ((a - b).abs() <= 8 * E * t.abs().sum(0)).all()
+
+
+def test_gradients_have_the_gains_own_shapes():
+    """Gains kept as rows (their values count, not their shape) get gradients of that shape."""
+    x = torch.randn(7, 48, device=DEV)
+    w, b = torch.randn(1, 48, device=DEV, requires_grad=True), torch.randn(1, 1, 48, device=DEV, requires_grad=True)
+    v, c = (t.detach().flatten().requires_grad_(True) for t in (w, b))
+    dy = torch.randn(7, 48, device=DEV)
+    ma.layer_norm(x, w, b).backward(dy)
+    ma.layer_norm(x, v, c).backward(dy)
+    assert w.grad.shape == w.shape and b.grad.shape == b.shape
+    assert torch.equal(w.grad.flatten(), v.grad) and torch.equal(b.grad.flatten(), c.grad)
