@@ -268,3 +268,17 @@ def test_token_gradients_of_inference_mode():
     opt.add_token_gradient(table, tokens, dout)
     with pytest.raises(ValueError, match="GPU"):  # and no complaint about versions
         opt.step()
+
+
+def test_star_import_with_and_without_torch():
+    """Without torch there are the names that need none; with it the operators too."""
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(_lib.__file__)))
+    hide = ("import sys, importlib.util as u; find = u.find_spec; "
+            "u.find_spec = lambda name, *a: None if name == 'torch' else find(name, *a); sys.modules['torch'] = None; ")
+    check = "from adamw_optimizer_step_muon_amd import *; print('muon_step' in dir(), 'layer_norm' in dir())"
+    for code, want in ((hide + check, "True False"), (check, "True True")):
+        out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+        assert out.stdout.strip() == want, out.stderr
