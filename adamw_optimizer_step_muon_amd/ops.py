@@ -221,6 +221,7 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     if out is None:
         out, stride = _empty(table, shape, out_dtype or torch.float32, stream), dim
     else:
+        _tensor("out", out, device)
         if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be {tuple(shape)} of {out_dtype or out.dtype}")
         _, _, stride = _rows("out", out, device)
@@ -233,11 +234,11 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     return out
 
 
-def _token_rows(tokens, dout, dim, device):
-    bits = _ints("tokens", tokens, device)
+def _token_rows(tokens, dout, dim=None, device=None):
     n, cols, stride = _rows("dout", dout, device)
-    if cols != dim or n != tokens.numel():
-        raise ValueError(f"dout {tuple(dout.shape)} does not match {tokens.numel()} tokens of {dim}")
+    bits = _ints("tokens", tokens, dout.device)
+    if (dim is not None and cols != dim) or n != tokens.numel():
+        raise ValueError(f"dout {tuple(dout.shape)} does not match {tokens.numel()} tokens of {dim or cols}")
     return bits, n, stride, _type("dout", dout.dtype)
 
 
@@ -247,8 +248,8 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
     (dim,), into `grad` (allocated when None) or, with accumulate, added to it."""
     if accumulate and grad is None:
         raise ValueError("accumulate needs a grad to add to")
+    bits, n, stride, dtype = _token_rows(tokens, dout)
     rows, dim, device = int(rows), dout.shape[-1], dout.device
-    bits, n, stride, dtype = _token_rows(tokens, dout, dim, device)
     given = grad
     if grad is None:
         grad = _empty(dout, (rows, dim), torch.float32, stream)
@@ -306,6 +307,7 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5, out=None
     if out is None:
         out, out_stride = _like(x, stream), max(dim, 1)
     else:
+        _tensor("out", out, device)
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have x's shape and type")
         _, _, out_stride = _rows("out", out, device)
@@ -378,6 +380,7 @@ def _dlogits(logits, dlogits, stream):
     """(dlogits, row stride)"""
     if dlogits is None:
         return _like(logits, stream), logits.shape[-1]
+    _tensor("dlogits", dlogits, logits.device)
     if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
         raise ValueError("dlogits must have the logits' shape and type")
     return dlogits, _rows("dlogits", dlogits, logits.device)[2]

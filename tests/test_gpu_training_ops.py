@@ -623,3 +623,14 @@ def test_a_backward_pass_and_a_step_captured_apart():
         ma.adamw_step_embedding(q[0], tokens, torch.tanh(a), q[1], q[2], step=1, lr=1e-2)
         torch.cuda.synchronize()
         assert torch.equal(table, q[0])
+
+
+def test_binding_refuses_outputs_that_are_no_tensors():
+    x, i = torch.zeros(6, 8, device=DEV), torch.zeros(6, dtype=torch.int64, device=DEV)
+    f, a = torch.zeros(6, device=DEV), torch.zeros(6, 1, device=DEV)
+    for call in (lambda: ma.embedding_forward(x, i, out=[1.0]), lambda: ma.layer_norm_forward(x, out=3),
+                 lambda: ma.distill_loss_grad(x, a, i[:, None], f, dlogits="x")):
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            call()
+    with pytest.raises(ValueError, match="dimension"):
+        ma.embedding_backward(f[0], i[0], 10)

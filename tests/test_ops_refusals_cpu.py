@@ -282,3 +282,10 @@ def test_star_import_with_and_without_torch():
     for code, want in ((hide + check, "True False"), (check, "True True")):
         out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
         assert out.stdout.strip() == want, out.stderr
+
+
+def test_binding_refuses_what_is_no_tensor():
+    i = torch.zeros(4, dtype=torch.int64)
+    for bad in (None, [1.0], 3):
+        with pytest.raises(TypeError, match="dout"):
+            ma.embedding_backward(bad, i, 10)
