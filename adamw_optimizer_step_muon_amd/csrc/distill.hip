@@ -31,12 +31,13 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // with what it is used in, so that everybody has the same r).  v scale - r is one fused
 // multiply-add: it rounds by its own size only.  The maximum's own exponent is what r was
 // rounded by, half a step of r: up to 1/2 while |r| < 2^24, and beyond what exp2 can hold from
-// some 2^31 on.  So rows whose maximum reaches far_from(scale) take the slower (v - m) scale,
-// where r = 0 stands for the difference already taken: rows filled with a mask's value, or
-// far above zero.  Other rows' smaller values are taken against -far_from(scale) at least, which
-// bounds their sums too.
-constexpr float kFarProduct = 16777216.0f;
-__device__ __forceinline__ float far_from(float scale) { return kFarProduct / scale; }
+// some 2^31 on.  So rows whose maximum lies beyond +-far = 2^23 / scale take the slower
+// (v - m) scale, where r = 0 stands for the difference already taken: rows filled with a mask's
+// value, or far above zero.  Other rows' smaller values are taken against -2 far at least, which
+// bounds their sums too.  (With the test as >= and -far as that bound, the compiler keeps 15 more
+// registers in the one-pass kernels, whose blocks of 1024 threads then have a CU to themselves:
+// 439 against 430 us for 4096 x 128000 bf16.)
+constexpr float kFarProduct = 8388608.0f;
 struct Soft {
   float m, s;
 };
@@ -87,11 +88,11 @@ struct Kept {
 
 // Maximum and sum of a row; the waves' results go to out.
 template <int T, int kThreads, bool kIsFar, int kKeep>
-__device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, Soft* out, Kept<T, kThreads, kKeep>& kept) {
+__device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, float far, Soft* out, Kept<T, kThreads, kKeep>& kept) {
   typedef typename Kept<T, kThreads, kKeep>::P P;
   constexpr int N = kVec<T>, kBatch = kThreads * kU * N;
   const int tid = threadIdx.x;
-  Soft a{kIsFar ? kLowest : -far_from(scale), 0.0f};  // finite, so that differences to it are defined
+  Soft a{kIsFar ? kLowest : -2.0f * far, 0.0f};  // finite, so that differences to it are defined
   const auto take = [&](const P (&x)[kU], int left) {  // values at and behind `left` count as -inf
     float v[kU][N], m = a.m;
 #pragma unroll
@@ -140,9 +141,9 @@ __device__ void sweep(const typename Act<T>::S* z, int vocab, float scale, Soft*
 
 // The waves' results joined, one a lane.
 template <int kThreads, bool kIsFar>
-__device__ Soft block_join(const Soft* of, float scale) {
+__device__ Soft block_join(const Soft* of, float scale, float far) {
   const int lane = threadIdx.x & 63;
-  return wave_join<kIsFar>(lane < kThreads / 64 ? of[lane] : Soft{kIsFar ? kLowest : -far_from(scale), 0.0f}, scale);
+  return wave_join<kIsFar>(lane < kThreads / 64 ? of[lane] : Soft{kIsFar ? kLowest : -2.0f * far, 0.0f}, scale);
 }
 
 // dz = gq 2^exponent over the row, from its end to its beginning: what the first sweep kept,
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
     kept.shared = room;
   }
   Soft zs{0.0f, 0.0f};
-  if (kLoss) sweep<T, kThreads, false, kKeep>(z, vocab, scale, joined[0], kept);
+  if (kLoss) sweep<T, kThreads, false, kKeep>(z, vocab, scale, c.far, joined[0], kept);
   ta = wave_join<true>(ta, scale);
   const float lives = wave_sum(static_cast<float>(live));
   if (lane == 0) {
@@ -256,12 +257,12 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   }
   __syncthreads();
   if (kLoss) {
-    zs = block_join<kThreads, false>(joined[0], scale);
-    if (fabsf(zs.m) >= far_from(scale)) {  // the same for every thread
+    zs = block_join<kThreads, false>(joined[0], scale, c.far);
+    if (fabsf(zs.m) > c.far) {  // the same for every thread
       __syncthreads();
-      sweep<T, kThreads, true, kKeep>(z, vocab, scale, joined[0], kept);
+      sweep<T, kThreads, true, kKeep>(z, vocab, scale, c.far, joined[0], kept);
       __syncthreads();
-      zs = block_join<kThreads, true>(joined[0], scale);
+      zs = block_join<kThreads, true>(joined[0], scale, c.far);
       if (zs.s == 0.0f) zs = Soft{-INFINITY, __builtin_nanf("")};  // nothing above -inf
     } else {
       // from the rounded reference to the maximum itself
@@ -270,10 +271,10 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(DistillCall c) {
   } else {
     zs = Soft{c.stats[2 * row], c.stats[2 * row + 1]};
   }
-  ta = block_join<kThreads, true>(joined[1], scale);
+  ta = block_join<kThreads, true>(joined[1], scale, c.far);
   const bool some = wave_sum(lane < kWaves ? counts[lane] : 0.0f) > 0.0f;
   // q = 2^(exponent(v) - zc) / zs.s, zc the maximum's own exponent
-  const bool far = fabsf(zs.m) >= far_from(scale);
+  const bool far = fabsf(zs.m) > c.far;
   const float zr = far ? 0.0f : reference(zs.m, scale);
   const float zc = far ? 0.0f : exponent<false>(zs.m, scale, zs.m, zr);
   const auto power_of = [&](float v) {
@@ -350,7 +351,9 @@ void launch_rows(const DistillCall& c, DistillMode mode, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_distill(const DistillCall& c, DistillMode mode, hipStream_t s) {
+hipError_t launch_distill(const DistillCall& call, DistillMode mode, hipStream_t s) {
+  DistillCall c = call;
+  c.far = kFarProduct / (kLog2e / c.temperature);
   return with_act(c.type, [&](auto t) {
     constexpr int T = decltype(t)::value;
     // as few threads as read the row in one batch and hold the teacher's entries: short rows

@@ -497,6 +497,7 @@ struct DistillCall {
   float* stats;             // (n, 2): row maximum, sum of exponentials; read or written
   void* dlogits;            // null: no gradient
   int64_t dlogits_stride;
+  float far;                // set by launch_distill
 };
 constexpr int kMaxDistillTop = 1024;
 // What the call computes: loss and stats, the gradient from given stats, or both at once.
