@@ -118,14 +118,11 @@ def _type(name, dtype) -> int:
     return code
 
 
-def _rows(name, t, device=None):
-    """(rows, columns, row stride in values) of an activation tensor (..., columns)."""
-    _tensor(name, t, device)
-    return layout(name, t)
-
-
-def layout(name, t):
-    """_rows' result, wherever the tensor lives."""
+def _rows(name, t, device=None, anywhere=False):
+    """(rows, columns, row stride in values) of an activation tensor (..., columns), on the GPU
+    or anywhere."""
+    if not anywhere:
+        _tensor(name, t, device)
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     dim = t.shape[-1]
@@ -153,9 +150,7 @@ def _ints(name, t, device=None) -> int:
 
 
 def _contiguous(t, stream):
-    """t itself, or a copy made on the call's stream (for the duration of the call)."""
-    if t.is_contiguous():
-        return t
+    """t, copied on the call's stream where it is not contiguous (to be kept for the call)."""
     with torch.cuda.stream(stream):
         return t.contiguous()
 
@@ -217,7 +212,8 @@ def embedding_forward(table, tokens, *, scale: float = 1.0, out=None, out_dtype=
     rows, dim = _table("table", table)
     device = table.device
     bits = _ints("tokens", tokens, device)
-    shape, given, at = tokens.shape + (dim,), out, _contiguous(tokens, stream)
+    shape, given = tokens.shape + (dim,), out
+    at = tokens if tokens.is_contiguous() else _contiguous(tokens, stream)
     if out is None:
         out, stride = _empty(table, shape, out_dtype or torch.float32, stream), dim
     else:
@@ -257,7 +253,7 @@ def embedding_backward(dout, tokens, rows: int, *, scale: float = 1.0, grad=None
         raise ValueError(f"grad must be ({rows}, {dim})")
     need = embedding_workspace_bytes(rows, dim, n)
     _keep, ws, size = _workspace(workspace, need, dout, stream)
-    at = _contiguous(tokens, stream)
+    at = tokens if tokens.is_contiguous() else _contiguous(tokens, stream)
     _call("ma_embedding_backward", device, stream, at.data_ptr(), bits, n, dout.data_ptr(),
           dtype, stride, scale, grad.data_ptr(), rows, dim, int(bool(accumulate)), ws, size)
     if given is not None:
@@ -284,11 +280,11 @@ def adamw_step_embedding(param, tokens, dout, exp_avg, exp_avg_sq, *, scale: flo
                        int(bool(cautious_wd)))
     need = embedding_workspace_bytes(rows, dim, n)
     _keep, ws, size = _workspace(workspace, need, param, stream)
-    at = _contiguous(tokens, stream)
+    at = tokens if tokens.is_contiguous() else _contiguous(tokens, stream)
     _call("ma_adamw_step_embedding", device, stream, param.data_ptr(), exp_avg.data_ptr(),
           exp_avg_sq.data_ptr(), rows, dim, at.data_ptr(), bits, n, dout.data_ptr(), dtype,
           stride, scale, ctypes.byref(hp), ws, size)
-    _wrote(param, exp_avg, exp_avg_sq)
+    increment_version((param, exp_avg, exp_avg_sq))
     if stream is not None:
         _record(stream, param, exp_avg, exp_avg_sq, tokens, dout, _keep)
 

@@ -249,7 +249,7 @@ class MuonAdamW:
             raise ValueError("scale must be finite in fp32")
         from . import ops
 
-        ops.layout("dout", dout)
+        ops._rows("dout", dout, anywhere=True)  # raises where they have no common stride
         self._token_grads.setdefault(id(param), []).append(
             (tokens, dout, scale, (_version(tokens), _version(dout)), _stream_of(param)))
 
