@@ -647,7 +647,8 @@ __device__ __forceinline__ bool among(const Few& s, uint32_t end, uint32_t v) {
   return any;
 }
 // scale times the sum over the found tokens of row v, of which entry i is the first or one
-// before it, in the order (and so with the bits) of row_gradient.
+// before it, in the tokens' order.  A gradient and a step of so few tokens both sum here, so
+// they agree bit for bit; row_gradient's order is the same for rows of at most a chunk's tokens.
 template <int T>
 __device__ __forceinline__ void few_gradient(const RowArgs& a, const Few& s, uint32_t i, uint32_t found, uint32_t v,
                                              int64_t c, int cnt, float (&g)[kNarrow]) {

@@ -366,7 +366,7 @@ __global__ __launch_bounds__(kThreads) void norm_dx_kernel(NormGradCall c) {
   }
 }
 
-// Rows of one group of the reduction over rows.
+// Groups of rows, at most, of the reduction over rows.
 constexpr int64_t kMaxGroups = 256;
 
 // Block (columns, group): partial sums of dy h and dy over the group's rows.

@@ -31,39 +31,27 @@ struct Act<kActBF16> {
   static __device__ __forceinline__ S down(float v) { return f2bf(v); }
 };
 
-// N consecutive values.  The vector type is aligned like one value only: rows of odd length
+// N consecutive values (two at least).  The vector type is aligned like one value only: rows of odd length
 // or stride start anywhere, and global memory takes wide accesses at any element's address,
 // so one kernel serves every layout (measured where it matters, at the kernels).
 template <typename S, int N>
 struct Pack {
   typedef S type __attribute__((ext_vector_type(N), aligned(sizeof(S))));
 };
-template <typename S>
-struct Pack<S, 1> {
-  typedef S type;
-};
 
 template <int T, int N>
 __device__ __forceinline__ void load_act(const typename Act<T>::S* p, float (&v)[N]) {
   typedef typename Pack<typename Act<T>::S, N>::type P;
   const P x = *reinterpret_cast<const P*>(p);
-  if constexpr (N == 1) {
-    v[0] = Act<T>::up(x);
-  } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = Act<T>::up(x[e]);
-  }
+  for (int e = 0; e < N; ++e) v[e] = Act<T>::up(x[e]);
 }
 template <int T, int N>
 __device__ __forceinline__ void store_act(typename Act<T>::S* p, const float (&v)[N]) {
   typedef typename Pack<typename Act<T>::S, N>::type P;
   P x;
-  if constexpr (N == 1) {
-    x = Act<T>::down(v[0]);
-  } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = Act<T>::down(v[e]);
-  }
+  for (int e = 0; e < N; ++e) x[e] = Act<T>::down(v[e]);
   *reinterpret_cast<P*>(p) = x;
 }
 // The first n of N values (n in 1..N); the others read as `fill`.

@@ -433,7 +433,7 @@ struct RowArgs {
   uint32_t rows;
   float scale;
 };
-// One table gradient's inputs (n >= 1, rows >= 1, dim >= 1).
+// One table gradient's inputs (rows >= 1, dim >= 1; n = 0: tokens and dout may be null).
 struct EmbeddingCall {
   const void* tokens;
   int token_bits;
