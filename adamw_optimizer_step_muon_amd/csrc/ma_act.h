@@ -31,9 +31,9 @@ struct Act<kActBF16> {
   static __device__ __forceinline__ S down(float v) { return f2bf(v); }
 };
 
-// N consecutive values (two at least).  The vector type is aligned like one value only: rows of odd length
-// or stride start anywhere, and global memory takes wide accesses at any element's address,
-// so one kernel serves every layout (measured where it matters, at the kernels).
+// N consecutive values (two at least).  The vector type is aligned like one value only: rows of
+// odd length or stride start anywhere, and global memory takes wide accesses at any element's
+// address, so one kernel serves every layout (measured where it matters, at the kernels).
 template <typename S, int N>
 struct Pack {
   typedef S type __attribute__((ext_vector_type(N), aligned(sizeof(S))));

@@ -509,7 +509,8 @@ def embedding(tokens, table, *, scale: float = 1.0, out_dtype=None, optimizer=No
     """scale * table[tokens], differentiable by the fp32 table; a token outside the table is
     padding (zero row, no gradient).  With `optimizer` (the MuonAdamW that holds the table in
     an "adamw" group) the backward pass sets no table.grad: it hands the tokens and output
-    gradients to optimizer.add_token_gradient, and the next step() applies them."""
+    gradients to optimizer.add_token_gradient, and the next step() applies them (not for loops
+    that clip or unscale gradients in between: see there)."""
     if optimizer is not None:
         optimizer.check_token_parameter(table)
     return _Embedding.apply(tokens, table, float(scale), out_dtype, optimizer)

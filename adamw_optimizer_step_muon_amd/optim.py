@@ -231,9 +231,11 @@ class MuonAdamW:
         ``param.grad``, are summed into ``param.grad`` at step() instead.  tokens (int32 or
         int64) and dout (tokens.shape + (dim,)) are kept, not copied, until zero_grad() and
         must not be modified before step(), which waits for the stream that is current here
-        where its own is another.  What reads ``param.grad`` between backward and
-        step (clipping by a global norm, say) does not see this gradient; ``scale`` can
-        carry a clipping factor."""
+        where its own is another.  What reads or changes ``param.grad`` between
+        backward and step (clipping by a global norm, a loss scaler's unscaling) does not
+        reach this gradient, and the ``scale`` that ``embedding`` hands over is that of its
+        forward pass: a training loop that needs either leaves ``optimizer`` out there, or
+        calls this once the factor is known, with a ``scale`` that holds it."""
         import torch
 
         self.check_token_parameter(param)

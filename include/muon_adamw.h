@@ -466,9 +466,11 @@ ma_status ma_layer_norm_backward(const void* dy, int64_t dy_stride, const void* 
  *   loss = tau^2 sum p (log p - log q)          (Kullback-Leibler divergence)
  * A row without a live entry has loss 0.  Repeated ids add up in q's target.  top = 1 is the
  * cross entropy of a label (tau = 1).  0 <= top <= 1024, vocab <= 2^30, n < 2^22.
- * A NaN among the teacher's logits with a valid id makes its row's loss NaN.
- * A student logit of -inf has q = 0 (loss inf where p > 0); a row of NaN, of +inf or of -inf
- * alone has loss NaN.
+ * A NaN or +inf among the teacher's logits with a valid id makes its row's loss NaN, and the
+ * row's gradient at the live ids.
+ * A student logit of -inf has q = 0 (loss inf where p > 0); a row with a NaN or +inf, or of -inf
+ * alone, has loss NaN where it has a live entry.  Finite logits of any size have a finite loss and gradient (the type's
+ * lowest value as a mask included), as far as the results fit their types.
  * loss: n fp32.  stats: (n, 2) fp32, max z and sum exp((z - max z) / tau) of each row, for
  * the backward call. */
 ma_status ma_distill_forward(const void* logits, int32_t type, int64_t stride, int64_t n, int64_t vocab,

@@ -295,3 +295,22 @@ def test_rows_filled_with_a_masks_value(vocab, dtype, tau, fills):
     assert (_np(stats)[:, 0] == Z.max(1)).all()
     _check(grad, rz, bz, dtype)
     assert torch.equal(ma.distill_backward(z, a, ids, stats, w, temperature=tau), grad)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_teachers_without_a_softmax(bad):
+    """A teacher's NaN or +inf: its row's loss, and its gradient at the live ids, are NaN, the
+    other rows what they are without it."""
+    z, a, ids, w = _inputs(6, 900, 4, torch.float32, 3)
+    ids = ids.long()
+    want, dz = ma.distill_loss_grad(z, a, ids, w)
+    a[5, 2] = bad
+    ids[5] = torch.tensor([7, 8, 9, -1], device=DEV)
+    loss, grad = ma.distill_loss_grad(z, a, ids, w)
+    assert torch.isnan(loss[5]) and torch.isnan(grad[5, 7:10]).all()
+    assert torch.equal(loss[:5], want[:5]) and torch.equal(grad[:5], dz[:5])
+    # a row without a live entry has no loss, whatever it holds
+    z[1, 3], z[5, 5] = float("nan"), float("inf")
+    a[5, 2] = 0.0
+    loss, _ = ma.distill_forward(z, a, ids)
+    assert loss[1] == 0 and torch.isnan(loss[5])
