@@ -171,7 +171,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
 // block b takes the rows with b in their low bits.  Every block reads all tokens (from the
 // L2), keeps its own in their order, sorts those by the other bits within its shared memory,
 // and knows its first place from the number of tokens of the blocks before it.  8191 tokens
-// take 11 us here and 25 us in the four launches of two counted passes, 16384 tokens 21 and 25 us.
+// take 9.7 us here and 23 us in the four kernels of two counted passes, 16384 tokens 18 and 27 us.
 struct OneLaunch {
   uint32_t keys[kOneLaunch];      // of all tokens
   uint16_t order[2][kOneLaunch];  // of the block's own
@@ -575,7 +575,7 @@ __global__ __launch_bounds__(kTileThreads) void grad_tiles_kernel(RowArgs a, flo
 }
 
 // The AdamW update of every row; 24 bytes of state per value and the output rows of the tokens.
-// 65536 x 1280 with 16384 tokens: 327 us of the call's 339 (6.3 TB/s; the AdamW kernel on a
+// 65536 x 1280 with 16384 tokens: 328 us of the call's 344 (6.2 TB/s; the AdamW kernel on a
 // given gradient runs at 5.7).  The state's loads are issued before the row is looked up
 // (359 us behind it); without the streaming accesses the call takes 386 us.
 template <int T, int kMode>
