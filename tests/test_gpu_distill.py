@@ -259,7 +259,9 @@ FILLS = [s * c for c in (1e7, 1e9, 5e9, 1e10, 1e12, 1e15, 1e20, 1e30) for s in (
 @pytest.mark.parametrize("dtype,tau,fills", [
     (torch.float32, 1e-3, FILLS), (torch.float32, 0.05, FILLS), (torch.float32, 1.0, FILLS), (torch.float32, 4.0, FILLS),
     (torch.bfloat16, 0.05, FILLS), (torch.bfloat16, 1.0, FILLS),
-    (torch.float16, 1e-6, [6e4, -6e4, 3e3, -3e3]), (torch.float16, 1e-2, [6e4, -6e4])])
+    (torch.float16, 1e-6, [6e4, -6e4, 3e3, -3e3]), (torch.float16, 1e-2, [6e4, -6e4]),
+    # on both sides of 2^23 / log2(e), where the form changes, and of twice that
+    (torch.float32, 1.0, [s * c for c in (5.5e6, 5814539.0, 5814540.0, 6e6, 1.16e7, 1.17e7) for s in (1.0, -1.0)])])
 def test_rows_filled_with_a_masks_value(vocab, dtype, tau, fills):
     """Finite fills of any size give what their differences give (the bounds at the head of this
     file): whole rows of one value, rows of which only some entries are left (so that whole
