@@ -151,6 +151,8 @@ def _ints(name, t, device=None) -> int:
 
 def _contiguous(t, stream):
     """t, copied on the call's stream where it is not contiguous (to be kept for the call)."""
+    if t.is_contiguous():
+        return t
     with torch.cuda.stream(stream):
         return t.contiguous()
 
