@@ -1,0 +1,439 @@
+"""Operators of a memory-lean training step around the AdamW parameters, as cases to be timed and compared.
+
+The LM head with its cross entropy, in pieces of the vocabulary and without keeping the logits; the
+AdamW step over many tensors with both moments in 8 bits, which also leaves the 16-bit copy that the
+head reads; and the norms after and before a block in one pass with its gate and residual scale.
+``run`` computes a case in elementary torch operations in 32 bits, or, where ``own`` is true, by the
+library's entry points.  Sizes follow workloads/configs.py: vocabularies of 65536 and 128000, the
+512 x 64 table and hidden sizes of 768, 1280, 2048 and 8192.
+"""
+import math
+
+import torch
+
+own = False
+
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+BYTES = {"fp32": 4, "fp16": 2, "bf16": 2}
+ADAMW = dict(lr=3e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
+STEP, SEED = 10, 20
+BLOCK = 64  # elements of a moment that share a scale
+NORM_EPS = 1e-5
+
+
+def listed():
+    return [
+        # scoring a handful of continuations with the 12-layer model: the head is read once
+        dict(name="head_loss_8_rows", op="head_loss", n=8, vocab=65536, dim=768, type="bf16", ignored=0),
+        # evaluation of the 20-layer model on a ragged batch, a third of it padding
+        dict(name="head_loss_4095_rows", op="head_loss", n=4095, vocab=65536, dim=1280, type="fp16", ignored=3),
+        # a small batch in full precision, as in a check of a training run
+        dict(name="head_step_511_rows_fp32", op="head_step", n=511, vocab=65536, dim=768, type="fp32", ignored=31),
+        # the backward pass of an autograd graph, a micro-batch of the 20-layer model
+        dict(name="head_grad_2048_rows", op="head_grad", n=2048, vocab=65536, dim=1280, type="bf16", ignored=31),
+        # loss and gradients of a micro-batch of the 24-layer model in one call
+        dict(name="head_step_8192_rows", op="head_step", n=8192, vocab=128000, dim=2048, type="bf16", ignored=31),
+        # the smallest table of the workloads with a few gains: latency only
+        dict(name="adamw8_tiny", op="adamw8", tables=1, rows=512, dim=64, vectors=4, type="fp32", copy=False),
+        # the AdamW group of the 20-layer model: table, head and gains, gradients in full precision
+        dict(name="adamw8_two_tables", op="adamw8", tables=2, rows=65536, dim=1280, vectors=40, type="fp32", copy=False),
+        # the head of the 24-layer model from a 16-bit gradient, leaving its 16-bit copy
+        dict(name="adamw8_head_bf16", op="adamw8", tables=1, rows=128000, dim=2048, vectors=1, type="bf16", copy=True),
+        # one decode step of eight sequences between two blocks: latency only
+        dict(name="residual_norm_8_rows", op="residual", n=8, dim=768, type="bf16", post=True, gate=True, gain=True, center=False),
+        # a training micro-batch of the 24-layer model between two blocks
+        dict(name="residual_norm_32k_rows", op="residual", n=32768, dim=2048, type="bf16", post=True, gate=True, gain=True, center=True),
+        # a short ragged batch of the 20-layer model in full precision, without a norm after the block
+        dict(name="residual_norm_grad_1023_rows", op="residual_grad", n=1023, dim=1280, type="fp32", post=False, gate=True, gain=True, center=True),
+        # a training micro-batch of the widest model
+        dict(name="residual_norm_grad_16k_rows", op="residual_grad", n=16384, dim=8192, type="bf16", post=True, gate=True, gain=True, center=False),
+    ]
+
+
+def _spread(rng, low, high):
+    return int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))
+
+
+def draw(rng):
+    op = rng.choice(["head_loss", "head_grad", "head_step", "head_step", "adamw8", "adamw8", "residual", "residual_grad"])
+    kind = rng.choice(["fp32", "fp16", "bf16", "bf16"])
+    if op.startswith("head"):
+        dim = _spread(rng, 33, 4096)
+        dim = dim if rng.random() < 0.3 else (dim + 7) // 8 * 8
+        vocab = _spread(rng, 500, 131072)
+        # full precision costs some ten times as much as 16 bits: fewer rows
+        most = (2 ** 40 if kind != "fp32" else 2 ** 36) // (dim * vocab)
+        return dict(op=op, n=_spread(rng, 1, max(2, min(16384, most))), vocab=vocab, dim=dim, type=kind,
+                    ignored=rng.choice([0, 2, 5, 31]))
+    dim = _spread(rng, 33, 8192 if op == "adamw8" else 16384)
+    dim = dim if rng.random() < 0.3 else (dim + 7) // 8 * 8
+    if op == "adamw8":
+        return dict(op=op, tables=rng.randint(0, 3), rows=_spread(rng, 500, max(501, min(131072, 2 ** 26 // dim))), dim=dim,
+                    vectors=_spread(rng, 1, 100), type=kind, copy=rng.random() < 0.5)
+    return dict(op=op, n=_spread(rng, 1, min(65536, 65536 * 1024 // dim)), dim=dim, type=kind, post=rng.random() < 0.6,
+                gate=rng.random() < 0.7, gain=rng.random() < 0.7, center=rng.random() < 0.5)
+
+
+def _normal(g, *shape, scale=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _power(exponent):
+    """2 ** exponent in 32 bits, exactly, for whole exponents of -126 to 127."""
+    return ((exponent.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _exponent(x):
+    """floor(log2 x) of positive x, exactly."""
+    return torch.frexp(x).exponent - 1
+
+
+def _moment(x, dtype, top):
+    """A moment (blocks, BLOCK) as a program holds it: 8-bit values and a power of two per block."""
+    e = (_exponent(x.abs().amax(1)) - top).clamp_(-126, 127)
+    return (x / _power(e)[:, None]).to(dtype).view(-1), (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(int(seed))
+    op, dtype = case["op"], TYPES[case["type"]]
+    s = {"case": case}
+    if op.startswith("head"):
+        n, vocab, dim = case["n"], case["vocab"], case["dim"]
+        s["weight"] = _normal(g, vocab, dim, scale=0.05, dtype=dtype)
+        s["labels"] = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+        # some labels are likely, some not: up to 12 on top of a logit of about its neighbours' size
+        sure = torch.rand(n, 1, generator=g, device="cuda") * 12.0
+        hidden = _normal(g, n, dim, scale=1.5 / math.sqrt(dim) / 0.05)
+        hidden += sure / (dim * 0.05 ** 2) * s["weight"][s["labels"]].float()
+        s["hidden"] = hidden.to(dtype)
+        if case["ignored"]:
+            # positions without a target: a prompt, padding, the last of a sequence
+            s["labels"][case["ignored"] // 2::case["ignored"]] = -100
+        # the mean over the rows; with the usual loss scale where fp16 would lose small gradients
+        s["row_weight"] = torch.full((n,), 65536.0 / max(n, 4096) if case["type"] == "fp16" else 1.0 / n, device="cuda")
+        if op == "head_grad":
+            s["lse"] = _head(s)[1]
+    elif op == "adamw8":
+        sizes = [case["rows"] * case["dim"]] * case["tables"] + [case["dim"]] * case["vectors"]
+        starts, total = [], 0
+        for size in sizes:
+            starts.append(total)
+            total += -(-size // BLOCK) * BLOCK
+        # one buffer each, the tensors' parts of it starting at a block
+        s["param"] = _normal(g, total, scale=0.02)
+        # gradients of rows differ by orders of magnitude, as those of rare and frequent tokens do
+        size = torch.exp(2.0 * _normal(g, total // BLOCK, 1)) * 1e-3
+        s["grad"] = (_normal(g, total // BLOCK, BLOCK) * size).view(-1).to(dtype)
+        s["exp_avg"], s["exp_avg_scale"] = _moment(_normal(g, total // BLOCK, BLOCK) * size * 0.3, torch.float8_e4m3fn, 7)
+        s["exp_avg_sq"], s["exp_avg_sq_scale"] = _moment((_normal(g, total // BLOCK, BLOCK) * size).square() + 1e-3 * size * size, torch.float8_e5m2, 14)
+        s["copy"] = torch.zeros(total, dtype=torch.bfloat16, device="cuda") if case["copy"] else None
+        shapes = [(case["rows"], case["dim"])] * case["tables"] + [(case["dim"],)] * case["vectors"]
+
+        def part(name, at, shape):
+            t = s[name]
+            return None if t is None else t[at:at + math.prod(shape)].view(shape)
+
+        s["segments"] = [
+            (part("param", at, shape), part("grad", at, shape),
+             part("exp_avg", at, shape), s["exp_avg_scale"][at // BLOCK:at // BLOCK + -(-math.prod(shape) // BLOCK)],
+             part("exp_avg_sq", at, shape), s["exp_avg_sq_scale"][at // BLOCK:at // BLOCK + -(-math.prod(shape) // BLOCK)],
+             part("copy", at, shape))
+            for at, shape in zip(starts, shapes)]
+        # the buffers between the tensors hold nothing
+        live = torch.zeros(total, dtype=torch.bool, device="cuda")
+        for at, size in zip(starts, sizes):
+            live[at:at + size] = True
+        for name in ("param", "grad", "exp_avg", "exp_avg_sq"):
+            t = s[name].view(torch.uint8) if s[name].element_size() == 1 else s[name]
+            t.mul_(live)
+    else:
+        n, dim = case["n"], case["dim"]
+        # a few channels carry most of the energy, as in a residual stream
+        channel = 1.0 + 10.0 * (torch.rand(dim, generator=g, device="cuda") < 0.01)
+        s["x"] = (_normal(g, n, dim) * channel + 0.25).to(dtype)
+        s["residual"] = (_normal(g, n, dim, scale=2.0) * channel).to(dtype)
+        s["scale"] = 0.5
+        s["gate"] = _normal(g, dim, scale=0.3) + 0.5 if case["gate"] else None
+        for name, used in (("post_weight", case["post"] and case["gain"]), ("weight", case["gain"])):
+            s[name] = 1.0 + _normal(g, dim, scale=0.1) if used else None
+        for name, used in (("post_bias", case["post"] and case["gain"] and case["center"]), ("bias", case["gain"] and case["center"])):
+            s[name] = _normal(g, dim, scale=0.1) if used else None
+        if op == "residual_grad":
+            s["out"], _, s["stats"] = _residual(s)
+            s["dy"] = _normal(g, n, dim, scale=1e-2, dtype=dtype)
+            s["dout"] = _normal(g, n, dim, scale=1e-2, dtype=dtype)
+    return s
+
+
+def work(case):
+    op, b = case["op"], BYTES[case["type"]]
+    if op.startswith("head"):
+        n, vocab, dim = case["n"], case["vocab"], case["dim"]
+        live = n - (len(range(case["ignored"] // 2, n, case["ignored"])) if case["ignored"] else 0)
+        read = n * (dim * b + 8) + vocab * dim * b
+        if op == "head_loss":
+            return {"bytes": read + n * 8, "flops": 2.0 * live * vocab * dim}
+        return {"bytes": 2 * read + n * 8, "flops": 6.0 * live * vocab * dim}
+    if op == "adamw8":
+        total = case["tables"] * case["rows"] * case["dim"] + case["vectors"] * case["dim"]
+        return {"bytes": total * (12.0 + b + 4.0 / BLOCK + (2 if case["copy"] else 0)), "flops": 30.0 * total}
+    values, gains = case["n"] * case["dim"], case["dim"] * 4 * (case["gate"] + case["gain"] * (1 + case["post"]) * (1 + case["center"]))
+    if op == "residual":
+        return {"bytes": 4 * values * b + case["n"] * 16 + gains, "flops": 16.0 * values}
+    return {"bytes": 6 * values * b + case["n"] * 16 + 2 * gains, "flops": 30.0 * values}
+
+
+# ---------------------------------------------------------------- the plain forms
+def _head(s, grad=False):
+    """Loss, logarithm of the sum of exponentials and, with grad, both gradients."""
+    labels, vocab = s["labels"], s["case"]["vocab"]
+    live = (labels >= 0) & (labels < vocab)
+    at = torch.where(live, labels, 0)
+    h, w = s["hidden"].float(), s["weight"].float()
+    z = h @ w.t()
+    top = z.amax(1, keepdim=True)
+    target = z.gather(1, at[:, None])[:, 0]
+    e = z.sub_(top).exp_()
+    total = e.sum(1, keepdim=True)
+    lse = torch.where(live, (top + torch.log(total))[:, 0], 0.0)
+    loss = torch.where(live, lse - target, 0.0)
+    if not grad:
+        return loss, lse
+    row_weight = torch.where(live, s["row_weight"], 0.0)[:, None]
+    dz = e.mul_(row_weight / total)
+    dz.scatter_add_(1, at[:, None], -row_weight)
+    return loss, (dz @ w).to(s["hidden"].dtype), (dz.t() @ h).to(s["weight"].dtype)
+
+
+def _uniform(total, shift):
+    """The 16 random bits of each element above `shift`, as a fraction: Murmur3's finalizer of the
+    element's number and of the key that seed and step make."""
+    mask = 0xffffffff
+
+    def mix(x):
+        x = ((x ^ (x >> 16)) * 0x85ebca6b) & mask
+        x = ((x ^ (x >> 13)) * 0xc2b2ae35) & mask
+        return x ^ (x >> 16)
+
+    key = mix(mix(mix(SEED & mask) ^ (SEED >> 32)) ^ STEP)
+    at = torch.arange(total, device="cuda")
+    bits = mix((((at & mask) * 0x9e3779b1) & mask) ^ ((key + (at >> 32) * 0x9e3779b1) & mask))
+    return ((bits >> shift) & 0xffff).float() / 65536.0
+
+
+def _round8(x, dtype, bits, low, top, fraction, floor):
+    """Blocks of a moment (blocks, BLOCK) to 8 bits: the largest value's exponent less `top` is the
+    block's scale, and each value goes up to the next one of the type with the probability of its
+    place between the two.  A positive value of a moment with `floor` stays positive."""
+    big = x.abs().amax(1)
+    e = torch.where(big > 0, _exponent(big) - top, -126).clamp(-126, 127)
+    y = (x / _power(e)[:, None]).double()
+    unit = torch.pow(2.0, (_exponent(y.abs()).clamp(min=low) - bits).double())
+    q = torch.floor(y.abs() / unit + fraction.view_as(y))
+    if floor:
+        q = torch.where((y > 0) & (q == 0), 1.0, q)
+    return (q * unit * torch.sign(y)).float().to(dtype).view(-1), (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+
+
+def _moments(s):
+    scales = [_power(s[name].view(torch.uint8).int() - 127)[:, None] for name in ("exp_avg_scale", "exp_avg_sq_scale")]
+    m = s["exp_avg"].float().view(-1, BLOCK) * scales[0]
+    v = s["exp_avg_sq"].float().view(-1, BLOCK) * scales[1]
+    return m, v
+
+
+def _adamw8(s):
+    h, p = ADAMW, s["param"].view(-1, BLOCK)
+    grad = s["grad"].float().view(-1, BLOCK)
+    m, v = _moments(s)
+    m = h["beta1"] * m + (1.0 - h["beta1"]) * grad
+    v = h["beta2"] * v + (1.0 - h["beta2"]) * grad * grad
+    update = (m / (1.0 - h["beta1"] ** STEP)) / (torch.sqrt(v / (1.0 - h["beta2"] ** STEP)) + h["eps"])
+    p.mul_(1.0 - h["lr"] * h["weight_decay"]).add_(update, alpha=-h["lr"])
+    total = p.numel()
+    m, me = _round8(m, torch.float8_e4m3fn, 3, -6, 7, _uniform(total, 0), False)
+    v, ve = _round8(v, torch.float8_e5m2, 2, -14, 14, _uniform(total, 16), True)
+    for name, t in (("exp_avg", m), ("exp_avg_scale", me), ("exp_avg_sq", v), ("exp_avg_sq_scale", ve)):
+        s[name].view(torch.uint8).copy_(t.view(torch.uint8))
+    if s["copy"] is not None:
+        s["copy"].copy_(s["param"])
+
+
+def _held(s):
+    """What a step leaves: the moments' 8-bit values and their blocks' scales are tensors of their types."""
+    names = ("param", "exp_avg", "exp_avg_scale", "exp_avg_sq", "exp_avg_sq_scale", "copy")
+    return {name: s[name] for name in names if s[name] is not None}
+
+
+def _statistics(x, center):
+    mean = x.mean(1, keepdim=True) if center else torch.zeros_like(x[:, :1])
+    c = x - mean
+    return mean, 1.0 / torch.sqrt((c * c).mean(1, keepdim=True) + NORM_EPS), c
+
+
+def _affine(x, weight, bias):
+    x = x if weight is None else x * weight
+    return x if bias is None else x + bias
+
+
+def _residual(s):
+    case, dtype = s["case"], s["x"].dtype
+    branch, mean1 = s["x"].float(), torch.zeros(case["n"], 1, device="cuda")
+    rstd1 = mean1
+    if case["post"]:
+        mean1, rstd1, c = _statistics(branch, case["center"])
+        branch = _affine(c * rstd1, s["post_weight"], s["post_bias"])
+    gate = s["scale"] if s["gate"] is None else s["scale"] * s["gate"]
+    out = s["residual"].float() + gate * branch
+    mean2, rstd2, c = _statistics(out, case["center"])
+    y = _affine(c * rstd2, s["weight"], s["bias"])
+    return out.to(dtype), y.to(dtype), torch.cat([mean1, rstd1, mean2, rstd2], 1).t().contiguous()
+
+
+def _norm_grad(u, h, rstd, center):
+    d = u - h * (u * h).mean(1, keepdim=True)
+    return rstd * (d - u.mean(1, keepdim=True) if center else d)
+
+
+def _residual_grad(s):
+    case, dtype, center = s["case"], s["x"].dtype, s["case"]["center"]
+    mean1, rstd1, mean2, rstd2 = (t[:, None] for t in s["stats"])
+    dy, x = s["dy"].float(), s["x"].float()
+    h2 = (s["out"].float() - mean2) * rstd2
+    d = s["dout"].float() + _norm_grad(_affine(dy, s["weight"], None), h2, rstd2, center)
+    gate = s["scale"] if s["gate"] is None else s["scale"] * s["gate"]
+    h1 = (x - mean1) * rstd1 if case["post"] else x
+    branch = _affine(h1, s["post_weight"], s["post_bias"])
+    db = d * gate
+    dx = _norm_grad(_affine(db, s["post_weight"], None), h1, rstd1, center) if case["post"] else db
+    return (dx.to(dtype), d.to(dtype),
+            None if s["weight"] is None else (dy * h2).sum(0),
+            None if s["bias"] is None else dy.sum(0),
+            None if s["post_weight"] is None else (db * h1).sum(0),
+            None if s["post_bias"] is None else db.sum(0),
+            None if s["gate"] is None else (d * branch).sum(0) * s["scale"])
+
+
+def run(state):
+    s, case = state, state["case"]
+    op = case["op"]
+    if own:
+        import adamw_optimizer_step_muon_amd as ma
+
+        if op == "head_loss":
+            return ma.head_loss_forward(s["hidden"], s["weight"], s["labels"])
+        if op == "head_grad":
+            return ma.head_loss_backward(s["hidden"], s["weight"], s["labels"], s["lse"], s["row_weight"])
+        if op == "head_step":
+            return ma.head_loss_grad(s["hidden"], s["weight"], s["labels"], s["row_weight"])
+        if op == "adamw8":
+            ma.adamw8_step_multi(s["segments"], step=STEP, seed=SEED, **ADAMW)
+            return _held(s)
+        gains = dict(post_norm=case["post"], post_weight=s["post_weight"], post_bias=s["post_bias"], gate=s["gate"],
+                     scale=s["scale"], center=case["center"])
+        if op == "residual":
+            return ma.residual_norm_forward(s["x"], s["residual"], s["weight"], s["bias"], eps=NORM_EPS, **gains)
+        return ma.residual_norm_backward(s["dout"], s["dy"], s["x"], s["out"], s["stats"], s["weight"], s["bias"], **gains)
+    if op == "head_loss":
+        return _head(s)
+    if op == "head_grad":
+        return _head(s, grad=True)[1:]
+    if op == "head_step":
+        return _head(s, grad=True)
+    if op == "adamw8":
+        _adamw8(s)
+        return _held(s)
+    return _residual(s) if op == "residual" else _residual_grad(s)
+
+
+# ---------------------------------------------------------------- 64 bits, from the definitions
+def _exact_norm(x, weight, bias, center):
+    mean = x.mean(1) if center else x.new_zeros(x.shape[0])
+    rstd = (x.sub(mean[:, None]).square().mean(1) + NORM_EPS).rsqrt()
+    y = torch.addcmul(x.new_zeros(()), x - mean[:, None], rstd[:, None])
+    y = y if weight is None else y * weight.double()
+    return y if bias is None else y + bias.double(), mean, rstd
+
+
+def _exact_norm_grad(upstream, unit, rstd, weight, center):
+    """The product of the norm's Jacobian, rstd (I - unit unit' / D [- 1 1' / D]), with upstream * weight."""
+    u = upstream if weight is None else upstream * weight.double()
+    out = u - unit * (torch.sum(u * unit, 1) / u.shape[1])[:, None]
+    if center:
+        out = out - torch.sum(u, 1, keepdim=True) / u.shape[1]
+    return out * rstd[:, None]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op, f64 = case["op"], torch.float64
+    if op.startswith("head"):
+        vocab = case["vocab"]
+        if 6.0 * case["n"] * vocab * case["dim"] > 3e14:
+            return None
+        h, w = s["hidden"].to(f64), s["weight"].to(f64)
+        log_q = torch.mm(h, w.t())
+        keep = (s["labels"] > -1) & (s["labels"] < vocab)
+        rows = torch.nonzero(keep)[:, 0]
+        at = s["labels"][rows]
+        lse = torch.logsumexp(log_q, 1)
+        loss = torch.zeros(case["n"], dtype=f64, device="cuda")
+        loss[rows] = lse[rows] - log_q[rows, at]
+        if op == "head_loss":
+            return loss, lse * keep
+        q = log_q.sub_((s["lse"].to(f64) if op == "head_grad" else lse)[:, None]).exp_()
+        q[rows, at] -= 1.0
+        q.mul_((s["row_weight"].to(f64) * keep)[:, None])
+        grads = torch.mm(q, w), torch.mm(q.t(), h)
+        return grads if op == "head_grad" else (loss, *grads)
+    if op == "adamw8":
+        b1, b2 = ADAMW["beta1"], ADAMW["beta2"]
+        grad = s["grad"].to(f64).view(-1, BLOCK)
+
+        def held(name):
+            scale = torch.exp2(s[name + "_scale"].view(torch.uint8).to(f64) - 127.0)
+            return s[name].to(f64).view(-1, BLOCK) * scale[:, None]
+
+        m = torch.lerp(grad, held("exp_avg"), b1)
+        v = torch.lerp(grad.square(), held("exp_avg_sq"), b2)
+        p = s["param"].to(f64).view(-1, BLOCK)
+        root = (v / (1.0 - b2 ** STEP)).sqrt().add_(ADAMW["eps"])
+        p = (p - ADAMW["lr"] * (ADAMW["weight_decay"] * p + m / (1.0 - b1 ** STEP) / root)).view(-1)
+
+        def scaled(x, top):
+            """What the 8-bit values stand for in the mean over the random bits."""
+            big = x.abs().amax(1, keepdim=True)
+            e = torch.where(big > 0, torch.floor(torch.log2(big)) - top, -126.0).clamp(-126.0, 127.0)
+            return (x * torch.exp2(-e)).view(-1)
+
+        # the second moment's two bits of mantissa leave it a random value, mostly some 7 % from its mean
+        out = {"param": p, "exp_avg": scaled(m, 7.0), "exp_avg_scale": None, "exp_avg_sq": None, "exp_avg_sq_scale": None}
+        return dict(out, copy=p) if case["copy"] else out
+    center = case["center"]
+    x, gate = s["x"].to(f64), torch.full((case["dim"],), s["scale"], dtype=f64, device="cuda")
+    if s["gate"] is not None:
+        gate = gate * s["gate"].to(f64)
+    if op == "residual":
+        zero = x.new_zeros(case["n"])
+        b, mean1, rstd1 = _exact_norm(x, s["post_weight"], s["post_bias"], center) if case["post"] else (x, zero, zero)
+        out = torch.addcmul(s["residual"].to(f64), b, gate)
+        y, mean2, rstd2 = _exact_norm(out, s["weight"], s["bias"], center)
+        return out, y, torch.stack([mean1, rstd1, mean2, rstd2])
+    # the definition's gradients for the saved statistics
+    mean1, rstd1, mean2, rstd2 = s["stats"].to(f64)
+    dy = s["dy"].to(f64)
+    unit = (s["out"].to(f64) - mean2[:, None]) * rstd2[:, None]
+    total = s["dout"].to(f64) + _exact_norm_grad(dy, unit, rstd2, s["weight"], center)
+    inner = (x - mean1[:, None]) * rstd1[:, None] if case["post"] else x
+    down = total * gate
+    dx = _exact_norm_grad(down, inner, rstd1, s["post_weight"], center) if case["post"] else down
+    dgate = None
+    if s["gate"] is not None:
+        branch = inner if s["post_weight"] is None else inner * s["post_weight"].to(f64)
+        branch = branch if s["post_bias"] is None else branch + s["post_bias"].to(f64)
+        dgate = torch.sum(total * branch, 0) * s["scale"]
+    return (dx, total, None if s["weight"] is None else torch.sum(dy * unit, 0),
+            None if s["bias"] is None else torch.sum(dy, 0),
+            None if s["post_weight"] is None else torch.sum(down * inner, 0),
+            None if s["post_bias"] is None else torch.sum(down, 0), dgate)
