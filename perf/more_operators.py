@@ -328,7 +328,7 @@ def run(state):
         if op == "head_step":
             return ma.head_loss_grad(s["hidden"], s["weight"], s["labels"], s["row_weight"])
         if op == "adamw8":
-            ma.adamw8_step_multi(s["segments"], step=STEP, seed=SEED, **ADAMW)
+            ma.adamw_byte_step_multi(s["segments"], step=STEP, seed=SEED, **ADAMW)
             return _held(s)
         gains = dict(post_norm=case["post"], post_weight=s["post_weight"], post_bias=s["post_bias"], gate=s["gate"],
                      scale=s["scale"], center=case["center"])
