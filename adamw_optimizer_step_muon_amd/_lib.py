@@ -32,9 +32,10 @@ EXPORTED = (
     "ma_embedding_forward", "ma_embedding_workspace_bytes", "ma_embedding_backward",
     "ma_adamw_step_embedding", "ma_layer_norm_forward", "ma_layer_norm_workspace_bytes",
     "ma_layer_norm_backward", "ma_distill_forward", "ma_distill_backward", "ma_distill_loss_grad",
+    "ma_adamw_byte_step_multi",
 )
 MA_STATIC_WORKSPACE_BYTES = 512 << 20
-ABI_VERSION = 5  # include/muon_adamw.h MA_ABI_VERSION
+ABI_VERSION = 6  # include/muon_adamw.h MA_ABI_VERSION
 
 
 class MuonAdamWError(RuntimeError):
@@ -76,6 +77,21 @@ class _PlanReport(ctypes.Structure):
 class _AdamWSegment(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
                 ("exp_avg_sq", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class _AdamWByteHParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int64), ("decoupled", ctypes.c_int32),
+                ("cautious_wd", ctypes.c_int32)]
+
+
+class _AdamWByteSegment(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("grad_type", ctypes.c_int32), ("copy_type", ctypes.c_int32)]
 
 
 class _AdamWHParams(ctypes.Structure):
@@ -198,7 +214,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             ("distill_backward", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
                                   ptr, i64, ptr]),
             ("distill_loss_grad", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
-                                   ptr, i64, ptr])):
+                                   ptr, i64, ptr]),
+            ("adamw_byte_step_multi", [ctypes.POINTER(_AdamWByteSegment), i32,
+                                        ctypes.POINTER(_AdamWByteHParams), ctypes.c_uint64, ptr])):
         fn = getattr(lib, "ma_" + name)
         fn.restype, fn.argtypes = ctypes.c_int, args
     lib.ma_embedding_workspace_bytes.restype = size

@@ -538,26 +538,47 @@ ma_status check_step_args(const ma_muon_bucket* buckets, int32_t n_buckets,
 }
 
 // AdamW hyperparameter checks and the per-step constants of the kernels.
-ma_status adamw_const(const ma_adamw_hparams* hp, AdamWConst* c) {
+// The constants of a step.  The hyperparameters as the ABI holds them: fp32, or double for the
+// moments in 8 bits; 1 - beta is rounded once from what they hold.
+template <typename H>
+ma_status adamw_const(const H* hp, AdamWConst* c) {
   if (!hp) return fail(MA_ERR_INVALID_ARG, "hparams is NULL");
   if (hp->step < 1) return fail(MA_ERR_INVALID_ARG, "step %lld < 1", (long long)hp->step);
-  if (!finite(hp->lr) || !finite(hp->beta1) || !finite(hp->beta2) || !finite(hp->eps) ||
-      !finite(hp->weight_decay))
+  c->lr = static_cast<float>(hp->lr);
+  c->beta1 = static_cast<float>(hp->beta1);
+  c->beta2 = static_cast<float>(hp->beta2);
+  c->eps = static_cast<float>(hp->eps);
+  c->wd = static_cast<float>(hp->weight_decay);
+  if (!finite(c->lr) || !finite(c->beta1) || !finite(c->beta2) || !finite(c->eps) || !finite(c->wd))
     return fail(MA_ERR_INVALID_ARG, "non-finite AdamW hyperparameter");
-  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
+  if (!(c->beta1 >= 0.0f && c->beta1 < 1.0f && c->beta2 >= 0.0f && c->beta2 < 1.0f))
     return fail(MA_ERR_INVALID_ARG, "betas must lie in [0, 1)");
-  c->lr = hp->lr;
-  c->beta1 = hp->beta1;
-  c->beta2 = hp->beta2;
   c->one_m_beta1 = static_cast<float>(1.0 - static_cast<double>(hp->beta1));
   c->one_m_beta2 = static_cast<float>(1.0 - static_cast<double>(hp->beta2));
-  c->eps = hp->eps;
-  c->wd = hp->weight_decay;
   const double t = static_cast<double>(hp->step);
   c->inv_bc1 = static_cast<float>(1.0 / (1.0 - std::pow(static_cast<double>(hp->beta1), t)));
   c->inv_bc2 = static_cast<float>(1.0 / (1.0 - std::pow(static_cast<double>(hp->beta2), t)));
   c->decoupled = hp->decoupled ? 1 : 0;
   c->cautious = hp->cautious_wd ? 1 : 0;
+  return MA_OK;
+}
+
+// A range of a call over many segments.  No written one may overlap any other: a sweep over
+// the ranges sorted by start (a range overlaps an earlier one iff it starts before the largest
+// end seen so far).
+struct Span {
+  uintptr_t lo, hi;
+  bool write;
+};
+ma_status check_spans(std::vector<Span>& spans) {
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t end_any = 0, end_write = 0;
+  for (const Span& x : spans) {
+    if (x.lo < (x.write ? end_any : end_write))
+      return fail(MA_ERR_INVALID_ARG, "segments overlap (a written range meets another range)");
+    end_any = std::max(end_any, x.hi);
+    if (x.write) end_write = std::max(end_write, x.hi);
+  }
   return MA_OK;
 }
 
@@ -570,6 +591,10 @@ constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 2;
 constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;  // room for a batch behind it in int
+
+// Blocks of one launch of the 8-bit step, 256 threads and 4096 elements each.
+constexpr int64_t kMaxAdamWByteBlocks = kMaxThreadsPerLaunch / 256;
+constexpr int64_t kMaxAdamWByteElements = kMaxAdamWByteBlocks * 4096;
 
 int64_t bytes_of(int type) { return type == MA_F32 ? 4 : 2; }
 
@@ -1629,13 +1654,7 @@ ma_status ma_adamw_step_multi(const ma_adamw_segment* segs, int32_t n_segs,
   if (st != MA_OK) return st;
   if (n_segs < 0) return fail(MA_ERR_INVALID_ARG, "n_segs %d < 0", n_segs);
   if (n_segs > 0 && !segs) return fail(MA_ERR_INVALID_ARG, "segs is NULL");
-  // every segment on its own, then no write range may overlap any other range (a sweep
-  // over the ranges sorted by start: a range overlaps an earlier one iff it starts
-  // before the largest end seen so far)
-  struct Span {
-    uintptr_t lo, hi;
-    bool write;
-  };
+  // every segment on its own, then no write range may overlap any other range
   std::vector<Span> spans;
   spans.reserve(static_cast<size_t>(n_segs) * 4);
   for (int32_t i = 0; i < n_segs; ++i) {
@@ -1653,14 +1672,7 @@ ma_status ma_adamw_step_multi(const ma_adamw_segment* segs, int32_t n_segs,
     spans.push_back({range_of(g.exp_avg, b).lo, range_of(g.exp_avg, b).hi, true});
     spans.push_back({range_of(g.exp_avg_sq, b).lo, range_of(g.exp_avg_sq, b).hi, true});
   }
-  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  uintptr_t end_any = 0, end_write = 0;
-  for (const Span& x : spans) {
-    if (x.lo < (x.write ? end_any : end_write))
-      return fail(MA_ERR_INVALID_ARG, "segments overlap (a written range meets another range)");
-    end_any = std::max(end_any, x.hi);
-    if (x.write) end_write = std::max(end_write, x.hi);
-  }
+  if (const ma_status over = check_spans(spans)) return over;
   // launches of up to kMaxAdamWSegs segments, in order
   AdamWSegTable t{};
   t.c = c;
@@ -1696,6 +1708,73 @@ ma_status ma_adamw_step_multi(const ma_adamw_segment* segs, int32_t n_segs,
     t.nseg = k + 1;
   }
   return flush();
+}
+
+ma_status ma_adamw_byte_step_multi(const ma_adamw_byte_segment* segs, int32_t n_segs,
+                               const ma_adamw_byte_hparams* hp, uint64_t seed, void* stream) {
+  g_last_error.clear();
+  AdamWConst c;
+  if (const ma_status st = adamw_const(hp, &c)) return st;
+  if (n_segs < 0) return fail(MA_ERR_INVALID_ARG, "n_segs %d < 0", n_segs);
+  if (n_segs > 0 && !segs) return fail(MA_ERR_INVALID_ARG, "segs is NULL");
+  std::vector<Span> spans;
+  spans.reserve(static_cast<size_t>(n_segs) * 7);
+  for (int32_t i = 0; i < n_segs; ++i) {
+    const ma_adamw_byte_segment& g = segs[i];
+    if (g.n < 0) return fail(MA_ERR_INVALID_ARG, "segment %d: n = %lld < 0", i, (long long)g.n);
+    if (g.n == 0) continue;
+    if (g.n > kMaxAdamWByteElements)
+      return fail(MA_ERR_UNSUPPORTED, "segment %d: %lld elements exceed one launch", i, (long long)g.n);
+    if (!g.param || !g.grad || !g.exp_avg || !g.exp_avg_scale || !g.exp_avg_sq || !g.exp_avg_sq_scale)
+      return fail(MA_ERR_INVALID_ARG, "segment %d: NULL pointer", i);
+    if (check_type(g.grad_type, "gradient")) return MA_ERR_INVALID_ARG;
+    if (g.copy && g.copy_type != MA_F16 && g.copy_type != MA_BF16)
+      return fail(MA_ERR_INVALID_ARG, "segment %d: the copy must be fp16 or bf16", i);
+    if ((reinterpret_cast<uintptr_t>(g.param) & 3u) ||
+        reinterpret_cast<uintptr_t>(g.grad) % static_cast<uintptr_t>(bytes_of(g.grad_type)) ||
+        (reinterpret_cast<uintptr_t>(g.copy) & 1u))
+      return fail(MA_ERR_INVALID_ARG, "segment %d: pointers must be aligned to their elements", i);
+    const int64_t blocks = (g.n + kAdamWByteBlock - 1) / kAdamWByteBlock;
+    const auto add = [&](const void* p, int64_t bytes, bool write) {
+      const Range r = range_of(p, bytes);
+      spans.push_back({r.lo, r.hi, write});
+    };
+    add(g.param, g.n * 4, true);
+    add(g.grad, g.n * bytes_of(g.grad_type), false);
+    add(g.exp_avg, g.n, true);
+    add(g.exp_avg_scale, blocks, true);
+    add(g.exp_avg_sq, g.n, true);
+    add(g.exp_avg_sq_scale, blocks, true);
+    if (g.copy) add(g.copy, g.n * 2, true);
+  }
+  if (const ma_status st = check_spans(spans)) return st;
+  AdamWByteTable t{};
+  t.c = c;
+  t.key = adamw_byte_key(seed, hp->step);
+  const auto flush = [&]() -> ma_status {
+    const hipError_t e = launch_adamw_byte(t, static_cast<hipStream_t>(stream));
+    t.nseg = 0;
+    t.block_start[0] = 0;
+    if (e != hipSuccess) return hip_fail(e, "adamw_byte launch");
+    return MA_OK;
+  };
+  int64_t first = 0;
+  for (int32_t i = 0; i < n_segs; ++i) {
+    const ma_adamw_byte_segment& g = segs[i];
+    if (g.n == 0) continue;
+    const int64_t nb = adamw_byte_blocks(g.n);
+    if (t.nseg == kMaxAdamWByteSegs || t.block_start[t.nseg] + nb > kMaxAdamWByteBlocks)
+      if (const ma_status st = flush()) return st;
+    t.seg[t.nseg] = AdamWByteSegment{g.param, g.grad,
+                                  static_cast<unsigned char*>(g.exp_avg), static_cast<unsigned char*>(g.exp_avg_scale),
+                                  static_cast<unsigned char*>(g.exp_avg_sq), static_cast<unsigned char*>(g.exp_avg_sq_scale),
+                                  static_cast<unsigned short*>(g.copy), g.n, first,
+                                  g.grad_type + 4 * (g.copy ? g.copy_type : 0)};
+    t.block_start[t.nseg + 1] = static_cast<uint32_t>(t.block_start[t.nseg] + nb);
+    ++t.nseg;
+    first += (g.n + kAdamWByteBlock - 1) / kAdamWByteBlock;
+  }
+  return t.nseg ? flush() : MA_OK;
 }
 
 // ---------------------------------------------------------------------------

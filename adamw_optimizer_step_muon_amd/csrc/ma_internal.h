@@ -394,6 +394,34 @@ hipError_t launch_stream_probe(const float* const* in, int reads, float* const* 
                                int64_t n, hipStream_t s);
 hipError_t launch_adamw_multi(const AdamWSegTable& t, hipStream_t s);
 
+// AdamW with both moments in 8 bits (adamw_byte.hip): segment i covers blocks [block_start[i],
+// block_start[i + 1]) of the grid, adamw_byte_blocks(n) of them (n >= 1).
+constexpr int kAdamWByteBlock = 64;  // elements that share a scale
+struct AdamWByteSegment {
+  float* p;
+  const void* g;
+  unsigned char* m;   // e4m3
+  unsigned char* ms;  // e8m0, one per block
+  unsigned char* v;   // e5m2
+  unsigned char* vs;
+  unsigned short* copy;
+  int64_t n;
+  int64_t first;  // blocks of the segments before it, which number its random bits
+  int32_t types;  // the gradient's ma_dtype; 4 times the copy's (0: no copy)
+};
+constexpr int kMaxAdamWByteSegs = 46;
+struct AdamWByteTable {
+  AdamWByteSegment seg[kMaxAdamWByteSegs];
+  uint32_t block_start[kMaxAdamWByteSegs + 1];
+  int32_t nseg;
+  uint32_t key;
+  AdamWConst c;
+};
+static_assert(sizeof(AdamWByteTable) <= 4096, "kernel arguments");
+int64_t adamw_byte_blocks(int64_t n);
+uint32_t adamw_byte_key(uint64_t seed, int64_t step);
+hipError_t launch_adamw_byte(const AdamWByteTable& t, hipStream_t s);
+
 // Matrix-core reference loop (mfma_probe.hip): `blocks` blocks of 512 threads, each wave
 // running `iters` rounds of 8 v_mfma_f32_32x32x16_bf16 on 16 fragments read once from
 // `operands` (16 x 64 x 8 bf16, 16-byte aligned); out: blocks x 512 floats; clocks

@@ -25,7 +25,8 @@ import functools
 import torch
 from torch.autograd.graph import increment_version
 
-from ._lib import _AdamWHParams, _check, _require_f32_cuda, _stream_handle, load
+from ._lib import (_AdamWByteHParams, _AdamWByteSegment, _AdamWHParams, _check, _require_f32_cuda,
+                   _stream_handle, load)
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _BITS = {torch.int32: 32, torch.int64: 64}
@@ -433,6 +434,80 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
     if stream is not None:
         _record(stream, logits, teacher, ids, row_weight, dlogits)
     return loss, dlogits
+
+
+# --------------------------------------------------------------------------
+# AdamW with both moments in 8 bits
+# --------------------------------------------------------------------------
+ADAMW_BYTE_BLOCK = 64  # elements that share a scale
+_ADAMW_BYTE_STATE = (("exp_avg", torch.float8_e4m3fn, 1), ("exp_avg_scale", torch.float8_e8m0fnu, ADAMW_BYTE_BLOCK),
+                 ("exp_avg_sq", torch.float8_e5m2, 1), ("exp_avg_sq_scale", torch.float8_e8m0fnu, ADAMW_BYTE_BLOCK))
+
+
+def adamw_byte_state(param):
+    """(exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale) of `param` before its first step:
+    zeros in the parameter's shape (e4m3 and e5m2) and scales of one (e8m0), one per block of 64
+    consecutive elements."""
+    scale = torch.full((-(-param.numel() // ADAMW_BYTE_BLOCK),), 127, dtype=torch.uint8, device=param.device)
+    scale = scale.view(torch.float8_e8m0fnu)
+    zeros = torch.zeros(param.shape, dtype=torch.uint8, device=param.device)
+    return (zeros.view(torch.float8_e4m3fn), scale,
+            zeros.clone().view(torch.float8_e5m2), scale.view(torch.uint8).clone().view(torch.float8_e8m0fnu))
+
+
+def adamw_byte_values(value, scale):
+    """What a moment's 8-bit values and their blocks' scales stand for, in fp32."""
+    flat = value.reshape(-1).float()
+    return flat.mul_(scale.float().repeat_interleave(ADAMW_BYTE_BLOCK)[:flat.numel()]).view(value.shape)
+
+
+def adamw_byte_step_multi(segments, *, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+                      eps: float = 1e-8, weight_decay: float = 0.0, decoupled: bool = True,
+                      cautious_wd: bool = False, seed: int = 0, stream=None) -> None:
+    """One AdamW step over many tensors with their moments in 8 bits (ma_adamw_byte_step_multi).  A
+    segment is (param, grad, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale) or, with one
+    more entry, ..., copy): param contiguous fp32, grad fp32, fp16 or bf16, the moments as
+    adamw_byte_state lays them out, and copy None or an fp16 or bf16 tensor that receives the stepped
+    parameter.  `seed` numbers the roundings' random bits, together with `step`."""
+    segments = list(segments)
+    if not segments:
+        return
+    arr, written = (_AdamWByteSegment * len(segments))(), []
+    device = None
+    for i, (p, g, *state) in enumerate(segments):
+        copy = state.pop() if len(state) == 5 else None
+        if len(state) != 4:
+            raise ValueError(f"segment {i} must hold 6 or 7 tensors")
+        for name, t in (("param", p), ("grad", g)):
+            _tensor(f"segment {i} {name}", t, device)
+            device = t.device
+        if p.dtype is not torch.float32 or not p.is_contiguous():
+            _require_f32_cuda(f"segment {i} param", p)
+        n = p.numel()
+        if g.numel() != n or not g.is_contiguous():
+            raise ValueError(f"segment {i} grad must be contiguous, of {n} values")
+        for (name, dtype, block), t in zip(_ADAMW_BYTE_STATE, state):
+            _tensor(f"segment {i} {name}", t, device)
+            if t.dtype is not dtype or not t.is_contiguous() or t.numel() != -(-n // block):
+                raise ValueError(f"segment {i} {name} must be contiguous {dtype} of {-(-n // block)} values "
+                                 f"(got {t.dtype}, {t.numel()})")
+        copied = 0
+        if copy is not None:
+            _tensor(f"segment {i} copy", copy, device)
+            if copy.dtype not in (torch.float16, torch.bfloat16) or copy.numel() != n or not copy.is_contiguous():
+                raise ValueError(f"segment {i} copy must be contiguous float16 or bfloat16 of {n} values")
+            copied = _DTYPES[copy.dtype]
+            written.append(copy)
+        arr[i] = (p.data_ptr(), g.data_ptr(), *(t.data_ptr() for t in state),
+                  0 if copy is None else copy.data_ptr(), n, _type(f"segment {i} grad", g.dtype), copied)
+        written.append(p)
+        written += state
+    hp = _AdamWByteHParams(lr, beta1, beta2, eps, weight_decay, int(step), int(bool(decoupled)),
+                           int(bool(cautious_wd)))
+    _call("ma_adamw_byte_step_multi", device, stream, arr, len(segments), ctypes.byref(hp), int(seed) & (2 ** 64 - 1))
+    increment_version(written)
+    if stream is not None:
+        _record(stream, *written, *(s[1] for s in segments))
 
 
 # --------------------------------------------------------------------------

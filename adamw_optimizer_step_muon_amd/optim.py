@@ -27,6 +27,12 @@ State is fp32 and zero-initialised: ``momentum_buffer`` (4 bytes per Muon parame
 can come as tokens and output gradients (``add_token_gradient``, which ``embedding(...,
 optimizer=...)`` calls in its backward pass); its dense form is then never built.
 
+An AdamW group's ``state_bits=8`` holds its moments in 8 bits instead (2 + 1/32 bytes per
+parameter, see adamw_byte_step_multi): ``exp_avg``, ``exp_avg_sq`` and their blocks' scales, with
+``seed`` for the roundings' random bits.  Its ``copies`` (one entry per parameter, None or a
+contiguous fp16 or bf16 tensor of its size) receive the stepped parameters, for a forward pass
+that reads 16-bit weights.  Token gradients are built densely there.
+
 A Muon group's ``ns_mode`` (0 by default) selects the Newton-Schulz route: 1 runs the
 Gram-space iteration ("DMuon", section 2.2) on fp16 operands for the buckets whose long
 side is at least 3.5x the other (MLP projections), the printed iteration elsewhere.
@@ -40,7 +46,7 @@ from . import _lib
 MUON_DEFAULTS = dict(lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True, ns_steps=5,
                      ns_coeffs=None, ns_eps=1e-7, cautious_wd=False, scale_mode=0, ns_mode=0)
 ADAMW_DEFAULTS = dict(lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
-                      decoupled=True, cautious_wd=False)
+                      decoupled=True, cautious_wd=False, state_bits=32, seed=0, copies=None)
 
 
 _F32_MAX = 3.4028234663852886e38
@@ -171,10 +177,37 @@ class MuonAdamW:
                     for k, p in enumerate(b.params):
                         self.state[id(p)] = {"momentum_buffer": b.momentum_view(k)}
             else:
+                self._check_state_bits(group)
                 for p in group["params"]:
-                    self.state[id(p)] = {"exp_avg": torch.zeros_like(p),
-                                         "exp_avg_sq": torch.zeros_like(p)}
+                    self.state[id(p)] = self._byte_state(p) if group["state_bits"] == 8 else {
+                        "exp_avg": torch.zeros_like(p), "exp_avg_sq": torch.zeros_like(p)}
             self.param_groups.append(group)
+
+    @staticmethod
+    def _check_state_bits(group) -> None:
+        import torch
+
+        if group["state_bits"] not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32 (got {group['state_bits']!r})")
+        if group["copies"] is None:
+            return
+        if group["state_bits"] != 8:
+            raise ValueError("copies are for groups with state_bits 8")
+        group["copies"] = list(group["copies"])
+        if len(group["copies"]) != len(group["params"]):
+            raise ValueError("copies must have one entry per parameter")
+        for p, c in zip(group["params"], group["copies"]):
+            if c is not None and (c.dtype not in (torch.float16, torch.bfloat16) or c.device != p.device
+                                  or c.numel() != p.numel() or not c.is_contiguous()):
+                raise ValueError("copies must be contiguous float16 or bfloat16 tensors of their "
+                                 "parameters' sizes")
+
+    @staticmethod
+    def _byte_state(p) -> Dict:
+        from . import ops
+
+        return dict(zip(("exp_avg", "exp_avg_scale", "exp_avg_sq", "exp_avg_sq_scale"),
+                        ops.adamw_byte_state(p)))
 
     @staticmethod
     def _bucket(params) -> List[_Bucket]:
@@ -228,7 +261,8 @@ class MuonAdamW:
         scale * dout[t] on row tokens[t] for every t, without building it: the next step()
         applies tokens and output gradients directly (adamw_step_embedding: no dense
         gradient is written or read).  Several additions, or one next to a dense
-        ``param.grad``, are summed into ``param.grad`` at step() instead.  tokens (int32 or
+        ``param.grad`` or for a group with moments in 8 bits, are summed into ``param.grad`` at
+        step() instead.  tokens (int32 or
         int64) and dout (tokens.shape + (dim,)) are kept, not copied, until zero_grad() and
         must not be modified before step(), which waits for the stream that is current here
         where its own is another.  What reads or changes ``param.grad`` between
@@ -269,12 +303,12 @@ class MuonAdamW:
                     if p.grad is not None:
                         _lib._require_f32_cuda("the grad that token gradients add to", p.grad)
 
-    def _take_token_gradient(self, p):
+    def _take_token_gradient(self, p, direct: bool):
         """The token gradient to step p with directly, or None where p.grad holds it all."""
         added = self._token_grads.get(id(p))
         if not added:
             return None
-        if len(added) == 1 and p.grad is None:
+        if direct and len(added) == 1 and p.grad is None:
             return added[0]
         from . import ops
 
@@ -296,7 +330,8 @@ class MuonAdamW:
         for gi, g in enumerate(self.param_groups):
             if g["kind"] == "adamw":
                 by_token = [(p, t) for p in g["params"]
-                            for t in [self._take_token_gradient(p)] if t is not None]
+                            for t in [self._take_token_gradient(p, g["state_bits"] == 32)]
+                            if t is not None]
                 live = [p for p in g["params"] if p.grad is not None]
                 if not live and not by_token:
                     continue
@@ -304,6 +339,16 @@ class MuonAdamW:
                 hp = dict(step=g["step"] + 1, lr=g["lr"], beta1=b1, beta2=b2, eps=g["eps"],
                           weight_decay=g["weight_decay"], decoupled=g["decoupled"],
                           cautious_wd=g["cautious_wd"])
+                if g["state_bits"] == 8:
+                    from . import ops
+
+                    copies = g["copies"] or [None] * len(g["params"])
+                    ops.adamw_byte_step_multi(
+                        [(p.data, p.grad, *self.state[id(p)].values(), c)
+                         for p, c in zip(g["params"], copies) if p.grad is not None],
+                        seed=g["seed"], **hp)
+                    g["step"] += 1
+                    continue
                 # the group's tensors in one fused pass (one launch per 48 tensors)
                 segs = [(p.data, p.grad, self.state[id(p)]["exp_avg"],
                          self.state[id(p)]["exp_avg_sq"]) for p in live]
@@ -351,11 +396,15 @@ class MuonAdamW:
                 state[idx] = {k: v.clone() for k, v in self.state[id(p)].items()}
                 ids.append(idx)
                 idx += 1
-            groups.append({k: v for k, v in g.items() if k != "params"} | {"params": ids})
+            groups.append({k: v for k, v in g.items() if k not in ("params", "copies")} | {"params": ids})
         return {"state": state, "param_groups": groups}
 
     def load_state_dict(self, sd: Dict) -> None:
         flat = [p for g in self.param_groups for p in g["params"]]
+        for (idx, st) in sd["state"].items():
+            # 8-bit moments mean nothing without their scales, and a cast would lose most values
+            if ("exp_avg_scale" in st) != ("exp_avg_scale" in self.state[id(flat[int(idx)])]):
+                raise ValueError("the state's moments have another number of bits (state_bits)")
         for (idx, st) in sd["state"].items():
             for k, v in st.items():
                 self.state[id(flat[int(idx)])][k].copy_(v)

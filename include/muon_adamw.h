@@ -10,8 +10,8 @@
  *   ma_adamw_step  the fused elementwise AdamW step over one flat fp32 range
  *                  (embeddings, LM head, normalisation gains, biases).
  *
- * and the training operators that produce the gradients of those AdamW parameters, or
- * spare them: ma_embedding_forward / _backward, ma_adamw_step_embedding (AdamW on a table
+ * ma_adamw_byte_step_multi is the AdamW step with both moments in 8 bits.  Beside them are the
+ * training operators that produce the gradients of those AdamW parameters, or spare them: ma_embedding_forward / _backward, ma_adamw_step_embedding (AdamW on a table
  * straight from its tokens), ma_layer_norm_forward / _backward and ma_distill_forward /
  * _backward / _loss_grad.
  *
@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MA_ABI_VERSION 5
+#define MA_ABI_VERSION 6
 
 typedef enum {
   MA_OK = 0,
@@ -63,6 +63,9 @@ typedef enum {
   MA_ERR_HIP = -4,         /* a HIP runtime call or launch failed */
   MA_ERR_INTERNAL = -5     /* ma_muon_check_plan found a launch that breaks its plan */
 } ma_status;
+
+/* Types of activations, gradients and 16-bit copies. */
+typedef enum { MA_F32 = 0, MA_F16 = 1, MA_BF16 = 2 } ma_dtype;
 
 /* One shape bucket of Muon matrices [NC]: K matrices of A x B, stacked (K, A, B).
  * K == 0 is an empty bucket (skipped).  The three buffers must not overlap. */
@@ -249,6 +252,48 @@ typedef struct {
 ma_status ma_adamw_step_multi(const ma_adamw_segment* segs, int32_t n_segs,
                               const ma_adamw_hparams* hp, void* stream);
 
+/* One tensor of ma_adamw_byte_step_multi: n elements (device pointers).  The moments are values of
+ * 8 bits, each with a power of two per block of 64 consecutive elements (the last may be short):
+ *   exp_avg     n OCP e4m3 values,  exp_avg_scale     ceil(n / 64) e8m0 bytes b: 2^(b - 127)
+ *   exp_avg_sq  n OCP e5m2 values,  exp_avg_sq_scale  the same
+ * Before step 1: values of zero, any scale but 255 (NaN). */
+typedef struct {
+  float* param;
+  const void* grad;        /* grad_type */
+  void* exp_avg;
+  void* exp_avg_scale;
+  void* exp_avg_sq;
+  void* exp_avg_sq_scale;
+  void* copy;              /* NULL, or n values of copy_type: the stepped parameter, rounded */
+  int64_t n;
+  int32_t grad_type;       /* ma_dtype */
+  int32_t copy_type;       /* MA_F16 or MA_BF16; ignored without a copy */
+} ma_adamw_byte_segment;
+
+/* ma_adamw_hparams in double: 1 - beta is rounded to fp32 once (from an fp32 beta2 of 0.9999 it
+ * would be off by 3e-4). */
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  int32_t decoupled;
+  int32_t cautious_wd;
+} ma_adamw_byte_hparams;
+
+/* ma_adamw_step over many tensors whose moments are held in 8 bits: 2 + 1/32 instead of 8 bytes
+ * of state per element.  The moments are widened (exactly), updated as ma_adamw_step does, and
+ * step the parameter before they are rounded back; grad may have 16 bits.  A block's scale is
+ * 2^(E - 7) for exp_avg and 2^(E - 14) for exp_avg_sq, E the exponent of its largest magnitude
+ * (at least 2^-126).  Each value goes up to the next one of its type with the probability of its
+ * place between its two neighbours (16 bits of a hash of seed, step and the element's number,
+ * counted over the list with every segment starting at a multiple of 64), so that slow averages
+ * keep moving; a positive exp_avg_sq stays positive.  The same inputs give the same bits on every
+ * call; results do not depend on alignment (pointers need their element's).  One launch per 46
+ * segments.  Segments with n == 0 are skipped.  No written range (all but grad) may overlap any
+ * other range of any segment.  NaN and Inf in a gradient make their element's state NaN or Inf.
+ * Errors: as ma_adamw_step_multi. */
+ma_status ma_adamw_byte_step_multi(const ma_adamw_byte_segment* segs, int32_t n_segs,
+                               const ma_adamw_byte_hparams* hp, uint64_t seed, void* stream);
+
 /* Host only: workspace bytes ma_newton_schulz needs for a (K, A, B) stack. */
 size_t ma_newton_schulz_workspace_bytes(int64_t K, int64_t A, int64_t B);
 
@@ -399,8 +444,6 @@ ma_status ma_muon_ns_time(const ma_muon_bucket* buckets, int32_t n_buckets,
  * misaligned pointers, sizes, types, overlap, non-finite scalars), MA_ERR_UNSUPPORTED
  * (sizes above the stated limits or one launch), MA_ERR_WORKSPACE, MA_ERR_HIP.
  * ------------------------------------------------------------------------------------ */
-typedef enum { MA_F32 = 0, MA_F16 = 1, MA_BF16 = 2 } ma_dtype;
-
 /* Lookup with scaling: out[t] = scale * table[token t], for n tokens (token_bits 32 or 64,
  * signed).  A token outside [0, rows) marks padding: nothing is read, out[t] = 0.
  * table: (rows, dim) fp32, rows < 2^31 - 1, dim <= 2^20; n <= 2^30 (0: no-op). */

@@ -22,12 +22,13 @@ function:
                                          first-step closed form, pure decay)
 * adamw_step with cautious_wd            special cases only ("parity unpinned"
                                          for the mixed-sign case)
+* adamw_byte (moments in 8 bits)         not on the pages: definitions, on adamw_step
 * training (embedding, layer norm,       not on the pages: definitions, against
   distillation)                          central differences and closed forms
 """
-from . import training
+from . import adamw_byte, training
 from .adamw import AdamWResult, adamw_step
 from .muon import QUINTIC, MuonResult, Route, muon_step, muon_step_bucket, newton_schulz, route, update_scale
 
-__all__ = ["AdamWResult", "adamw_step", "QUINTIC", "MuonResult", "Route", "muon_step",
+__all__ = ["AdamWResult", "adamw_byte", "adamw_step", "QUINTIC", "MuonResult", "Route", "muon_step",
            "muon_step_bucket", "newton_schulz", "route", "training", "update_scale"]

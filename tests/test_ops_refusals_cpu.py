@@ -289,3 +289,74 @@ def test_binding_refuses_what_is_no_tensor():
     for bad in (None, [1.0], 3):
         with pytest.raises(TypeError, match="dout"):
             ma.embedding_backward(bad, i, 10)
+
+
+BYTE = dict(param=A, grad=B, exp_avg=C, exp_avg_scale=C + 4096, exp_avg_sq=D, exp_avg_sq_scale=D + 4096, copy=F, n=1000,
+            grad_type=2, copy_type=2)
+
+
+def _byte_hp(**kw):
+    return _lib._AdamWByteHParams(**{**dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1, decoupled=1,
+                                            cautious_wd=0), **kw})
+
+
+def _byte_step(lib, *segments, n=None, hp={}, seed=0):
+    arr = (_lib._AdamWByteSegment * len(segments))(*(_lib._AdamWByteSegment(*s.values()) for s in segments))
+    return lib.ma_adamw_byte_step_multi(arr, len(segments) if n is None else n, ctypes.byref(_byte_hp(**hp)), seed, None)
+
+
+@pytest.mark.parametrize("changes,status", [
+    (dict(param=None), INVALID), (dict(grad=None), INVALID), (dict(exp_avg=None), INVALID),
+    (dict(exp_avg_scale=None), INVALID), (dict(exp_avg_sq=None), INVALID), (dict(exp_avg_sq_scale=None), INVALID),
+    (dict(param=A + 2), INVALID), (dict(grad=B + 1), INVALID), (dict(grad=B + 2, grad_type=0), INVALID),
+    (dict(copy=F + 1), INVALID), (dict(grad_type=3), INVALID), (dict(grad_type=-1), INVALID), (dict(copy_type=0), INVALID),
+    (dict(copy_type=3), INVALID), (dict(n=-1), INVALID), (dict(grad=A + 3998), INVALID), (dict(exp_avg=A), INVALID),
+    (dict(exp_avg_scale=C + 999), INVALID), (dict(exp_avg_sq=C), INVALID), (dict(exp_avg_sq_scale=C + 4096 + 15), INVALID),
+    (dict(copy=A), INVALID), (dict(copy=B), INVALID), (dict(n=1 << 37), UNSUPPORTED),
+])
+def test_byte_step(lib, changes, status):
+    assert set(changes) <= set(BYTE)
+    assert _byte_step(lib, {**BYTE, **changes}) == status and lib.ma_last_error()
+
+
+def test_byte_step_lists(lib):
+    other = {k: v + (1 << 30) if v is not None and k not in ("n", "grad_type", "copy_type") else v for k, v in BYTE.items()}
+    assert _byte_step(lib, BYTE, dict(other, param=BYTE["copy"])) == INVALID
+    assert _byte_step(lib, BYTE, dict(other, grad=BYTE["exp_avg"])) == INVALID
+    assert _byte_step(lib, BYTE, n=-1) == INVALID
+    assert _byte_step(lib, BYTE, hp=dict(step=0)) == INVALID
+    assert _byte_step(lib, BYTE, hp=dict(lr=NAN)) == INVALID
+    assert _byte_step(lib, BYTE, hp=dict(eps=1e300)) == INVALID  # no fp32 number
+    assert _byte_step(lib, BYTE, hp=dict(beta2=1.0)) == INVALID
+    assert lib.ma_adamw_byte_step_multi(None, 1, ctypes.byref(_byte_hp()), 0, None) == INVALID
+    assert lib.ma_adamw_byte_step_multi(None, 0, ctypes.byref(_byte_hp()), 0, None) == 0
+    assert lib.ma_adamw_byte_step_multi(None, 0, None, 0, None) == INVALID
+
+
+def test_byte_state():
+    p = torch.zeros(5, 13)
+    m, ms, v, vs = ma.adamw_byte_state(p)
+    assert m.shape == v.shape == p.shape and ms.shape == vs.shape == (2,)
+    assert (m.dtype, ms.dtype, v.dtype) == (torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.float8_e5m2)
+    assert len({t.data_ptr() for t in (m, ms, v, vs)}) == 4
+    assert torch.equal(ma.adamw_byte_values(m, ms), p)
+    m.view(torch.uint8).fill_(torch.tensor(1.5).to(torch.float8_e4m3fn).view(torch.uint8).item())
+    ms.view(torch.uint8)[1] = 129
+    want = torch.full((65,), 1.5)
+    want[64] = 6.0
+    assert torch.equal(ma.adamw_byte_values(m, ms), want.view(5, 13))
+
+
+def test_byte_group_refusals():
+    p = torch.nn.Parameter(torch.zeros(4, 3))
+    for bad in (dict(state_bits=16), dict(copies=[None]), dict(state_bits=8, copies=[]),
+                dict(state_bits=8, copies=[torch.zeros(12)]), dict(state_bits=8, copies=[torch.zeros(11, dtype=torch.bfloat16)])):
+        with pytest.raises(ValueError):
+            ma.MuonAdamW([{"kind": "adamw", "params": [p], **bad}])
+    with pytest.raises(ValueError, match="GPU"):
+        ma.adamw_byte_step_multi([(p.data, p.data, *ma.adamw_byte_state(p))], step=1, lr=1e-3)
+    with pytest.raises(TypeError):
+        ma.adamw_byte_step_multi([(None, p.data, *ma.adamw_byte_state(p))], step=1, lr=1e-3)
+    with pytest.raises(ValueError, match="6 or 7"):
+        ma.adamw_byte_step_multi([(p.data, p.data)], step=1, lr=1e-3)
+    ma.adamw_byte_step_multi([], step=1, lr=1e-3)
