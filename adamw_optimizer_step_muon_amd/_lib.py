@@ -32,7 +32,8 @@ EXPORTED = (
     "ma_embedding_forward", "ma_embedding_workspace_bytes", "ma_embedding_backward",
     "ma_adamw_step_embedding", "ma_layer_norm_forward", "ma_layer_norm_workspace_bytes",
     "ma_layer_norm_backward", "ma_distill_forward", "ma_distill_backward", "ma_distill_loss_grad",
-    "ma_adamw_byte_step_multi",
+    "ma_adamw_byte_step_multi", "ma_head_loss_workspace_bytes", "ma_head_loss_forward",
+    "ma_head_loss_backward", "ma_head_loss_grad",
 )
 MA_STATIC_WORKSPACE_BYTES = 512 << 20
 ABI_VERSION = 6  # include/muon_adamw.h MA_ABI_VERSION
@@ -215,12 +216,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                   ptr, i64, ptr]),
             ("distill_loss_grad", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
                                    ptr, i64, ptr]),
+            ("head_loss_forward", [ptr, i32, i64, i64, i64, ptr, i64, i64, ptr, i32, ptr, ptr, ptr,
+                                   size, ptr]),
+            ("head_loss_backward", [ptr, i32, i64, i64, i64, ptr, i64, i64, ptr, i32, ptr, ptr, ptr,
+                                    i64, ptr, i32, i64, i32, ptr, size, ptr]),
+            ("head_loss_grad", [ptr, i32, i64, i64, i64, ptr, i64, i64, ptr, i32, ptr, ptr, ptr,
+                                i64, ptr, i32, i64, i32, ptr, size, ptr]),
             ("adamw_byte_step_multi", [ctypes.POINTER(_AdamWByteSegment), i32,
                                         ctypes.POINTER(_AdamWByteHParams), ctypes.c_uint64, ptr])):
         fn = getattr(lib, "ma_" + name)
         fn.restype, fn.argtypes = ctypes.c_int, args
     lib.ma_embedding_workspace_bytes.restype = size
     lib.ma_embedding_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.ma_head_loss_workspace_bytes.restype = size
+    lib.ma_head_loss_workspace_bytes.argtypes = [i32, i64, i64, i64, ptr, i64, i32]
     lib.ma_layer_norm_workspace_bytes.restype = size
     lib.ma_layer_norm_workspace_bytes.argtypes = [i64, i64]
     _lib = lib

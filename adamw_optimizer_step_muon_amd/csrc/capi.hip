@@ -726,6 +726,69 @@ ma_status check_dlogits(const DistillCall& c, const Range* in, int ins, Range* d
   return MA_OK;
 }
 
+ma_status check_head_size(int32_t type, int64_t n, int64_t dim, int64_t vocab) {
+  if (const ma_status st = check_type(type, "hidden")) return st;
+  if (n < 0 || dim < 1 || vocab < 1)
+    return fail(MA_ERR_INVALID_ARG, "%lld rows of %lld, vocabulary of %lld", (long long)n, (long long)dim, (long long)vocab);
+  if (n > kMaxThreadsPerLaunch / 1024 || dim > kMaxDim || vocab > kMaxVocab)
+    return fail(MA_ERR_UNSUPPORTED, "%lld rows of %lld, vocabulary of %lld", (long long)n, (long long)dim, (long long)vocab);
+  return MA_OK;
+}
+// Everything of a call but its outputs, whose ranges the caller has put in out; runs it.
+ma_status run_head(HeadCall& c, HeadWork work, const Range* out, int outs, void* ws, size_t ws_bytes, void* stream) {
+  Range r[12] = {};
+  for (int i = 0; i < outs; ++i) r[i] = out[i];
+  Range* in = r + outs;  // workspace, hidden, weight, labels, lse, row_weight
+  if (const ma_status st = check_bits(c.label_bits, "label")) return st;
+  if (const ma_status st = check_rows(c.weight_in, c.type, c.vocab, c.dim, c.weight_in_stride, "weight", &in[2])) return st;
+  const bool gradients = work != kHeadForward;
+  const HeadPlan p = plan_head(c.type, c.n, c.dim, c.vocab, head_weight_copied(c.type, c.dim, c.weight_in, c.weight_in_stride), gradients);
+  if (head_threads(c.type, c.n, c.dim, c.vocab, p) > kMaxThreadsPerLaunch)
+    return fail(MA_ERR_UNSUPPORTED, "%lld rows with a vocabulary of %lld exceed one launch", (long long)c.n, (long long)c.vocab);
+  if (const ma_status st = check_rows(c.hidden, c.type, c.n, c.dim, c.hidden_stride, "hidden", &in[1])) return st;
+  if (const ma_status st = check_pointer(c.labels, c.label_bits / 8, "labels")) return st;
+  in[3] = range_of(c.labels, c.n * (c.label_bits / 8));
+  if (work == kHeadBackward)
+    if (const ma_status st = check_floats(c.lse_in, c.n, "lse", &in[4])) return st;
+  if (gradients)
+    if (const ma_status st = check_floats(c.row_weight, c.n, "row_weight", &in[5])) return st;
+  if (const ma_status st = check_workspace(ws, ws_bytes, static_cast<size_t>(p.bytes), &in[0])) return st;
+  if (const ma_status st = check_disjoint(r, outs + 6, outs + 1, "outputs, workspace or inputs")) return st;
+  const hipError_t e = launch_head(c, p, ws, work, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "head loss launch");
+  return MA_OK;
+}
+// The gradients of a call (either may be NULL): their ranges.
+ma_status check_head_gradients(HeadCall& c, void* dhidden, int64_t dhidden_stride, void* dweight, int32_t dweight_type,
+                               int64_t dweight_stride, int32_t accumulate, Range* r) {
+  if (dhidden && c.n > 0)
+    if (const ma_status st = check_rows(dhidden, c.type, c.n, c.dim, dhidden_stride, "dhidden", &r[0])) return st;
+  if (dweight) {
+    if (dweight_type != MA_F32 && dweight_type != c.type)
+      return fail(MA_ERR_INVALID_ARG, "dweight must be fp32 or of the weight's type");
+    if (accumulate && dweight_type != MA_F32)
+      return fail(MA_ERR_INVALID_ARG, "gradients are added in fp32 only");
+    if (const ma_status st = check_rows(dweight, dweight_type, c.vocab, c.dim, dweight_stride, "dweight", &r[1])) return st;
+  }
+  c.dhidden = dhidden;
+  c.dhidden_stride = dhidden_stride;
+  c.dweight = dweight;
+  c.dweight_type = dweight_type;
+  c.dweight_stride = dweight_stride;
+  c.add = accumulate != 0;
+  return MA_OK;
+}
+
+// The weight's gradient over no rows: zeros, unless it is added to.
+ma_status clear_head_gradient(const HeadCall& c, void* stream) {
+  if (!c.dweight || c.add) return MA_OK;
+  const int64_t blocks = (c.vocab + 3) / 4;
+  if (blocks * 256 > kMaxThreadsPerLaunch) return fail(MA_ERR_UNSUPPORTED, "vocabulary of %lld exceeds one launch", (long long)c.vocab);
+  const hipError_t e = launch_head_clear(c, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "head loss launch");
+  return MA_OK;
+}
+
 // Each device's copy of the static workspace (resolved once per device).
 constexpr int kMaxDevices = 64;
 std::mutex g_static_mu;
@@ -1960,6 +2023,64 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
   const hipError_t e = launch_distill(c, kDistillBoth, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "distillation launch");
   return MA_OK;
+}
+
+size_t ma_head_loss_workspace_bytes(int32_t type, int64_t n, int64_t dim, int64_t vocab, const void* weight,
+                                    int64_t weight_stride, int32_t gradients) {
+  if (type < MA_F32 || type > MA_BF16 || n < 1 || dim < 1 || vocab < 1 || n > kMaxThreadsPerLaunch / 1024 ||
+      dim > kMaxDim || vocab > kMaxVocab)
+    return 0;
+  return static_cast<size_t>(plan_head(type, n, dim, vocab, head_weight_copied(type, dim, weight, weight_stride), gradients != 0).bytes);
+}
+
+ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
+                               const void* weight, int64_t weight_stride, int64_t vocab, const void* labels,
+                               int32_t label_bits, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_head_size(type, n, dim, vocab)) return st;
+  if (n == 0) return MA_OK;
+  HeadCall c{type, hidden, hidden_stride, n, dim, weight, weight_stride, vocab, labels, label_bits};
+  c.loss = loss;
+  c.lse_out = lse;
+  Range out[2] = {};
+  if (const ma_status st = check_floats(loss, n, "loss", &out[0])) return st;
+  if (const ma_status st = check_floats(lse, n, "lse", &out[1])) return st;
+  return run_head(c, kHeadForward, out, 2, workspace, workspace_bytes, stream);
+}
+
+ma_status ma_head_loss_backward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
+                                const void* weight, int64_t weight_stride, int64_t vocab, const void* labels,
+                                int32_t label_bits, const float* lse, const float* row_weight, void* dhidden,
+                                int64_t dhidden_stride, void* dweight, int32_t dweight_type, int64_t dweight_stride,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_head_size(type, n, dim, vocab)) return st;
+  HeadCall c{type, hidden, hidden_stride, n, dim, weight, weight_stride, vocab, labels, label_bits};
+  c.lse_in = lse;
+  c.row_weight = row_weight;
+  Range out[2] = {};
+  if (const ma_status st = check_head_gradients(c, dhidden, dhidden_stride, dweight, dweight_type, dweight_stride, accumulate, out)) return st;
+  if (n == 0) return clear_head_gradient(c, stream);
+  if (!dhidden && !dweight) return MA_OK;
+  return run_head(c, kHeadBackward, out, 2, workspace, workspace_bytes, stream);
+}
+
+ma_status ma_head_loss_grad(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
+                            const void* weight, int64_t weight_stride, int64_t vocab, const void* labels,
+                            int32_t label_bits, const float* row_weight, float* loss, void* dhidden,
+                            int64_t dhidden_stride, void* dweight, int32_t dweight_type, int64_t dweight_stride,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_head_size(type, n, dim, vocab)) return st;
+  HeadCall c{type, hidden, hidden_stride, n, dim, weight, weight_stride, vocab, labels, label_bits};
+  c.row_weight = row_weight;
+  c.loss = loss;
+  Range out[3] = {};
+  if (const ma_status st = check_head_gradients(c, dhidden, dhidden_stride, dweight, dweight_type, dweight_stride, accumulate, out)) return st;
+  if (n == 0) return clear_head_gradient(c, stream);
+  if (const ma_status st = check_floats(loss, n, "loss", &out[2])) return st;
+  return run_head(c, kHeadBoth, out, 3, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,930 @@
+// The LM head with its softmax cross entropy, without keeping the logits.
+//
+//   z = h W^T,  lse_r = log sum_v exp z_rv,  loss_r = lse_r - z_r,label
+//   g = w_r (exp(z - lse) - [v = label]),  dh = g W,  dW = g^T h
+//
+// h: n hidden rows of D values, W: vocab x D, both of one type; labels outside the vocabulary mark
+// rows without a target.  The logits of the forward pass live in registers only: every tile of
+// 256 rows x 256 vocabulary entries leaves its rows' maxima and sums of exponentials, which a
+// second kernel joins.  The backward pass works through pieces of the vocabulary: a piece's logits
+// are computed again, its g is written to the workspace in the hidden type (n x piece values), and
+// two products take it to dh (a sum over pieces, fp32) and to the piece's rows of dW.
+// Arithmetic: 2 n vocab D FLOP forward, 6 n vocab D with the gradients; the logits' second product,
+// the price of not keeping them, makes it 8.
+//
+// Rows with a target (and, for gradients, a weight that is not zero) are gathered first into a
+// padded copy, so the others cost nothing and whatever they hold reaches no result, and tiles need
+// no checks along the rows.
+//
+// Rounding: products of 16-bit values are exact and summed in fp32.  g is rounded once to the
+// hidden type, as the matrix cores take it, after a scaling by a power of two that brings the
+// largest row weight near 2^14: fp16 then keeps probabilities down to 2^-38.  fp32 runs on the fp32
+// matrix instructions.  Every sum has a fixed order: the same inputs give the same bits.
+#include "gemm_tile.h"
+#include "ma_act.h"
+#include "ma_internal.h"
+
+namespace ma {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// ---------------------------------------------------------------------------
+// Rows: which of them take part, and their copies
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 1024;
+
+// One block: numbers the live rows, and finds the power of two for their weights.
+__global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
+  __shared__ int counts[kRowThreads];
+  __shared__ float tops[kRowThreads / 64];
+  const int t = threadIdx.x;
+  const int64_t per = (c.n + kRowThreads - 1) / kRowThreads;
+  const int64_t lo = t * per < c.n ? t * per : c.n, hi = lo + per < c.n ? lo + per : c.n;
+  const auto label_of = [&](int64_t r) -> int64_t {
+    return c.label_bits == 64 ? static_cast<const int64_t*>(c.labels)[r] : static_cast<const int32_t*>(c.labels)[r];
+  };
+  const auto live = [&](int64_t r) {
+    const int64_t l = label_of(r);
+    return l >= 0 && l < c.vocab && !(c.row_weight && c.row_weight[r] == 0.0f);
+  };
+  int mine = 0;
+  float top = 0.0f;
+  for (int64_t r = lo; r < hi; ++r) {
+    if (!live(r)) continue;
+    ++mine;
+    if (c.row_weight) top = fmaxf(top, fabsf(c.row_weight[r]));
+  }
+  counts[t] = mine;
+  top = wave_max(top);
+  if ((t & 63) == 0) tops[t >> 6] = top;
+  __syncthreads();
+  for (int d = 1; d < kRowThreads; d <<= 1) {
+    const int before = t >= d ? counts[t - d] : 0;
+    __syncthreads();
+    counts[t] += before;
+    __syncthreads();
+  }
+  for (int w = 0; w < kRowThreads / 64; ++w) top = fmaxf(top, tops[w]);
+  // the largest weight times 2^shift lies in [2^13, 2^14); fp32 needs no scaling
+  int shift = 13 - (static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 127);
+  if (top == 0.0f || c.type == kActF32) shift = 0;
+  shift = shift > 126 ? 126 : shift;
+  if (t == 0) {
+    c.head->live = counts[kRowThreads - 1];
+    c.head->unscale = __builtin_ldexpf(1.0f, -shift);
+  }
+  int at = counts[t] - mine;
+  for (int64_t r = lo; r < hi; ++r) {
+    if (!live(r)) {
+      c.place[r] = -1;
+      if (c.lse_out) c.lse_out[r] = 0.0f;
+      if (c.loss) c.loss[r] = 0.0f;
+      continue;
+    }
+    c.place[r] = at;
+    c.row_of[at] = static_cast<int>(r);
+    c.label[at] = static_cast<int>(label_of(r));
+    if (c.row_weight) {
+      // exp(z - top) factor = weight exp(z - lse)
+      const float w = __builtin_ldexpf(c.row_weight[r], shift);
+      c.weight[at] = w;
+      c.top[at] = c.lse_in ? c.lse_in[r] : c.tops[r];
+      c.factor[at] = c.lse_in ? w : w / c.sums[r];
+    }
+    ++at;
+  }
+}
+
+// The live rows' padded copies (dim_pad values, zeros behind dim), and zero rows behind the last up
+// to a whole tile.  A wave per row.
+template <typename S>
+__global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int live = c.head->live;
+  if (at >= (live + kHeadTile - 1) / kHeadTile * static_cast<int64_t>(kHeadTile)) return;
+  S* out = static_cast<S*>(c.hidden_pad) + at * c.dim_pad;
+  const S* in = at < live ? static_cast<const S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
+  typedef typename Pack<S, 4>::type P;
+  for (int64_t i = lane * 4; i < c.dim_pad; i += 256) {
+    P x = 0;
+    if (in) {
+      if (i + 4 <= c.dim) {
+        x = *reinterpret_cast<const P*>(in + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < c.dim) x[e] = in[i + e];
+      }
+    }
+    *reinterpret_cast<P*>(out + i) = x;
+  }
+}
+
+// W in rows of dim_pad values, for rows that are not aligned to 16 bytes.  A wave per row.
+__global__ __launch_bounds__(256) void head_weight_kernel(HeadCall c) {
+  const int lane = threadIdx.x & 63;
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (v >= c.vocab) return;
+  const unsigned short* in = static_cast<const unsigned short*>(c.weight_in) + v * c.weight_in_stride;
+  unsigned short* out = static_cast<unsigned short*>(c.weight_pad) + v * c.dim_pad;
+  typedef Pack<unsigned short, 4>::type P;
+  for (int64_t i = lane * 4; i < c.dim_pad; i += 256) {
+    P x = 0;
+    if (i + 4 <= c.dim) {
+      x = *reinterpret_cast<const P*>(in + i);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < c.dim) x[e] = in[i + e];
+    }
+    *reinterpret_cast<P*>(out + i) = x;
+  }
+}
+
+// dW of no rows at all.  A wave per row.
+__global__ __launch_bounds__(256) void head_clear_kernel(HeadCall c) {
+  const int lane = threadIdx.x & 63;
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (v >= c.vocab) return;
+  if (c.dweight_type == kActF32) {
+    for (int64_t i = lane; i < c.dim; i += 64) static_cast<float*>(c.dweight)[v * c.dweight_stride + i] = 0.0f;
+  } else {
+    for (int64_t i = lane; i < c.dim; i += 64) static_cast<unsigned short*>(c.dweight)[v * c.dweight_stride + i] = 0;
+  }
+}
+
+// Joins the tiles' maxima and sums of a row.  A wave per live row.
+__global__ __launch_bounds__(256) void head_join_kernel(HeadCall c) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (at >= c.head->live) return;
+  const float2* part = c.partial + at * c.tiles;
+  float top = -INFINITY;
+  for (int64_t i = lane; i < c.tiles; i += 64) top = fmaxf(top, part[i].x);
+  top = wave_max(top);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  for (int64_t i = lane; i < c.tiles; i += 64) {
+    const float2 p = part[i];
+    // a tile of -inf alone has no share
+    sum += p.x == -INFINITY ? p.y : p.y * __builtin_amdgcn_exp2f((p.x - base) * kLog2e);
+  }
+  sum = wave_sum(sum);
+  if (lane != 0) return;
+  const float log_sum = logf(sum);
+  const int r = c.row_of[at];
+  if (c.loss) c.loss[r] = (top - c.target[at]) + log_sum;
+  if (c.lse_out) c.lse_out[r] = top + log_sum;
+  if (c.tops) {
+    c.tops[r] = top;
+    c.sums[r] = sum;
+  }
+}
+
+// dh from the sums of the splits, a wave per row; rows without a gradient are zero.
+template <int T>
+__global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
+  typedef typename Act<T>::S S;
+  const int lane = threadIdx.x & 63;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (r >= c.n) return;
+  S* out = static_cast<S*>(c.dhidden) + r * c.dhidden_stride;
+  const int at = c.place[r];
+  const float unscale = c.head->unscale;
+  for (int64_t i = lane * 4; i < c.dim; i += 256) {
+    const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (at >= 0) {
+      for (int s = 0; s < c.splits; ++s) {
+        const float* in = c.sum + (s * c.rows_pad + at) * c.sum_stride + i;
+        const f32x4 x = *reinterpret_cast<const f32x4*>(in);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += x[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= unscale;
+    }
+    store_part<T, 4>(out + i, cnt, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles
+// ---------------------------------------------------------------------------
+// What a tile computes: the rows' statistics, g, the sum dh, or rows of dW.
+enum HeadMode { kStats = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
+
+// Blocks go round-robin to the 8 XCDs: each XCD takes a contiguous run of tiles, whose operands its
+// L2 then shares.  Logits: bands of 4 vocabulary tiles, all rows of a band after each other; the
+// others: all columns of a row tile after each other.  False for blocks behind the last tile.
+__device__ __forceinline__ bool head_tile(int mode, int mt, int nt, int splits, int& m, int& n, int& split) {
+  const int tiles = mt * nt * splits;
+  const int per = (tiles + 7) / 8, b = static_cast<int>(blockIdx.x);
+  const int t = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || t >= tiles) return false;
+  split = 0;
+  if (mode == kStats || mode == kGrad) {
+    const int band = t / (4 * mt), rest = t - band * 4 * mt, left = nt - band * 4, width = left < 4 ? left : 4;
+    m = rest / width;
+    n = band * 4 + rest % width;
+  } else {
+    split = t / (mt * nt);
+    const int rest = t - split * mt * nt;
+    n = rest % nt;
+    m = rest / nt;
+  }
+  return true;
+}
+
+// Accumulators of a wave: tile i of 32 rows, tile j of 32 columns; the lane holds row (lane & 31)
+// and columns 8 q + 4 (lane / 32) + e in element 4 q + e.
+template <int T, int kMode, int BM, int BN, int WM, int WN, int WTM, int WTN>
+__device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&acc)[WTM][WTN], int m0, int n0, int split,
+                                              int live, char* smem) {
+  typedef typename Act<T>::S S;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN, frow = lane & 31, half = lane >> 5;
+  const int row0 = wm * (WTM * 32) + frow, col0 = wn * (WTN * 32) + 4 * half;
+  if constexpr (kMode == kStats) {
+    float2* shared = reinterpret_cast<float2*>(smem);  // [WN][BM]
+    const int count = c.vocab - n0 < BN ? static_cast<int>(c.vocab - n0) : BN;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WTM; ++i) {
+      const int row = row0 + i * 32;
+      const int label = m0 + row < live ? c.label[m0 + row] - n0 : -1;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int col = col0 + j * 32 + 8 * (k >> 2) + (k & 3);
+          if (col < count) top = fmaxf(top, acc[i][j][k]);
+          if (col == label) c.target[m0 + row] = acc[i][j][k];
+        }
+      const float base = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int col = col0 + j * 32 + 8 * (k >> 2) + (k & 3);
+          const float e = __builtin_amdgcn_exp2f((acc[i][j][k] - base) * kLog2e);
+          sum += col < count ? e : 0.0f;
+        }
+      // the other half of the columns
+      const float top2 = __shfl_xor(top, 32, 64), sum2 = __shfl_xor(sum, 32, 64);
+      const float both = fmaxf(top, top2), b = both == -INFINITY ? 0.0f : both;
+      sum = (top == -INFINITY ? sum : sum * __builtin_amdgcn_exp2f((top - b) * kLog2e)) +
+            (top2 == -INFINITY ? sum2 : sum2 * __builtin_amdgcn_exp2f((top2 - b) * kLog2e));
+      if (half == 0) shared[wn * BM + row] = make_float2(both, sum);
+    }
+    __syncthreads();
+    for (int row = threadIdx.x; row < BM; row += 64 * WM * WN) {
+      if (m0 + row >= live) break;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) top = fmaxf(top, shared[w * BM + row].x);
+      const float b = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) {
+        const float2 p = shared[w * BM + row];
+        sum += p.x == -INFINITY ? p.y : p.y * __builtin_amdgcn_exp2f((p.x - b) * kLog2e);
+      }
+      c.partial[static_cast<int64_t>(m0 + row) * c.tiles + n0 / BN] = make_float2(top, sum);
+    }
+  } else if constexpr (kMode == kGrad) {
+    // n0 counts from the piece's first entry
+    const int64_t left = c.vocab - c.piece_start - n0;
+    const int count = left < BN ? static_cast<int>(left) : BN;
+    S* out = static_cast<S*>(c.g) + static_cast<int64_t>(m0) * c.piece + n0;
+    if constexpr (T != kActF32) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WTM; ++i) {
+      const int row = row0 + i * 32;
+      const bool on = m0 + row < live;
+      const float top = on ? c.top[m0 + row] : 0.0f, factor = on ? c.factor[m0 + row] : 0.0f;
+      const float weight = on ? c.weight[m0 + row] : 0.0f;
+      const int label = on ? static_cast<int>(c.label[m0 + row] - c.piece_start) - n0 : -1;
+      const int most = on ? count : 0;
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = col0 + j * 32 + 8 * q;
+          float g[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - top) * kLog2e);
+            g[e] = __builtin_fmaf(p, factor, col + e == label ? -weight : 0.0f);
+            if (col + e >= most) g[e] = 0.0f;
+          }
+          if constexpr (T == kActF32) {
+            *reinterpret_cast<f32x4*>(out + static_cast<int64_t>(row) * c.piece + col) = f32x4{g[0], g[1], g[2], g[3]};
+          } else {
+            // staged so that whole rows of the tile leave; 16-byte chunks are XOR-ed with the row
+            u32x2 x;
+            x[0] = Act<T>::down(g[0]) | (static_cast<unsigned>(Act<T>::down(g[1])) << 16);
+            x[1] = Act<T>::down(g[2]) | (static_cast<unsigned>(Act<T>::down(g[3])) << 16);
+            *reinterpret_cast<u32x2*>(smem + row * (BN * 2) + ((((col >> 3) ^ row) & (BN / 8 - 1)) << 4) + (col & 4) * 2) = x;
+          }
+        }
+    }
+    if constexpr (T != kActF32) {
+      __syncthreads();
+      constexpr int kChunks = BN / 8;
+#pragma unroll
+      for (int it = 0; it < BM * kChunks / (64 * WM * WN); ++it) {
+        const int idx = threadIdx.x + it * (64 * WM * WN), row = idx / kChunks, ch = idx % kChunks;
+        const u32x4 x = *reinterpret_cast<const u32x4*>(smem + row * (BN * 2) + (((ch ^ row) & (kChunks - 1)) << 4));
+        *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(row) * c.piece + ch * 8) = x;
+      }
+    }
+  } else if constexpr (kMode == kHidden) {
+    float* out = c.sum + (static_cast<int64_t>(split) * c.rows_pad + m0) * c.sum_stride;
+#pragma unroll
+    for (int i = 0; i < WTM; ++i)
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = n0 + col0 + j * 32 + 8 * q;
+          if (col >= c.sum_stride) continue;  // a multiple of 4
+          f32x4* p = reinterpret_cast<f32x4*>(out + static_cast<int64_t>(row0 + i * 32) * c.sum_stride + col);
+          f32x4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (!c.first) x += *p;
+          *p = x;
+        }
+  } else {
+    const float unscale = c.head->unscale;
+#pragma unroll
+    for (int i = 0; i < WTM; ++i) {
+      const int64_t v = c.piece_start + m0 + row0 + i * 32;
+      if (v >= c.vocab) continue;
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = n0 + col0 + j * 32 + 8 * q;
+          const int cnt = c.dim - col < 4 ? static_cast<int>(c.dim - col) : 4;
+          if (cnt <= 0) continue;
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = acc[i][j][4 * q + e] * unscale;
+          const int64_t at = v * c.dweight_stride + col;
+          if (T == kActF32 || c.dweight_type == kActF32) {
+            float* p = static_cast<float*>(c.dweight) + at;
+            if (c.add) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (e < cnt) x[e] += p[e];
+            }
+            store_part<kActF32, 4>(p, cnt, x);
+          } else {
+            store_part<T, 4>(static_cast<S*>(c.dweight) + at, cnt, x);
+          }
+        }
+    }
+  }
+}
+
+// 16-bit operands: BM x 256 tiles of 8 waves (2 x 4), v_mfma_f32_32x32x16, stages of 64 of the
+// summed index, loaded straight into LDS.  Operands are contiguous along that index (hidden rows and
+// W in the logits, g in dh) or across it (W in dh; g and the hidden rows in dW), which the
+// transposing LDS reads take, so nothing is stored twice.  The accumulators hold a row a lane
+// (operands passed to the matrix instruction the other way round), so a row's maximum and sum
+// need two lanes and four waves only.
+// LDS rings: 3 stages of A and 2 of B for 256 rows (160 KiB), 3 and 3 for fewer.
+template <int BM_, int kMode>
+struct HeadCfg {
+  static constexpr int BM = BM_, BN = 256, BK = 64, WM = 2, WN = 4, kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int SA = 3, SB = BM == 256 ? 2 : 3, LA = SA - 1, LB = SB - 1;
+  static constexpr int WTM = BM / (WM * 32), WTN = BN / (WN * 32);
+  static constexpr bool kAT = kMode == kWeight, kBT = kMode == kHidden || kMode == kWeight;
+  static constexpr int kDmaA = BM * BK / 512 / kWaves, kDmaB = BN * BK / 512 / kWaves, kDma = kDmaA + kDmaB;
+  static constexpr int kAElems = BM * BK, kBElems = BN * BK, kBBase = SA * kAElems;
+  static constexpr int kLds = (SA * kAElems + SB * kBElems) * 2;
+  static_assert(kLds <= 160 * 1024 && BM * BN * 2 <= kLds && kDmaA >= 1, "LDS");
+};
+
+template <int T>
+__device__ __forceinline__ f32x16 head_mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  if constexpr (T == kActBF16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <int T, int BM, int kMode>
+__global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
+  typedef HeadCfg<BM, kMode> C;
+  __shared__ __attribute__((aligned(16))) unsigned short smem[C::kLds / 2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int live = c.head->live;
+  if (live == 0 && kMode != kWeight) return;
+  const int row_tiles = (live + BM - 1) / BM, dim_tiles = static_cast<int>((c.dim + 255) / 256);
+  int mi, ni, split;
+  {
+    int mt, nt, splits = 1;
+    if constexpr (kMode == kStats || kMode == kGrad) {
+      mt = row_tiles;
+      nt = c.piece_tiles;
+    } else if constexpr (kMode == kHidden) {
+      mt = row_tiles;
+      nt = dim_tiles;
+      splits = c.splits;
+    } else {
+      mt = c.piece_tiles;
+      nt = dim_tiles;
+    }
+    if (!head_tile(kMode, mt, nt, splits, mi, ni, split)) return;
+  }
+  const int m0 = mi * BM, n0 = ni * C::BN;
+
+  // operands: base at the tile's first element, row stride, bytes that may be read from there
+  const unsigned short* W = static_cast<const unsigned short*>(c.weight_use) + c.piece_start * c.weight_stride;
+  const int64_t w_left = c.vocab - c.piece_start;  // rows of W from the piece on
+  const unsigned short *gA, *gB;
+  int lda, ldb, k_from = 0, nk;
+  int64_t left_b;  // values of B behind gB
+  if constexpr (kMode == kStats || kMode == kGrad) {
+    gA = static_cast<const unsigned short*>(c.hidden_pad) + static_cast<int64_t>(m0) * c.dim_pad;
+    lda = static_cast<int>(c.dim_pad);
+    gB = W + static_cast<int64_t>(n0) * c.weight_stride;
+    ldb = static_cast<int>(c.weight_stride);
+    left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use;
+    nk = static_cast<int>(c.dim_pad / C::BK);
+  } else if constexpr (kMode == kHidden) {
+    const int all = c.piece_tiles * (256 / C::BK), per = (all + c.splits - 1) / c.splits;
+    k_from = split * per;
+    nk = all - k_from < per ? all - k_from : per;
+    nk = nk < 0 ? 0 : nk;
+    gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(m0) * c.piece + k_from * C::BK;
+    lda = static_cast<int>(c.piece);
+    gB = W + static_cast<int64_t>(k_from) * C::BK * c.weight_stride + n0;
+    ldb = static_cast<int>(c.weight_stride);
+    left_b = (w_left - static_cast<int64_t>(k_from) * C::BK - 1) * c.weight_stride + c.dim_use - n0;
+  } else {
+    nk = (live + C::BK - 1) / C::BK;
+    gA = static_cast<const unsigned short*>(c.g) + m0;
+    lda = static_cast<int>(c.piece);
+    gB = static_cast<const unsigned short*>(c.hidden_pad) + n0;
+    ldb = static_cast<int>(c.dim_pad);
+    left_b = static_cast<int64_t>(nk) * C::BK * c.dim_pad - n0;
+  }
+
+  const auto issue_a = [&](int kt, int i) {
+    unsigned short* s = smem + (kt % C::SA) * C::kAElems;
+    const int q = i * C::kWaves + wave;
+    if constexpr (C::kAT) {
+      constexpr int kChunks = BM / 8, kRows = 64 / kChunks;
+      const int r0 = q * kRows, r = r0 + lane / kChunks, ch = lane % kChunks;
+      dma16<C::kBT>(gA + static_cast<int64_t>(kt) * C::BK * lda, (r * lda + swz_kn(r, ch) * 8) * 2,
+                    static_cast<unsigned>(((C::BK - 1) * lda + BM) * 2), s + r0 * BM);
+    } else {
+      const int r0 = q * 8, r = r0 + lane / 8;
+      dma16<C::kBT>(gA + kt * C::BK, (r * lda + swz<64>(r, lane % 8) * 8) * 2,
+                    static_cast<unsigned>(((BM - 1) * lda + C::BK) * 2), s + r0 * C::BK);
+    }
+  };
+  const auto issue_b = [&](int kt, int i) {
+    unsigned short* s = smem + C::kBBase + (kt % C::SB) * C::kBElems;
+    const int q = i * C::kWaves + wave;
+    // reads behind the operand's end return zeros: vocabulary entries behind the last, and (below)
+    // columns behind the hidden size, where W's next row follows
+    if constexpr (C::kBT) {
+      constexpr int kChunks = C::BN / 8, kRows = 64 / kChunks;
+      const int r0 = q * kRows, r = r0 + lane / kChunks, ch = lane % kChunks;
+      const int64_t left = left_b - static_cast<int64_t>(kt) * C::BK * ldb;
+      const int64_t most = static_cast<int64_t>(C::BK - 1) * ldb + C::BN;
+      const int64_t values = left < 0 ? 0 : left < most ? left : most;
+      dma16<C::kBT>(gB + static_cast<int64_t>(kt) * C::BK * ldb, (r * ldb + swz_kn(r, ch) * 8) * 2,
+                    static_cast<unsigned>(values * 2), s + r0 * C::BN);
+    } else {
+      const int r0 = q * 8, r = r0 + lane / 8, ch = swz<64>(r, lane % 8);
+      const int64_t left = left_b - kt * C::BK;
+      const int64_t most = static_cast<int64_t>(C::BN - 1) * ldb + C::BK;
+      const int64_t values = left < 0 ? 0 : left < most ? left : most;
+      const int off = kt * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
+      dma16<C::kBT>(gB + kt * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
+    }
+  };
+  // group v of the loads: A of stage v + LA, B of stage v + LB (the shorter lead first)
+  const auto issue_group = [&](int v) {
+#pragma unroll
+    for (int i = 0; i < C::kDmaB; ++i)
+      if (v + C::LB >= 0 && v + C::LB < nk) issue_b(v + C::LB, i);
+#pragma unroll
+    for (int i = 0; i < C::kDmaA; ++i)
+      if (v + C::LA >= 0 && v + C::LA < nk) issue_a(v + C::LA, i);
+  };
+  // until stage st has landed: what was issued after it may stay in flight
+  const auto wait_stage = [&](int st) {
+    if (st + 1 >= nk) wait_vmcnt<0>();
+    else if constexpr (C::SA != C::SB) wait_vmcnt<C::kDmaA>();
+    else wait_vmcnt<C::kDma>();
+  };
+  const int frow = lane & 31, fkh = lane >> 5;
+  const auto read_t = [&](const unsigned short* s, int width, int col0, int kk) {
+    // rows kk 16 + 8 (lane / 32) + 0..7 of column col0 + lane % 32, two transposing reads of 4 rows
+    const int g16 = lane >> 4, sl = lane & 15;
+    const int col = col0 + 16 * (g16 & 1) + 4 * (sl & 3), row = kk * 16 + 8 * (g16 >> 1) + (sl >> 2);
+    const s16x4 lo = lds_read_tr(s + row * width + swz_kn(row, col >> 3) * 8 + (col & 7));
+    const s16x4 hi = lds_read_tr(s + (row + 4) * width + swz_kn(row + 4, col >> 3) * 8 + (col & 7));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  const auto read_k = [&](const unsigned short* s, int r, int kk) {
+    return *reinterpret_cast<const bf16x8*>(s + r * C::BK + swz<64>(r, kk * 2 + fkh) * 8);
+  };
+  const auto load_frags = [&](int kt, int kk, bf16x8 (&fa)[C::WTM], bf16x8 (&fb)[C::WTN]) {
+    const unsigned short* as = smem + (kt % C::SA) * C::kAElems;
+    const unsigned short* bs = smem + C::kBBase + (kt % C::SB) * C::kBElems;
+#pragma unroll
+    for (int i = 0; i < C::WTM; ++i) {
+      const int r = wm * (C::WTM * 32) + i * 32;
+      if constexpr (C::kAT) fa[i] = read_t(as, BM, r, kk);
+      else fa[i] = read_k(as, r + frow, kk);
+    }
+#pragma unroll
+    for (int j = 0; j < C::WTN; ++j) {
+      const int r = wn * (C::WTN * 32) + j * 32;
+      if constexpr (C::kBT) fb[j] = read_t(bs, C::BN, r, kk);
+      else fb[j] = read_k(bs, r + frow, kk);
+    }
+  };
+
+  f32x16 acc[C::WTM][C::WTN];
+#pragma unroll
+  for (int i = 0; i < C::WTM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::WTN; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
+
+  if (nk > 0) {
+    constexpr int KK = C::BK / 16;
+#pragma unroll
+    for (int v = -C::LA; v < 0; ++v) issue_group(v);
+    bf16x8 fa[2][C::WTM], fb[2][C::WTN];
+    wait_stage(0);
+    stage_barrier();
+    load_frags(0, 0, fa[0], fb[0]);
+    const auto run_stage = [&](int kt, auto steady) {
+      constexpr bool kSteady = decltype(steady)::value;
+      if constexpr (kSteady) {
+#pragma unroll
+        for (int i = 0; i < C::kDmaB; ++i) issue_b(kt + C::LB, i);
+#pragma unroll
+        for (int i = 0; i < C::kDmaA; ++i) issue_a(kt + C::LA, i);
+      } else {
+        issue_group(kt);
+      }
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        const int cur = kk & 1;
+        if (kk + 1 < KK) {
+          load_frags(kt, kk + 1, fa[cur ^ 1], fb[cur ^ 1]);
+        } else if (kSteady || kt + 1 < nk) {
+          // stage kt + 1 has landed and every wave's reads of this stage are done
+          if constexpr (kSteady) {
+            if constexpr (C::SA != C::SB) wait_vmcnt<C::kDmaA>();
+            else wait_vmcnt<C::kDma>();
+          } else {
+            wait_stage(kt + 1);
+          }
+          stage_barrier();
+          load_frags(kt + 1, 0, fa[cur ^ 1], fb[cur ^ 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < C::WTM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::WTN; ++j) acc[i][j] = head_mfma<T>(fb[cur][j], fa[cur][i], acc[i][j]);
+      }
+    };
+    int kt = 0;
+    for (; kt < nk - C::SA; ++kt) run_stage(kt, std::true_type{});
+    for (; kt < nk; ++kt) run_stage(kt, std::false_type{});
+  }
+  head_epilogue<T, kMode, BM, C::BN, C::WM, C::WN>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(smem));
+}
+
+// fp32 operands: 128 x 128 tiles of 4 waves (2 x 2), v_mfma_f32_32x32x2, stages of 16 of the summed
+// index that pass through registers into LDS rows of one index each, whatever the operand's order.
+template <int kMode>
+__global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
+  constexpr int B = 128, BK = 16, LD = B + 4;
+  __shared__ __attribute__((aligned(16))) float smem[2][2][BK * LD];
+  constexpr bool kAT = kMode == kWeight, kBT = kMode == kHidden || kMode == kWeight;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int live = c.head->live;
+  if (live == 0 && kMode != kWeight) return;
+  const int row_tiles = (live + B - 1) / B, dim_tiles = static_cast<int>((c.dim + B - 1) / B);
+  int mi, ni, split;
+  {
+    int mt, nt, splits = 1;
+    if constexpr (kMode == kStats || kMode == kGrad) {
+      mt = row_tiles;
+      nt = c.piece_tiles;
+    } else if constexpr (kMode == kHidden) {
+      mt = row_tiles;
+      nt = dim_tiles;
+      splits = c.splits;
+    } else {
+      mt = c.piece_tiles;
+      nt = dim_tiles;
+    }
+    if (!head_tile(kMode, mt, nt, splits, mi, ni, split)) return;
+  }
+  const int m0 = mi * B, n0 = ni * B;
+  const float* W = static_cast<const float*>(c.weight_use) + c.piece_start * c.weight_stride;
+  const int64_t w_left = c.vocab - c.piece_start;
+  // operand (row, k): contiguous along k, or along the rows (T); rows and ks below their counts
+  const float *gA, *gB;
+  int64_t lda, ldb, rows_b;
+  int k0 = 0, k1, ks_b;  // the summed indices k0 .. k1 - 1, and where B's end
+  if constexpr (kMode == kStats || kMode == kGrad) {
+    gA = static_cast<const float*>(c.hidden_pad) + static_cast<int64_t>(m0) * c.dim_pad;
+    lda = c.dim_pad;
+    gB = W + static_cast<int64_t>(n0) * c.weight_stride;
+    ldb = c.weight_stride;
+    rows_b = w_left - n0;
+    k1 = static_cast<int>(c.dim_pad);
+    ks_b = static_cast<int>(c.dim);
+  } else if constexpr (kMode == kHidden) {
+    const int all = c.piece_tiles * (B / BK), per = (all + c.splits - 1) / c.splits;
+    k0 = split * per * BK;
+    k1 = min(all, (split + 1) * per) * BK;
+    gA = static_cast<const float*>(c.g) + static_cast<int64_t>(m0) * c.piece;
+    lda = c.piece;
+    gB = W + n0;
+    ldb = c.weight_stride;
+    rows_b = c.dim - n0;
+    ks_b = w_left < k1 ? static_cast<int>(w_left) : k1;
+  } else {
+    k1 = (live + BK - 1) / BK * BK;
+    gA = static_cast<const float*>(c.g) + m0;
+    lda = c.piece;
+    gB = static_cast<const float*>(c.hidden_pad) + n0;
+    ldb = c.dim_pad;
+    rows_b = c.dim_pad - n0;
+    ks_b = k1;
+  }
+  // a thread's two vectors of 4 values of an operand's stage: A is padded to whole tiles, B checked
+  typedef Pack<float, 4>::type P;
+  f32x4 ra[2], rb[2];
+  const auto load = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = tid + u * 256;
+      if constexpr (kAT) ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(k + x / 32) * lda + x % 32 * 4);
+      else ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(x / 4) * lda + k + x % 4 * 4);
+      const int row = kBT ? x % 32 * 4 : x / 4, kk = k + (kBT ? x / 32 : x % 4 * 4);
+      const float* p = gB + (kBT ? static_cast<int64_t>(kk) * ldb + row : static_cast<int64_t>(row) * ldb + kk);
+      // the values that are there: along the rows, or along k
+      const int64_t there = kBT ? (kk < ks_b ? rows_b - row : 0) : (row < rows_b ? ks_b - kk : 0);
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (there >= 4) {
+        const P w = *reinterpret_cast<const P*>(p);
+        v = f32x4{w[0], w[1], w[2], w[3]};
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e < there) v[e] = p[e];
+      }
+      rb[u] = v;
+    }
+  };
+  const auto store = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = tid + u * 256;
+      float *a = smem[buf][0], *b = smem[buf][1];
+      if constexpr (kAT) {
+        *reinterpret_cast<f32x4*>(a + x / 32 * LD + x % 32 * 4) = ra[u];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[(x % 4 * 4 + e) * LD + x / 4] = ra[u][e];
+      }
+      if constexpr (kBT) {
+        *reinterpret_cast<f32x4*>(b + x / 32 * LD + x % 32 * 4) = rb[u];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[(x % 4 * 4 + e) * LD + x / 4] = rb[u][e];
+      }
+    }
+  };
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
+  if (k0 < k1) {
+    load(k0);
+    store(0);
+    __syncthreads();
+    int buf = 0;
+    for (int k = k0; k < k1; k += BK, buf ^= 1) {
+      const bool more = k + BK < k1;
+      if (more) load(k + BK);
+      const float *a = smem[buf][0] + (lane >> 5) * LD + wm * 64 + (lane & 31);
+      const float *b = smem[buf][1] + (lane >> 5) * LD + wn * 64 + (lane & 31);
+#pragma unroll
+      for (int kk = 0; kk < BK; kk += 2) {
+        const float a0 = a[kk * LD], a1 = a[kk * LD + 32], b0 = b[kk * LD], b1 = b[kk * LD + 32];
+        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a0, acc[0][0], 0, 0, 0);
+        acc[0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a0, acc[0][1], 0, 0, 0);
+        acc[1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a1, acc[1][0], 0, 0, 0);
+        acc[1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a1, acc[1][1], 0, 0, 0);
+      }
+      if (more) store(buf ^ 1);
+      __syncthreads();
+    }
+  }
+  head_epilogue<kActF32, kMode, B, B, 2, 2>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(&smem[0][0][0]));
+}
+
+// Host: blocks of a launch over `tiles` tiles at most (see head_tile).
+dim3 head_grid(int64_t tiles) { return dim3(static_cast<unsigned>(8 * ((tiles + 7) / 8))); }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int T, int BM, int kMode>
+hipError_t launch_head_gemm(const HeadCall& c, int64_t tiles, hipStream_t s) {
+  if constexpr (T == kActF32)
+    hipLaunchKernelGGL((head_gemm32_kernel<kMode>), head_grid(tiles), dim3(256), 0, s, c);
+  else
+    hipLaunchKernelGGL((head_gemm_kernel<T, BM, kMode>), head_grid(tiles), dim3(512), 0, s, c);
+  return hipGetLastError();
+}
+
+template <int T, int kMode>
+hipError_t launch_head_rows(const HeadCall& c, int64_t cols, hipStream_t s) {
+  if constexpr (T == kActF32) return launch_head_gemm<T, 128, kMode>(c, ceil_div(c.n, 128) * cols, s);
+  else if (c.n <= 64) return launch_head_gemm<T, 64, kMode>(c, cols, s);
+  else if (c.n <= 128) return launch_head_gemm<T, 128, kMode>(c, cols, s);
+  else return launch_head_gemm<T, 256, kMode>(c, ceil_div(c.n, 256) * cols, s);
+}
+
+template <int T>
+hipError_t gather(const HeadCall& c, hipStream_t s) {
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kRowThreads), 0, s, c);
+  hipLaunchKernelGGL((head_gather_kernel<typename Act<T>::S>), dim3(static_cast<unsigned>(c.rows_pad / 4)), dim3(256), 0, s, c);
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t forward(const HeadCall& call, hipStream_t s) {
+  HeadCall c = call;
+  c.row_weight = nullptr;
+  c.lse_in = nullptr;
+  constexpr int kTile = T == kActF32 ? 128 : 256;
+  c.piece_start = 0;
+  c.piece_tiles = static_cast<int>(ceil_div(c.vocab, kTile));
+  c.tiles = c.piece_tiles;
+  if (const hipError_t e = gather<T>(c, s)) return e;
+  if (const hipError_t e = launch_head_rows<T, kStats>(c, c.piece_tiles, s)) return e;
+  hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t backward(const HeadCall& call, hipStream_t s) {
+  HeadCall c = call;
+  c.loss = nullptr;
+  c.lse_out = nullptr;
+  constexpr int kTile = T == kActF32 ? 128 : 256;
+  if (const hipError_t e = gather<T>(c, s)) return e;
+  const int64_t dim_tiles = ceil_div(c.dim, kTile);
+  for (int64_t v = 0; v < c.vocab; v += c.piece) {
+    c.piece_start = v;
+    c.first = v == 0;
+    const int64_t here = c.vocab - v < c.piece ? c.vocab - v : c.piece;
+    c.piece_tiles = static_cast<int>(ceil_div(here, kTile));
+    if (const hipError_t e = launch_head_rows<T, kGrad>(c, c.piece_tiles, s)) return e;
+    if (c.dhidden)
+      if (const hipError_t e = launch_head_rows<T, kHidden>(c, dim_tiles * c.splits, s)) return e;
+    if (c.dweight)
+      if (const hipError_t e = launch_head_gemm<T, 256, kWeight>(c, c.piece_tiles * dim_tiles, s)) return e;
+  }
+  if (c.dhidden)
+    hipLaunchKernelGGL((head_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
+  return hipGetLastError();
+}
+
+int64_t align_up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
+
+}  // namespace
+
+bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride) {
+  // (offsets inside a tile of 256 rows have 31 bits)
+  return type != kActF32 && ((reinterpret_cast<uintptr_t>(weight) & 15u) || stride % 8 || dim % 8 || stride > (1 << 22));
+}
+
+int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p) {
+  const int64_t rows = type == kActF32 ? 128 : n <= 64 ? 64 : n <= 128 ? 128 : 256, tile = type == kActF32 ? 128 : 256;
+  const int64_t row_tiles = ceil_div(n, rows), dim_tiles = ceil_div(dim, tile);
+  int64_t tiles = row_tiles * ceil_div(vocab, tile);
+  const int64_t others[] = {row_tiles * dim_tiles * p.splits, p.piece / tile * dim_tiles};
+  for (const int64_t t : others) tiles = t > tiles ? t : tiles;
+  return (tiles + 8) * 512;
+}
+
+HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, bool gradients) {
+  const int64_t size = type == kActF32 ? 4 : 2, tile = type == kActF32 ? 128 : 256;
+  HeadPlan p{};
+  p.rows_pad = align_up(n, kHeadTile);
+  p.dim_pad = align_up(dim, 64);
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at = align_up(at + bytes, 256);
+    return here;
+  };
+  p.head = take(sizeof(HeadInfo));
+  p.place = take(n * 4);
+  p.row_of = take(n * 4);
+  p.label = take(n * 4);
+  p.target = take(n * 4);
+  p.weight = take(n * 4);
+  p.top = take(n * 4);
+  p.factor = take(n * 4);
+  p.tops = take(n * 4);
+  p.sums = take(n * 4);
+  // a tile's columns behind the hidden size are read (and dropped) up to a whole tile
+  p.hidden = take((p.rows_pad * p.dim_pad + tile) * size);
+  p.weight_pad = copied ? take(vocab * p.dim_pad * size) : 0;
+  // the statistics of the forward pass lie where the backward pass has g
+  const int64_t tiles = ceil_div(vocab, tile);
+  int64_t piece = kHeadPieceBytes / (p.rows_pad * size) / tile;
+  piece = piece < 1 ? 1 : piece;
+  p.pieces = ceil_div(tiles, piece);
+  p.piece = ceil_div(tiles, p.pieces) * tile;
+  const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.piece * size : 0;
+  p.partial = take(stats > g ? stats : g);
+  p.splits = 1;
+  p.sum_stride = align_up(dim, 4);
+  if (gradients) {
+    // enough blocks for the chip: two a compute unit, each with 1024 vocabulary entries at least
+    const int64_t rows = type == kActF32 ? 128 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+    const int64_t blocks = ceil_div(n, rows) * ceil_div(dim, tile);
+    int64_t splits = 512 / blocks, most = p.piece / 1024;
+    splits = splits > most ? most : splits;
+    p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+    p.sum = take(p.splits * p.rows_pad * p.sum_stride * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_head_clear(const HeadCall& c, hipStream_t s) {
+  hipLaunchKernelGGL(head_clear_kernel, dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
+  return hipGetLastError();
+}
+
+hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace, HeadWork work, hipStream_t s) {
+  HeadCall c = call;
+  char* ws = static_cast<char*>(workspace);
+  c.head = reinterpret_cast<HeadInfo*>(ws + p.head);
+  c.place = reinterpret_cast<int*>(ws + p.place);
+  c.row_of = reinterpret_cast<int*>(ws + p.row_of);
+  c.label = reinterpret_cast<int*>(ws + p.label);
+  c.target = reinterpret_cast<float*>(ws + p.target);
+  c.weight = reinterpret_cast<float*>(ws + p.weight);
+  c.top = reinterpret_cast<float*>(ws + p.top);
+  c.factor = reinterpret_cast<float*>(ws + p.factor);
+  c.tops = work == kHeadBoth ? reinterpret_cast<float*>(ws + p.tops) : nullptr;
+  c.sums = work == kHeadBoth ? reinterpret_cast<float*>(ws + p.sums) : nullptr;
+  c.hidden_pad = ws + p.hidden;
+  c.partial = reinterpret_cast<float2*>(ws + p.partial);
+  c.g = ws + p.partial;
+  c.sum = reinterpret_cast<float*>(ws + p.sum);
+  c.rows_pad = p.rows_pad;
+  c.dim_pad = p.dim_pad;
+  c.sum_stride = p.sum_stride;
+  c.piece = p.piece;
+  c.splits = p.splits;
+  c.weight_use = c.weight_in;
+  c.weight_stride = c.weight_in_stride;
+  c.dim_use = c.dim;
+  if (p.weight_pad) {
+    c.weight_pad = ws + p.weight_pad;
+    c.weight_use = c.weight_pad;
+    c.weight_stride = c.dim_use = p.dim_pad;
+    hipLaunchKernelGGL(head_weight_kernel, dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
+    if (const hipError_t e = hipGetLastError()) return e;
+  }
+  return with_act(c.type, [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    if (work != kHeadBackward)
+      if (const hipError_t e = forward<T>(c, s)) return e;
+    return work != kHeadForward ? backward<T>(c, s) : hipSuccess;
+  });
+}
+
+}  // namespace ma

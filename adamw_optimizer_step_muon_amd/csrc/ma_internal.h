@@ -532,4 +532,65 @@ constexpr int kMaxDistillTop = 1024;
 enum DistillMode { kDistillForward = 0, kDistillBackward = 1, kDistillBoth = 2 };
 hipError_t launch_distill(const DistillCall& c, DistillMode mode, hipStream_t s);
 
+// The LM head's cross entropy (head_loss.hip).
+constexpr int kHeadTile = 256;  // gathered rows are padded to a multiple of this
+constexpr int64_t kHeadPieceBytes = int64_t{512} << 20;  // of g, for up to 2^20 rows
+struct HeadInfo {
+  int live;       // rows that take part
+  float unscale;  // of the products with g
+};
+// Workspace: byte offsets, and what its sizes settle.
+struct HeadPlan {
+  int64_t head, place, row_of, label, target, weight, top, factor, tops, sums, hidden, weight_pad, partial, sum, bytes;
+  int64_t rows_pad, dim_pad, sum_stride, piece, pieces;
+  int splits;
+};
+// Whether the weight's rows must be copied to be aligned to 16 bytes.
+bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride);
+HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, bool gradients);
+// Threads of the call's largest launch, at most.
+int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p);
+struct HeadCall {
+  int type;
+  const void* hidden;
+  int64_t hidden_stride, n, dim;
+  const void* weight_in;
+  int64_t weight_in_stride, vocab;
+  const void* labels;
+  int label_bits;
+  const float* lse_in;      // backward alone
+  const float* row_weight;  // gradients
+  float* loss;              // may be null
+  float* lse_out;           // may be null
+  void* dhidden;            // may be null
+  int64_t dhidden_stride;
+  void* dweight;            // may be null
+  int dweight_type;         // the weight's type or fp32
+  int64_t dweight_stride;
+  bool add;                 // to an fp32 dweight
+  // set by launch_head
+  HeadInfo* head;
+  int* place;      // per row: its number among the live ones, or -1
+  int* row_of;     // per live row, from here on
+  int* label;
+  float* target;   // the label's logit
+  float* weight;   // row weight, scaled
+  float* top;      // g = exp(z - top) factor - [label] weight
+  float* factor;
+  float* tops;     // per row: largest logit and sum of exponentials, for both directions at once
+  float* sums;
+  void* hidden_pad;
+  void* weight_pad;
+  const void* weight_use;
+  float2* partial;  // per live row and tile
+  void* g;          // rows_pad x piece
+  float* sum;       // splits x rows_pad x sum_stride
+  int64_t rows_pad, dim_pad, dim_use, weight_stride, sum_stride, piece, tiles, piece_start;
+  int piece_tiles, splits;
+  bool first;
+};
+hipError_t launch_head_clear(const HeadCall& c, hipStream_t s);  // dweight = 0
+enum HeadWork { kHeadForward = 0, kHeadBackward = 1, kHeadBoth = 2 };
+hipError_t launch_head(const HeadCall& c, const HeadPlan& p, void* workspace, HeadWork work, hipStream_t s);
+
 }  // namespace ma

@@ -1,9 +1,10 @@
-"""Training operators around the AdamW parameters: embedding, layer norm, distillation.
+"""Training operators around the AdamW parameters: embedding, layer norm, distillation, the LM
+head's cross entropy, and the AdamW step with moments in 8 bits.
 
 Two layers.  The entry points (``embedding_forward`` and the like) are the C ABI's calls
 without the ma_ prefix: tensors are checked, their pointers and the stream handed over, a
-negative status raised as MuonAdamWError.  ``embedding``, ``layer_norm`` and ``distill_loss``
-are the same operators for torch's autograd, so that ``loss.backward()`` runs the library's
+negative status raised as MuonAdamWError.  ``embedding``, ``layer_norm``, ``distill_loss`` and
+``head_loss`` are the same operators for torch's autograd, so that ``loss.backward()`` runs the library's
 kernels; ``embedding`` can hand its table gradient to a MuonAdamW in token form, which
 ``step()`` then applies without building the dense gradient.
 
@@ -437,6 +438,113 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
 
 
 # --------------------------------------------------------------------------
+# the LM head's cross entropy
+# --------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def _head_workspace(dtype: int, n: int, dim: int, vocab: int, aligned: int, stride: int, gradients: bool) -> int:
+    # of the weight's address only its alignment counts
+    return int(load().ma_head_loss_workspace_bytes(dtype, n, dim, vocab, 256 + aligned, stride, gradients))
+
+
+def head_loss_workspace_bytes(hidden, weight, *, gradients: bool = True) -> int:
+    """Workspace of the head loss calls on these tensors; gradients False: of the forward call."""
+    n, dim, _ = _rows("hidden", hidden, anywhere=True)
+    vocab, _, stride = _rows("weight", weight, anywhere=True)
+    return _head_workspace(_type("hidden", hidden.dtype), n, dim, vocab, weight.data_ptr() % 16, stride, bool(gradients))
+
+
+def _head(hidden, weight, labels, gradients, workspace, stream):
+    """The leading arguments shared by the three calls, the number of rows, the workspace, and
+    what the arguments' addresses need alive."""
+    n, dim, hidden_stride = _rows("hidden", hidden)
+    device, dtype = hidden.device, _type("hidden", hidden.dtype)
+    vocab, wdim, weight_stride = _rows("weight", weight, device)
+    if weight.dim() != 2 or wdim != dim or weight.dtype != hidden.dtype:
+        raise ValueError(f"weight must be (vocab, {dim}) of {hidden.dtype}")
+    bits = _ints("labels", labels, device)
+    if labels.shape != hidden.shape[:-1]:
+        raise ValueError("labels must have the hidden states' leading dimensions")
+    at = labels if labels.is_contiguous() else _contiguous(labels, stream)
+    need = _head_workspace(dtype, n, dim, vocab, weight.data_ptr() % 16, weight_stride, gradients)
+    keep, ws, size = _workspace(workspace, need, hidden, stream)
+    return (hidden.data_ptr(), dtype, hidden_stride, n, dim, weight.data_ptr(), weight_stride, vocab, at.data_ptr(),
+            bits), n, (ws, size), (keep, at)
+
+
+def _head_gradients(hidden, weight, hidden_grad, weight_grad, dweight, accumulate, stream):
+    """(dhidden, dweight, their arguments)"""
+    if dweight is not None and not weight_grad:
+        raise ValueError("a gradient buffer is given for a gradient that is not wanted")
+    if accumulate and dweight is None and weight_grad:
+        raise ValueError("accumulate needs a dweight to add to")
+    dhidden = _like(hidden, stream) if hidden_grad else None
+    stride = max(hidden.shape[-1], 1)
+    dtype = _type("weight", weight.dtype)
+    if dweight is not None:
+        _tensor("dweight", dweight, hidden.device)
+        if dweight.shape != weight.shape or dweight.dtype not in (torch.float32, weight.dtype):
+            raise ValueError("dweight must have the weight's shape, and its type or float32")
+        dtype, stride = _type("dweight", dweight.dtype), _rows("dweight", dweight, hidden.device)[2]
+    elif weight_grad:
+        dweight = _like(weight, stream)
+    return dhidden, dweight, (_address(dhidden), max(hidden.shape[-1], 1), _address(dweight), dtype, stride,
+                              int(bool(accumulate)))
+
+
+def _address(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def head_loss_forward(hidden, weight, labels, *, workspace=None, stream=None):
+    """(loss, lse) of ma_head_loss_forward: the softmax cross entropy of labels (int32 or int64, the
+    hidden states' leading dimensions) under the logits hidden (..., dim) @ weight (vocab, dim).T,
+    which are not kept.  hidden and weight have one type; weight is the head in that type (see
+    adamw_byte_step_multi's copies).  A label outside the vocabulary marks a row without a target:
+    loss and lse 0.  lse, the logarithm of the sum of exponentials, is the backward pass's input."""
+    args, _, space, _keep = _head(hidden, weight, labels, False, workspace, stream)
+    loss = _empty(hidden, hidden.shape[:-1], torch.float32, stream)
+    lse = _like(loss, stream)
+    _call("ma_head_loss_forward", hidden.device, stream, *args, loss.data_ptr(), lse.data_ptr(), *space)
+    if stream is not None:
+        _record(stream, hidden, weight, labels, *_keep)
+    return loss, lse
+
+
+def head_loss_backward(hidden, weight, labels, lse, row_weight, *, hidden_grad: bool = True,
+                       weight_grad: bool = True, dweight=None, accumulate: bool = False,
+                       workspace=None, stream=None):
+    """(dhidden, dweight) of ma_head_loss_backward: the gradients of sum row_weight * loss.  Either
+    can be left out (None).  dweight has the weight's type, or is given: of that type, or float32
+    and with accumulate added to.  The logits' gradients are rounded to the hidden type once."""
+    args, n, space, _keep = _head(hidden, weight, labels, True, workspace, stream)
+    device, given = hidden.device, dweight
+    rows = _floats("lse", lse, n, device), _floats("row_weight", row_weight, n, device)
+    dhidden, dweight, outs = _head_gradients(hidden, weight, hidden_grad, weight_grad, dweight, accumulate, stream)
+    _call("ma_head_loss_backward", device, stream, *args, *rows, *outs, *space)
+    if given is not None:
+        _wrote(given)
+    if stream is not None:
+        _record(stream, hidden, weight, labels, lse, row_weight, given, *_keep)
+    return dhidden, dweight
+
+
+def head_loss_grad(hidden, weight, labels, row_weight, *, hidden_grad: bool = True, weight_grad: bool = True,
+                   dweight=None, accumulate: bool = False, workspace=None, stream=None):
+    """(loss, dhidden, dweight) in one call (ma_head_loss_grad), for a row_weight known beforehand."""
+    args, n, space, _keep = _head(hidden, weight, labels, True, workspace, stream)
+    device, given = hidden.device, dweight
+    row = _floats("row_weight", row_weight, n, device)
+    loss = _empty(hidden, hidden.shape[:-1], torch.float32, stream)
+    dhidden, dweight, outs = _head_gradients(hidden, weight, hidden_grad, weight_grad, dweight, accumulate, stream)
+    _call("ma_head_loss_grad", device, stream, *args, row, loss.data_ptr(), *outs, *space)
+    if given is not None:
+        _wrote(given)
+    if stream is not None:
+        _record(stream, hidden, weight, labels, row_weight, given, *_keep)
+    return loss, dhidden, dweight
+
+
+# --------------------------------------------------------------------------
 # AdamW with both moments in 8 bits
 # --------------------------------------------------------------------------
 ADAMW_BYTE_BLOCK = 64  # elements that share a scale
@@ -582,6 +690,32 @@ class _DistillLoss(torch.autograd.Function):
                                 temperature=ctx.temperature), None, None, None
 
 
+class _HeadLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, labels, copy):
+        # (under autograd a weight of another type is the parameter that `copy` stands for)
+        used = weight.detach().to(hidden.dtype) if copy is None else copy
+        labels = labels.contiguous()
+        loss, lse = head_loss_forward(hidden, used, labels)
+        ctx.save_for_backward(hidden, used, labels, lse)
+        ctx.dtype = weight.dtype
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        hidden, used, labels, lse = ctx.saved_tensors
+        hidden_grad, weight_grad = ctx.needs_input_grad[:2]
+        if not (hidden_grad or weight_grad):
+            return None, None, None, None
+        dweight = None
+        if weight_grad and ctx.dtype != used.dtype:
+            dweight = torch.empty(used.shape, dtype=ctx.dtype, device=used.device)
+        dhidden, dweight = head_loss_backward(hidden, used, labels, lse, dloss.contiguous(), hidden_grad=hidden_grad,
+                                              weight_grad=weight_grad, dweight=dweight)
+        return dhidden, dweight, None, None
+
+
 def embedding(tokens, table, *, scale: float = 1.0, out_dtype=None, optimizer=None):
     """scale * table[tokens], differentiable by the fp32 table; a token outside the table is
     padding (zero row, no gradient).  With `optimizer` (the MuonAdamW that holds the table in
@@ -603,3 +737,16 @@ def distill_loss(logits, teacher, ids, *, temperature: float = 1.0):
     """The distillation loss of each row (see distill_forward), differentiable by the logits;
     the teacher is constant."""
     return _DistillLoss.apply(logits, teacher, ids, float(temperature))
+
+
+def head_loss(hidden, weight, labels, *, copy=None):
+    """The softmax cross entropy of each label under the LM head's logits (see head_loss_forward),
+    differentiable by the hidden states and the weight.  An fp32 weight under 16-bit hidden states
+    is rounded to their type for the call, or `copy` is read in its place: the weight in that type,
+    as a MuonAdamW group with 8-bit moments keeps it (`copies`).  The weight's gradient is fp32
+    then."""
+    if copy is not None and (copy.shape != weight.shape or copy.dtype != hidden.dtype):
+        raise ValueError("copy must have the weight's shape and the hidden states' type")
+    if weight.dtype not in (torch.float32, hidden.dtype):
+        raise ValueError("weight must be float32 or have the hidden states' type")
+    return _HeadLoss.apply(hidden, weight, labels, copy)

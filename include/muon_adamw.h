@@ -536,6 +536,49 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
                                int64_t top, float temperature, const float* row_weight, float* loss,
                                void* dlogits, int64_t dlogits_stride, void* stream);
 
+/* The LM head with its softmax cross entropy, without keeping the logits.  For n rows of hidden
+ * states h (dim values), a head W (vocab rows of dim values, weight_stride apart) of the same type,
+ * and a label per row (label_bits 32 or 64, signed):
+ *   z = h W^T,  lse = log sum_v exp z_v,  loss = lse - z_label
+ * A row whose label lies outside [0, vocab) has no target: loss and lse are 0, and whatever it holds
+ * reaches no result.  Products are summed in fp32 (16-bit operands on the bf16 or fp16 matrix
+ * instructions, fp32 on the fp32 ones).  A NaN among the hidden states of a row, or an infinite
+ * logit of it, makes its loss NaN; a NaN in W makes all of them NaN.
+ * n < 2^22, dim <= 2^20, vocab <= 2^30.  n = 0 is a no-op, but for a dweight that is not added to.
+ *
+ * Host only: workspace bytes of the calls (gradients = 1 for _backward and _grad).  Of `weight`
+ * only the alignment counts: rows that do not start at multiples of 16 bytes (or of a dim that is no
+ * multiple of 8) are copied there.  Otherwise some 2 dim bytes a row, and at most 512 MiB of logits'
+ * gradients (up to 2^20 rows) with 4 dim bytes a row and split for the gradients.  0 for invalid
+ * sizes, which the calls then report. */
+size_t ma_head_loss_workspace_bytes(int32_t type, int64_t n, int64_t dim, int64_t vocab, const void* weight,
+                                    int64_t weight_stride, int32_t gradients);
+
+/* loss, lse: n fp32 each. */
+ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
+                               const void* weight, int64_t weight_stride, int64_t vocab, const void* labels,
+                               int32_t label_bits, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* The gradients of sum row_weight[r] loss[r] (row_weight, lse: n fp32):
+ *   g = row_weight (exp(z - lse) - [v = label]),  dhidden = g W,  dweight (+)= g^T h
+ * g is rounded once to the hidden type (2^-9 of each term of the sums for bf16, 2^-12 for fp16).
+ * Rows without a target or of weight 0 have gradient 0, whatever they hold.  dhidden has the hidden
+ * type; dweight is (vocab, dim) of dweight_type, the hidden type or MA_F32, and is added to with
+ * accumulate = 1 (MA_F32 only).  Either may be NULL. */
+ma_status ma_head_loss_backward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
+                                const void* weight, int64_t weight_stride, int64_t vocab, const void* labels,
+                                int32_t label_bits, const float* lse, const float* row_weight, void* dhidden,
+                                int64_t dhidden_stride, void* dweight, int32_t dweight_type, int64_t dweight_stride,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Both directions, for callers that know row_weight beforehand. */
+ma_status ma_head_loss_grad(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
+                            const void* weight, int64_t weight_stride, int64_t vocab, const void* labels,
+                            int32_t label_bits, const float* row_weight, float* loss, void* dhidden,
+                            int64_t dhidden_stride, void* dweight, int32_t dweight_type, int64_t dweight_stride,
+                            int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

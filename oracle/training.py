@@ -91,3 +91,31 @@ def distill_grad(logits, teacher, ids, row_weight, temperature=1.0):
         dz[r, np.asarray(ids)[r, i]] -= p[r, i]
     w = _f64(row_weight)[:, None]
     return np.where(w == 0, 0.0, w * temperature * dz)
+
+
+def head_loss(hidden, weight, labels):
+    """(loss, lse) of each row's label under the logits hidden weight^T; 0 without a target."""
+    hidden, weight, labels = _f64(hidden), _f64(weight), np.asarray(labels)
+    loss, lse = np.zeros(labels.size), np.zeros(labels.size)
+    for r, label in enumerate(labels.reshape(-1)):
+        if 0 <= label < weight.shape[0]:
+            z = weight @ hidden[r]
+            lse[r] = z.max() + np.log(np.sum(np.exp(z - z.max())))
+            loss[r] = lse[r] - z[label]
+    return loss, lse
+
+
+def head_loss_grad(hidden, weight, labels, row_weight):
+    """The gradients of sum row_weight * loss by the hidden states and the weight."""
+    hidden, weight, labels = _f64(hidden), _f64(weight), np.asarray(labels).reshape(-1)
+    dh, dw = np.zeros_like(hidden), np.zeros_like(weight)
+    for r, label in enumerate(labels):
+        if 0 <= label < weight.shape[0]:
+            z = weight @ hidden[r]
+            g = np.exp(z - z.max())
+            g /= g.sum()
+            g[label] -= 1.0
+            g *= row_weight[r]
+            dh[r] = g @ weight
+            dw += np.outer(g, hidden[r])
+    return dh, dw

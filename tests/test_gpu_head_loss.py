@@ -1,0 +1,321 @@
+"""The LM head's cross entropy against plain torch in 64 bits.
+
+Bounds (e = 2^-24, u the hidden type's half step; products of 16-bit values are exact, those of fp32
+are rounded):
+  a sum of K products by the matrix instructions, each of which takes at least two at a time, is off
+  by (K / 2 + 32) e of the sum of their magnitudes: dz for the logits (K = dim);
+  an exponential by 4 e for its argument's two roundings and itself, plus the argument's rounding
+  2 e |z - top|, and a sum of V of them by at most V / 64 + 128 additions: with x exp(-x) <= 1/e that
+  is (V / 64 + 140) e of the sum, and so of lse, absolutely; dz enters it at most once, and loss twice;
+  g = w (p - [label]) by w p (dz + 6 e + 2 e |z - lse|) + 2 e |g|, its rounding by u |g| and, below the
+  type's least normal number, 2^-25 of a weight scaled to at least 2^13: 2^-38 of the largest one;
+  both gradients by g's error times the other operand's magnitude, the sums' errors as above, and
+  their own rounding.
+"""
+import numpy as np
+import pytest
+
+from oracle import training
+
+torch = pytest.importorskip("torch")
+ma = pytest.importorskip("adamw_optimizer_step_muon_amd")
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+E = 2.0 ** -24
+TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
+HALF = {torch.float32: 0.0, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+SIZES = [(1, 1, 1), (1, 500, 64), (3, 257, 33), (5, 1000, 100), (64, 300, 72), (65, 511, 40), (128, 640, 256), (130, 777, 128),
+         (257, 1025, 264), (300, 2500, 520), (511, 5000, 1001), (700, 3001, 768)]
+
+
+def _strided(x, extra, offset):
+    n, d = x.shape
+    buf = torch.full((n, d + extra), float("nan"), dtype=x.dtype, device=DEV)
+    view = buf[:, offset:offset + d]
+    view.copy_(x)
+    return view
+
+
+def _inputs(n, vocab, dim, dtype, seed, ignored=5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    w = (torch.randn(vocab, dim, generator=g, device=DEV) * 0.3).to(dtype)
+    labels = torch.randint(0, vocab, (n,), generator=g, device=DEV)
+    h = torch.randn(n, dim, generator=g, device=DEV) * 4 / dim ** 0.5
+    h += torch.rand(n, 1, generator=g, device=DEV) * 10 / (dim * 0.09) * w[labels].float()
+    if ignored:
+        labels[ignored // 2::ignored] = torch.tensor([-100, vocab, -1, vocab + 7], device=DEV).repeat(n)[:labels[ignored // 2::ignored].numel()]
+    rw = torch.rand(n, generator=g, device=DEV) + 0.01
+    return h.to(dtype), w, labels, rw
+
+
+def _reference(h, w, labels, rw=None, lse=None):
+    """loss, lse, their bounds, and with rw dh, dW and theirs."""
+    H, W = h.double(), w.double()
+    dtype, (n, dim), vocab = h.dtype, h.shape, w.shape[0]
+    live = (labels >= 0) & (labels < vocab)
+    at = torch.where(live, labels, 0)
+    H = torch.where(live[:, None], H, 0.0)
+    z = H @ W.t()
+    dz = (dim / 2 + 32) * E * (H.abs() @ W.abs().t())
+    true = torch.logsumexp(z, 1)
+    target = z.gather(1, at[:, None])[:, 0]
+    sum_err = (vocab / 64 + 140) * E
+    err = dz.amax(1) + sum_err + 2 * E * true.abs()
+    loss = torch.where(live, true - target, 0.0)
+    out = [loss, torch.where(live, true, 0.0), 2 * err + 3 * E * (loss.abs() + target.abs()), err + 2 * E * true.abs()]
+    if rw is None:
+        return out
+    R = torch.where(live, rw.double(), 0.0)[:, None]
+    by = true if lse is None else lse.double()
+    p = torch.exp(z - by[:, None])
+    g = p * R
+    dg = g.abs() * (dz + 6 * E + 2 * E * (z - by[:, None]).abs() + (sum_err + dz.amax(1, keepdim=True) if lse is None else 0.0))
+    g.scatter_add_(1, at[:, None], -R)
+    dg += (2 * E + HALF[dtype]) * g.abs()
+    if dtype == torch.float16:
+        dg += 2.0 ** -38 * R.abs().max() * (R != 0)
+    dh, dw = g @ W, g.t() @ H
+    bound = []
+    for exact, size, k in ((dh, (g.abs() + dg) @ W.abs(), vocab), (dw, (g.abs() + dg).t() @ H.abs(), n)):
+        bound.append((k / 2 + 64) * E * size)
+    bound[0] += dg @ W.abs()
+    bound[1] += dg.t() @ H.abs()
+    rounded = [b * 1.01 + torch.finfo(dtype).eps / 2 * (x.abs() + b) + TINY[dtype] for b, x in zip(bound, (dh, dw))]
+    return out + [dh, dw, *rounded, bound[1]]
+
+
+def _near(got, want, bound):
+    assert bool(((got.double() - want).abs() <= bound * 1.01 + 1e-300).all()), \
+        ((got.double() - want).abs() / (bound + 1e-300)).max().item()
+
+
+@pytest.mark.parametrize("n,vocab,dim", SIZES)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_forward(n, vocab, dim, dtype):
+    h, w, labels, _ = _inputs(n, vocab, dim, dtype, n + dim)
+    loss, lse, dloss, dlse = _reference(h, w, labels)
+    got = ma.head_loss_forward(h, w, labels)
+    _near(got[0], loss, dloss)
+    _near(got[1], lse, dlse)
+    # strides, alignment, index type and a second call change nothing
+    hs, ws = _strided(h, dim % 3 + 1, 1), _strided(w, 8 - dim % 8 if dim % 2 else 3, dim % 2 * 8 // 8)
+    for args in ((hs, ws, labels), (h, w, labels.int()), (h, w, labels)):
+        again = ma.head_loss_forward(*args)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("n,vocab,dim", SIZES)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients(n, vocab, dim, dtype):
+    h, w, labels, rw = _inputs(n, vocab, dim, dtype, 3 * n + dim)
+    rw[n // 2] = 0.0
+    loss, lse, dloss, _, dh, dw, bh, bw, bw32 = _reference(h, w, labels, rw)
+    got = ma.head_loss_grad(h, w, labels, rw)
+    _near(got[0], loss, dloss)
+    _near(got[1], dh, bh)
+    _near(got[2], dw, bw)
+    assert got[1].dtype == got[2].dtype == dtype
+    # into an fp32 buffer, written and added to
+    grad = torch.full((vocab, dim), 7.0, device=DEV)
+    _, _, same = ma.head_loss_grad(h, w, labels, rw, dweight=grad, hidden_grad=False)
+    assert same is grad
+    _near(grad, dw, bw32 + 2 * E * dw.abs())
+    before = grad.clone()
+    ma.head_loss_grad(h, w, labels, rw, dweight=grad, accumulate=True, hidden_grad=False)
+    assert torch.equal(grad, before + before)
+    # strided and unaligned operands
+    hs, ws = _strided(h, 5, 3), _strided(w, 3, 1)
+    again = ma.head_loss_grad(hs, ws, labels.int(), rw)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    # the backward call on its own, from the rounded lse
+    lse32 = ma.head_loss_forward(h, w, labels)[1]
+    _, _, _, _, dh, dw, bh, bw, _ = _reference(h, w, labels, rw, lse32)
+    back = ma.head_loss_backward(h, w, labels, lse32, rw)
+    _near(back[0], dh, bh)
+    _near(back[1], dw, bw)
+    only = ma.head_loss_backward(h, w, labels, lse32, rw, weight_grad=False)
+    assert only[1] is None and torch.equal(only[0], back[0])
+    only = ma.head_loss_backward(h, w, labels, lse32, rw, hidden_grad=False)
+    assert only[0] is None and torch.equal(only[1], back[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,vocab,dim", [(4099, 70003, 72), (40, 70003, 128), (1, 131072, 320)])
+def test_long_vocabularies(n, vocab, dim, dtype):
+    """Several pieces of the vocabulary, and sums over it split over blocks."""
+    h, w, labels, rw = _inputs(n, vocab, dim, dtype, n)
+    loss, lse, dloss, dlse, dh, dw, bh, bw, _ = _reference(h, w, labels, rw)
+    got = ma.head_loss_grad(h, w, labels, rw)
+    _near(got[0], loss, dloss)
+    _near(got[1], dh, bh)
+    _near(got[2], dw, bw)
+
+
+def test_matches_the_oracle():
+    h, w, labels, rw = _inputs(30, 50, 24, torch.float32, 1)
+    loss, lse = training.head_loss(h.cpu(), w.cpu(), labels.cpu())
+    dh, dw = training.head_loss_grad(h.cpu(), w.cpu(), labels.cpu(), rw.cpu().double().numpy())
+    got = ma.head_loss_grad(h, w, labels, rw)
+    for a, b in zip(got, (loss, dh, dw)):
+        assert np.abs(a.double().cpu().numpy() - b).max() < 200 * E * max(1.0, np.abs(b).max())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_without_a_target(dtype):
+    """Their hidden states may hold anything; their results are zeros."""
+    h, w, labels, rw = _inputs(300, 700, 136, dtype, 4, ignored=0)
+    on = torch.ones(300, dtype=torch.bool, device=DEV)
+    on[[0, 7, 64, 299]] = False
+    want = ma.head_loss_grad(h[on], w, labels[on], rw[on])
+    bad, l2, rw2 = h.clone(), labels.clone(), rw.clone()
+    bad[0], bad[7], bad[64] = float("nan"), float("inf"), -float("inf")
+    l2[[0, 7]], rw2[[64, 299]] = torch.tensor([-100, 700], device=DEV), 0.0
+    loss, dh, dw = ma.head_loss_grad(bad, w, l2, rw2)
+    assert torch.equal(loss[on], want[0]) and (loss[[0, 7]] == 0).all() and torch.isnan(loss[64])
+    assert torch.equal(dh[on], want[1]) and (dh[~on] == 0).all()
+    assert torch.equal(dw, want[2])
+    none = torch.full_like(labels, -100)
+    loss, dh, dw = ma.head_loss_grad(bad, w, none, rw)
+    assert not loss.any() and not dh.any() and not dw.any()
+    loss, lse = ma.head_loss_forward(bad, w, none)
+    assert not loss.any() and not lse.any()
+    grad = torch.ones(700, 136, device=DEV)
+    ma.head_loss_grad(bad, w, labels, torch.zeros_like(rw), dweight=grad, accumulate=True)
+    assert (grad == 1).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_rows(dtype):
+    h, w, labels, rw = _inputs(1, 50, 40, dtype, 4, ignored=0)
+    h, labels, rw = h[:0], labels[:0], rw[:0]
+    assert ma.head_loss_forward(h, w, labels)[0].shape == (0,)
+    loss, dh, dw = ma.head_loss_grad(h, w, labels, rw)
+    assert loss.shape == (0,) and dh.shape == (0, 40) and not dw.any()
+    grad = torch.ones(50, 40, device=DEV)
+    ma.head_loss_grad(h, w, labels, rw, dweight=grad, accumulate=True)
+    assert (grad == 1).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_infinities_and_large_logits(dtype):
+    h, w, labels, rw = _inputs(70, 300, 64, dtype, 6, ignored=0)
+    loss, dh, dw = ma.head_loss_grad(h * 500, w, labels, rw)
+    ref = _reference(h * 500, w, labels, rw)
+    _near(loss, ref[0], ref[2])
+    assert torch.isfinite(dh).all() and torch.isfinite(dw).all()
+    bad = h.clone()
+    bad[3, 5], bad[9, 1] = float("nan"), float("inf")
+    loss, lse = ma.head_loss_forward(bad, w, labels)
+    clean = ma.head_loss_forward(h, w, labels)[0]
+    keep = torch.ones(70, dtype=torch.bool, device=DEV)
+    keep[[3, 9]] = False
+    assert torch.isnan(loss[~keep]).all() and torch.equal(loss[keep], clean[keep])
+
+
+def test_gradient_by_differences():
+    h, w, labels, rw = (t.double() if t.is_floating_point() else t for t in _inputs(6, 40, 16, torch.float32, 8))
+    _, dh, dw = ma.head_loss_grad(h.float(), w.float(), labels, rw.float())
+    total = lambda a, b: (training.head_loss(a.cpu(), b.cpu(), labels.cpu())[0] * rw.cpu().numpy()).sum()  # noqa: E731
+    step = 1e-5
+    for t, grad, which in ((h, dh, 0), (w, dw, 1)):
+        for i in range(0, t.numel(), 7):
+            values = []
+            for sign in (1, -1):
+                moved = t.clone().view(-1)
+                moved[i] += sign * step
+                values.append(total(*((moved.view_as(t), w) if which == 0 else (h, moved.view_as(t)))))
+            assert abs((values[0] - values[1]) / (2 * step) - grad.reshape(-1)[i].item()) < 1e-5
+
+
+def test_leading_dimensions_workspaces_and_versions():
+    h, w, labels, rw = _inputs(24, 100, 48, torch.bfloat16, 9)
+    want = ma.head_loss_grad(h, w, labels, rw)
+    need = ma.head_loss_workspace_bytes(h, w)
+    assert ma.head_loss_workspace_bytes(h, w, gradients=False) <= need
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    got = ma.head_loss_grad(h.view(2, 3, 4, 48), w, labels.view(2, 3, 4), rw, workspace=ws)
+    assert got[0].shape == (2, 3, 4) and got[1].shape == (2, 3, 4, 48)
+    assert all(torch.equal(a.reshape(b.shape), b) for a, b in zip(got, want))
+    with pytest.raises(ma.MuonAdamWError, match="workspace"):
+        ma.head_loss_grad(h, w, labels, rw, workspace=ws[:need - 256])
+    grad = torch.zeros(100, 48, device=DEV)
+    version = grad._version
+    ma.head_loss_grad(h, w, labels, rw, dweight=grad)
+    assert grad._version == version + 1
+    wide = torch.full((100, 60), 5.0, dtype=torch.bfloat16, device=DEV)
+    ma.head_loss_grad(h, w, labels, rw, dweight=wide[:, 7:55])
+    assert torch.equal(wide[:, 7:55], want[2]) and (wide[:, :7] == 5).all() and (wide[:, 55:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_stream_and_graph(dtype):
+    h, w, labels, rw = _inputs(300, 1000, 72, dtype, 10)
+    want = ma.head_loss_grad(h, w, labels, rw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ma.head_loss_grad(h, w, labels.repeat(2, 1).t()[:, 0], rw, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    static = h.clone()
+    with torch.cuda.graph(graph):
+        got = ma.head_loss_grad(static, w, labels, rw)
+    for scale in (1.0, 0.5, 1.0):
+        static.copy_(h * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ma.head_loss_grad(h * scale, w, labels, rw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("copied", [False, True])
+def test_autograd(dtype, copied):
+    h, w, labels, _ = _inputs(50, 200, 40, dtype, 11)
+    param = torch.nn.Parameter(w.float())
+    hidden = h.clone().requires_grad_(True)
+    copy = w if copied else None
+    loss = ma.head_loss(hidden.view(5, 10, 40), param, labels.view(5, 10), copy=copy)
+    assert loss.shape == (5, 10)
+    loss.mean().backward()
+    rw = torch.full((50,), 1 / 50, device=DEV)
+    lse = ma.head_loss_forward(h, w, labels)[1]
+    grad = torch.empty(200, 40, device=DEV)
+    dh, _ = ma.head_loss_backward(h, w, labels, lse, rw, dweight=grad)
+    assert torch.equal(hidden.grad, dh) and torch.equal(param.grad, grad) and param.grad.dtype == torch.float32
+    # only one of the two, or none
+    ma.head_loss(h, param, labels).mean().backward()
+    assert torch.equal(param.grad, grad + grad)
+    hidden.grad = None
+    ma.head_loss(hidden, w, labels).mean().backward()
+    assert torch.equal(hidden.grad, dh)
+    low = w.clone().requires_grad_(True)
+    ma.head_loss(h, low, labels).mean().backward()
+    assert low.grad.dtype == dtype
+
+
+def test_training_step_with_an_8_bit_state_and_a_copy():
+    """Embedding, layer norm, head and the 8-bit step together: the loss's gradients reach the
+    parameters, and the head's copy follows them."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    table = torch.nn.Parameter(torch.randn(200, 64, generator=g, device=DEV) * 0.1)
+    head = torch.nn.Parameter(torch.randn(200, 64, generator=g, device=DEV) * 0.1)
+    gain = torch.nn.Parameter(torch.ones(64, device=DEV))
+    copy = head.detach().to(torch.bfloat16)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": [table, head, gain], "lr": 1e-2, "state_bits": 8,
+                         "copies": [None, copy, None]}])
+    tokens = torch.randint(0, 200, (4, 33), generator=g, device=DEV)
+    for _ in range(3):
+        x = ma.embedding(tokens[:, :-1], table, out_dtype=torch.bfloat16, optimizer=opt)
+        y = ma.layer_norm(x, gain)
+        loss = ma.head_loss(y, head, tokens[:, 1:], copy=copy).mean()
+        loss.backward()
+        lse = ma.head_loss_forward(y.detach(), copy, tokens[:, 1:])[1]
+        want = torch.empty_like(head)
+        ma.head_loss_backward(y.detach(), copy, tokens[:, 1:], lse, torch.full((4, 32), 1 / 128, device=DEV), dweight=want)
+        assert torch.equal(head.grad, want) and gain.grad is not None and torch.isfinite(gain.grad).all()
+        opt.step()
+        assert torch.equal(copy, head.detach().to(torch.bfloat16))
+        opt.zero_grad()
