@@ -23,11 +23,13 @@ __all__ = ["LIB_PATH", "MFMA_PROBE_OPERAND_VALUES", "MFMA_PROBE_THREADS", "MuonA
 
 # The training operators are torch.autograd functions, so their module needs torch; it is
 # imported with the first of these names that is used.
-_OPS = ("ADAMW_BYTE_BLOCK", "adamw_byte_state", "adamw_byte_step_multi", "adamw_byte_values", "adamw_step_embedding", "distill_backward", "distill_forward", "distill_loss",
+_OPS = ("ADAMW_BYTE_BLOCK", "adamw_byte_state", "adamw_byte_step_multi", "adamw_byte_values",
+        "adamw_step_embedding", "distill_backward", "distill_forward", "distill_loss",
         "distill_loss_grad", "embedding", "embedding_backward", "embedding_forward",
         "embedding_workspace_bytes", "head_loss", "head_loss_backward", "head_loss_forward",
-        "head_loss_grad", "head_loss_workspace_bytes", "layer_norm", "layer_norm_backward", "layer_norm_forward",
-        "layer_norm_workspace_bytes")
+        "head_loss_grad", "head_loss_workspace_bytes", "layer_norm", "layer_norm_backward",
+        "layer_norm_forward", "layer_norm_workspace_bytes", "residual_norm",
+        "residual_norm_backward", "residual_norm_forward", "residual_norm_workspace_bytes")
 if importlib.util.find_spec("torch") is not None:  # else `import *` has the rest
     __all__ += _OPS
 

@@ -33,7 +33,8 @@ EXPORTED = (
     "ma_adamw_step_embedding", "ma_layer_norm_forward", "ma_layer_norm_workspace_bytes",
     "ma_layer_norm_backward", "ma_distill_forward", "ma_distill_backward", "ma_distill_loss_grad",
     "ma_adamw_byte_step_multi", "ma_head_loss_workspace_bytes", "ma_head_loss_forward",
-    "ma_head_loss_backward", "ma_head_loss_grad",
+    "ma_head_loss_backward", "ma_head_loss_grad", "ma_residual_norm_forward",
+    "ma_residual_norm_workspace_bytes", "ma_residual_norm_backward",
 )
 MA_STATIC_WORKSPACE_BYTES = 512 << 20
 ABI_VERSION = 6  # include/muon_adamw.h MA_ABI_VERSION
@@ -78,6 +79,16 @@ class _PlanReport(ctypes.Structure):
 class _AdamWSegment(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
                 ("exp_avg_sq", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class _ResidualNormParams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("post_weight", "post_bias", "gate", "weight", "bias")] + \
+        [("scale", ctypes.c_float), ("eps", ctypes.c_float), ("post_norm", ctypes.c_int32),
+         ("center", ctypes.c_int32)]
+
+
+class _ResidualNormGrads(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("dpost_weight", "dpost_bias", "dgate", "dweight", "dbias")]
 
 
 class _AdamWByteHParams(ctypes.Structure):
@@ -216,6 +227,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                   ptr, i64, ptr]),
             ("distill_loss_grad", [ptr, i32, i64, i64, i64, ptr, i32, ptr, i32, i64, f32, ptr, ptr,
                                    ptr, i64, ptr]),
+            ("residual_norm_forward", [ptr, i64, ptr, i64, i32, i64, i64,
+                                       ctypes.POINTER(_ResidualNormParams), ptr, i64, ptr, i64, ptr, ptr]),
+            ("residual_norm_backward", [ptr, i64, ptr, i64, ptr, i64, ptr, i64, ptr, i32, i64, i64,
+                                        ctypes.POINTER(_ResidualNormParams),
+                                        ctypes.POINTER(_ResidualNormGrads), ptr, i64, ptr, i64, ptr, size,
+                                        ptr]),
             ("head_loss_forward", [ptr, i32, i64, i64, i64, ptr, i64, i64, ptr, i32, ptr, ptr, ptr,
                                    size, ptr]),
             ("head_loss_backward", [ptr, i32, i64, i64, i64, ptr, i64, i64, ptr, i32, ptr, ptr, ptr,
@@ -230,6 +247,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ma_embedding_workspace_bytes.argtypes = [i64, i64, i64]
     lib.ma_head_loss_workspace_bytes.restype = size
     lib.ma_head_loss_workspace_bytes.argtypes = [i32, i64, i64, i64, ptr, i64, i32]
+    lib.ma_residual_norm_workspace_bytes.restype = size
+    lib.ma_residual_norm_workspace_bytes.argtypes = [i64, i64]
     lib.ma_layer_norm_workspace_bytes.restype = size
     lib.ma_layer_norm_workspace_bytes.argtypes = [i64, i64]
     _lib = lib

@@ -726,6 +726,21 @@ ma_status check_dlogits(const DistillCall& c, const Range* in, int ins, Range* d
   return MA_OK;
 }
 
+// The gains of a residual norm, and their five ranges.
+ma_status check_residual_params(const ma_residual_norm_params* p, int64_t dim, ResidualGains* g, Range* r) {
+  if (!p) return fail(MA_ERR_INVALID_ARG, "params is NULL");
+  if (!finite(p->scale)) return fail(MA_ERR_INVALID_ARG, "non-finite scale");
+  if (!finite(p->eps) || p->eps < 0.0f) return fail(MA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!p->post_norm && (p->post_weight || p->post_bias))
+    return fail(MA_ERR_INVALID_ARG, "gains of a norm that the call has not");
+  const float* const gains[5] = {p->post_weight, p->post_bias, p->gate, p->weight, p->bias};
+  for (int k = 0; k < 5; ++k)
+    if (gains[k])
+      if (const ma_status st = check_floats(gains[k], dim, "a gain, gate or bias", &r[k])) return st;
+  *g = ResidualGains{p->post_weight, p->post_bias, p->gate, p->weight, p->bias, p->scale, p->eps, p->post_norm != 0, p->center != 0};
+  return MA_OK;
+}
+
 ma_status check_head_size(int32_t type, int64_t n, int64_t dim, int64_t vocab) {
   if (const ma_status st = check_type(type, "hidden")) return st;
   if (n < 0 || dim < 1 || vocab < 1)
@@ -2081,6 +2096,79 @@ ma_status ma_head_loss_grad(const void* hidden, int32_t type, int64_t hidden_str
   if (n == 0) return clear_head_gradient(c, stream);
   if (const ma_status st = check_floats(loss, n, "loss", &out[2])) return st;
   return run_head(c, kHeadBoth, out, 3, workspace, workspace_bytes, stream);
+}
+
+ma_status ma_residual_norm_forward(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                   int32_t type, int64_t n, int64_t dim, const ma_residual_norm_params* params,
+                                   void* out, int64_t out_stride, void* y, int64_t y_stride, float* stats, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_norm_size(n, dim)) return st;
+  if (const ma_status st = check_type(type, "x")) return st;
+  Range r[10] = {};
+  ResidualGains g;
+  if (const ma_status st = check_residual_params(params, dim, &g, r + 5)) return st;
+  if (n == 0) return MA_OK;
+  if (const ma_status st = check_rows(y, type, n, dim, y_stride, "y", &r[0])) return st;
+  if (const ma_status st = check_floats(stats, 4 * n, "stats", &r[1])) return st;
+  if (const ma_status st = check_rows(out, type, n, dim, out_stride, "out", &r[2])) return st;
+  if (const ma_status st = check_rows(x, type, n, dim, x_stride, "x", &r[3])) return st;
+  if (const ma_status st = check_rows(residual, type, n, dim, residual_stride, "residual", &r[4])) return st;
+  // the residual may be stepped in place
+  if (out == residual && out_stride == residual_stride) r[4] = Range{0, 0};
+  if (const ma_status st = check_disjoint(r, 10, 3, "outputs or inputs")) return st;
+  const ResidualCall c{x, residual, type, x_stride, residual_stride, n, dim, g, out, y, out_stride, y_stride, stats};
+  const hipError_t e = launch_residual_forward(c, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "residual norm launch");
+  return MA_OK;
+}
+
+size_t ma_residual_norm_workspace_bytes(int64_t n, int64_t dim) {
+  if (n < 1 || dim < 1 || dim > kMaxDim || n > kMaxThreadsPerLaunch / 1024) return 0;
+  return residual_workspace_bytes(n, dim);
+}
+
+ma_status ma_residual_norm_backward(const void* dout, int64_t dout_stride, const void* dy, int64_t dy_stride,
+                                    const void* x, int64_t x_stride, const void* out, int64_t out_stride,
+                                    const float* stats, int32_t type, int64_t n, int64_t dim,
+                                    const ma_residual_norm_params* params, const ma_residual_norm_grads* grads, void* dx,
+                                    int64_t dx_stride, void* dresidual, int64_t dresidual_stride, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (const ma_status st = check_norm_size(n, dim)) return st;
+  if (const ma_status st = check_type(type, "x")) return st;
+  if (!grads) return fail(MA_ERR_INVALID_ARG, "grads is NULL");
+  Range r[18] = {};
+  ResidualGains g;
+  if (const ma_status st = check_residual_params(params, dim, &g, r + 13)) return st;
+  if ((grads->dpost_weight || grads->dpost_bias) && !g.post)
+    return fail(MA_ERR_INVALID_ARG, "gradients of a norm that the call has not");
+  float* const wanted[5] = {grads->dpost_weight, grads->dpost_bias, grads->dgate, grads->dweight, grads->dbias};
+  bool reduce = false;
+  for (int k = 0; k < 5; ++k)
+    if (wanted[k]) {
+      reduce = true;
+      if (const ma_status st = check_floats(wanted[k], dim, "a parameter's gradient", &r[k])) return st;
+    }
+  if (n > 0) {
+    if (const ma_status st = check_rows(dx, type, n, dim, dx_stride, "dx", &r[5])) return st;
+    if (const ma_status st = check_rows(dresidual, type, n, dim, dresidual_stride, "dresidual", &r[6])) return st;
+    if (dout)
+      if (const ma_status st = check_rows(dout, type, n, dim, dout_stride, "dout", &r[8])) return st;
+    if (const ma_status st = check_rows(dy, type, n, dim, dy_stride, "dy", &r[9])) return st;
+    if (const ma_status st = check_rows(x, type, n, dim, x_stride, "x", &r[10])) return st;
+    if (const ma_status st = check_rows(out, type, n, dim, out_stride, "out", &r[11])) return st;
+    if (const ma_status st = check_floats(stats, 4 * n, "stats", &r[12])) return st;
+  }
+  if (const ma_status st = check_workspace(workspace, workspace_bytes,
+                                           reduce ? ma_residual_norm_workspace_bytes(n, dim) : 0, &r[7])) return st;
+  if (const ma_status st = check_disjoint(r, 18, 8, "gradients, workspace or inputs")) return st;
+  if (n == 0 && !reduce) return MA_OK;
+  ResidualGradCall c{dout, dy, x, out, type, dout_stride, dy_stride, x_stride, out_stride, n, dim, g, stats, dx, dresidual,
+                     dx_stride, dresidual_stride, wanted[0], wanted[1], wanted[2], wanted[3], wanted[4],
+                     static_cast<float*>(workspace)};
+  const hipError_t e = launch_residual_backward(c, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "residual norm gradient launch");
+  return MA_OK;
 }
 
 }  // extern "C"

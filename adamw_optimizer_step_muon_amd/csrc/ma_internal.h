@@ -532,6 +532,53 @@ constexpr int kMaxDistillTop = 1024;
 enum DistillMode { kDistillForward = 0, kDistillBackward = 1, kDistillBoth = 2 };
 hipError_t launch_distill(const DistillCall& c, DistillMode mode, hipStream_t s);
 
+// The norms around a block (residual_norm.hip).
+struct ResidualGains {
+  const float* post_weight;  // any of these five may be null
+  const float* post_bias;
+  const float* gate;
+  const float* weight;
+  const float* bias;
+  float scale, eps;
+  bool post, center;
+};
+struct ResidualCall {
+  const void* x;
+  const void* residual;
+  int type;
+  int64_t x_stride, residual_stride, n, dim;
+  ResidualGains g;
+  void* out;  // may be the residual itself
+  void* y;
+  int64_t out_stride, y_stride;
+  float* stats;  // (4, n): mean1, rstd1, mean2, rstd2
+};
+hipError_t launch_residual_forward(const ResidualCall& c, hipStream_t s);
+struct ResidualGradCall {
+  const void* dout;  // null: zeros
+  const void* dy;
+  const void* x;
+  const void* out;
+  int type;
+  int64_t dout_stride, dy_stride, x_stride, out_stride, n, dim;
+  ResidualGains g;
+  const float* stats;
+  void* dx;
+  void* dresidual;
+  int64_t dx_stride, dresidual_stride;
+  float* dpost_weight;  // any of these five may be null
+  float* dpost_bias;
+  float* dgate;
+  float* dweight;
+  float* dbias;
+  float* workspace;
+  // set by launch_residual_backward
+  float* means;
+  bool reduce;
+};
+size_t residual_workspace_bytes(int64_t n, int64_t dim);
+hipError_t launch_residual_backward(const ResidualGradCall& c, hipStream_t s);
+
 // The LM head's cross entropy (head_loss.hip).
 constexpr int kHeadTile = 256;  // gathered rows are padded to a multiple of this
 constexpr int64_t kHeadPieceBytes = int64_t{512} << 20;  // of g, for up to 2^20 rows

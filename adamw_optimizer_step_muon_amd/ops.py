@@ -1,10 +1,10 @@
-"""Training operators around the AdamW parameters: embedding, layer norm, distillation, the LM
-head's cross entropy, and the AdamW step with moments in 8 bits.
+"""Training operators around the AdamW parameters: embedding, layer norm, the norms around a
+block, distillation, the LM head's cross entropy, and the AdamW step with moments in 8 bits.
 
 Two layers.  The entry points (``embedding_forward`` and the like) are the C ABI's calls
 without the ma_ prefix: tensors are checked, their pointers and the stream handed over, a
-negative status raised as MuonAdamWError.  ``embedding``, ``layer_norm``, ``distill_loss`` and
-``head_loss`` are the same operators for torch's autograd, so that ``loss.backward()`` runs the library's
+negative status raised as MuonAdamWError.  ``embedding``, ``layer_norm``, ``residual_norm``,
+``distill_loss`` and ``head_loss`` are the same operators for torch's autograd, so that ``loss.backward()`` runs the library's
 kernels; ``embedding`` can hand its table gradient to a MuonAdamW in token form, which
 ``step()`` then applies without building the dense gradient.
 
@@ -27,7 +27,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from ._lib import (_AdamWByteHParams, _AdamWByteSegment, _AdamWHParams, _check, _require_f32_cuda,
-                   _stream_handle, load)
+                   _ResidualNormGrads, _ResidualNormParams, _stream_handle, load)
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _BITS = {torch.int32: 32, torch.int64: 64}
@@ -169,6 +169,10 @@ def _floats(name, t, count, device=None) -> int:
     if t.numel() != count:
         raise ValueError(f"{name} must hold {count} values (got {t.numel()})")
     return t.data_ptr()
+
+
+def _address(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _table(name, t, device=None):
@@ -358,6 +362,91 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, weight_grad: bool = T
 
 
 # --------------------------------------------------------------------------
+# the norms around a block
+# --------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def residual_norm_workspace_bytes(n: int, dim: int) -> int:
+    """Workspace of residual_norm_backward for n rows."""
+    return int(load().ma_residual_norm_workspace_bytes(int(n), int(dim)))
+
+
+def _residual_params(dim, device, weight, bias, post_norm, post_weight, post_bias, gate, scale, center, eps):
+    if not post_norm and (post_weight is not None or post_bias is not None):
+        raise ValueError("post_weight and post_bias are for a call with post_norm")
+    return _ResidualNormParams(
+        _floats("post_weight", post_weight, dim, device), _floats("post_bias", post_bias, dim, device),
+        _floats("gate", gate, dim, device), _floats("weight", weight, dim, device),
+        _floats("bias", bias, dim, device), scale, eps, int(bool(post_norm)), int(bool(center)))
+
+
+def _alike(name, t, like, device):
+    """The row stride of a tensor of the shape and type of `like`."""
+    _tensor(name, t, device)
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} must have x's shape and type")
+    return _rows(name, t, device)[2]
+
+
+def residual_norm_forward(x, residual, weight=None, bias=None, *, post_norm: bool = True, post_weight=None,
+                          post_bias=None, gate=None, scale: float = 1.0, center: bool = True,
+                          eps: float = 1e-5, out=None, stream=None):
+    """(out, y, stats) of ma_residual_norm_forward over x's last dimension: the residual stream
+    behind a block with output x, out = residual + scale * gate * norm(x) (with post_norm False:
+    of x itself), and y = norm(out), the next block's input.  The norms are layer norms with fp32
+    gains and biases, or None; center False makes them root-mean-square norms.  gate: an fp32
+    vector or None.  out and y have x's type (out may be given, also as the residual itself);
+    stats (4, *x.shape[:-1], fp32) are the backward pass's input."""
+    n, dim, x_stride = _rows("x", x)
+    device, dtype = x.device, _type("x", x.dtype)
+    residual_stride = _alike("residual", residual, x, device)
+    params = _residual_params(dim, device, weight, bias, post_norm, post_weight, post_bias, gate, scale, center, eps)
+    given = out
+    if out is None:
+        out, out_stride = _like(x, stream), max(dim, 1)
+    else:
+        out_stride = _alike("out", out, x, device)
+    y = _like(x, stream)
+    stats = _empty(x, (4,) + x.shape[:-1], torch.float32, stream)
+    _call("ma_residual_norm_forward", device, stream, x.data_ptr(), x_stride, residual.data_ptr(), residual_stride,
+          dtype, n, dim, ctypes.byref(params), out.data_ptr(), out_stride, y.data_ptr(), max(dim, 1), stats.data_ptr())
+    if given is not None:
+        _wrote(given)
+    if stream is not None:
+        _record(stream, x, residual, weight, bias, post_weight, post_bias, gate, out)
+    return out, y, stats
+
+
+def residual_norm_backward(dout, dy, x, out, stats, weight=None, bias=None, *, post_norm: bool = True,
+                           post_weight=None, post_bias=None, gate=None, scale: float = 1.0,
+                           center: bool = True, param_grads=True, workspace=None, stream=None):
+    """(dx, dresidual, dweight, dbias, dpost_weight, dpost_bias, dgate) of ma_residual_norm_backward;
+    dout None means zeros.  A parameter that is None has no gradient (None); param_grads is True or
+    False for all of them, or five truth values in the order of the result."""
+    n, dim, x_stride = _rows("x", x)
+    device, dtype = x.device, _type("x", x.dtype)
+    dout_stride = dim if dout is None else _alike("dout", dout, x, device)
+    dy_stride, out_stride = _alike("dy", dy, x, device), _alike("out", out, x, device)
+    # (eps is in the statistics)
+    params = _residual_params(dim, device, weight, bias, post_norm, post_weight, post_bias, gate, scale, center, 0.0)
+    if isinstance(param_grads, bool):
+        param_grads = (param_grads,) * 5
+    grads = [None if t is None or not want else _empty(x, dim, torch.float32, stream)
+             for t, want in zip((weight, bias, post_weight, post_bias, gate), param_grads)]
+    at = [_address(t) for t in grads]
+    dx = _like(x, stream)
+    dresidual = _like(dx, stream)
+    need = residual_norm_workspace_bytes(n, dim) if any(t is not None for t in grads) else 0
+    _keep, ws, size = _workspace(workspace, need, x, stream)
+    _call("ma_residual_norm_backward", device, stream, _address(dout), dout_stride, dy.data_ptr(), dy_stride,
+          x.data_ptr(), x_stride, out.data_ptr(), out_stride, _floats("stats", stats, 4 * n, device), dtype, n, dim,
+          ctypes.byref(params), ctypes.byref(_ResidualNormGrads(at[2], at[3], at[4], at[0], at[1])), dx.data_ptr(),
+          max(dim, 1), dresidual.data_ptr(), max(dim, 1), ws, size)
+    if stream is not None:
+        _record(stream, dout, dy, x, out, stats, weight, bias, post_weight, post_bias, gate, _keep)
+    return dx, dresidual, *grads
+
+
+# --------------------------------------------------------------------------
 # distillation
 # --------------------------------------------------------------------------
 def _distill(logits, teacher, ids, temperature, stream):
@@ -489,10 +578,6 @@ def _head_gradients(hidden, weight, hidden_grad, weight_grad, dweight, accumulat
         dweight = _like(weight, stream)
     return dhidden, dweight, (_address(dhidden), max(hidden.shape[-1], 1), _address(dweight), dtype, stride,
                               int(bool(accumulate)))
-
-
-def _address(t) -> int:
-    return 0 if t is None else t.data_ptr()
 
 
 def head_loss_forward(hidden, weight, labels, *, workspace=None, stream=None):
@@ -671,6 +756,32 @@ class _LayerNorm(torch.autograd.Function):
         return dx, dw, db, None
 
 
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, post_weight, post_bias, gate, post_norm, scale, center, eps):
+        ctx.set_materialize_grads(False)
+        ctx.how = dict(post_norm=post_norm, scale=scale, center=center)
+        out, y, stats = residual_norm_forward(x, residual, weight, bias, post_weight=post_weight, post_bias=post_bias,
+                                              gate=gate, eps=eps, **ctx.how)
+        ctx.save_for_backward(x, out, stats, weight, bias, post_weight, post_bias, gate)
+        return out, y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, dy):
+        x, out, stats, *gains = ctx.saved_tensors
+        if dout is None and dy is None:
+            return (None,) * 11
+        dout = dout if dout is None else _rowed(dout)
+        dy = torch.zeros_like(out) if dy is None else _rowed(dy)
+        weight, bias, post_weight, post_bias, gate = gains
+        dx, dresidual, *grads = residual_norm_backward(dout, dy, x, out, stats, weight, bias, post_weight=post_weight,
+                                                       post_bias=post_bias, gate=gate,
+                                                       param_grads=ctx.needs_input_grad[2:7], **ctx.how)
+        grads = [g if g is None else g.view(t.shape) for g, t in zip(grads, gains)]
+        return dx, dresidual, *grads, None, None, None, None
+
+
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, teacher, ids, temperature):
@@ -731,6 +842,14 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     """Layer norm over the last dimension with fp32 weight and bias (or None),
     differentiable by all three."""
     return _LayerNorm.apply(x, weight, bias, float(eps))
+
+
+def residual_norm(x, residual, weight=None, bias=None, *, post_norm: bool = True, post_weight=None, post_bias=None,
+                  gate=None, scale: float = 1.0, center: bool = True, eps: float = 1e-5):
+    """(out, y): the residual stream behind a block with output x, and the next block's input (see
+    residual_norm_forward); differentiable by x, the residual and all gains, biases and the gate."""
+    return _ResidualNorm.apply(x, residual, weight, bias, post_weight, post_bias, gate, bool(post_norm), float(scale),
+                               bool(center), float(eps))
 
 
 def distill_loss(logits, teacher, ids, *, temperature: float = 1.0):

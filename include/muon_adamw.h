@@ -501,6 +501,60 @@ ma_status ma_layer_norm_backward(const void* dy, int64_t dy_stride, const void* 
                                  float* dweight, float* dbias, int32_t accumulate, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* The norms after and before a block, with its gate and residual scale, of n rows of dim values
+ * (dim <= 2^20, n < 2^22):
+ *   b = norm(x) post_weight + post_bias      (post_norm = 0: b = x)
+ *   out = residual + scale gate b
+ *   y = norm(out) weight + bias              (of out before its rounding)
+ * norm(x) = (x - mean) rstd with rstd = 1 / sqrt(mean of (x - mean)^2 + eps) and the row's mean, or
+ * with center = 0 a mean of 0 (root mean square).  Gains, gate and biases: dim fp32 values each,
+ * NULL for ones / zeros; post_weight and post_bias need post_norm. */
+typedef struct {
+  const float* post_weight;
+  const float* post_bias;
+  const float* gate;
+  const float* weight;
+  const float* bias;
+  float scale;
+  float eps;
+  int32_t post_norm;
+  int32_t center;
+} ma_residual_norm_params;
+
+/* x, residual, out and y have type `type`; out may be the residual itself (same address and stride).
+ * stats: (4, n) fp32: mean and rstd of the first norm (zeros without one), then of the second;
+ * with out they are what the backward pass needs. */
+ma_status ma_residual_norm_forward(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                   int32_t type, int64_t n, int64_t dim, const ma_residual_norm_params* params,
+                                   void* out, int64_t out_stride, void* y, int64_t y_stride, float* stats, void* stream);
+
+/* The parameters' gradients (dim fp32 values each, written; NULL: not wanted). */
+typedef struct {
+  float* dpost_weight;
+  float* dpost_bias;
+  float* dgate;
+  float* dweight;
+  float* dbias;
+} ma_residual_norm_grads;
+
+/* Host only: workspace bytes of ma_residual_norm_backward (needed when a parameter's gradient is
+ * wanted). */
+size_t ma_residual_norm_workspace_bytes(int64_t n, int64_t dim);
+
+/* Its gradients from dout (NULL: zeros) and dy, with u and h a norm's incoming gradient and
+ * normalised row, N(u, h) = rstd (u - mean of u - h mean of (u h)), the mean of u only with center:
+ *   dresidual = dout + N(dy weight, h2)
+ *   dx = N(dresidual scale gate post_weight, h1)     (post_norm = 0: dresidual scale gate)
+ *   dweight = sum dy h2, dbias = sum dy, and with d = dresidual before its rounding
+ *   dpost_weight = scale gate sum d h1, dpost_bias = scale gate sum d, dgate = scale sum d b
+ * out and stats are the forward pass's.  n = 0 clears the parameters' gradients. */
+ma_status ma_residual_norm_backward(const void* dout, int64_t dout_stride, const void* dy, int64_t dy_stride,
+                                    const void* x, int64_t x_stride, const void* out, int64_t out_stride,
+                                    const float* stats, int32_t type, int64_t n, int64_t dim,
+                                    const ma_residual_norm_params* params, const ma_residual_norm_grads* grads, void* dx,
+                                    int64_t dx_stride, void* dresidual, int64_t dresidual_stride, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 /* Distillation from a teacher's top logits.  Per row: `vocab` student logits z (type `type`,
  * rows `stride` apart), `top` teacher logits a (teacher_type, rows contiguous) with their
  * vocabulary ids (id_bits 32 or 64, signed), temperature tau in [1e-6, 1e6]:

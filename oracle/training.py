@@ -119,3 +119,43 @@ def head_loss_grad(hidden, weight, labels, row_weight):
             dh[r] = g @ weight
             dw += np.outer(g, hidden[r])
     return dh, dw
+
+
+def _norm(x, center, eps):
+    mean = x.mean(1) if center else np.zeros(len(x))
+    rstd = 1.0 / np.sqrt(((x - mean[:, None]) ** 2).mean(1) + eps)
+    return (x - mean[:, None]) * rstd[:, None], mean, rstd
+
+
+def residual_norm(x, residual, weight=None, bias=None, post_norm=True, post_weight=None, post_bias=None, gate=None,
+                  scale=1.0, center=True, eps=1e-5):
+    """(out, y, stats) of the norms around a block."""
+    x, residual = _f64(x), _f64(residual)
+    zero = np.zeros(len(x))
+    b, mean1, rstd1 = _norm(x, center, eps) if post_norm else (x, zero, zero)
+    b = b * (1.0 if post_weight is None else _f64(post_weight)) + (0.0 if post_bias is None else _f64(post_bias))
+    out = residual + scale * (1.0 if gate is None else _f64(gate)) * b
+    h, mean2, rstd2 = _norm(out, center, eps)
+    y = h * (1.0 if weight is None else _f64(weight)) + (0.0 if bias is None else _f64(bias))
+    return out, y, np.stack([mean1, rstd1, mean2, rstd2])
+
+
+def residual_norm_grad(dout, dy, x, out, stats, weight=None, post_norm=True, post_weight=None, post_bias=None, gate=None,
+                       scale=1.0, center=True):
+    """(dx, dresidual, dweight, dbias, dpost_weight, dpost_bias, dgate) for given statistics."""
+    dout, dy, x, out = (_f64(t) for t in (dout, dy, x, out))
+    mean1, rstd1, mean2, rstd2 = (_f64(t)[:, None] for t in stats)
+    one = np.ones(x.shape[1])
+    weight, post_weight, gate = (one if t is None else _f64(t) for t in (weight, post_weight, gate))
+    post_bias = np.zeros_like(one) if post_bias is None else _f64(post_bias)
+
+    def back(u, h, rstd):
+        mean = u.mean(1, keepdims=True) if center else 0.0
+        return rstd * (u - mean - h * (u * h).mean(1, keepdims=True))
+
+    h2 = (out - mean2) * rstd2
+    d = dout + back(dy * weight, h2, rstd2)
+    h1 = (x - mean1) * rstd1 if post_norm else x
+    b, db = h1 * post_weight + post_bias, d * scale * gate
+    dx = back(db * post_weight, h1, rstd1) if post_norm else db
+    return dx, d, (dy * h2).sum(0), dy.sum(0), (db * h1).sum(0), db.sum(0), (d * scale * b).sum(0)

@@ -360,3 +360,121 @@ def test_byte_group_refusals():
     with pytest.raises(ValueError, match="6 or 7"):
         ma.adamw_byte_step_multi([(p.data, p.data)], step=1, lr=1e-3)
     ma.adamw_byte_step_multi([], step=1, lr=1e-3)
+
+
+HEAD = dict(h=A, type=2, hs=64, n=10, dim=64, w=B, ws=64, vocab=1000, labels=C, bits=64)
+HEAD_FORWARD = dict(HEAD, loss=D, lse=D + 4096, space=F, size=1 << 40, stream=None)
+HEAD_GRADS = dict(dh=G, dhs=64, dw=G + (1 << 30), dwt=0, dws=64, add=0, space=F, size=1 << 38, stream=None)
+HEAD_BACKWARD = dict(HEAD, lse=D, rw=D + 4096, **HEAD_GRADS)
+HEAD_GRAD = dict(HEAD, rw=D, loss=D + 4096, **HEAD_GRADS)
+HEAD_BAD = [
+    (dict(h=None), INVALID), (dict(w=None), INVALID), (dict(labels=None), INVALID), (dict(h=A + 1), INVALID),
+    (dict(w=B + 1), INVALID), (dict(labels=C + 4), INVALID), (dict(type=3), INVALID), (dict(bits=16), INVALID),
+    (dict(hs=63), INVALID), (dict(ws=8), INVALID), (dict(n=-1), INVALID), (dict(dim=0), INVALID), (dict(vocab=0), INVALID),
+    (dict(space=None), WORKSPACE), (dict(space=F + 64), WORKSPACE), (dict(size=1000), WORKSPACE), (dict(space=A), INVALID),
+    (dict(space=B), INVALID), (dict(n=1 << 22), UNSUPPORTED), (dict(dim=2 ** 20 + 1, hs=1 << 21, ws=1 << 21), UNSUPPORTED),
+    (dict(vocab=2 ** 30 + 1), UNSUPPORTED), (dict(hs=1 << 41), UNSUPPORTED), (dict(n=1 << 21, vocab=1 << 29), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("changes,status", HEAD_BAD + [
+    (dict(loss=None), INVALID), (dict(lse=None), INVALID), (dict(loss=D + 1), INVALID), (dict(loss=D + 4096), INVALID),
+    (dict(lse=A + 8), INVALID), (dict(loss=C), INVALID), (dict(loss=B), INVALID)])
+def test_head_forward(lib, changes, status):
+    _refused(lib, "ma_head_loss_forward", HEAD_FORWARD, changes, status)
+
+
+HEAD_BAD_GRADS = HEAD_BAD + [
+    (dict(rw=None), INVALID), (dict(dwt=1), INVALID), (dict(dwt=2, add=1), INVALID), (dict(dhs=10), INVALID),
+    (dict(dws=10), INVALID), (dict(dh=A), INVALID), (dict(dw=B), INVALID), (dict(dh=G + (1 << 30)), INVALID),
+    (dict(dw=G + (1 << 30) + 2), INVALID), (dict(dh=G + 1), INVALID), (dict(dh=C), INVALID), (dict(dw=F + 256), INVALID)]
+
+
+@pytest.mark.parametrize("changes,status", HEAD_BAD_GRADS + [(dict(lse=None), INVALID), (dict(dh=D), INVALID)])
+def test_head_backward(lib, changes, status):
+    _refused(lib, "ma_head_loss_backward", HEAD_BACKWARD, changes, status)
+
+
+@pytest.mark.parametrize("changes,status", HEAD_BAD_GRADS + [(dict(loss=None), INVALID), (dict(loss=D), INVALID)])
+def test_head_grad(lib, changes, status):
+    _refused(lib, "ma_head_loss_grad", HEAD_GRAD, changes, status)
+
+
+def test_head_workspace(lib):
+    size = lambda n, dim, vocab, at=256, stride=None, grads=1, type=2: lib.ma_head_loss_workspace_bytes(  # noqa: E731
+        type, n, dim, vocab, at, dim if stride is None else stride, grads)
+    assert size(0, 64, 10) == size(5, 0, 10) == size(5, 64, 0) == size(5, 64, 10, type=3) == 0
+    # a copy of the head only where its rows are not aligned
+    for bad in (dict(at=258), dict(stride=68), dict(stride=1 << 23)):
+        assert size(5, 64, 50000, **bad) - size(5, 64, 50000) == 50000 * 64 * 2
+    assert size(5, 60, 50000, grads=0) - size(5, 64, 50000, grads=0) == 50000 * 64 * 2
+    assert size(5, 60, 50000, at=4, type=0) == size(5, 60, 50000, type=0)
+    # the logits of 8192 rows would take 2 GiB in 16 bits
+    assert size(8192, 2048, 128000) < (512 << 20) + 8192 * 2048 * 2 * 8 + (1 << 20)
+    assert size(8192, 2048, 128000, grads=0) < 100 << 20
+    need = size(10, 64, 1000)
+    assert lib.ma_head_loss_grad(*{**HEAD_GRAD, "size": need - 1}.values()) == WORKSPACE
+
+
+def test_head_binding_refusals():
+    h, w = torch.zeros(4, 8), torch.zeros(10, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        ma.head_loss_forward(h, w, torch.zeros(4, dtype=torch.long))
+    with pytest.raises(TypeError):
+        ma.head_loss_forward(None, w, torch.zeros(4, dtype=torch.long))
+    with pytest.raises(ValueError, match="copy"):
+        ma.head_loss(h, w, torch.zeros(4, dtype=torch.long), copy=w.half())
+    with pytest.raises(ValueError, match="float32"):
+        ma.head_loss(h, w.half(), torch.zeros(4, dtype=torch.long))
+
+
+RES_PARAMS = dict(post_weight=C, post_bias=C + 4096, gate=C + 8192, weight=C + 12288, bias=C + 16384, scale=0.5, eps=1e-5,
+                  post_norm=1, center=1)
+RES = dict(x=A, xs=64, res=B, rs=64, type=2, n=10, dim=64, params=None, out=D, outs=64, y=F, ys=64, stats=G, stream=None)
+
+
+@pytest.mark.parametrize("changes,params,status", [
+    (dict(x=None), {}, INVALID), (dict(res=None), {}, INVALID), (dict(out=None), {}, INVALID), (dict(y=None), {}, INVALID),
+    (dict(stats=None), {}, INVALID), (dict(x=A + 1), {}, INVALID), (dict(stats=G + 2), {}, INVALID), (dict(type=5), {}, INVALID),
+    (dict(xs=3), {}, INVALID), (dict(rs=63), {}, INVALID), (dict(outs=0), {}, INVALID), (dict(ys=1), {}, INVALID),
+    (dict(n=-1), {}, INVALID), (dict(dim=0), {}, INVALID), (dict(out=A), {}, INVALID), (dict(out=B + 16), {}, INVALID),
+    (dict(out=B, outs=65), {}, INVALID), (dict(y=B), {}, INVALID), (dict(y=D), {}, INVALID), (dict(stats=C), {}, INVALID),
+    (dict(n=1 << 22), {}, UNSUPPORTED), (dict(dim=1 << 21), {}, UNSUPPORTED),
+    ({}, dict(scale=NAN), INVALID), ({}, dict(eps=-1.0), INVALID), ({}, dict(eps=NAN), INVALID), ({}, dict(weight=C + 1), INVALID),
+    ({}, dict(post_norm=0), INVALID), ({}, dict(post_norm=0, post_weight=None), INVALID), ({}, dict(gate=D), INVALID),
+])
+def test_residual_norm(lib, changes, params, status):
+    p = _lib._ResidualNormParams(*{**RES_PARAMS, **params}.values())
+    _refused(lib, "ma_residual_norm_forward", dict(RES, params=ctypes.byref(p)), changes, status)
+    assert lib.ma_residual_norm_forward(*RES.values()) == INVALID  # no parameters
+
+
+RES_GRAD = dict(dout=A, dos=64, dy=A + 4096, dys=64, x=B, xs=64, out=B + 4096, outs=64, stats=G, type=2, n=10, dim=64,
+                params=None, grads=None, dx=D, dxs=64, dres=D + 4096, dress=64, ws=F, size=1 << 30, stream=None)
+RES_GRADS = dict(dpost_weight=G + 4096, dpost_bias=G + 8192, dgate=G + 12288, dweight=G + 16384, dbias=G + 20480)
+
+
+@pytest.mark.parametrize("changes,params,grads,status", [
+    (dict(dy=None), {}, {}, INVALID), (dict(x=None), {}, {}, INVALID), (dict(out=None), {}, {}, INVALID),
+    (dict(stats=None), {}, {}, INVALID), (dict(dx=None), {}, {}, INVALID), (dict(dres=None), {}, {}, INVALID),
+    (dict(dos=1), {}, {}, INVALID), (dict(dys=1), {}, {}, INVALID), (dict(dxs=1), {}, {}, INVALID), (dict(dx=A), {}, {}, INVALID),
+    (dict(dres=A + 4096), {}, {}, INVALID), (dict(dx=D + 4096), {}, {}, INVALID), (dict(ws=None), {}, {}, WORKSPACE),
+    (dict(ws=F + 16), {}, {}, WORKSPACE), (dict(size=100), {}, {}, WORKSPACE), (dict(ws=B), {}, {}, INVALID),
+    ({}, dict(post_norm=0, post_weight=None, post_bias=None), {}, INVALID), ({}, {}, dict(dgate=G + 4096), INVALID),
+    ({}, {}, dict(dweight=G + 1), INVALID), ({}, {}, dict(dbias=C), INVALID), (dict(type=4), {}, {}, INVALID),
+])
+def test_residual_norm_gradient(lib, changes, params, grads, status):
+    p = _lib._ResidualNormParams(*{**RES_PARAMS, **params}.values())
+    g = _lib._ResidualNormGrads(*{**RES_GRADS, **grads}.values())
+    args = dict(RES_GRAD, params=ctypes.byref(p), grads=ctypes.byref(g))
+    _refused(lib, "ma_residual_norm_backward", args, changes, status)
+    assert lib.ma_residual_norm_backward(*{**args, "grads": None}.values()) == INVALID
+    assert ma.residual_norm_workspace_bytes(0, 64) == 0 < ma.residual_norm_workspace_bytes(5, 64)
+
+
+def test_residual_norm_binding_refusals():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        ma.residual_norm_forward(x, x)
+    with pytest.raises(TypeError):
+        ma.residual_norm_forward(None, x)
