@@ -18,8 +18,12 @@
 //
 // Rounding: products of 16-bit values are exact and summed in fp32.  g is rounded once to the
 // hidden type, as the matrix cores take it, after a scaling by a power of two that brings the
-// largest row weight near 2^14: fp16 then keeps probabilities down to 2^-38.  fp32 runs on the fp32
-// matrix instructions.  Every sum has a fixed order: the same inputs give the same bits.
+// largest row weight near 2^14: fp16 then keeps probabilities down to 2^-38.  Every sum has a fixed
+// order: the same inputs give the same bits.
+// fp32 operands: up to kSplitRows rows on the fp32 matrix instructions; above as three bf16 planes
+// each (x = x0 + x1 + x2 to 2^-24 of itself: three times 8 bits), whose six products of 2^-16 and more
+// run as one sum six times as long, the smallest first: the three that are left out are 2^-24 of the
+// product together.
 #include "gemm_tile.h"
 #include "ma_act.h"
 #include "ma_internal.h"
@@ -96,51 +100,74 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
   }
 }
 
-// The live rows' padded copies (dim_pad values, zeros behind dim), and zero rows behind the last up
-// to a whole tile.  A wave per row.
-template <typename S>
-__global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int live = c.head->live;
-  if (at >= (live + kHeadTile - 1) / kHeadTile * static_cast<int64_t>(kHeadTile)) return;
-  S* out = static_cast<S*>(c.hidden_pad) + at * c.dim_pad;
-  const S* in = at < live ? static_cast<const S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
+// Planes of operands that the 16-bit tiles read: one, or three for fp32 values in bf16.
+template <int T>
+struct Planes {
+  static constexpr int kCount = T == kActF32 ? 3 : 1;
+  // four values into the planes at out, out + stride, ..
+  static __device__ __forceinline__ void store(const float (&v)[4], unsigned short* out, int64_t stride) {
+    float rest[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      unsigned short x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = f2bf(rest[e]);
+        rest[e] -= bf2f(x[e]);
+      }
+      u32x2 w;
+      w[0] = x[0] | (static_cast<unsigned>(x[1]) << 16);
+      w[1] = x[2] | (static_cast<unsigned>(x[3]) << 16);
+      *reinterpret_cast<u32x2*>(out + k * stride) = w;
+    }
+  }
+};
+
+// A row of dim values from `in` (null: zeros) to a padded row at `out`, as it is or in planes.  A wave.
+template <int T, bool kPlanes>
+__device__ __forceinline__ void head_copy_row(const typename Act<T>::S* in, void* out, int64_t at, int64_t plane,
+                                              int64_t dim, int64_t dim_pad) {
+  typedef typename Act<T>::S S;
   typedef typename Pack<S, 4>::type P;
-  for (int64_t i = lane * 4; i < c.dim_pad; i += 256) {
+  for (int64_t i = (threadIdx.x & 63) * 4; i < dim_pad; i += 256) {
     P x = 0;
     if (in) {
-      if (i + 4 <= c.dim) {
+      if (i + 4 <= dim) {
         x = *reinterpret_cast<const P*>(in + i);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (i + e < c.dim) x[e] = in[i + e];
+          if (i + e < dim) x[e] = in[i + e];
       }
     }
-    *reinterpret_cast<P*>(out + i) = x;
+    if constexpr (kPlanes) {
+      const float v[4] = {x[0], x[1], x[2], x[3]};
+      Planes<T>::store(v, static_cast<unsigned short*>(out) + at + i, plane);
+    } else {
+      *reinterpret_cast<P*>(static_cast<S*>(out) + at + i) = x;
+    }
   }
 }
 
-// W in rows of dim_pad values, for rows that are not aligned to 16 bytes.  A wave per row.
+// The live rows' padded copies (dim_pad values, zeros behind dim), and zero rows behind the last up
+// to a whole tile.  A wave per row.
+template <int T, bool kPlanes>
+__global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int live = c.head->live;
+  if (at >= (live + kHeadTile - 1) / kHeadTile * static_cast<int64_t>(kHeadTile)) return;
+  const auto* in = at < live ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
+  head_copy_row<T, kPlanes>(in, c.hidden_pad, at * c.dim_pad, c.hidden_plane, c.dim, c.dim_pad);
+}
+
+// W in rows of dim_pad values: rows that are not aligned to 16 bytes, or fp32's planes.  A wave per
+// row.
+template <int T>
 __global__ __launch_bounds__(256) void head_weight_kernel(HeadCall c) {
-  const int lane = threadIdx.x & 63;
   const int64_t v = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (v >= c.vocab) return;
-  const unsigned short* in = static_cast<const unsigned short*>(c.weight_in) + v * c.weight_in_stride;
-  unsigned short* out = static_cast<unsigned short*>(c.weight_pad) + v * c.dim_pad;
-  typedef Pack<unsigned short, 4>::type P;
-  for (int64_t i = lane * 4; i < c.dim_pad; i += 256) {
-    P x = 0;
-    if (i + 4 <= c.dim) {
-      x = *reinterpret_cast<const P*>(in + i);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < c.dim) x[e] = in[i + e];
-    }
-    *reinterpret_cast<P*>(out + i) = x;
-  }
+  head_copy_row<T, T == kActF32>(static_cast<const typename Act<T>::S*>(c.weight_in) + v * c.weight_in_stride, c.weight_pad,
+                                 v * c.dim_pad, c.weight_plane, c.dim, c.dim_pad);
 }
 
 // dW of no rows at all.  A wave per row.
@@ -240,7 +267,7 @@ __device__ __forceinline__ bool head_tile(int mode, int mt, int nt, int splits, 
 
 // Accumulators of a wave: tile i of 32 rows, tile j of 32 columns; the lane holds row (lane & 31)
 // and columns 8 q + 4 (lane / 32) + e in element 4 q + e.
-template <int T, int kMode, int BM, int BN, int WM, int WN, int WTM, int WTN>
+template <int T, bool kPlanes, int kMode, int BM, int BN, int WM, int WN, int WTM, int WTN>
 __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&acc)[WTM][WTN], int m0, int n0, int split,
                                               int live, char* smem) {
   typedef typename Act<T>::S S;
@@ -254,26 +281,34 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
 #pragma unroll
     for (int i = 0; i < WTM; ++i) {
       const int row = row0 + i * 32;
-      const int label = m0 + row < live ? c.label[m0 + row] - n0 : -1;
-      float top = -INFINITY;
+      // few waves meet a label among their columns
+      const int label = m0 + row < live ? c.label[m0 + row] - n0 - wn * (WTN * 32) : -1;
+      if (__any(label >= 0 && label < WTN * 32)) {
 #pragma unroll
-      for (int j = 0; j < WTN; ++j)
+        for (int j = 0; j < WTN; ++j)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int col = col0 + j * 32 + 8 * (k >> 2) + (k & 3);
-          if (col < count) top = fmaxf(top, acc[i][j][k]);
-          if (col == label) c.target[m0 + row] = acc[i][j][k];
-        }
-      const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f;
+          for (int k = 0; k < 16; ++k)
+            if (j * 32 + 4 * half + 8 * (k >> 2) + (k & 3) == label) c.target[m0 + row] = acc[i][j][k];
+      }
+      float top = -INFINITY, sum = 0.0f, base;
+      const auto gather = [&](auto mask) {  // mask: the vocabulary ends within this tile
+        constexpr bool kMask = decltype(mask)::value;
 #pragma unroll
-      for (int j = 0; j < WTN; ++j)
+        for (int j = 0; j < WTN; ++j)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int col = col0 + j * 32 + 8 * (k >> 2) + (k & 3);
-          const float e = __builtin_amdgcn_exp2f((acc[i][j][k] - base) * kLog2e);
-          sum += col < count ? e : 0.0f;
-        }
+          for (int k = 0; k < 16; ++k)
+            if (!kMask || col0 + j * 32 + 8 * (k >> 2) + (k & 3) < count) top = fmaxf(top, acc[i][j][k]);
+        base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float e = __builtin_amdgcn_exp2f((acc[i][j][k] - base) * kLog2e);
+            sum += !kMask || col0 + j * 32 + 8 * (k >> 2) + (k & 3) < count ? e : 0.0f;
+          }
+      };
+      if (count < BN) gather(std::true_type{});
+      else gather(std::false_type{});
       // the other half of the columns
       const float top2 = __shfl_xor(top, 32, 64), sum2 = __shfl_xor(sum, 32, 64);
       const float both = fmaxf(top, top2), b = both == -INFINITY ? 0.0f : both;
@@ -300,47 +335,78 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
     // n0 counts from the piece's first entry
     const int64_t left = c.vocab - c.piece_start - n0;
     const int count = left < BN ? static_cast<int>(left) : BN;
-    S* out = static_cast<S*>(c.g) + static_cast<int64_t>(m0) * c.piece + n0;
-    if constexpr (T != kActF32) __syncthreads();
+    constexpr bool kStaged = kPlanes || T != kActF32;
+    if constexpr (kStaged) __syncthreads();
 #pragma unroll
     for (int i = 0; i < WTM; ++i) {
       const int row = row0 + i * 32;
+      // a padded row's logits are zeros, and so is its factor
       const bool on = m0 + row < live;
       const float top = on ? c.top[m0 + row] : 0.0f, factor = on ? c.factor[m0 + row] : 0.0f;
-      const float weight = on ? c.weight[m0 + row] : 0.0f;
-      const int label = on ? static_cast<int>(c.label[m0 + row] - c.piece_start) - n0 : -1;
-      const int most = on ? count : 0;
+      const int label = on ? static_cast<int>(c.label[m0 + row] - c.piece_start) - n0 - wn * (WTN * 32) : -1;
+      float g[WTN][16];
 #pragma unroll
       for (int j = 0; j < WTN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = col0 + j * 32 + 8 * q;
-          float g[4];
+        for (int k = 0; k < 16; ++k) g[j][k] = factor * __builtin_amdgcn_exp2f((acc[i][j][k] - top) * kLog2e);
+      if (__any(label >= 0 && label < WTN * 32)) {
+        const float weight = on ? c.weight[m0 + row] : 0.0f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = __builtin_amdgcn_exp2f((acc[i][j][4 * q + e] - top) * kLog2e);
-            g[e] = __builtin_fmaf(p, factor, col + e == label ? -weight : 0.0f);
-            if (col + e >= most) g[e] = 0.0f;
-          }
-          if constexpr (T == kActF32) {
-            *reinterpret_cast<f32x4*>(out + static_cast<int64_t>(row) * c.piece + col) = f32x4{g[0], g[1], g[2], g[3]};
-          } else {
-            // staged so that whole rows of the tile leave; 16-byte chunks are XOR-ed with the row
-            u32x2 x;
-            x[0] = Act<T>::down(g[0]) | (static_cast<unsigned>(Act<T>::down(g[1])) << 16);
-            x[1] = Act<T>::down(g[2]) | (static_cast<unsigned>(Act<T>::down(g[3])) << 16);
-            *reinterpret_cast<u32x2*>(smem + row * (BN * 2) + ((((col >> 3) ^ row) & (BN / 8 - 1)) << 4) + (col & 4) * 2) = x;
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (j * 32 + 4 * half + 8 * (k >> 2) + (k & 3) == label)
+              g[j][k] = __builtin_fmaf(__builtin_amdgcn_exp2f((acc[i][j][k] - top) * kLog2e), factor, -weight);
+      }
+      if (count < BN) {
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (col0 + j * 32 + 8 * (k >> 2) + (k & 3) >= count) g[j][k] = 0.0f;
+      }
+      if constexpr (!kStaged) {
+        float* out = static_cast<float*>(c.g) + static_cast<int64_t>(m0 + row) * c.piece + n0 + col0;
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(out + j * 32 + 8 * q) = f32x4{g[j][4 * q], g[j][4 * q + 1], g[j][4 * q + 2], g[j][4 * q + 3]};
+      } else {
+        // a wave stages its 32 rows of 64 columns, chunks of 16 bytes XOR-ed with the row, so that
+        // whole 128-byte lines leave
+        static_assert(WTN == 2, "eight chunks a row");
+        char* stage = smem + wave * (32 * 128);
+#pragma unroll
+        for (int plane = 0; plane < (kPlanes ? 3 : 1); ++plane) {
+#pragma unroll
+          for (int j = 0; j < WTN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              unsigned short x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float& v = g[j][4 * q + e];
+                if constexpr (kPlanes) {
+                  x[e] = f2bf(v);
+                  v -= bf2f(x[e]);
+                } else {
+                  x[e] = Act<T>::down(v);
+                }
+              }
+              u32x2 w;
+              w[0] = x[0] | (static_cast<unsigned>(x[1]) << 16);
+              w[1] = x[2] | (static_cast<unsigned>(x[3]) << 16);
+              *reinterpret_cast<u32x2*>(stage + frow * 128 + (((j * 4 + q) ^ (frow & 7)) << 4) + half * 8) = w;
+            }
+          unsigned short* out = static_cast<unsigned short*>(c.g) + plane * c.g_plane + n0 + wn * 64;
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int r = it * 8 + (lane >> 3), ch = lane & 7;
+            const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+            *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(m0 + wm * (WTM * 32) + i * 32 + r) * c.piece + ch * 8) = x;
           }
         }
-    }
-    if constexpr (T != kActF32) {
-      __syncthreads();
-      constexpr int kChunks = BN / 8;
-#pragma unroll
-      for (int it = 0; it < BM * kChunks / (64 * WM * WN); ++it) {
-        const int idx = threadIdx.x + it * (64 * WM * WN), row = idx / kChunks, ch = idx % kChunks;
-        const u32x4 x = *reinterpret_cast<const u32x4*>(smem + row * (BN * 2) + (((ch ^ row) & (kChunks - 1)) << 4));
-        *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(row) * c.piece + ch * 8) = x;
       }
     }
   } else if constexpr (kMode == kHidden) {
@@ -391,7 +457,7 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
   }
 }
 
-// 16-bit operands: BM x 256 tiles of 8 waves (2 x 4), v_mfma_f32_32x32x16, stages of 64 of the
+// 16-bit operands (or planes of them): BM x 256 tiles of 8 waves (2 x 4), v_mfma_f32_32x32x16, stages of 64 of the
 // summed index, loaded straight into LDS.  Operands are contiguous along that index (hidden rows and
 // W in the logits, g in dh) or across it (W in dh; g and the hidden rows in dW), which the
 // transposing LDS reads take, so nothing is stored twice.  The accumulators hold a row a lane
@@ -407,12 +473,12 @@ struct HeadCfg {
   static constexpr int kDmaA = BM * BK / 512 / kWaves, kDmaB = BN * BK / 512 / kWaves, kDma = kDmaA + kDmaB;
   static constexpr int kAElems = BM * BK, kBElems = BN * BK, kBBase = SA * kAElems;
   static constexpr int kLds = (SA * kAElems + SB * kBElems) * 2;
-  static_assert(kLds <= 160 * 1024 && BM * BN * 2 <= kLds && kDmaA >= 1, "LDS");
+  static_assert(kLds <= 160 * 1024 && kDmaA >= 1, "LDS");
 };
 
 template <int T>
 __device__ __forceinline__ f32x16 head_mfma(bf16x8 a, bf16x8 b, f32x16 c) {
-  if constexpr (T == kActBF16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  if constexpr (T != kActF16) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
@@ -448,7 +514,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   const unsigned short* W = static_cast<const unsigned short*>(c.weight_use) + c.piece_start * c.weight_stride;
   const int64_t w_left = c.vocab - c.piece_start;  // rows of W from the piece on
   const unsigned short *gA, *gB;
-  int lda, ldb, k_from = 0, nk;
+  int lda, ldb, k_from = 0, steps;  // steps: stages along the summed index
   int64_t left_b;  // values of B behind gB
   if constexpr (kMode == kStats || kMode == kGrad) {
     gA = static_cast<const unsigned short*>(c.hidden_pad) + static_cast<int64_t>(m0) * c.dim_pad;
@@ -456,60 +522,85 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     gB = W + static_cast<int64_t>(n0) * c.weight_stride;
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use;
-    nk = static_cast<int>(c.dim_pad / C::BK);
+    steps = static_cast<int>(c.dim_pad / C::BK);
   } else if constexpr (kMode == kHidden) {
     const int all = c.piece_tiles * (256 / C::BK), per = (all + c.splits - 1) / c.splits;
     k_from = split * per;
-    nk = all - k_from < per ? all - k_from : per;
-    nk = nk < 0 ? 0 : nk;
+    steps = all - k_from < per ? all - k_from : per;
+    steps = steps < 0 ? 0 : steps;
     gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(m0) * c.piece + k_from * C::BK;
     lda = static_cast<int>(c.piece);
     gB = W + static_cast<int64_t>(k_from) * C::BK * c.weight_stride + n0;
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - static_cast<int64_t>(k_from) * C::BK - 1) * c.weight_stride + c.dim_use - n0;
   } else {
-    nk = (live + C::BK - 1) / C::BK;
+    steps = (live + C::BK - 1) / C::BK;
     gA = static_cast<const unsigned short*>(c.g) + m0;
     lda = static_cast<int>(c.piece);
     gB = static_cast<const unsigned short*>(c.hidden_pad) + n0;
     ldb = static_cast<int>(c.dim_pad);
-    left_b = static_cast<int64_t>(nk) * C::BK * c.dim_pad - n0;
+    left_b = static_cast<int64_t>(steps) * C::BK * c.dim_pad - n0;
   }
+
+  // fp32's six products of planes, the smallest first; stage kt of the sum is step kt % steps of
+  // product kt / steps
+  constexpr int kProducts = T == kActF32 ? 6 : 1;
+  const int nk = steps * kProducts;
+  const int64_t plane_a = kMode == kStats || kMode == kGrad ? c.hidden_plane : c.g_plane;
+  const int64_t plane_b = kMode == kWeight ? c.hidden_plane : c.weight_plane;
+  const auto at_a = [&](int kt, int& step) -> const unsigned short* {
+    step = kt;
+    if constexpr (kProducts == 1) return gA;
+    const int product = kt / steps;
+    step = kt - product * steps;
+    return gA + (0x010210 >> (4 * product) & 15) * plane_a;
+  };
+  const auto at_b = [&](int kt, int& step) -> const unsigned short* {
+    step = kt;
+    if constexpr (kProducts == 1) return gB;
+    const int product = kt / steps;
+    step = kt - product * steps;
+    return gB + (0x001012 >> (4 * product) & 15) * plane_b;
+  };
 
   const auto issue_a = [&](int kt, int i) {
     unsigned short* s = smem + (kt % C::SA) * C::kAElems;
     const int q = i * C::kWaves + wave;
+    int step;
+    const unsigned short* base = at_a(kt, step);
     if constexpr (C::kAT) {
       constexpr int kChunks = BM / 8, kRows = 64 / kChunks;
       const int r0 = q * kRows, r = r0 + lane / kChunks, ch = lane % kChunks;
-      dma16<C::kBT>(gA + static_cast<int64_t>(kt) * C::BK * lda, (r * lda + swz_kn(r, ch) * 8) * 2,
+      dma16<C::kBT>(base + static_cast<int64_t>(step) * C::BK * lda, (r * lda + swz_kn(r, ch) * 8) * 2,
                     static_cast<unsigned>(((C::BK - 1) * lda + BM) * 2), s + r0 * BM);
     } else {
       const int r0 = q * 8, r = r0 + lane / 8;
-      dma16<C::kBT>(gA + kt * C::BK, (r * lda + swz<64>(r, lane % 8) * 8) * 2,
+      dma16<C::kBT>(base + step * C::BK, (r * lda + swz<64>(r, lane % 8) * 8) * 2,
                     static_cast<unsigned>(((BM - 1) * lda + C::BK) * 2), s + r0 * C::BK);
     }
   };
   const auto issue_b = [&](int kt, int i) {
     unsigned short* s = smem + C::kBBase + (kt % C::SB) * C::kBElems;
     const int q = i * C::kWaves + wave;
+    int step;
+    const unsigned short* base = at_b(kt, step);
     // reads behind the operand's end return zeros: vocabulary entries behind the last, and (below)
     // columns behind the hidden size, where W's next row follows
     if constexpr (C::kBT) {
       constexpr int kChunks = C::BN / 8, kRows = 64 / kChunks;
       const int r0 = q * kRows, r = r0 + lane / kChunks, ch = lane % kChunks;
-      const int64_t left = left_b - static_cast<int64_t>(kt) * C::BK * ldb;
+      const int64_t left = left_b - static_cast<int64_t>(step) * C::BK * ldb;
       const int64_t most = static_cast<int64_t>(C::BK - 1) * ldb + C::BN;
       const int64_t values = left < 0 ? 0 : left < most ? left : most;
-      dma16<C::kBT>(gB + static_cast<int64_t>(kt) * C::BK * ldb, (r * ldb + swz_kn(r, ch) * 8) * 2,
+      dma16<C::kBT>(base + static_cast<int64_t>(step) * C::BK * ldb, (r * ldb + swz_kn(r, ch) * 8) * 2,
                     static_cast<unsigned>(values * 2), s + r0 * C::BN);
     } else {
       const int r0 = q * 8, r = r0 + lane / 8, ch = swz<64>(r, lane % 8);
-      const int64_t left = left_b - kt * C::BK;
+      const int64_t left = left_b - step * C::BK;
       const int64_t most = static_cast<int64_t>(C::BN - 1) * ldb + C::BK;
       const int64_t values = left < 0 ? 0 : left < most ? left : most;
-      const int off = kt * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
-      dma16<C::kBT>(gB + kt * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
+      const int off = step * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
+      dma16<C::kBT>(base + step * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
     }
   };
   // group v of the loads: A of stage v + LA, B of stage v + LB (the shorter lead first)
@@ -608,7 +699,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     for (; kt < nk - C::SA; ++kt) run_stage(kt, std::true_type{});
     for (; kt < nk; ++kt) run_stage(kt, std::false_type{});
   }
-  head_epilogue<T, kMode, BM, C::BN, C::WM, C::WN>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(smem));
+  head_epilogue<T, T == kActF32, kMode, BM, C::BN, C::WM, C::WN>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(smem));
 }
 
 // fp32 operands: 128 x 128 tiles of 4 waves (2 x 2), v_mfma_f32_32x32x2, stages of 16 of the summed
@@ -746,7 +837,16 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
       __syncthreads();
     }
   }
-  head_epilogue<kActF32, kMode, B, B, 2, 2>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(&smem[0][0][0]));
+  head_epilogue<kActF32, false, kMode, B, B, 2, 2>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(&smem[0][0][0]));
+}
+
+// Host: whether fp32 runs on bf16 planes, and the tiles' columns.
+bool head_split(int type, int64_t n) { return type == kActF32 && n > kSplitRows; }
+int64_t head_tile_size(int type, bool split) { return type == kActF32 && !split ? 128 : 256; }
+// A tile's rows, in the products whose rows are the call's.
+int64_t head_tile_rows(int type, int64_t n) {
+  if (type == kActF32) return head_split(type, n) ? 256 : 128;
+  return n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
 // Host: blocks of a launch over `tiles` tiles at most (see head_tile).
@@ -754,67 +854,82 @@ dim3 head_grid(int64_t tiles) { return dim3(static_cast<unsigned>(8 * ((tiles + 
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int T, int BM, int kMode>
+// kSplit: fp32 on bf16 planes.
+template <int T, bool kSplit, int BM, int kMode>
 hipError_t launch_head_gemm(const HeadCall& c, int64_t tiles, hipStream_t s) {
-  if constexpr (T == kActF32)
+  if constexpr (T == kActF32 && !kSplit)
     hipLaunchKernelGGL((head_gemm32_kernel<kMode>), head_grid(tiles), dim3(256), 0, s, c);
   else
     hipLaunchKernelGGL((head_gemm_kernel<T, BM, kMode>), head_grid(tiles), dim3(512), 0, s, c);
   return hipGetLastError();
 }
 
-template <int T, int kMode>
+template <int T, bool kSplit, int kMode>
 hipError_t launch_head_rows(const HeadCall& c, int64_t cols, hipStream_t s) {
-  if constexpr (T == kActF32) return launch_head_gemm<T, 128, kMode>(c, ceil_div(c.n, 128) * cols, s);
-  else if (c.n <= 64) return launch_head_gemm<T, 64, kMode>(c, cols, s);
-  else if (c.n <= 128) return launch_head_gemm<T, 128, kMode>(c, cols, s);
-  else return launch_head_gemm<T, 256, kMode>(c, ceil_div(c.n, 256) * cols, s);
+  if constexpr (T == kActF32 && !kSplit) {
+    return launch_head_gemm<T, kSplit, 128, kMode>(c, ceil_div(c.n, 128) * cols, s);
+  } else {
+    if constexpr (!kSplit) {  // (more rows are split than these tiles take)
+      if (c.n <= 64) return launch_head_gemm<T, kSplit, 64, kMode>(c, cols, s);
+      if (c.n <= 128) return launch_head_gemm<T, kSplit, 128, kMode>(c, cols, s);
+    }
+    return launch_head_gemm<T, kSplit, 256, kMode>(c, ceil_div(c.n, 256) * cols, s);
+  }
 }
 
-template <int T>
+template <int T, bool kSplit>
 hipError_t gather(const HeadCall& c, hipStream_t s) {
   hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kRowThreads), 0, s, c);
-  hipLaunchKernelGGL((head_gather_kernel<typename Act<T>::S>), dim3(static_cast<unsigned>(c.rows_pad / 4)), dim3(256), 0, s, c);
+  hipLaunchKernelGGL((head_gather_kernel<T, kSplit>), dim3(static_cast<unsigned>(c.rows_pad / 4)), dim3(256), 0, s, c);
   return hipGetLastError();
 }
 
-template <int T>
+template <int T, bool kSplit>
 hipError_t forward(const HeadCall& call, hipStream_t s) {
   HeadCall c = call;
   c.row_weight = nullptr;
   c.lse_in = nullptr;
-  constexpr int kTile = T == kActF32 ? 128 : 256;
   c.piece_start = 0;
-  c.piece_tiles = static_cast<int>(ceil_div(c.vocab, kTile));
+  c.piece_tiles = static_cast<int>(ceil_div(c.vocab, head_tile_size(T, kSplit)));
   c.tiles = c.piece_tiles;
-  if (const hipError_t e = gather<T>(c, s)) return e;
-  if (const hipError_t e = launch_head_rows<T, kStats>(c, c.piece_tiles, s)) return e;
+  if (const hipError_t e = gather<T, kSplit>(c, s)) return e;
+  if (const hipError_t e = launch_head_rows<T, kSplit, kStats>(c, c.piece_tiles, s)) return e;
   hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
   return hipGetLastError();
 }
 
-template <int T>
+template <int T, bool kSplit>
 hipError_t backward(const HeadCall& call, hipStream_t s) {
   HeadCall c = call;
   c.loss = nullptr;
   c.lse_out = nullptr;
-  constexpr int kTile = T == kActF32 ? 128 : 256;
-  if (const hipError_t e = gather<T>(c, s)) return e;
-  const int64_t dim_tiles = ceil_div(c.dim, kTile);
+  const int64_t tile = head_tile_size(T, kSplit), dim_tiles = ceil_div(c.dim, tile);
+  if (const hipError_t e = gather<T, kSplit>(c, s)) return e;
   for (int64_t v = 0; v < c.vocab; v += c.piece) {
     c.piece_start = v;
     c.first = v == 0;
     const int64_t here = c.vocab - v < c.piece ? c.vocab - v : c.piece;
-    c.piece_tiles = static_cast<int>(ceil_div(here, kTile));
-    if (const hipError_t e = launch_head_rows<T, kGrad>(c, c.piece_tiles, s)) return e;
+    c.piece_tiles = static_cast<int>(ceil_div(here, tile));
+    if (const hipError_t e = launch_head_rows<T, kSplit, kGrad>(c, c.piece_tiles, s)) return e;
     if (c.dhidden)
-      if (const hipError_t e = launch_head_rows<T, kHidden>(c, dim_tiles * c.splits, s)) return e;
+      if (const hipError_t e = launch_head_rows<T, kSplit, kHidden>(c, dim_tiles * c.splits, s)) return e;
     if (c.dweight)
-      if (const hipError_t e = launch_head_gemm<T, 256, kWeight>(c, c.piece_tiles * dim_tiles, s)) return e;
+      if (const hipError_t e = launch_head_gemm<T, kSplit, 256, kWeight>(c, c.piece_tiles * dim_tiles, s)) return e;
   }
   if (c.dhidden)
     hipLaunchKernelGGL((head_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
   return hipGetLastError();
+}
+
+template <int T, bool kSplit>
+hipError_t run_work(const HeadCall& c, HeadWork work, hipStream_t s) {
+  if (c.weight_pad) {
+    hipLaunchKernelGGL((head_weight_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
+    if (const hipError_t e = hipGetLastError()) return e;
+  }
+  if (work != kHeadBackward)
+    if (const hipError_t e = forward<T, kSplit>(c, s)) return e;
+  return work != kHeadForward ? backward<T, kSplit>(c, s) : hipSuccess;
 }
 
 int64_t align_up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
@@ -827,8 +942,8 @@ bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t strid
 }
 
 int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p) {
-  const int64_t rows = type == kActF32 ? 128 : n <= 64 ? 64 : n <= 128 ? 128 : 256, tile = type == kActF32 ? 128 : 256;
-  const int64_t row_tiles = ceil_div(n, rows), dim_tiles = ceil_div(dim, tile);
+  const int64_t tile = head_tile_size(type, p.split);
+  const int64_t row_tiles = ceil_div(n, head_tile_rows(type, n)), dim_tiles = ceil_div(dim, tile);
   int64_t tiles = row_tiles * ceil_div(vocab, tile);
   const int64_t others[] = {row_tiles * dim_tiles * p.splits, p.piece / tile * dim_tiles};
   for (const int64_t t : others) tiles = t > tiles ? t : tiles;
@@ -836,8 +951,10 @@ int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const Head
 }
 
 HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, bool gradients) {
-  const int64_t size = type == kActF32 ? 4 : 2, tile = type == kActF32 ? 128 : 256;
   HeadPlan p{};
+  p.split = head_split(type, n);
+  // bytes of a value of the gathered rows, g and a copied W
+  const int64_t size = p.split ? 6 : type == kActF32 ? 4 : 2, tile = head_tile_size(type, p.split);
   p.rows_pad = align_up(n, kHeadTile);
   p.dim_pad = align_up(dim, 64);
   int64_t at = 0;
@@ -856,26 +973,31 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   p.factor = take(n * 4);
   p.tops = take(n * 4);
   p.sums = take(n * 4);
-  // a tile's columns behind the hidden size are read (and dropped) up to a whole tile
-  p.hidden = take((p.rows_pad * p.dim_pad + tile) * size);
-  p.weight_pad = copied ? take(vocab * p.dim_pad * size) : 0;
+  // (fp32: a tile's columns behind the hidden size are read, and dropped, up to a whole tile)
+  p.hidden = take(p.rows_pad * p.dim_pad * size + tile * 4);
+  p.weight_pad = copied || p.split ? take(vocab * p.dim_pad * size) : 0;
   // the statistics of the forward pass lie where the backward pass has g
   const int64_t tiles = ceil_div(vocab, tile);
   int64_t piece = kHeadPieceBytes / (p.rows_pad * size) / tile;
   piece = piece < 1 ? 1 : piece;
-  p.pieces = ceil_div(tiles, piece);
-  p.piece = ceil_div(tiles, p.pieces) * tile;
+  p.piece = ceil_div(tiles, ceil_div(tiles, piece)) * tile;
   const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.piece * size : 0;
   p.partial = take(stats > g ? stats : g);
   p.splits = 1;
   p.sum_stride = align_up(dim, 4);
   if (gradients) {
-    // enough blocks for the chip: two a compute unit, each with 1024 vocabulary entries at least
-    const int64_t rows = type == kActF32 ? 128 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
-    const int64_t blocks = ceil_div(n, rows) * ceil_div(dim, tile);
-    int64_t splits = 512 / blocks, most = p.piece / 1024;
-    splits = splits > most ? most : splits;
-    p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+    // dh's tiles are few: the sum over the piece is split where that fills more of the chip's 256
+    // compute units (a block each), by 1024 vocabulary entries at least
+    const int64_t blocks = ceil_div(n, head_tile_rows(type, n)) * ceil_div(dim, tile);
+    double best = 0.0;
+    for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 1024 <= p.piece); ++splits) {
+      const int64_t all = blocks * splits;
+      const double busy = static_cast<double>(all) / (256 * ceil_div(all, 256));
+      if (busy > best + 0.05) {
+        best = busy;
+        p.splits = static_cast<int>(splits);
+      }
+    }
     p.sum = take(p.splits * p.rows_pad * p.sum_stride * 4);
   }
   p.bytes = at;
@@ -912,18 +1034,20 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.weight_use = c.weight_in;
   c.weight_stride = c.weight_in_stride;
   c.dim_use = c.dim;
+  c.hidden_plane = p.rows_pad * p.dim_pad;
+  c.weight_plane = c.vocab * p.dim_pad;
+  c.g_plane = p.rows_pad * p.piece;
+  c.weight_pad = nullptr;
   if (p.weight_pad) {
     c.weight_pad = ws + p.weight_pad;
     c.weight_use = c.weight_pad;
     c.weight_stride = c.dim_use = p.dim_pad;
-    hipLaunchKernelGGL(head_weight_kernel, dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
-    if (const hipError_t e = hipGetLastError()) return e;
   }
   return with_act(c.type, [&](auto t) {
     constexpr int T = decltype(t)::value;
-    if (work != kHeadBackward)
-      if (const hipError_t e = forward<T>(c, s)) return e;
-    return work != kHeadForward ? backward<T>(c, s) : hipSuccess;
+    if constexpr (T == kActF32)
+      if (p.split) return run_work<T, true>(c, work, s);
+    return run_work<T, false>(c, work, s);
   });
 }
 

@@ -582,6 +582,7 @@ hipError_t launch_residual_backward(const ResidualGradCall& c, hipStream_t s);
 // The LM head's cross entropy (head_loss.hip).
 constexpr int kHeadTile = 256;  // gathered rows are padded to a multiple of this
 constexpr int64_t kHeadPieceBytes = int64_t{512} << 20;  // of g, for up to 2^20 rows
+constexpr int64_t kSplitRows = 128;  // fp32 calls of more rows run on bf16 planes
 struct HeadInfo {
   int live;       // rows that take part
   float unscale;  // of the products with g
@@ -589,8 +590,9 @@ struct HeadInfo {
 // Workspace: byte offsets, and what its sizes settle.
 struct HeadPlan {
   int64_t head, place, row_of, label, target, weight, top, factor, tops, sums, hidden, weight_pad, partial, sum, bytes;
-  int64_t rows_pad, dim_pad, sum_stride, piece, pieces;
+  int64_t rows_pad, dim_pad, sum_stride, piece;
   int splits;
+  bool split;  // fp32 values as three bf16 planes
 };
 // Whether the weight's rows must be copied to be aligned to 16 bytes.
 bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride);
@@ -633,6 +635,7 @@ struct HeadCall {
   void* g;          // rows_pad x piece
   float* sum;       // splits x rows_pad x sum_stride
   int64_t rows_pad, dim_pad, dim_use, weight_stride, sum_stride, piece, tiles, piece_start;
+  int64_t hidden_plane, weight_plane, g_plane;  // values from one plane to the next
   int piece_tiles, splits;
   bool first;
 };

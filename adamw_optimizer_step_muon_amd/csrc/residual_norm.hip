@@ -504,24 +504,26 @@ __global__ __launch_bounds__(kThreads) void residual_dw_kernel(ResidualGradCall 
 // Sums the groups' shares, and makes the gradients of them: a block takes 64 columns, each wave
 // every kJoinWaves-th group, and joins the waves' sums in order.
 constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(64 * kJoinWaves) void residual_join_kernel(ResidualGradCall c, int64_t groups, int cols) {
-  __shared__ float shared[4][kJoinWaves][64];
+template <int kCols>
+__global__ __launch_bounds__(64 * kJoinWaves) void residual_join_kernel(ResidualGradCall c, int64_t groups) {
+  __shared__ float shared[kCols][kJoinWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (i < c.dim) {
+    const float* in = c.workspace + i;
+#pragma unroll 4
     for (int64_t g = wave; g < groups; g += kJoinWaves)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < cols) s[k] += c.workspace[(g * cols + k) * c.dim + i];
+      for (int k = 0; k < kCols; ++k) s[k] += in[(g * kCols + k) * c.dim];
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) shared[k][wave][lane] = s[k];
+  for (int k = 0; k < kCols; ++k) shared[k][wave][lane] = s[k];
   __syncthreads();
   if (wave != 0 || i >= c.dim) return;
   for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] += shared[k][w][lane];
+    for (int k = 0; k < kCols; ++k) s[k] += shared[k][w][lane];
   const float gate = c.g.scale * (c.g.gate ? c.g.gate[i] : 1.0f);
   if (c.dweight) c.dweight[i] = s[0];
   if (c.dbias) c.dbias[i] = s[2];
@@ -590,8 +592,11 @@ hipError_t launch_residual_backward(const ResidualGradCall& call, hipStream_t s)
         }
       }
     }
-    if (c.reduce)
-      hipLaunchKernelGGL(residual_join_kernel, dim3(static_cast<unsigned>((c.dim + 63) / 64)), dim3(64 * kJoinWaves), 0, s, c, groups, cols);
+    if (c.reduce) {
+      const dim3 grid(static_cast<unsigned>((c.dim + 63) / 64));
+      if (cols == 4) hipLaunchKernelGGL(residual_join_kernel<4>, grid, dim3(64 * kJoinWaves), 0, s, c, groups);
+      else hipLaunchKernelGGL(residual_join_kernel<2>, grid, dim3(64 * kJoinWaves), 0, s, c, groups);
+    }
     return hipGetLastError();
   });
 }
