@@ -36,9 +36,60 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // ---------------------------------------------------------------------------
 // Rows: which of them take part, and their copies
 // ---------------------------------------------------------------------------
+// Planes of operands that the 16-bit tiles read: one, or three for fp32 values in bf16.
+template <int T>
+struct Planes {
+  static constexpr int kCount = T == kActF32 ? 3 : 1;
+  // four values into the planes at out, out + stride, ..
+  static __device__ __forceinline__ void store(const float (&v)[4], unsigned short* out, int64_t stride) {
+    float rest[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      unsigned short x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = f2bf(rest[e]);
+        rest[e] -= bf2f(x[e]);
+      }
+      u32x2 w;
+      w[0] = x[0] | (static_cast<unsigned>(x[1]) << 16);
+      w[1] = x[2] | (static_cast<unsigned>(x[3]) << 16);
+      *reinterpret_cast<u32x2*>(out + k * stride) = w;
+    }
+  }
+};
+
+// A row of dim values from `in` (null: zeros) to a padded row at `out`, as it is or in planes.  A wave.
+template <int T, bool kPlanes>
+__device__ __forceinline__ void head_copy_row(const typename Act<T>::S* in, void* out, int64_t at, int64_t plane,
+                                              int64_t dim, int64_t dim_pad) {
+  typedef typename Act<T>::S S;
+  typedef typename Pack<S, 4>::type P;
+  for (int64_t i = (threadIdx.x & 63) * 4; i < dim_pad; i += 256) {
+    P x = 0;
+    if (in) {
+      if (i + 4 <= dim) {
+        x = *reinterpret_cast<const P*>(in + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < dim) x[e] = in[i + e];
+      }
+    }
+    if constexpr (kPlanes) {
+      const float v[4] = {x[0], x[1], x[2], x[3]};
+      Planes<T>::store(v, static_cast<unsigned short*>(out) + at + i, plane);
+    } else {
+      *reinterpret_cast<P*>(static_cast<S*>(out) + at + i) = x;
+    }
+  }
+}
+
 constexpr int kRowThreads = 1024;
 
-// One block: numbers the live rows, and finds the power of two for their weights.
+// One block: numbers the live rows, and finds the power of two for their weights.  kCopy: gathers
+// them too.
+template <int T, bool kCopy>
 __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
   __shared__ int counts[kRowThreads];
   __shared__ float tops[kRowThreads / 64];
@@ -98,53 +149,12 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     }
     ++at;
   }
-}
-
-// Planes of operands that the 16-bit tiles read: one, or three for fp32 values in bf16.
-template <int T>
-struct Planes {
-  static constexpr int kCount = T == kActF32 ? 3 : 1;
-  // four values into the planes at out, out + stride, ..
-  static __device__ __forceinline__ void store(const float (&v)[4], unsigned short* out, int64_t stride) {
-    float rest[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      unsigned short x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = f2bf(rest[e]);
-        rest[e] -= bf2f(x[e]);
-      }
-      u32x2 w;
-      w[0] = x[0] | (static_cast<unsigned>(x[1]) << 16);
-      w[1] = x[2] | (static_cast<unsigned>(x[3]) << 16);
-      *reinterpret_cast<u32x2*>(out + k * stride) = w;
-    }
-  }
-};
-
-// A row of dim values from `in` (null: zeros) to a padded row at `out`, as it is or in planes.  A wave.
-template <int T, bool kPlanes>
-__device__ __forceinline__ void head_copy_row(const typename Act<T>::S* in, void* out, int64_t at, int64_t plane,
-                                              int64_t dim, int64_t dim_pad) {
-  typedef typename Act<T>::S S;
-  typedef typename Pack<S, 4>::type P;
-  for (int64_t i = (threadIdx.x & 63) * 4; i < dim_pad; i += 256) {
-    P x = 0;
-    if (in) {
-      if (i + 4 <= dim) {
-        x = *reinterpret_cast<const P*>(in + i);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < dim) x[e] = in[i + e];
-      }
-    }
-    if constexpr (kPlanes) {
-      const float v[4] = {x[0], x[1], x[2], x[3]};
-      Planes<T>::store(v, static_cast<unsigned short*>(out) + at + i, plane);
-    } else {
-      *reinterpret_cast<P*>(static_cast<S*>(out) + at + i) = x;
+  if constexpr (kCopy) {
+    __syncthreads();
+    const int all = counts[kRowThreads - 1], padded = (all + c.row_tile - 1) / c.row_tile * c.row_tile;
+    for (int row = t >> 6; row < padded; row += kRowThreads / 64) {
+      const auto* in = row < all ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[row] * c.hidden_stride : nullptr;
+      head_copy_row<T, false>(in, c.hidden_pad, row * c.dim_pad, 0, c.dim, c.dim_pad);
     }
   }
 }
@@ -155,7 +165,7 @@ template <int T, bool kPlanes>
 __global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int live = c.head->live;
-  if (at >= (live + kHeadTile - 1) / kHeadTile * static_cast<int64_t>(kHeadTile)) return;
+  if (at >= (live + c.row_tile - 1) / c.row_tile * static_cast<int64_t>(c.row_tile)) return;
   const auto* in = at < live ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
   head_copy_row<T, kPlanes>(in, c.hidden_pad, at * c.dim_pad, c.hidden_plane, c.dim, c.dim_pad);
 }
@@ -224,6 +234,7 @@ __global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
     const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (at >= 0) {
+#pragma unroll 4
       for (int s = 0; s < c.splits; ++s) {
         const float* in = c.sum + (s * c.rows_pad + at) * c.sum_stride + i;
         const f32x4 x = *reinterpret_cast<const f32x4*>(in);
@@ -879,7 +890,14 @@ hipError_t launch_head_rows(const HeadCall& c, int64_t cols, hipStream_t s) {
 
 template <int T, bool kSplit>
 hipError_t gather(const HeadCall& c, hipStream_t s) {
-  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kRowThreads), 0, s, c);
+  if constexpr (!kSplit) {
+    // one launch for both where a block's copying takes no longer than a second launch, some 4 us
+    if (c.n <= 64 && c.row_tile * c.dim_pad <= 128 * 1024) {
+      hipLaunchKernelGGL((head_rows_kernel<T, true>), dim3(1), dim3(kRowThreads), 0, s, c);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((head_rows_kernel<T, false>), dim3(1), dim3(kRowThreads), 0, s, c);
   hipLaunchKernelGGL((head_gather_kernel<T, kSplit>), dim3(static_cast<unsigned>(c.rows_pad / 4)), dim3(256), 0, s, c);
   return hipGetLastError();
 }
@@ -986,15 +1004,16 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   p.splits = 1;
   p.sum_stride = align_up(dim, 4);
   if (gradients) {
-    // dh's tiles are few: the sum over the piece is split where that fills more of the chip's 256
-    // compute units (a block each), by 1024 vocabulary entries at least
-    const int64_t blocks = ceil_div(n, head_tile_rows(type, n)) * ceil_div(dim, tile);
+    // dh's tiles are few: the sum over the piece is split, by 1024 vocabulary entries at least, where
+    // the fuller chip (a block on each of 256 compute units, 4.7 TFLOP/s each) saves more than the
+    // sums' traffic (8 bytes each way a value, 4.8 TB/s) costs
+    const int64_t rows = head_tile_rows(type, n), blocks = ceil_div(n, rows) * ceil_div(dim, tile);
+    const double work = 2.0 * rows * tile * p.piece * (p.split ? 6 : type == kActF32 ? 16 : 1) / 4.7e12;
     double best = 0.0;
     for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 1024 <= p.piece); ++splits) {
-      const int64_t all = blocks * splits;
-      const double busy = static_cast<double>(all) / (256 * ceil_div(all, 256));
-      if (busy > best + 0.05) {
-        best = busy;
+      const double time = work * ceil_div(blocks * splits, 256) / splits + 8.0 * splits * n * dim / 4.8e12;
+      if (splits == 1 || time < best) {
+        best = time;
         p.splits = static_cast<int>(splits);
       }
     }
@@ -1031,6 +1050,7 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.sum_stride = p.sum_stride;
   c.piece = p.piece;
   c.splits = p.splits;
+  c.row_tile = static_cast<int>(head_tile_rows(c.type, c.n));
   c.weight_use = c.weight_in;
   c.weight_stride = c.weight_in_stride;
   c.dim_use = c.dim;

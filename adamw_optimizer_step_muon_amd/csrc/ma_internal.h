@@ -636,7 +636,7 @@ struct HeadCall {
   float* sum;       // splits x rows_pad x sum_stride
   int64_t rows_pad, dim_pad, dim_use, weight_stride, sum_stride, piece, tiles, piece_start;
   int64_t hidden_plane, weight_plane, g_plane;  // values from one plane to the next
-  int piece_tiles, splits;
+  int piece_tiles, splits, row_tile;  // row_tile: the gathered rows are padded to it
   bool first;
 };
 hipError_t launch_head_clear(const HeadCall& c, hipStream_t s);  // dweight = 0
