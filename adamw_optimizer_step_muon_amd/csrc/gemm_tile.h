@@ -96,9 +96,13 @@ __device__ __forceinline__ void dma16(const unsigned short* base, int voff, unsi
   if constexpr (kAsm) {
     const int lds = __builtin_amdgcn_readfirstlane(static_cast<int>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned short*)(l))));
-    // m0 (the LDS address) is an input operand: the compiler sets it and knows its value
+    // m0 (the LDS address) is an input operand: the compiler sets it and knows its value.  A scalar
+    // register that a vector instruction wrote needs five wait states before a buffer load reads
+    // it, and the compiler does not count them for an assembly statement: where it kept the base
+    // address in vector registers, v_readfirstlane came two before the load, which then now and
+    // then read another address.
     asm volatile(
-        "s_nop 0\n\t"
+        "s_nop 4\n\t"
         "buffer_load_dwordx4 %0, %1, 0 offen lds"
         :
         : "v"(voff), "s"(r), "{m0}"(lds)
