@@ -10,15 +10,17 @@
 // are computed again, its g is written to the workspace in the hidden type (n x piece values), and
 // two products take it to dh (a sum over pieces, fp32) and to the piece's rows of dW.
 // Arithmetic: 2 n vocab D FLOP forward, 6 n vocab D with the gradients; the logits' second product,
-// the price of not keeping them, makes it 8.
+// the price of not keeping them, makes it 8.  Both directions in one call keep the logits (fp32)
+// where those of all rows take no more than the piece's 512 MiB and the product costs more than
+// writing and reading them.
 //
 // Rows with a target (and, for gradients, a weight that is not zero) are gathered first into a
 // padded copy, so the others cost nothing and whatever they hold reaches no result, and tiles need
 // no checks along the rows.
 //
 // Rounding: products of 16-bit values are exact and summed in fp32.  g is rounded once to the
-// hidden type, as the matrix cores take it, after a scaling by a power of two that brings the
-// largest row weight near 2^14: fp16 then keeps probabilities down to 2^-38.  Every sum has a fixed
+// hidden type, as the matrix cores take it, after a scaling that makes the largest row weight 2^14:
+// fp16 then keeps probabilities down to 2^-38.  Every sum has a fixed
 // order: the same inputs give the same bits.
 // fp32 operands: up to kSplitRows rows on the fp32 matrix instructions; above as three bf16 planes
 // each (x = x0 + x1 + x2 to 2^-24 of itself: three times 8 bits), whose six products of 2^-16 and more
@@ -101,7 +103,8 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
   };
   const auto live = [&](int64_t r) {
     const int64_t l = label_of(r);
-    return l >= 0 && l < c.vocab && !(c.row_weight && c.row_weight[r] == 0.0f);
+    // (kept logits are numbered by the labels alone)
+    return l >= 0 && l < c.vocab && (c.kept || !(c.row_weight && c.row_weight[r] == 0.0f));
   };
   int mine = 0;
   float top = 0.0f;
@@ -121,13 +124,12 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     __syncthreads();
   }
   for (int w = 0; w < kRowThreads / 64; ++w) top = fmaxf(top, tops[w]);
-  // the largest weight times 2^shift lies in [2^13, 2^14); fp32 needs no scaling
-  int shift = 13 - (static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 127);
-  if (top == 0.0f || c.type == kActF32) shift = 0;
-  shift = shift > 126 ? 126 : shift;
+  // weights are scaled so that the largest becomes 2^14 (exactly: then g of an unlikely label, nearly
+  // the weight itself, hardly rounds); fp32 needs no scaling
+  const bool scaled = c.type != kActF32 && top != 0.0f;
   if (t == 0) {
     c.head->live = counts[kRowThreads - 1];
-    c.head->unscale = __builtin_ldexpf(1.0f, -shift);
+    c.head->unscale = scaled ? top * 0x1p-14f : 1.0f;
   }
   int at = counts[t] - mine;
   for (int64_t r = lo; r < hi; ++r) {
@@ -142,10 +144,10 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     c.label[at] = static_cast<int>(label_of(r));
     if (c.row_weight) {
       // exp(z - top) factor = weight exp(z - lse)
-      const float w = __builtin_ldexpf(c.row_weight[r], shift);
+      const float w = scaled ? c.row_weight[r] / top * 0x1p14f : c.row_weight[r];
       c.weight[at] = w;
       c.top[at] = c.lse_in ? c.lse_in[r] : c.tops[r];
-      c.factor[at] = c.lse_in ? w : w / c.sums[r];
+      c.factor[at] = c.lse_in || w == 0.0f ? w : w / c.sums[r];
     }
     ++at;
   }
@@ -153,7 +155,8 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     __syncthreads();
     const int all = counts[kRowThreads - 1], padded = (all + c.row_tile - 1) / c.row_tile * c.row_tile;
     for (int row = t >> 6; row < padded; row += kRowThreads / 64) {
-      const auto* in = row < all ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[row] * c.hidden_stride : nullptr;
+      const bool there = row < all && !(c.kept && c.row_weight && c.weight[row] == 0.0f);
+      const auto* in = there ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[row] * c.hidden_stride : nullptr;
       head_copy_row<T, false>(in, c.hidden_pad, row * c.dim_pad, 0, c.dim, c.dim_pad);
     }
   }
@@ -166,7 +169,9 @@ __global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int live = c.head->live;
   if (at >= (live + c.row_tile - 1) / c.row_tile * static_cast<int64_t>(c.row_tile)) return;
-  const auto* in = at < live ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
+  // (kept logits: a row of weight 0 takes part as zeros)
+  const bool there = at < live && !(c.kept && c.row_weight && c.weight[at] == 0.0f);
+  const auto* in = there ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
   head_copy_row<T, kPlanes>(in, c.hidden_pad, at * c.dim_pad, c.hidden_plane, c.dim, c.dim_pad);
 }
 
@@ -220,6 +225,58 @@ __global__ __launch_bounds__(256) void head_join_kernel(HeadCall c) {
   }
 }
 
+// g from kept logits, 8 values a thread; a block takes 2048 columns of a row.
+template <int T, bool kPlanes>
+__global__ __launch_bounds__(256) void head_convert_kernel(HeadCall c) {
+  const int64_t at = blockIdx.y, col = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  const int live = c.head->live;
+  if (at >= (live + c.row_tile - 1) / c.row_tile * static_cast<int64_t>(c.row_tile) || col >= c.piece) return;
+  const bool on = at < live;
+  const float top = on ? c.top[at] : 0.0f, factor = on ? c.factor[at] : 0.0f, weight = on ? c.weight[at] : 0.0f;
+  const int64_t label = on ? c.label[at] : -1;
+  const float* in = c.z + at * c.piece + col;
+  float g[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4 z = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(in + 4 * h));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t v = col + 4 * h + e;
+      const float p = __builtin_amdgcn_exp2f((z[e] - top) * kLog2e);
+      g[4 * h + e] = __builtin_fmaf(p, factor, v == label ? -weight : 0.0f);
+      if (v >= c.vocab || weight == 0.0f) g[4 * h + e] = 0.0f;
+    }
+  }
+  const int64_t out = at * c.piece + col;
+  if constexpr (T == kActF32 && !kPlanes) {
+    // in place
+    float* p = static_cast<float*>(c.g) + out;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4*>(p + 4 * h) = f32x4{g[4 * h], g[4 * h + 1], g[4 * h + 2], g[4 * h + 3]};
+  } else {
+#pragma unroll
+    for (int plane = 0; plane < (kPlanes ? 3 : 1); ++plane) {
+      u32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        unsigned short x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& v = g[2 * k + e];
+          if constexpr (kPlanes) {
+            x[e] = f2bf(v);
+            v -= bf2f(x[e]);
+          } else {
+            x[e] = Act<T>::down(v);
+          }
+        }
+        w[k] = x[0] | (static_cast<unsigned>(x[1]) << 16);
+      }
+      *reinterpret_cast<u32x4*>(static_cast<unsigned short*>(c.g) + plane * c.g_plane + out) = w;
+    }
+  }
+}
+
 // dh from the sums of the splits, a wave per row; rows without a gradient are zero.
 template <int T>
 __global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
@@ -245,6 +302,39 @@ __global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
       for (int e = 0; e < 4; ++e) v[e] *= unscale;
     }
     store_part<T, 4>(out + i, cnt, v);
+  }
+}
+
+// dW from the sums of the splits, a wave per vocabulary entry.
+template <int T>
+__global__ __launch_bounds__(256) void head_weight_out_kernel(HeadCall c) {
+  const int lane = threadIdx.x & 63;
+  const int64_t v = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (v >= c.vocab) return;
+  const float unscale = c.head->unscale;
+  for (int64_t i = lane * 4; i < c.dim; i += 256) {
+    const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < c.weight_splits; ++s) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(c.weight_sum + (s * c.weight_rows + v) * c.sum_stride + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += y[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= unscale;
+    const int64_t at = v * c.dweight_stride + i;
+    if (T == kActF32 || c.dweight_type == kActF32) {
+      float* p = static_cast<float*>(c.dweight) + at;
+      if (c.add) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < cnt) x[e] += p[e];
+      }
+      store_part<kActF32, 4>(p, cnt, x);
+    } else {
+      store_part<T, 4>(static_cast<typename Act<T>::S*>(c.dweight) + at, cnt, x);
+    }
   }
 }
 
@@ -300,6 +390,15 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (j * 32 + 4 * half + 8 * (k >> 2) + (k & 3) == label) c.target[m0 + row] = acc[i][j][k];
+      }
+      if (c.kept) {
+        float* z = c.z + static_cast<int64_t>(m0 + row) * c.piece + n0 + col0;
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(z + j * 32 + 8 * q) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       }
       float top = -INFINITY, sum = 0.0f, base;
       const auto gather = [&](auto mask) {  // mask: the vocabulary ends within this tile
@@ -435,6 +534,20 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
           if (!c.first) x += *p;
           *p = x;
         }
+  } else if (c.weight_splits > 1) {
+    // (one piece)
+    float* out = c.weight_sum + (split * c.weight_rows + m0) * c.sum_stride;
+#pragma unroll
+    for (int i = 0; i < WTM; ++i)
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int col = n0 + col0 + j * 32 + 8 * q;
+          if (col < c.sum_stride)
+            *reinterpret_cast<f32x4*>(out + static_cast<int64_t>(row0 + i * 32) * c.sum_stride + col) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
   } else {
     const float unscale = c.head->unscale;
 #pragma unroll
@@ -516,6 +629,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     } else {
       mt = c.piece_tiles;
       nt = dim_tiles;
+      splits = c.weight_splits;
     }
     if (!head_tile(kMode, mt, nt, splits, mi, ni, split)) return;
   }
@@ -535,7 +649,9 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use;
     steps = static_cast<int>(c.dim_pad / C::BK);
   } else if constexpr (kMode == kHidden) {
-    const int all = c.piece_tiles * (256 / C::BK), per = (all + c.splits - 1) / c.splits;
+    // stages that hold an entry of the vocabulary: none begins behind W's end
+    const int64_t entries = w_left < c.piece_tiles * 256 ? w_left : c.piece_tiles * 256;
+    const int all = static_cast<int>((entries + C::BK - 1) / C::BK), per = (all + c.splits - 1) / c.splits;
     k_from = split * per;
     steps = all - k_from < per ? all - k_from : per;
     steps = steps < 0 ? 0 : steps;
@@ -545,10 +661,13 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - static_cast<int64_t>(k_from) * C::BK - 1) * c.weight_stride + c.dim_use - n0;
   } else {
-    steps = (live + C::BK - 1) / C::BK;
-    gA = static_cast<const unsigned short*>(c.g) + m0;
+    const int all = (live + C::BK - 1) / C::BK, per = (all + c.weight_splits - 1) / c.weight_splits;
+    k_from = split * per;
+    steps = all - k_from < per ? all - k_from : per;
+    steps = steps < 0 ? 0 : steps;
+    gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(k_from) * C::BK * c.piece + m0;
     lda = static_cast<int>(c.piece);
-    gB = static_cast<const unsigned short*>(c.hidden_pad) + n0;
+    gB = static_cast<const unsigned short*>(c.hidden_pad) + static_cast<int64_t>(k_from) * C::BK * c.dim_pad + n0;
     ldb = static_cast<int>(c.dim_pad);
     left_b = static_cast<int64_t>(steps) * C::BK * c.dim_pad - n0;
   }
@@ -602,14 +721,14 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
       const int r0 = q * kRows, r = r0 + lane / kChunks, ch = lane % kChunks;
       const int64_t left = left_b - static_cast<int64_t>(step) * C::BK * ldb;
       const int64_t most = static_cast<int64_t>(C::BK - 1) * ldb + C::BN;
-      const int64_t values = left < 0 ? 0 : left < most ? left : most;
+      const int64_t values = left < most ? left : most;
       dma16<C::kBT>(base + static_cast<int64_t>(step) * C::BK * ldb, (r * ldb + swz_kn(r, ch) * 8) * 2,
                     static_cast<unsigned>(values * 2), s + r0 * C::BN);
     } else {
       const int r0 = q * 8, r = r0 + lane / 8, ch = swz<64>(r, lane % 8);
       const int64_t left = left_b - step * C::BK;
       const int64_t most = static_cast<int64_t>(C::BN - 1) * ldb + C::BK;
-      const int64_t values = left < 0 ? 0 : left < most ? left : most;
+      const int64_t values = left < most ? left : most;
       const int off = step * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
       dma16<C::kBT>(base + step * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
     }
@@ -854,16 +973,30 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
 // Host: whether fp32 runs on bf16 planes, and the tiles' columns.
 bool head_split(int type, int64_t n) { return type == kActF32 && n > kSplitRows; }
 int64_t head_tile_size(int type, bool split) { return type == kActF32 && !split ? 128 : 256; }
-// A tile's rows, in the products whose rows are the call's.
-int64_t head_tile_rows(int type, int64_t n) {
+// The rows that gathered ones are padded to a multiple of, and a tile's at most.
+int64_t head_row_tile(int type, int64_t n) {
   if (type == kActF32) return head_split(type, n) ? 256 : 128;
   return n <= 64 ? 64 : n <= 128 ? 128 : 256;
+}
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align_up(int64_t x, int64_t q) { return ceil_div(x, q) * q; }
+// Rounds of the chip (256 compute units, a block each) that a product's tiles take, in units of a
+// 256-row tile: smaller ones take 0.62 and 0.45 of it instead of a half and a quarter.
+double head_rounds(int64_t tiles, int64_t rows) {
+  return static_cast<double>(ceil_div(tiles, 256)) * (rows == 256 ? 1.0 : rows == 128 ? 0.62 : 0.45);
+}
+// A tile's rows, in a product of `cols` tiles beside each other.
+int64_t head_best_rows(int type, int64_t n, int64_t cols) {
+  const int64_t most = head_row_tile(type, n);
+  if (type == kActF32 && !head_split(type, n)) return most;
+  int64_t best = most;
+  for (int64_t rows = most / 2; rows >= 64; rows /= 2)
+    if (head_rounds(ceil_div(n, rows) * cols, rows) < head_rounds(ceil_div(n, best) * cols, best)) best = rows;
+  return best;
 }
 
 // Host: blocks of a launch over `tiles` tiles at most (see head_tile).
 dim3 head_grid(int64_t tiles) { return dim3(static_cast<unsigned>(8 * ((tiles + 7) / 8))); }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // kSplit: fp32 on bf16 planes.
 template <int T, bool kSplit, int BM, int kMode>
@@ -875,17 +1008,13 @@ hipError_t launch_head_gemm(const HeadCall& c, int64_t tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
+// A product whose rows are the call's, in tiles of `rows` and `cols` of them beside each other.
 template <int T, bool kSplit, int kMode>
-hipError_t launch_head_rows(const HeadCall& c, int64_t cols, hipStream_t s) {
-  if constexpr (T == kActF32 && !kSplit) {
-    return launch_head_gemm<T, kSplit, 128, kMode>(c, ceil_div(c.n, 128) * cols, s);
-  } else {
-    if constexpr (!kSplit) {  // (more rows are split than these tiles take)
-      if (c.n <= 64) return launch_head_gemm<T, kSplit, 64, kMode>(c, cols, s);
-      if (c.n <= 128) return launch_head_gemm<T, kSplit, 128, kMode>(c, cols, s);
-    }
-    return launch_head_gemm<T, kSplit, 256, kMode>(c, ceil_div(c.n, 256) * cols, s);
-  }
+hipError_t launch_head_rows(const HeadCall& c, int64_t rows, int64_t cols, hipStream_t s) {
+  const int64_t tiles = ceil_div(c.n, rows) * cols;
+  if (rows == 64) return launch_head_gemm<T, kSplit, 64, kMode>(c, tiles, s);
+  if (rows == 128) return launch_head_gemm<T, kSplit, 128, kMode>(c, tiles, s);
+  return launch_head_gemm<T, kSplit, 256, kMode>(c, tiles, s);
 }
 
 template <int T, bool kSplit>
@@ -911,7 +1040,7 @@ hipError_t forward(const HeadCall& call, hipStream_t s) {
   c.piece_tiles = static_cast<int>(ceil_div(c.vocab, head_tile_size(T, kSplit)));
   c.tiles = c.piece_tiles;
   if (const hipError_t e = gather<T, kSplit>(c, s)) return e;
-  if (const hipError_t e = launch_head_rows<T, kSplit, kStats>(c, c.piece_tiles, s)) return e;
+  if (const hipError_t e = launch_head_rows<T, kSplit, kStats>(c, c.stats_rows, c.piece_tiles, s)) return e;
   hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
   return hipGetLastError();
 }
@@ -928,11 +1057,21 @@ hipError_t backward(const HeadCall& call, hipStream_t s) {
     c.first = v == 0;
     const int64_t here = c.vocab - v < c.piece ? c.vocab - v : c.piece;
     c.piece_tiles = static_cast<int>(ceil_div(here, tile));
-    if (const hipError_t e = launch_head_rows<T, kSplit, kGrad>(c, c.piece_tiles, s)) return e;
+    if (c.kept) {
+      const dim3 grid(static_cast<unsigned>(ceil_div(c.piece, 2048)), static_cast<unsigned>(align_up(c.n, c.row_tile)));
+      hipLaunchKernelGGL((head_convert_kernel<T, kSplit>), grid, dim3(256), 0, s, c);
+      if (const hipError_t e = hipGetLastError()) return e;
+    } else if (const hipError_t e = launch_head_rows<T, kSplit, kGrad>(c, c.grad_rows, c.piece_tiles, s)) {
+      return e;
+    }
     if (c.dhidden)
-      if (const hipError_t e = launch_head_rows<T, kSplit, kHidden>(c, dim_tiles * c.splits, s)) return e;
+      if (const hipError_t e = launch_head_rows<T, kSplit, kHidden>(c, c.hidden_rows, dim_tiles * c.splits, s)) return e;
     if (c.dweight)
-      if (const hipError_t e = launch_head_gemm<T, kSplit, 256, kWeight>(c, c.piece_tiles * dim_tiles, s)) return e;
+      if (const hipError_t e = launch_head_gemm<T, kSplit, 256, kWeight>(c, c.piece_tiles * dim_tiles * c.weight_splits, s)) return e;
+  }
+  if (c.dweight && c.weight_splits > 1) {
+    hipLaunchKernelGGL((head_weight_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
+    if (const hipError_t e = hipGetLastError()) return e;
   }
   if (c.dhidden)
     hipLaunchKernelGGL((head_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
@@ -950,8 +1089,6 @@ hipError_t run_work(const HeadCall& c, HeadWork work, hipStream_t s) {
   return work != kHeadForward ? backward<T, kSplit>(c, s) : hipSuccess;
 }
 
-int64_t align_up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
-
 }  // namespace
 
 bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride) {
@@ -960,10 +1097,10 @@ bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t strid
 }
 
 int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p) {
-  const int64_t tile = head_tile_size(type, p.split);
-  const int64_t row_tiles = ceil_div(n, head_tile_rows(type, n)), dim_tiles = ceil_div(dim, tile);
-  int64_t tiles = row_tiles * ceil_div(vocab, tile);
-  const int64_t others[] = {row_tiles * dim_tiles * p.splits, p.piece / tile * dim_tiles};
+  const int64_t tile = head_tile_size(type, p.split), dim_tiles = ceil_div(dim, tile);
+  int64_t tiles = ceil_div(n, p.stats_rows) * ceil_div(vocab, tile);
+  const int64_t others[] = {ceil_div(n, p.hidden_rows) * dim_tiles * p.splits, ceil_div(n, p.grad_rows) * (p.piece / tile),
+                            p.piece / tile * dim_tiles * p.weight_splits};
   for (const int64_t t : others) tiles = t > tiles ? t : tiles;
   return (tiles + 8) * 512;
 }
@@ -999,25 +1136,51 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   int64_t piece = kHeadPieceBytes / (p.rows_pad * size) / tile;
   piece = piece < 1 ? 1 : piece;
   p.piece = ceil_div(tiles, ceil_div(tiles, piece)) * tile;
+  // kept logits: one product of the logits against 8 bytes of traffic each (1.2 PFLOP/s, 6 or 16
+  // times less in fp32, and 4.8 TB/s); in fp32 g takes their place
+  const int64_t logits = p.rows_pad * p.piece * 4, cost = dim * (p.split ? 6 : type == kActF32 ? 16 : 1);
+  p.kept = gradients && p.piece >= vocab && logits <= kHeadPieceBytes && cost >= 1024 && p.rows_pad <= 65535;
   const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.piece * size : 0;
   p.partial = take(stats > g ? stats : g);
-  p.splits = 1;
+  p.logits = p.kept ? take(logits) : 0;
   p.sum_stride = align_up(dim, 4);
+  p.stats_rows = head_best_rows(type, n, tiles);
+  p.grad_rows = head_best_rows(type, n, p.piece / tile);
+  p.hidden_rows = head_row_tile(type, n);
+  p.splits = p.weight_splits = 1;
   if (gradients) {
-    // dh's tiles are few: the sum over the piece is split, by 1024 vocabulary entries at least, where
-    // the fuller chip (a block on each of 256 compute units, 4.7 TFLOP/s each) saves more than the
-    // sums' traffic (8 bytes each way a value, 4.8 TB/s) costs
-    const int64_t rows = head_tile_rows(type, n), blocks = ceil_div(n, rows) * ceil_div(dim, tile);
-    const double work = 2.0 * rows * tile * p.piece * (p.split ? 6 : type == kActF32 ? 16 : 1) / 4.7e12;
+    // Both gradients may have few tiles: the sums over the piece, and over the rows where there is
+    // one piece, are split (by 1024 vocabulary entries and 256 rows at least) where the fuller chip
+    // (4.7 TFLOP/s on each of 256 compute units) saves more than the sums' traffic (8 bytes each way a
+    // value, 4.8 TB/s) and a launch, 4 us, cost.
+    const int64_t dim_tiles = ceil_div(dim, tile), products = p.split ? 6 : type == kActF32 ? 16 : 1;
+    const double unit = 2.0 * 256 * tile * products / 4.7e12;  // seconds of a 256-row tile per summed index
     double best = 0.0;
-    for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 1024 <= p.piece); ++splits) {
-      const double time = work * ceil_div(blocks * splits, 256) / splits + 8.0 * splits * n * dim / 4.8e12;
-      if (splits == 1 || time < best) {
-        best = time;
-        p.splits = static_cast<int>(splits);
+    for (int64_t rows = head_row_tile(type, n); rows >= 64; rows /= 2) {
+      if (rows < p.hidden_rows && type == kActF32 && !p.split) break;
+      const int64_t blocks = ceil_div(n, rows) * dim_tiles;
+      for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 1024 <= p.piece); ++splits) {
+        const double time = unit * p.piece * head_rounds(blocks * splits, rows) / splits + 8.0 * splits * n * dim / 4.8e12;
+        if (best == 0.0 || time < best) {
+          best = time;
+          p.hidden_rows = rows;
+          p.splits = static_cast<int>(splits);
+        }
       }
     }
     p.sum = take(p.splits * p.rows_pad * p.sum_stride * 4);
+    if (p.piece >= vocab && (type != kActF32 || p.split)) {
+      const int64_t blocks = ceil_div(vocab, tile) * dim_tiles;
+      best = unit * n * head_rounds(blocks, 256);
+      for (int64_t splits = 2; splits <= 64 && splits * 256 <= n; ++splits) {
+        const double time = unit * n * head_rounds(blocks * splits, 256) / splits + 8.0 * splits * vocab * dim / 4.8e12 + 4e-6;
+        if (time < best) {
+          best = time;
+          p.weight_splits = static_cast<int>(splits);
+        }
+      }
+      if (p.weight_splits > 1) p.weight_sum = take(p.weight_splits * p.piece * p.sum_stride * 4);
+    }
   }
   p.bytes = at;
   return p;
@@ -1043,14 +1206,22 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.sums = work == kHeadBoth ? reinterpret_cast<float*>(ws + p.sums) : nullptr;
   c.hidden_pad = ws + p.hidden;
   c.partial = reinterpret_cast<float2*>(ws + p.partial);
-  c.g = ws + p.partial;
+  c.kept = p.kept && work == kHeadBoth;
+  c.z = reinterpret_cast<float*>(ws + p.logits);
+  c.g = c.kept && c.type == kActF32 && !p.split ? ws + p.logits : ws + p.partial;
   c.sum = reinterpret_cast<float*>(ws + p.sum);
   c.rows_pad = p.rows_pad;
   c.dim_pad = p.dim_pad;
   c.sum_stride = p.sum_stride;
   c.piece = p.piece;
   c.splits = p.splits;
-  c.row_tile = static_cast<int>(head_tile_rows(c.type, c.n));
+  c.row_tile = static_cast<int>(head_row_tile(c.type, c.n));
+  c.stats_rows = p.stats_rows;
+  c.grad_rows = p.grad_rows;
+  c.hidden_rows = p.hidden_rows;
+  c.weight_splits = p.weight_splits;
+  c.weight_sum = reinterpret_cast<float*>(ws + p.weight_sum);
+  c.weight_rows = p.piece;
   c.weight_use = c.weight_in;
   c.weight_stride = c.weight_in_stride;
   c.dim_use = c.dim;

@@ -602,9 +602,11 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
  *
  * Host only: workspace bytes of the calls (gradients = 1 for _backward and _grad).  Of `weight`
  * only the alignment counts: rows that do not start at multiples of 16 bytes (or of a dim that is no
- * multiple of 8) are copied there.  Otherwise some 2 dim bytes a row, and at most 512 MiB of logits'
- * gradients (up to 2^20 rows) with 4 dim bytes a row and split for the gradients.  0 for invalid
- * sizes, which the calls then report. */
+ * multiple of 8) are copied there, and in fp32 with more than 128 rows all of it, in 6 bytes a value.
+ * Otherwise some 2 dim bytes a row (6 in fp32), and for the gradients at most 512 MiB of the logits'
+ * (up to 2^20 rows), as much for logits that are few enough to be kept from one direction to the
+ * other, and 4 dim bytes a row once or several times.  0 for invalid sizes, which the calls then
+ * report. */
 size_t ma_head_loss_workspace_bytes(int32_t type, int64_t n, int64_t dim, int64_t vocab, const void* weight,
                                     int64_t weight_stride, int32_t gradients);
 
