@@ -89,51 +89,48 @@ __device__ __forceinline__ void head_copy_row(const typename Act<T>::S* in, void
 
 constexpr int kRowThreads = 1024;
 
-// One block: numbers the live rows, and finds the power of two for their weights.  kCopy: gathers
-// them too.
+// One block: numbers the live rows, and finds the scaling of their weights.  kCopy: gathers them too.
 template <int T, bool kCopy>
 __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
-  __shared__ int counts[kRowThreads];
-  __shared__ float tops[kRowThreads / 64];
-  const int t = threadIdx.x;
-  const int64_t per = (c.n + kRowThreads - 1) / kRowThreads;
-  const int64_t lo = t * per < c.n ? t * per : c.n, hi = lo + per < c.n ? lo + per : c.n;
+  constexpr int kWaves = kRowThreads / 64;
+  __shared__ int counts[2][kWaves];
+  __shared__ float tops[kWaves];
+  __shared__ int copied[kCopy ? 64 : 1];
+  const int t = threadIdx.x, wave = t >> 6;
   const auto label_of = [&](int64_t r) -> int64_t {
     return c.label_bits == 64 ? static_cast<const int64_t*>(c.labels)[r] : static_cast<const int32_t*>(c.labels)[r];
   };
-  const auto live = [&](int64_t r) {
-    const int64_t l = label_of(r);
-    // (kept logits are numbered by the labels alone)
-    return l >= 0 && l < c.vocab && (c.kept || !(c.row_weight && c.row_weight[r] == 0.0f));
-  };
-  int mine = 0;
+  const auto in_vocab = [&](int64_t l) { return l >= 0 && l < c.vocab; };
+  // the largest weight of a row with a target
   float top = 0.0f;
-  for (int64_t r = lo; r < hi; ++r) {
-    if (!live(r)) continue;
-    ++mine;
-    if (c.row_weight) top = fmaxf(top, fabsf(c.row_weight[r]));
-  }
-  counts[t] = mine;
-  top = wave_max(top);
-  if ((t & 63) == 0) tops[t >> 6] = top;
-  __syncthreads();
-  for (int d = 1; d < kRowThreads; d <<= 1) {
-    const int before = t >= d ? counts[t - d] : 0;
+  if (c.row_weight) {
+#pragma unroll 4
+    for (int64_t r = t; r < c.n; r += kRowThreads)
+      if (in_vocab(label_of(r))) top = fmaxf(top, fabsf(c.row_weight[r]));
+    top = wave_max(top);
+    if ((t & 63) == 0) tops[wave] = top;
     __syncthreads();
-    counts[t] += before;
-    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w]);
   }
-  for (int w = 0; w < kRowThreads / 64; ++w) top = fmaxf(top, tops[w]);
   // weights are scaled so that the largest becomes 2^14 (exactly: then g of an unlikely label, nearly
   // the weight itself, hardly rounds); fp32 needs no scaling
-  const bool scaled = c.type != kActF32 && top != 0.0f;
-  if (t == 0) {
-    c.head->live = counts[kRowThreads - 1];
-    c.head->unscale = scaled ? top * 0x1p-14f : 1.0f;
-  }
-  int at = counts[t] - mine;
-  for (int64_t r = lo; r < hi; ++r) {
-    if (!live(r)) {
+  const bool scaled = T != kActF32 && top != 0.0f;
+  int base = 0, turn = 0;
+  for (int64_t first = 0; first < c.n; first += kRowThreads, turn ^= 1) {
+    const int64_t r = first + t, label = r < c.n ? label_of(r) : -1;
+    const float given = c.row_weight && r < c.n ? c.row_weight[r] : 1.0f;
+    // (kept logits are numbered by the labels alone)
+    const bool live = in_vocab(label) && (c.kept || given != 0.0f);
+    const unsigned long long mask = __ballot(live);
+    if ((t & 63) == 0) counts[turn][wave] = __popcll(mask);
+    __syncthreads();
+    int at = base + __popcll(mask & ((1ull << (t & 63)) - 1));
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) at += counts[turn][w];
+      base += counts[turn][w];
+    }
+    if (r >= c.n) continue;
+    if (!live) {
       c.place[r] = -1;
       if (c.lse_out) c.lse_out[r] = 0.0f;
       if (c.loss) c.loss[r] = 0.0f;
@@ -141,23 +138,42 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     }
     c.place[r] = at;
     c.row_of[at] = static_cast<int>(r);
-    c.label[at] = static_cast<int>(label_of(r));
+    c.label[at] = static_cast<int>(label);
+    float w = given;
     if (c.row_weight) {
       // exp(z - top) factor = weight exp(z - lse)
-      const float w = scaled ? c.row_weight[r] / top * 0x1p14f : c.row_weight[r];
+      if (scaled) w = given / top * 0x1p14f;
       c.weight[at] = w;
       c.top[at] = c.lse_in ? c.lse_in[r] : c.tops[r];
       c.factor[at] = c.lse_in || w == 0.0f ? w : w / c.sums[r];
     }
-    ++at;
+    // (kept logits: a row of weight 0 takes part as zeros)
+    if constexpr (kCopy) copied[at] = w == 0.0f ? -1 : static_cast<int>(r);
+  }
+  if (t == 0) {
+    c.head->live = base;
+    c.head->unscale = scaled ? top * 0x1p-14f : 1.0f;
   }
   if constexpr (kCopy) {
+    typedef typename Act<T>::S S;
+    typedef typename Pack<S, 4>::type P;
     __syncthreads();
-    const int all = counts[kRowThreads - 1], padded = (all + c.row_tile - 1) / c.row_tile * c.row_tile;
-    for (int row = t >> 6; row < padded; row += kRowThreads / 64) {
-      const bool there = row < all && !(c.kept && c.row_weight && c.weight[row] == 0.0f);
-      const auto* in = there ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[row] * c.hidden_stride : nullptr;
-      head_copy_row<T, false>(in, c.hidden_pad, row * c.dim_pad, 0, c.dim, c.dim_pad);
+    const int padded = (base + c.row_tile - 1) / c.row_tile * c.row_tile, each = static_cast<int>(c.dim_pad / 4);
+#pragma unroll 4
+    for (int x = t; x < padded * each; x += kRowThreads) {
+      const int row = x / each, i = (x - row * each) * 4, from = row < base ? copied[row] : -1;
+      P v = 0;
+      if (from >= 0) {
+        const S* in = static_cast<const S*>(c.hidden) + from * c.hidden_stride + i;
+        if (i + 4 <= c.dim) {
+          v = *reinterpret_cast<const P*>(in);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < c.dim) v[e] = in[e];
+        }
+      }
+      *reinterpret_cast<P*>(static_cast<S*>(c.hidden_pad) + row * c.dim_pad + i) = v;
     }
   }
 }
@@ -277,7 +293,7 @@ __global__ __launch_bounds__(256) void head_convert_kernel(HeadCall c) {
   }
 }
 
-// dh from the sums of the splits, a wave per row; rows without a gradient are zero.
+// dh from the sums of the splits, a wave per 256 columns of a row; rows without a gradient are zero.
 template <int T>
 __global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
   typedef typename Act<T>::S S;
@@ -287,54 +303,52 @@ __global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
   S* out = static_cast<S*>(c.dhidden) + r * c.dhidden_stride;
   const int at = c.place[r];
   const float unscale = c.head->unscale;
-  for (int64_t i = lane * 4; i < c.dim; i += 256) {
-    const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (at >= 0) {
-#pragma unroll 4
-      for (int s = 0; s < c.splits; ++s) {
-        const float* in = c.sum + (s * c.rows_pad + at) * c.sum_stride + i;
-        const f32x4 x = *reinterpret_cast<const f32x4*>(in);
+  const int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + lane * 4;
+  if (i >= c.dim) return;
+  const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (at >= 0) {
+#pragma unroll 8
+    for (int s = 0; s < c.splits; ++s) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(c.sum + (s * c.rows_pad + at) * c.sum_stride + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += x[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= unscale;
+      for (int e = 0; e < 4; ++e) v[e] += x[e];
     }
-    store_part<T, 4>(out + i, cnt, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= unscale;
   }
+  store_part<T, 4>(out + i, cnt, v);
 }
 
-// dW from the sums of the splits, a wave per vocabulary entry.
+// The piece's rows of dW from the sums of the splits, a wave per 256 columns of a row.
 template <int T>
 __global__ __launch_bounds__(256) void head_weight_out_kernel(HeadCall c) {
   const int lane = threadIdx.x & 63;
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (v >= c.vocab) return;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), v = c.piece_start + row;
+  const int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + lane * 4;
+  if (row >= c.piece || v >= c.vocab || i >= c.dim) return;
   const float unscale = c.head->unscale;
-  for (int64_t i = lane * 4; i < c.dim; i += 256) {
-    const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
-    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int s = 0; s < c.weight_splits; ++s) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(c.weight_sum + (s * c.weight_rows + v) * c.sum_stride + i);
+  const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
+  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int s = 0; s < c.weight_splits; ++s) {
+    const f32x4 y = *reinterpret_cast<const f32x4*>(c.weight_sum + (s * c.piece + row) * c.sum_stride + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] += y[e];
+    for (int e = 0; e < 4; ++e) x[e] += y[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] *= unscale;
+  const int64_t at = v * c.dweight_stride + i;
+  if (T == kActF32 || c.dweight_type == kActF32) {
+    float* p = static_cast<float*>(c.dweight) + at;
+    if (c.add) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < cnt) x[e] += p[e];
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] *= unscale;
-    const int64_t at = v * c.dweight_stride + i;
-    if (T == kActF32 || c.dweight_type == kActF32) {
-      float* p = static_cast<float*>(c.dweight) + at;
-      if (c.add) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < cnt) x[e] += p[e];
-      }
-      store_part<kActF32, 4>(p, cnt, x);
-    } else {
-      store_part<T, 4>(static_cast<typename Act<T>::S*>(c.dweight) + at, cnt, x);
-    }
+    store_part<kActF32, 4>(p, cnt, x);
+  } else {
+    store_part<T, 4>(static_cast<typename Act<T>::S*>(c.dweight) + at, cnt, x);
   }
 }
 
@@ -535,8 +549,7 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
           *p = x;
         }
   } else if (c.weight_splits > 1) {
-    // (one piece)
-    float* out = c.weight_sum + (split * c.weight_rows + m0) * c.sum_stride;
+    float* out = c.weight_sum + (split * c.piece + m0) * c.sum_stride;
 #pragma unroll
     for (int i = 0; i < WTM; ++i)
 #pragma unroll
@@ -548,6 +561,35 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
             *reinterpret_cast<f32x4*>(out + static_cast<int64_t>(row0 + i * 32) * c.sum_stride + col) =
                 f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         }
+  } else if (T != kActF32 && c.weight_lines) {
+    // rows of dW that start at multiples of 16 bytes leave in whole lines, as g does
+    if constexpr (T != kActF32) {
+      const float unscale = c.head->unscale;
+      char* stage = smem + wave * (32 * 128);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WTM; ++i) {
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            u32x2 w;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              w[e] = Act<T>::down(acc[i][j][4 * q + 2 * e] * unscale) |
+                     (static_cast<unsigned>(Act<T>::down(acc[i][j][4 * q + 2 * e + 1] * unscale)) << 16);
+            *reinterpret_cast<u32x2*>(stage + frow * 128 + (((j * 4 + q) ^ (frow & 7)) << 4) + half * 8) = w;
+          }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int r = it * 8 + (lane >> 3), ch = lane & 7, col = n0 + wn * 64 + ch * 8;
+          const int64_t v = c.piece_start + m0 + wm * (WTM * 32) + i * 32 + r;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+          if (v < c.vocab && col < c.dim)
+            *reinterpret_cast<u32x4*>(static_cast<S*>(c.dweight) + v * c.dweight_stride + col) = x;
+        }
+      }
+    }
   } else {
     const float unscale = c.head->unscale;
 #pragma unroll
@@ -832,18 +874,21 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   head_epilogue<T, T == kActF32, kMode, BM, C::BN, C::WM, C::WN>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(smem));
 }
 
-// fp32 operands: 128 x 128 tiles of 4 waves (2 x 2), v_mfma_f32_32x32x2, stages of 16 of the summed
-// index that pass through registers into LDS rows of one index each, whatever the operand's order.
-template <int kMode>
+// fp32 operands: BM x 128 tiles of 4 waves, v_mfma_f32_32x32x2, stages of the summed index that pass
+// through registers into LDS rows of one index each, whatever the operand's order.  Few rows are
+// bound by memory and its latency: 32- and 64-row tiles, with longer stages.
+template <int BM, int kMode>
 __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
-  constexpr int B = 128, BK = 16, LD = B + 4;
-  __shared__ __attribute__((aligned(16))) float smem[2][2][BK * LD];
+  constexpr int B = 128, BK = BM == 128 ? 16 : 32, LA = BM + 4, LB = B + 4;
+  constexpr int WM = BM == 32 ? 1 : 2, WN = 4 / WM, WTM = BM / (WM * 32), WTN = B / (WN * 32);
+  constexpr int kA = BM * BK / 1024, kB = B * BK / 1024;  // vectors of 4 values a thread and stage
+  __shared__ __attribute__((aligned(16))) float smem[2][BK * (LA + LB)];
   constexpr bool kAT = kMode == kWeight, kBT = kMode == kHidden || kMode == kWeight;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const int live = c.head->live;
   if (live == 0 && kMode != kWeight) return;
-  const int row_tiles = (live + B - 1) / B, dim_tiles = static_cast<int>((c.dim + B - 1) / B);
+  const int row_tiles = (live + BM - 1) / BM, dim_tiles = static_cast<int>((c.dim + B - 1) / B);
   int mi, ni, split;
   {
     int mt, nt, splits = 1;
@@ -860,7 +905,7 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     }
     if (!head_tile(kMode, mt, nt, splits, mi, ni, split)) return;
   }
-  const int m0 = mi * B, n0 = ni * B;
+  const int m0 = mi * BM, n0 = ni * B;
   const float* W = static_cast<const float*>(c.weight_use) + c.piece_start * c.weight_stride;
   const int64_t w_left = c.vocab - c.piece_start;
   // operand (row, k): contiguous along k, or along the rows (T); rows and ks below their counts
@@ -876,7 +921,9 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     k1 = static_cast<int>(c.dim_pad);
     ks_b = static_cast<int>(c.dim);
   } else if constexpr (kMode == kHidden) {
-    const int all = c.piece_tiles * (B / BK), per = (all + c.splits - 1) / c.splits;
+    // (zeros behind W's end)
+    const int64_t entries = w_left < c.piece_tiles * B ? w_left : c.piece_tiles * B;
+    const int all = static_cast<int>((entries + BK - 1) / BK), per = (all + c.splits - 1) / c.splits;
     k0 = split * per * BK;
     k1 = min(all, (split + 1) * per) * BK;
     gA = static_cast<const float*>(c.g) + static_cast<int64_t>(m0) * c.piece;
@@ -894,16 +941,20 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     rows_b = c.dim_pad - n0;
     ks_b = k1;
   }
-  // a thread's two vectors of 4 values of an operand's stage: A is padded to whole tiles, B checked
+  // a thread's vectors of an operand's stage: A is padded to whole tiles, B checked
   typedef Pack<float, 4>::type P;
-  f32x4 ra[2], rb[2];
+  f32x4 ra[kA], rb[kB];
   const auto load = [&](int k) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kA; ++u) {
       const int x = tid + u * 256;
-      if constexpr (kAT) ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(k + x / 32) * lda + x % 32 * 4);
-      else ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(x / 4) * lda + k + x % 4 * 4);
-      const int row = kBT ? x % 32 * 4 : x / 4, kk = k + (kBT ? x / 32 : x % 4 * 4);
+      if constexpr (kAT) ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(k + x / (BM / 4)) * lda + x % (BM / 4) * 4);
+      else ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(x / (BK / 4)) * lda + k + x % (BK / 4) * 4);
+    }
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      const int x = tid + u * 256;
+      const int row = kBT ? x % (B / 4) * 4 : x / (BK / 4), kk = k + (kBT ? x / (B / 4) : x % (BK / 4) * 4);
       const float* p = gB + (kBT ? static_cast<int64_t>(kk) * ldb + row : static_cast<int64_t>(row) * ldb + kk);
       // the values that are there: along the rows, or along k
       const int64_t there = kBT ? (kk < ks_b ? rows_b - row : 0) : (row < rows_b ? ks_b - kk : 0);
@@ -920,29 +971,33 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     }
   };
   const auto store = [&](int buf) {
+    float *a = smem[buf], *b = smem[buf] + BK * LA;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kA; ++u) {
       const int x = tid + u * 256;
-      float *a = smem[buf][0], *b = smem[buf][1];
       if constexpr (kAT) {
-        *reinterpret_cast<f32x4*>(a + x / 32 * LD + x % 32 * 4) = ra[u];
+        *reinterpret_cast<f32x4*>(a + x / (BM / 4) * LA + x % (BM / 4) * 4) = ra[u];
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[(x % 4 * 4 + e) * LD + x / 4] = ra[u][e];
+        for (int e = 0; e < 4; ++e) a[(x % (BK / 4) * 4 + e) * LA + x / (BK / 4)] = ra[u][e];
       }
+    }
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      const int x = tid + u * 256;
       if constexpr (kBT) {
-        *reinterpret_cast<f32x4*>(b + x / 32 * LD + x % 32 * 4) = rb[u];
+        *reinterpret_cast<f32x4*>(b + x / (B / 4) * LB + x % (B / 4) * 4) = rb[u];
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[(x % 4 * 4 + e) * LD + x / 4] = rb[u][e];
+        for (int e = 0; e < 4; ++e) b[(x % (BK / 4) * 4 + e) * LB + x / (BK / 4)] = rb[u][e];
       }
     }
   };
-  f32x16 acc[2][2];
+  f32x16 acc[WTM][WTN];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < WTM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < WTN; ++j)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
   if (k0 < k1) {
@@ -953,21 +1008,25 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     for (int k = k0; k < k1; k += BK, buf ^= 1) {
       const bool more = k + BK < k1;
       if (more) load(k + BK);
-      const float *a = smem[buf][0] + (lane >> 5) * LD + wm * 64 + (lane & 31);
-      const float *b = smem[buf][1] + (lane >> 5) * LD + wn * 64 + (lane & 31);
+      const float* a = smem[buf] + (lane >> 5) * LA + wm * (WTM * 32) + (lane & 31);
+      const float* b = smem[buf] + BK * LA + (lane >> 5) * LB + wn * (WTN * 32) + (lane & 31);
 #pragma unroll
       for (int kk = 0; kk < BK; kk += 2) {
-        const float a0 = a[kk * LD], a1 = a[kk * LD + 32], b0 = b[kk * LD], b1 = b[kk * LD + 32];
-        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a0, acc[0][0], 0, 0, 0);
-        acc[0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a0, acc[0][1], 0, 0, 0);
-        acc[1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a1, acc[1][0], 0, 0, 0);
-        acc[1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a1, acc[1][1], 0, 0, 0);
+        float fa[WTM], fb[WTN];
+#pragma unroll
+        for (int i = 0; i < WTM; ++i) fa[i] = a[kk * LA + i * 32];
+#pragma unroll
+        for (int j = 0; j < WTN; ++j) fb[j] = b[kk * LB + j * 32];
+#pragma unroll
+        for (int i = 0; i < WTM; ++i)
+#pragma unroll
+          for (int j = 0; j < WTN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
       }
       if (more) store(buf ^ 1);
       __syncthreads();
     }
   }
-  head_epilogue<kActF32, false, kMode, B, B, 2, 2>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(&smem[0][0][0]));
+  head_epilogue<kActF32, false, kMode, BM, B, WM, WN>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(&smem[0][0]));
 }
 
 // Host: whether fp32 runs on bf16 planes, and the tiles' columns.
@@ -975,7 +1034,7 @@ bool head_split(int type, int64_t n) { return type == kActF32 && n > kSplitRows;
 int64_t head_tile_size(int type, bool split) { return type == kActF32 && !split ? 128 : 256; }
 // The rows that gathered ones are padded to a multiple of, and a tile's at most.
 int64_t head_row_tile(int type, int64_t n) {
-  if (type == kActF32) return head_split(type, n) ? 256 : 128;
+  if (type == kActF32) return head_split(type, n) ? 256 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
   return n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1002,7 +1061,7 @@ dim3 head_grid(int64_t tiles) { return dim3(static_cast<unsigned>(8 * ((tiles + 
 template <int T, bool kSplit, int BM, int kMode>
 hipError_t launch_head_gemm(const HeadCall& c, int64_t tiles, hipStream_t s) {
   if constexpr (T == kActF32 && !kSplit)
-    hipLaunchKernelGGL((head_gemm32_kernel<kMode>), head_grid(tiles), dim3(256), 0, s, c);
+    hipLaunchKernelGGL((head_gemm32_kernel<BM, kMode>), head_grid(tiles), dim3(256), 0, s, c);
   else
     hipLaunchKernelGGL((head_gemm_kernel<T, BM, kMode>), head_grid(tiles), dim3(512), 0, s, c);
   return hipGetLastError();
@@ -1012,16 +1071,22 @@ hipError_t launch_head_gemm(const HeadCall& c, int64_t tiles, hipStream_t s) {
 template <int T, bool kSplit, int kMode>
 hipError_t launch_head_rows(const HeadCall& c, int64_t rows, int64_t cols, hipStream_t s) {
   const int64_t tiles = ceil_div(c.n, rows) * cols;
-  if (rows == 64) return launch_head_gemm<T, kSplit, 64, kMode>(c, tiles, s);
-  if (rows == 128) return launch_head_gemm<T, kSplit, 128, kMode>(c, tiles, s);
-  return launch_head_gemm<T, kSplit, 256, kMode>(c, tiles, s);
+  if constexpr (T == kActF32 && !kSplit) {
+    if (rows == 32) return launch_head_gemm<T, kSplit, 32, kMode>(c, tiles, s);
+    if (rows == 64) return launch_head_gemm<T, kSplit, 64, kMode>(c, tiles, s);
+    return launch_head_gemm<T, kSplit, 128, kMode>(c, tiles, s);
+  } else {
+    if (rows == 64) return launch_head_gemm<T, kSplit, 64, kMode>(c, tiles, s);
+    if (rows == 128) return launch_head_gemm<T, kSplit, 128, kMode>(c, tiles, s);
+    return launch_head_gemm<T, kSplit, 256, kMode>(c, tiles, s);
+  }
 }
 
 template <int T, bool kSplit>
 hipError_t gather(const HeadCall& c, hipStream_t s) {
   if constexpr (!kSplit) {
     // one launch for both where a block's copying takes no longer than a second launch, some 4 us
-    if (c.n <= 64 && c.row_tile * c.dim_pad <= 128 * 1024) {
+    if (c.n <= 64 && c.row_tile * c.dim_pad <= 128 * 1024) {  // (at most 64 rows a tile)
       hipLaunchKernelGGL((head_rows_kernel<T, true>), dim3(1), dim3(kRowThreads), 0, s, c);
       return hipGetLastError();
     }
@@ -1067,14 +1132,16 @@ hipError_t backward(const HeadCall& call, hipStream_t s) {
     if (c.dhidden)
       if (const hipError_t e = launch_head_rows<T, kSplit, kHidden>(c, c.hidden_rows, dim_tiles * c.splits, s)) return e;
     if (c.dweight)
-      if (const hipError_t e = launch_head_gemm<T, kSplit, 256, kWeight>(c, c.piece_tiles * dim_tiles * c.weight_splits, s)) return e;
-  }
-  if (c.dweight && c.weight_splits > 1) {
-    hipLaunchKernelGGL((head_weight_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
-    if (const hipError_t e = hipGetLastError()) return e;
+      if (const hipError_t e = launch_head_gemm<T, kSplit, T == kActF32 && !kSplit ? 128 : 256, kWeight>(c, c.piece_tiles * dim_tiles * c.weight_splits, s)) return e;
+    if (c.dweight && c.weight_splits > 1) {
+      const dim3 grid(static_cast<unsigned>(ceil_div(here, 4)), static_cast<unsigned>(ceil_div(c.dim, 256)));
+      hipLaunchKernelGGL((head_weight_out_kernel<T>), grid, dim3(256), 0, s, c);
+      if (const hipError_t e = hipGetLastError()) return e;
+    }
   }
   if (c.dhidden)
-    hipLaunchKernelGGL((head_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
+    hipLaunchKernelGGL((head_out_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.n, 4)), static_cast<unsigned>(ceil_div(c.dim, 256))),
+                       dim3(256), 0, s, c);
   return hipGetLastError();
 }
 
@@ -1149,17 +1216,16 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   p.hidden_rows = head_row_tile(type, n);
   p.splits = p.weight_splits = 1;
   if (gradients) {
-    // Both gradients may have few tiles: the sums over the piece, and over the rows where there is
-    // one piece, are split (by 1024 vocabulary entries and 256 rows at least) where the fuller chip
+    // Both gradients may have few tiles: the sums over the piece, and over the rows, are split (by 256 vocabulary entries and 128 rows at least) where the fuller chip
     // (4.7 TFLOP/s on each of 256 compute units) saves more than the sums' traffic (8 bytes each way a
     // value, 4.8 TB/s) and a launch, 4 us, cost.
     const int64_t dim_tiles = ceil_div(dim, tile), products = p.split ? 6 : type == kActF32 ? 16 : 1;
     const double unit = 2.0 * 256 * tile * products / 4.7e12;  // seconds of a 256-row tile per summed index
     double best = 0.0;
-    for (int64_t rows = head_row_tile(type, n); rows >= 64; rows /= 2) {
-      if (rows < p.hidden_rows && type == kActF32 && !p.split) break;
+    const int64_t most = head_row_tile(type, n), least = type == kActF32 && !p.split ? most : 64;
+    for (int64_t rows = most; rows >= least; rows /= 2) {
       const int64_t blocks = ceil_div(n, rows) * dim_tiles;
-      for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 1024 <= p.piece); ++splits) {
+      for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 256 <= p.piece); ++splits) {
         const double time = unit * p.piece * head_rounds(blocks * splits, rows) / splits + 8.0 * splits * n * dim / 4.8e12;
         if (best == 0.0 || time < best) {
           best = time;
@@ -1169,11 +1235,11 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
       }
     }
     p.sum = take(p.splits * p.rows_pad * p.sum_stride * 4);
-    if (p.piece >= vocab && (type != kActF32 || p.split)) {
-      const int64_t blocks = ceil_div(vocab, tile) * dim_tiles;
+    if (type != kActF32 || p.split) {
+      const int64_t blocks = p.piece / tile * dim_tiles;
       best = unit * n * head_rounds(blocks, 256);
-      for (int64_t splits = 2; splits <= 64 && splits * 256 <= n; ++splits) {
-        const double time = unit * n * head_rounds(blocks * splits, 256) / splits + 8.0 * splits * vocab * dim / 4.8e12 + 4e-6;
+      for (int64_t splits = 2; splits <= 64 && splits * 128 <= n; ++splits) {
+        const double time = unit * n * head_rounds(blocks * splits, 256) / splits + 8.0 * splits * p.piece * dim / 4.8e12 + 4e-6;
         if (time < best) {
           best = time;
           p.weight_splits = static_cast<int>(splits);
@@ -1221,7 +1287,8 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.hidden_rows = p.hidden_rows;
   c.weight_splits = p.weight_splits;
   c.weight_sum = reinterpret_cast<float*>(ws + p.weight_sum);
-  c.weight_rows = p.piece;
+  c.weight_lines = c.dweight && c.dweight_type != kActF32 && reinterpret_cast<uintptr_t>(c.dweight) % 16 == 0 &&
+                   c.dweight_stride % 8 == 0 && c.dim % 8 == 0;
   c.weight_use = c.weight_in;
   c.weight_stride = c.weight_in_stride;
   c.dim_use = c.dim;

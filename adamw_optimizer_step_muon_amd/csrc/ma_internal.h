@@ -637,12 +637,12 @@ struct HeadCall {
   void* g;          // rows_pad x piece
   float* z;         // kept logits, rows_pad x piece
   float* sum;       // splits x rows_pad x sum_stride
-  float* weight_sum;  // weight_splits x weight_rows x sum_stride
-  int64_t weight_rows, stats_rows, grad_rows, hidden_rows;
+  float* weight_sum;  // weight_splits x piece x sum_stride
+  int64_t stats_rows, grad_rows, hidden_rows;
   int64_t rows_pad, dim_pad, dim_use, weight_stride, sum_stride, piece, tiles, piece_start;
   int64_t hidden_plane, weight_plane, g_plane;  // values from one plane to the next
   int piece_tiles, splits, weight_splits, row_tile;  // row_tile: the gathered rows are padded to it
-  bool first, kept;
+  bool first, kept, weight_lines;  // weight_lines: dW's rows start at multiples of 16 bytes
 };
 hipError_t launch_head_clear(const HeadCall& c, hipStream_t s);  // dweight = 0
 enum HeadWork { kHeadForward = 0, kHeadBackward = 1, kHeadBoth = 2 };

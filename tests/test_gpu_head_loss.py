@@ -26,7 +26,7 @@ TYPES = [torch.float32, torch.float16, torch.bfloat16]
 E = 2.0 ** -24
 TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
 HALF = {torch.float32: 0.0, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
-SIZES = [(1, 1, 1), (1, 500, 64), (3, 257, 33), (5, 1000, 100), (64, 300, 72), (65, 511, 40), (128, 640, 256), (130, 777, 128),
+SIZES = [(1, 1, 1), (1, 500, 64), (3, 257, 33), (5, 1000, 100), (20, 777, 130), (64, 300, 72), (65, 511, 40), (128, 640, 256), (130, 777, 128),
          (257, 1025, 264), (300, 2500, 520), (511, 5000, 1001), (700, 3001, 768), (3001, 610, 200), (300, 900, 1100)]
 
 
