@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 import torch
 from torch.autograd.graph import increment_version
@@ -633,6 +634,8 @@ def head_loss_grad(hidden, weight, labels, row_weight, *, hidden_grad: bool = Tr
 # AdamW with both moments in 8 bits
 # --------------------------------------------------------------------------
 ADAMW_BYTE_BLOCK = 64  # elements that share a scale
+_BYTE_SEGMENT = struct.Struct("=7Qq2i")  # _AdamWByteSegment
+_HALVES = (torch.float16, torch.bfloat16)
 _ADAMW_BYTE_STATE = (("exp_avg", torch.float8_e4m3fn, 1), ("exp_avg_scale", torch.float8_e8m0fnu, ADAMW_BYTE_BLOCK),
                  ("exp_avg_sq", torch.float8_e5m2, 1), ("exp_avg_sq_scale", torch.float8_e8m0fnu, ADAMW_BYTE_BLOCK))
 
@@ -665,42 +668,73 @@ def adamw_byte_step_multi(segments, *, step: int, lr: float, beta1: float = 0.9,
     segments = list(segments)
     if not segments:
         return
-    arr, written = (_AdamWByteSegment * len(segments))(), []
+    buf, written, at = bytearray(len(segments) * _BYTE_SEGMENT.size), [], 0
     device = None
-    for i, (p, g, *state) in enumerate(segments):
-        copy = state.pop() if len(state) == 5 else None
-        if len(state) != 4:
+    for i, seg in enumerate(segments):
+        if len(seg) == 7:
+            p, g, m, ms, v, vs, copy = seg
+        elif len(seg) == 6:
+            (p, g, m, ms, v, vs), copy = seg, None
+        else:
             raise ValueError(f"segment {i} must hold 6 or 7 tensors")
-        for name, t in (("param", p), ("grad", g)):
-            _tensor(f"segment {i} {name}", t, device)
-            device = t.device
-        if p.dtype is not torch.float32 or not p.is_contiguous():
-            _require_f32_cuda(f"segment {i} param", p)
-        n = p.numel()
-        if g.numel() != n or not g.is_contiguous():
-            raise ValueError(f"segment {i} grad must be contiguous, of {n} values")
-        for (name, dtype, block), t in zip(_ADAMW_BYTE_STATE, state):
-            _tensor(f"segment {i} {name}", t, device)
-            if t.dtype is not dtype or not t.is_contiguous() or t.numel() != -(-n // block):
-                raise ValueError(f"segment {i} {name} must be contiguous {dtype} of {-(-n // block)} values "
-                                 f"(got {t.dtype}, {t.numel()})")
-        copied = 0
+        # the usual segment passes in as few looks at its tensors as there can be; the reasons
+        # of the others are found by _refuse_byte_segment
+        try:
+            n, index = p.numel(), p.get_device()
+            blocks = -(-n // ADAMW_BYTE_BLOCK)
+            fine = (index >= 0 and (device is None or index == device.index)
+                    and p.dtype is torch.float32 and p.is_contiguous()
+                    and g.numel() == n and g.is_contiguous() and g.get_device() == index
+                    and m.dtype is torch.float8_e4m3fn and m.numel() == n and m.is_contiguous() and m.get_device() == index
+                    and v.dtype is torch.float8_e5m2 and v.numel() == n and v.is_contiguous() and v.get_device() == index
+                    and ms.dtype is torch.float8_e8m0fnu and ms.numel() == blocks and ms.is_contiguous()
+                    and ms.get_device() == index
+                    and vs.dtype is torch.float8_e8m0fnu and vs.numel() == blocks and vs.is_contiguous()
+                    and vs.get_device() == index
+                    and (copy is None or (copy.dtype in _HALVES and copy.numel() == n and copy.is_contiguous()
+                                          and copy.get_device() == index)))
+            grad_type = _DTYPES[g.dtype]
+        except (AttributeError, KeyError):
+            fine = False
+        if not fine:
+            _refuse_byte_segment(i, p, g, (m, ms, v, vs), copy, device)
+        if device is None:
+            device = p.device
+        written += (p, m, ms, v, vs)
+        copied = address = 0
         if copy is not None:
-            _tensor(f"segment {i} copy", copy, device)
-            if copy.dtype not in (torch.float16, torch.bfloat16) or copy.numel() != n or not copy.is_contiguous():
-                raise ValueError(f"segment {i} copy must be contiguous float16 or bfloat16 of {n} values")
-            copied = _DTYPES[copy.dtype]
+            copied, address = _DTYPES[copy.dtype], copy.data_ptr()
             written.append(copy)
-        arr[i] = (p.data_ptr(), g.data_ptr(), *(t.data_ptr() for t in state),
-                  0 if copy is None else copy.data_ptr(), n, _type(f"segment {i} grad", g.dtype), copied)
-        written.append(p)
-        written += state
+        _BYTE_SEGMENT.pack_into(buf, at, p.data_ptr(), g.data_ptr(), m.data_ptr(), ms.data_ptr(), v.data_ptr(),
+                                vs.data_ptr(), address, n, grad_type, copied)
+        at += _BYTE_SEGMENT.size
     hp = _AdamWByteHParams(lr, beta1, beta2, eps, weight_decay, int(step), int(bool(decoupled)),
                            int(bool(cautious_wd)))
+    arr = (_AdamWByteSegment * len(segments)).from_buffer(buf)
     _call("ma_adamw_byte_step_multi", device, stream, arr, len(segments), ctypes.byref(hp), int(seed) & (2 ** 64 - 1))
     increment_version(written)
     if stream is not None:
         _record(stream, *written, *(s[1] for s in segments))
+
+
+def _refuse_byte_segment(i, p, g, state, copy, device):
+    """Raises what is wrong with a segment of adamw_byte_step_multi."""
+    for name, t in (("param", p), ("grad", g)):
+        _tensor(f"segment {i} {name}", t, device)
+        device = t.device
+    _require_f32_cuda(f"segment {i} param", p)
+    n = p.numel()
+    _type(f"segment {i} grad", g.dtype)
+    if g.numel() != n or not g.is_contiguous():
+        raise ValueError(f"segment {i} grad must be contiguous, of {n} values")
+    for (name, dtype, block), t in zip(_ADAMW_BYTE_STATE, state):
+        _tensor(f"segment {i} {name}", t, device)
+        if t.dtype is not dtype or not t.is_contiguous() or t.numel() != -(-n // block):
+            raise ValueError(f"segment {i} {name} must be contiguous {dtype} of {-(-n // block)} values "
+                             f"(got {t.dtype}, {t.numel()})")
+    if copy is not None:
+        _tensor(f"segment {i} copy", copy, device)
+    raise ValueError(f"segment {i} copy must be contiguous float16 or bfloat16 of {n} values")
 
 
 # --------------------------------------------------------------------------

@@ -478,3 +478,23 @@ def test_residual_norm_binding_refusals():
         ma.residual_norm_forward(x, x)
     with pytest.raises(TypeError):
         ma.residual_norm_forward(None, x)
+
+
+def test_byte_segment_layout():
+    from adamw_optimizer_step_muon_amd import ops
+
+    assert ops._BYTE_SEGMENT.size == ctypes.sizeof(_lib._AdamWByteSegment)
+    raw = bytearray(ops._BYTE_SEGMENT.pack(1, 2, 3, 4, 5, 6, 7, -8, 1, 2))
+    seg = _lib._AdamWByteSegment.from_buffer(raw)
+    assert [getattr(seg, f) for f, _ in seg._fields_] == [1, 2, 3, 4, 5, 6, 7, -8, 1, 2]
+
+
+def test_byte_segment_refusals():
+    """Each tensor of a segment that is not as it has to be is named (on the CPU: none gets further
+    than its device, so the checks are called with one)."""
+    from adamw_optimizer_step_muon_amd import ops
+
+    p = torch.zeros(70)
+    for bad in (p.half(), torch.zeros(140)[::2], None):
+        with pytest.raises((ValueError, TypeError), match="segment 3 param"):
+            ops._refuse_byte_segment(3, bad, p, ma.adamw_byte_state(p), None, None)
