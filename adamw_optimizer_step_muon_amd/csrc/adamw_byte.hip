@@ -114,7 +114,12 @@ __device__ __forceinline__ void element(float& p, float g, float& m, float& v, c
   if (kMode == kCoupled) g = __builtin_fmaf(c.wd, p, g);
   m = c.beta1 * m + c.one_m_beta1 * g;
   v = c.beta2 * v + c.one_m_beta2 * g * g;
-  const float upd = (m * c.inv_bc1) / (__builtin_sqrtf(v * c.inv_bc2) + c.eps);
+  // the update is not rounded into the state: root and reciprocal within one unit of the last place
+  // (scaled where v is subnormal, which the instruction takes for zero)
+  const float vhat = v * c.inv_bc2;
+  const bool tiny = vhat < 0x1p-96f;
+  const float root = __builtin_amdgcn_sqrtf(tiny ? vhat * 0x1p32f : vhat) * (tiny ? 0x1p-16f : 1.0f);
+  const float upd = (m * c.inv_bc1) * __builtin_amdgcn_rcpf(root + c.eps);
   if (kMode != kCoupled) {
     const float keep = 1.0f - c.lr * c.wd;
     p = p * ((kMode == kDecoupledCautious && !(upd * p > 0.0f)) ? 1.0f : keep);
@@ -209,6 +214,7 @@ __global__ __launch_bounds__(kThreads) void adamw_byte_kernel(AdamWByteTable tab
     const float mscale = scale_of(ms[u]), vscale = scale_of(vs[u]);
     const int64_t number = seg.first * kAdamWByteBlock + i;
     const uint32_t key = kt->key + static_cast<uint32_t>(number >> 32) * 0x9e3779b1u;
+    const uint32_t spread = static_cast<uint32_t>(number) * 0x9e3779b1u;
     uint32_t mr[kEach], vr[kEach];
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -220,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void adamw_byte_kernel(AdamWByteTable tab
       // elements behind the end must not enter their block's scale
       if (k >= cnt[u]) m[k] = v[k] = 0.0f;
       // (a group of four never passes a multiple of 2^32)
-      const uint32_t bits = mix((static_cast<uint32_t>(number + k) * 0x9e3779b1u) ^ key);
+      const uint32_t bits = mix((spread + k * 0x9e3779b1u) ^ key);
       mr[k] = bits & 0xffffu;
       vr[k] = bits >> 16;
     }
