@@ -89,23 +89,26 @@ __device__ __forceinline__ i32x4 buffer_rsrc(const unsigned short* base, unsigne
 // stage, then s_barrier).  Only the kernels with transposing reads use it: elsewhere
 // the intrinsic schedules better (the asm's memory clobber measured 3 % slower on the
 // 256-tile kernels that read X^T).
-template <bool kAsm>
+//
+// kWait: wait states ahead of the assembly's load, less one.  A scalar register that a vector
+// instruction wrote needs five before a buffer load reads it, and the compiler does not count them
+// for an assembly statement: where it keeps the base address in vector registers, v_readfirstlane
+// came two before the load, which then now and then read another address.  0 is for kernels whose
+// listing shows their bases made by scalar instructions (tests search the listings); 4 measured
+// 1 % slower on the 20-layer model's optimizer step.
+template <bool kAsm, int kWait = 0>
 __device__ __forceinline__ void dma16(const unsigned short* base, int voff, unsigned bytes,
                                       unsigned short* l) {
   const i32x4 r = buffer_rsrc(base, bytes);
   if constexpr (kAsm) {
     const int lds = __builtin_amdgcn_readfirstlane(static_cast<int>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned short*)(l))));
-    // m0 (the LDS address) is an input operand: the compiler sets it and knows its value.  A scalar
-    // register that a vector instruction wrote needs five wait states before a buffer load reads
-    // it, and the compiler does not count them for an assembly statement: where it kept the base
-    // address in vector registers, v_readfirstlane came two before the load, which then now and
-    // then read another address.
+    // m0 (the LDS address) is an input operand: the compiler sets it and knows its value
     asm volatile(
-        "s_nop 4\n\t"
+        "s_nop %3\n\t"
         "buffer_load_dwordx4 %0, %1, 0 offen lds"
         :
-        : "v"(voff), "s"(r), "{m0}"(lds)
+        : "v"(voff), "s"(r), "{m0}"(lds), "n"(kWait)
         : "memory");
   } else {
     raw_buffer_load_lds(r, (__attribute__((address_space(3))) unsigned*)(l), 16, voff, 0, 0, 0);

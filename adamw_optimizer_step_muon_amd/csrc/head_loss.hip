@@ -366,6 +366,8 @@ __device__ __forceinline__ bool head_tile(int mode, int mt, int nt, int splits, 
   const int per = (tiles + 7) / 8, b = static_cast<int>(blockIdx.x);
   const int t = (b & 7) * per + (b >> 3);
   if ((b >> 3) >= per || t >= tiles) return false;
+  // (integer divisions run on the vector unit: taken back to scalars, the operands' addresses are
+  // made by scalar instructions)
   split = 0;
   if (mode == kStats || mode == kGrad) {
     const int band = t / (4 * mt), rest = t - band * 4 * mt, left = nt - band * 4, width = left < 4 ? left : 4;
@@ -377,6 +379,9 @@ __device__ __forceinline__ bool head_tile(int mode, int mt, int nt, int splits, 
     n = rest % nt;
     m = rest / nt;
   }
+  m = __builtin_amdgcn_readfirstlane(m);
+  n = __builtin_amdgcn_readfirstlane(n);
+  split = __builtin_amdgcn_readfirstlane(split);
   return true;
 }
 
@@ -693,7 +698,8 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   } else if constexpr (kMode == kHidden) {
     // stages that hold an entry of the vocabulary: none begins behind W's end
     const int64_t entries = w_left < c.piece_tiles * 256 ? w_left : c.piece_tiles * 256;
-    const int all = static_cast<int>((entries + C::BK - 1) / C::BK), per = (all + c.splits - 1) / c.splits;
+    const int all = static_cast<int>((entries + C::BK - 1) / C::BK);
+    const int per = __builtin_amdgcn_readfirstlane((all + c.splits - 1) / c.splits);
     k_from = split * per;
     steps = all - k_from < per ? all - k_from : per;
     steps = steps < 0 ? 0 : steps;
@@ -703,7 +709,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - static_cast<int64_t>(k_from) * C::BK - 1) * c.weight_stride + c.dim_use - n0;
   } else {
-    const int all = (live + C::BK - 1) / C::BK, per = (all + c.weight_splits - 1) / c.weight_splits;
+    const int all = (live + C::BK - 1) / C::BK, per = __builtin_amdgcn_readfirstlane((all + c.weight_splits - 1) / c.weight_splits);
     k_from = split * per;
     steps = all - k_from < per ? all - k_from : per;
     steps = steps < 0 ? 0 : steps;
@@ -723,14 +729,14 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   const auto at_a = [&](int kt, int& step) -> const unsigned short* {
     step = kt;
     if constexpr (kProducts == 1) return gA;
-    const int product = kt / steps;
+    const int product = __builtin_amdgcn_readfirstlane(kt / steps);
     step = kt - product * steps;
     return gA + (0x010210 >> (4 * product) & 15) * plane_a;
   };
   const auto at_b = [&](int kt, int& step) -> const unsigned short* {
     step = kt;
     if constexpr (kProducts == 1) return gB;
-    const int product = kt / steps;
+    const int product = __builtin_amdgcn_readfirstlane(kt / steps);
     step = kt - product * steps;
     return gB + (0x001012 >> (4 * product) & 15) * plane_b;
   };
@@ -743,11 +749,11 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     if constexpr (C::kAT) {
       constexpr int kChunks = BM / 8, kRows = 64 / kChunks;
       const int r0 = q * kRows, r = r0 + lane / kChunks, ch = lane % kChunks;
-      dma16<C::kBT>(base + static_cast<int64_t>(step) * C::BK * lda, (r * lda + swz_kn(r, ch) * 8) * 2,
+      dma16<C::kBT, 4>(base + static_cast<int64_t>(step) * C::BK * lda, (r * lda + swz_kn(r, ch) * 8) * 2,
                     static_cast<unsigned>(((C::BK - 1) * lda + BM) * 2), s + r0 * BM);
     } else {
       const int r0 = q * 8, r = r0 + lane / 8;
-      dma16<C::kBT>(base + step * C::BK, (r * lda + swz<64>(r, lane % 8) * 8) * 2,
+      dma16<C::kBT, 4>(base + step * C::BK, (r * lda + swz<64>(r, lane % 8) * 8) * 2,
                     static_cast<unsigned>(((BM - 1) * lda + C::BK) * 2), s + r0 * C::BK);
     }
   };
@@ -764,7 +770,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
       const int64_t left = left_b - static_cast<int64_t>(step) * C::BK * ldb;
       const int64_t most = static_cast<int64_t>(C::BK - 1) * ldb + C::BN;
       const int64_t values = left < most ? left : most;
-      dma16<C::kBT>(base + static_cast<int64_t>(step) * C::BK * ldb, (r * ldb + swz_kn(r, ch) * 8) * 2,
+      dma16<C::kBT, 4>(base + static_cast<int64_t>(step) * C::BK * ldb, (r * ldb + swz_kn(r, ch) * 8) * 2,
                     static_cast<unsigned>(values * 2), s + r0 * C::BN);
     } else {
       const int r0 = q * 8, r = r0 + lane / 8, ch = swz<64>(r, lane % 8);
@@ -772,7 +778,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
       const int64_t most = static_cast<int64_t>(C::BN - 1) * ldb + C::BK;
       const int64_t values = left < most ? left : most;
       const int off = step * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
-      dma16<C::kBT>(base + step * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
+      dma16<C::kBT, 4>(base + step * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
     }
   };
   // group v of the loads: A of stage v + LA, B of stage v + LB (the shorter lead first)
