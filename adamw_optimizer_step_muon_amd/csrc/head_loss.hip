@@ -193,11 +193,11 @@ __global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
 
 // W in rows of dim_pad values: rows that are not aligned to 16 bytes, or fp32's planes.  A wave per
 // row.
-template <int T>
+template <int T, bool kPlanes>
 __global__ __launch_bounds__(256) void head_weight_kernel(HeadCall c) {
   const int64_t v = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (v >= c.vocab) return;
-  head_copy_row<T, T == kActF32>(static_cast<const typename Act<T>::S*>(c.weight_in) + v * c.weight_in_stride, c.weight_pad,
+  head_copy_row<T, kPlanes>(static_cast<const typename Act<T>::S*>(c.weight_in) + v * c.weight_in_stride, c.weight_pad,
                                  v * c.dim_pad, c.weight_plane, c.dim, c.dim_pad);
 }
 
@@ -634,11 +634,12 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
 // transposing LDS reads take, so nothing is stored twice.  The accumulators hold a row a lane
 // (operands passed to the matrix instruction the other way round), so a row's maximum and sum
 // need two lanes and four waves only.
-// LDS rings: 3 stages of A and 2 of B for 256 rows (160 KiB), 3 and 3 for fewer.
+// LDS rings: 3 stages of A and 2 of B for 256 rows (160 KiB), 3 and 3 for 128, 4 and 4 for 64, whose
+// short stages are bound by the loads' latency.
 template <int BM_, int kMode>
 struct HeadCfg {
   static constexpr int BM = BM_, BN = 256, BK = 64, WM = 2, WN = 4, kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int SA = 3, SB = BM == 256 ? 2 : 3, LA = SA - 1, LB = SB - 1;
+  static constexpr int SA = BM == 64 ? 4 : 3, SB = BM == 256 ? 2 : SA, LA = SA - 1, LB = SB - 1;
   static constexpr int WTM = BM / (WM * 32), WTN = BN / (WN * 32);
   static constexpr bool kAT = kMode == kWeight, kBT = kMode == kHidden || kMode == kWeight;
   static constexpr int kDmaA = BM * BK / 512 / kWaves, kDmaB = BN * BK / 512 / kWaves, kDma = kDmaA + kDmaB;
@@ -792,9 +793,14 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   };
   // until stage st has landed: what was issued after it may stay in flight
   const auto wait_stage = [&](int st) {
-    if (st + 1 >= nk) wait_vmcnt<0>();
-    else if constexpr (C::SA != C::SB) wait_vmcnt<C::kDmaA>();
-    else wait_vmcnt<C::kDma>();
+    if (st + 1 >= nk) {
+      wait_vmcnt<0>();
+    } else if constexpr (C::SA != C::SB) {
+      wait_vmcnt<C::kDmaA>();
+    } else {
+      if (C::LA >= 3 && st + 2 < nk) wait_vmcnt<(C::LA - 1) * C::kDma>();
+      else wait_vmcnt<C::kDma>();
+    }
   };
   const int frow = lane & 31, fkh = lane >> 5;
   const auto read_t = [&](const unsigned short* s, int width, int col0, int kk) {
@@ -860,7 +866,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
           // stage kt + 1 has landed and every wave's reads of this stage are done
           if constexpr (kSteady) {
             if constexpr (C::SA != C::SB) wait_vmcnt<C::kDmaA>();
-            else wait_vmcnt<C::kDma>();
+            else wait_vmcnt<(C::LA - 1) * C::kDma>();
           } else {
             wait_stage(kt + 1);
           }
@@ -885,7 +891,8 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
 // bound by memory and its latency: 32- and 64-row tiles, with longer stages.
 template <int BM, int kMode>
 __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
-  constexpr int B = 128, BK = BM == 128 ? 16 : 32, LA = BM + 4, LB = B + 4;
+  constexpr int B = 128, BK = BM == 128 ? 16 : 32, LA = BM + (kMode == kWeight ? 4 : 2),
+                LB = B + (kMode == kHidden || kMode == kWeight ? 4 : 2);  // vectors along k are stored a value at a time
   constexpr int WM = BM == 32 ? 1 : 2, WN = 4 / WM, WTM = BM / (WM * 32), WTN = B / (WN * 32);
   constexpr int kA = BM * BK / 1024, kB = B * BK / 1024;  // vectors of 4 values a thread and stage
   __shared__ __attribute__((aligned(16))) float smem[2][BK * (LA + LB)];
@@ -914,69 +921,68 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
   const int m0 = mi * BM, n0 = ni * B;
   const float* W = static_cast<const float*>(c.weight_use) + c.piece_start * c.weight_stride;
   const int64_t w_left = c.vocab - c.piece_start;
-  // operand (row, k): contiguous along k, or along the rows (T); rows and ks below their counts
+  // operand (row, k): contiguous along k, or along the rows (T)
   const float *gA, *gB;
-  int64_t lda, ldb, rows_b;
-  int k0 = 0, k1, ks_b;  // the summed indices k0 .. k1 - 1, and where B's end
+  int lda, ldb;
+  int64_t left_b;  // values of B behind gB: reads behind them return zeros
+  int k0 = 0, k1;  // the summed indices k0 .. k1 - 1
   if constexpr (kMode == kStats || kMode == kGrad) {
     gA = static_cast<const float*>(c.hidden_pad) + static_cast<int64_t>(m0) * c.dim_pad;
-    lda = c.dim_pad;
+    lda = static_cast<int>(c.dim_pad);
     gB = W + static_cast<int64_t>(n0) * c.weight_stride;
-    ldb = c.weight_stride;
-    rows_b = w_left - n0;
-    k1 = static_cast<int>(c.dim_pad);
-    ks_b = static_cast<int>(c.dim);
+    ldb = static_cast<int>(c.weight_stride);
+    left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use;
+    k1 = static_cast<int>((c.dim + BK - 1) / BK * BK);  // no stage begins behind the row's end
   } else if constexpr (kMode == kHidden) {
-    // (zeros behind W's end)
     const int64_t entries = w_left < c.piece_tiles * B ? w_left : c.piece_tiles * B;
     const int all = static_cast<int>((entries + BK - 1) / BK), per = (all + c.splits - 1) / c.splits;
     k0 = split * per * BK;
     k1 = min(all, (split + 1) * per) * BK;
     gA = static_cast<const float*>(c.g) + static_cast<int64_t>(m0) * c.piece;
-    lda = c.piece;
+    lda = static_cast<int>(c.piece);
     gB = W + n0;
-    ldb = c.weight_stride;
-    rows_b = c.dim - n0;
-    ks_b = w_left < k1 ? static_cast<int>(w_left) : k1;
+    ldb = static_cast<int>(c.weight_stride);
+    left_b = (w_left - 1) * c.weight_stride + c.dim_use - n0;
   } else {
     k1 = (live + BK - 1) / BK * BK;
     gA = static_cast<const float*>(c.g) + m0;
-    lda = c.piece;
+    lda = static_cast<int>(c.piece);
     gB = static_cast<const float*>(c.hidden_pad) + n0;
-    ldb = c.dim_pad;
-    rows_b = c.dim_pad - n0;
-    ks_b = k1;
+    ldb = static_cast<int>(c.dim_pad);
+    left_b = static_cast<int64_t>(k1) * c.dim_pad - n0;
   }
-  // a thread's vectors of an operand's stage: A is padded to whole tiles, B checked
-  typedef Pack<float, 4>::type P;
-  f32x4 ra[kA], rb[kB];
-  const auto load = [&](int k) {
+  // a thread's vectors of an operand's stage (A is padded to whole tiles)
+  constexpr int D = 3;  // stages in registers on their way
+  f32x4 ra[D][kA], rb[D][kB];
+  const auto load = [&](int k, f32x4 (&ra)[kA], f32x4 (&rb)[kB]) {
+    const float* a = gA + (kAT ? static_cast<int64_t>(k) * lda : k);
 #pragma unroll
     for (int u = 0; u < kA; ++u) {
       const int x = tid + u * 256;
-      if constexpr (kAT) ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(k + x / (BM / 4)) * lda + x % (BM / 4) * 4);
-      else ra[u] = *reinterpret_cast<const f32x4*>(gA + static_cast<int64_t>(x / (BK / 4)) * lda + k + x % (BK / 4) * 4);
+      ra[u] = *reinterpret_cast<const f32x4*>(a + (kAT ? x / (BM / 4) * lda + x % (BM / 4) * 4 : x / (BK / 4) * lda + x % (BK / 4) * 4));
     }
+    const int64_t from = kBT ? static_cast<int64_t>(k) * ldb : k;
+    const int64_t most = kBT ? static_cast<int64_t>(BK - 1) * ldb + B : static_cast<int64_t>(B - 1) * ldb + BK;
+    const int64_t values = left_b - from < most ? left_b - from : most;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(gB + from), 0, static_cast<int>(values * 4), 0x00020000);
 #pragma unroll
     for (int u = 0; u < kB; ++u) {
       const int x = tid + u * 256;
-      const int row = kBT ? x % (B / 4) * 4 : x / (BK / 4), kk = k + (kBT ? x / (B / 4) : x % (BK / 4) * 4);
-      const float* p = gB + (kBT ? static_cast<int64_t>(kk) * ldb + row : static_cast<int64_t>(row) * ldb + kk);
-      // the values that are there: along the rows, or along k
-      const int64_t there = kBT ? (kk < ks_b ? rows_b - row : 0) : (row < rows_b ? ks_b - kk : 0);
-      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (there >= 4) {
-        const P w = *reinterpret_cast<const P*>(p);
-        v = f32x4{w[0], w[1], w[2], w[3]};
-      } else {
+      const int at = kBT ? x / (B / 4) * ldb + x % (B / 4) * 4 : x / (BK / 4) * ldb + x % (BK / 4) * 4;
+      rb[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, 0, 0));
+    }
+    if (!kBT && k + BK > c.dim_use) {
+      // the row's end: W's next row follows
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (e < there) v[e] = p[e];
+      for (int u = 0; u < kB; ++u) {
+        const int kk = k + (tid + u * 256) % (BK / 4) * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (kk + e >= c.dim_use) rb[u][e] = 0.0f;
       }
-      rb[u] = v;
     }
   };
-  const auto store = [&](int buf) {
+  const auto store = [&](int buf, const f32x4 (&ra)[kA], const f32x4 (&rb)[kB]) {
     float *a = smem[buf], *b = smem[buf] + BK * LA;
 #pragma unroll
     for (int u = 0; u < kA; ++u) {
@@ -1006,30 +1012,36 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     for (int j = 0; j < WTN; ++j)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
-  if (k0 < k1) {
-    load(k0);
-    store(0);
+  const int steps = k0 < k1 ? (k1 - k0) / BK : 0;
+  if (steps > 0) {
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+      if (u < steps) load(k0 + u * BK, ra[u], rb[u]);
+    store(0, ra[0], rb[0]);
     __syncthreads();
-    int buf = 0;
-    for (int k = k0; k < k1; k += BK, buf ^= 1) {
-      const bool more = k + BK < k1;
-      if (more) load(k + BK);
-      const float* a = smem[buf] + (lane >> 5) * LA + wm * (WTM * 32) + (lane & 31);
-      const float* b = smem[buf] + BK * LA + (lane >> 5) * LB + wn * (WTN * 32) + (lane & 31);
+    for (int first = 0; first < steps; first += D) {
 #pragma unroll
-      for (int kk = 0; kk < BK; kk += 2) {
-        float fa[WTM], fb[WTN];
+      for (int u = 0; u < D; ++u) {
+        const int s = first + u;
+        if (s >= steps) break;
+        if (s + D < steps) load(k0 + (s + D) * BK, ra[u], rb[u]);
+        const float* a = smem[s & 1] + (lane >> 5) * LA + wm * (WTM * 32) + (lane & 31);
+        const float* b = smem[s & 1] + BK * LA + (lane >> 5) * LB + wn * (WTN * 32) + (lane & 31);
 #pragma unroll
-        for (int i = 0; i < WTM; ++i) fa[i] = a[kk * LA + i * 32];
+        for (int kk = 0; kk < BK; kk += 2) {
+          float fa[WTM], fb[WTN];
 #pragma unroll
-        for (int j = 0; j < WTN; ++j) fb[j] = b[kk * LB + j * 32];
+          for (int i = 0; i < WTM; ++i) fa[i] = a[kk * LA + i * 32];
 #pragma unroll
-        for (int i = 0; i < WTM; ++i)
+          for (int j = 0; j < WTN; ++j) fb[j] = b[kk * LB + j * 32];
 #pragma unroll
-          for (int j = 0; j < WTN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+          for (int i = 0; i < WTM; ++i)
+#pragma unroll
+            for (int j = 0; j < WTN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        }
+        if (s + 1 < steps) store((s + 1) & 1, ra[(u + 1) % D], rb[(u + 1) % D]);
+        __syncthreads();
       }
-      if (more) store(buf ^ 1);
-      __syncthreads();
     }
   }
   head_epilogue<kActF32, false, kMode, BM, B, WM, WN>(c, acc, m0, n0, split, live, reinterpret_cast<char*>(&smem[0][0]));
@@ -1154,7 +1166,7 @@ hipError_t backward(const HeadCall& call, hipStream_t s) {
 template <int T, bool kSplit>
 hipError_t run_work(const HeadCall& c, HeadWork work, hipStream_t s) {
   if (c.weight_pad) {
-    hipLaunchKernelGGL((head_weight_kernel<T>), dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
+    hipLaunchKernelGGL((head_weight_kernel<T, kSplit>), dim3(static_cast<unsigned>(ceil_div(c.vocab, 4))), dim3(256), 0, s, c);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   if (work != kHeadBackward)
@@ -1166,7 +1178,8 @@ hipError_t run_work(const HeadCall& c, HeadWork work, hipStream_t s) {
 
 bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride) {
   // (offsets inside a tile of 256 rows have 31 bits)
-  return type != kActF32 && ((reinterpret_cast<uintptr_t>(weight) & 15u) || stride % 8 || dim % 8 || stride > (1 << 22));
+  if (type == kActF32) return stride > (1 << 21);
+  return (reinterpret_cast<uintptr_t>(weight) & 15u) || stride % 8 || dim % 8 || stride > (1 << 22);
 }
 
 int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p) {
