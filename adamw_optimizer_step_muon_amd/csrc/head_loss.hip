@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
   }
   // weights are scaled so that the largest becomes 2^14 (exactly: then g of an unlikely label, nearly
   // the weight itself, hardly rounds); fp32 needs no scaling
-  const bool scaled = T != kActF32 && top != 0.0f;
+  const bool scaled = T != kActF32 && top > 0.0f && top <= 3.4028234663852886e38f;
   int base = 0, turn = 0;
   for (int64_t first = 0; first < c.n; first += kRowThreads, turn ^= 1) {
     const int64_t r = first + t, label = r < c.n ? label_of(r) : -1;
@@ -1188,7 +1188,9 @@ int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const Head
   const int64_t others[] = {ceil_div(n, p.hidden_rows) * dim_tiles * p.splits, ceil_div(n, p.grad_rows) * (p.piece / tile),
                             p.piece / tile * dim_tiles * p.weight_splits};
   for (const int64_t t : others) tiles = t > tiles ? t : tiles;
-  return (tiles + 8) * 512;
+  // the kernels with a wave for each vocabulary entry
+  const int64_t waves = p.weight_pad || p.weight_splits > 1 ? vocab * 64 + 256 : 0;
+  return (tiles + 8) * 512 > waves ? (tiles + 8) * 512 : waves;
 }
 
 HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, bool gradients) {

@@ -595,9 +595,10 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
  * and a label per row (label_bits 32 or 64, signed):
  *   z = h W^T,  lse = log sum_v exp z_v,  loss = lse - z_label
  * A row whose label lies outside [0, vocab) has no target: loss and lse are 0, and whatever it holds
- * reaches no result.  Products are summed in fp32 (16-bit operands on the bf16 or fp16 matrix
- * instructions, fp32 on the fp32 ones).  A NaN among the hidden states of a row, or an infinite
- * logit of it, makes its loss NaN; a NaN in W makes all of them NaN.
+ * reaches no result.  Products are summed in fp32: 16-bit operands on the bf16 or fp16 matrix
+ * instructions, fp32 ones on the fp32 instructions for up to 128 rows and, for more, as three bf16
+ * planes each (2^-24 of every product is lost; magnitudes up to 2^127).  A NaN or an infinity in a
+ * row's hidden states makes that row's loss NaN (or its loss infinite), one in W may make all of them NaN.
  * n < 2^22, dim <= 2^20, vocab <= 2^30.  n = 0 is a no-op, but for a dweight that is not added to.
  *
  * Host only: workspace bytes of the calls (gradients = 1 for _backward and _grad).  Of `weight`

@@ -187,6 +187,58 @@ def test_rows_without_a_target(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,dim", [(300, 136), (300, 1100), (40, 136), (90, 200)])
+def test_rows_without_a_target_among_others(dtype, n, dim):
+    """Their hidden states may hold anything; their results are zeros, and the others' are what they
+    are without them (kept logits, which the longer rows and few fp32 ones have, among them)."""
+    h, w, labels, rw = _inputs(n, 700, dim, dtype, 4, ignored=0)
+    rw[1] = 2.0  # the largest weight, which all are scaled by
+    on = torch.ones(n, dtype=torch.bool, device=DEV)
+    on[[0, 7, 20, n - 1]] = False
+    bad, l2, rw2 = h.clone(), labels.clone(), rw.clone()
+    bad[0], bad[7], bad[20] = float("nan"), float("inf"), -float("inf")
+    l2[[0, 7]], rw2[[20, n - 1]] = torch.tensor([-100, 700], device=DEV), 0.0
+    loss, dh, dw = ma.head_loss_grad(bad, w, l2, rw2)
+    ref = _reference(torch.where(on[:, None], h, 0.0), w, torch.where(on, labels, -1), rw)
+    _near(loss[on], ref[0][on], ref[2][on])
+    assert (loss[[0, 7]] == 0).all() and torch.isnan(loss[20])
+    _near(dh, ref[4], ref[6])
+    assert (dh[~on] == 0).all()
+    _near(dw, ref[5], ref[7])
+    lse = ma.head_loss_forward(bad, w, l2)[1]
+    back = ma.head_loss_backward(bad, w, l2, lse, rw2)
+    assert (back[0][~on] == 0).all() and torch.isfinite(back[1]).all()
+    none = torch.full_like(labels, -100)
+    loss, dh, dw = ma.head_loss_grad(bad, w, none, rw)
+    assert not loss.any() and not dh.any() and not dw.any()
+    loss, lse = ma.head_loss_forward(bad, w, none)
+    assert not loss.any() and not lse.any()
+    grad = torch.ones(700, dim, device=DEV)
+    ma.head_loss_grad(bad, w, labels, torch.zeros_like(rw), dweight=grad, accumulate=True)
+    assert (grad == 1).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_row_weights_of_any_size(dtype):
+    """Weights that differ by orders of magnitude, negative ones, and an infinite one, which reaches
+    its row's and the weight's gradient alone."""
+    h, w, labels, rw = _inputs(150, 400, 72, dtype, 12, ignored=0)
+    scale = 1e-3 if dtype == torch.float16 else 1e20
+    rw = (rw - 0.5) * scale * torch.exp(-torch.arange(150, device=DEV) / 20.0)
+    ref = _reference(h, w, labels, rw)
+    _, dh, dw = ma.head_loss_grad(h, w, labels, rw)
+    _near(dh, ref[4], ref[6])
+    _near(dw, ref[5], ref[7])
+    rw = torch.full((150,), 1 / 150, device=DEV)
+    clean = ma.head_loss_grad(h, w, labels, rw)[1]
+    rw[40] = float("inf")
+    dh = ma.head_loss_grad(h, w, labels, rw)[1]
+    on = torch.arange(150, device=DEV) != 40
+    assert not torch.isfinite(dh[40]).any()
+    assert torch.isfinite(dh[on]).all() and (dh[on].float() - clean[on].float()).abs().max() < 0.05 * clean.float().abs().max()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_no_rows(dtype):
     h, w, labels, rw = _inputs(1, 50, 40, dtype, 4, ignored=0)
     h, labels, rw = h[:0], labels[:0], rw[:0]
