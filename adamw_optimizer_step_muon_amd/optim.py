@@ -31,7 +31,8 @@ An AdamW group's ``state_bits=8`` holds its moments in 8 bits instead (2 + 1/32 
 parameter, see adamw_byte_step_multi): ``exp_avg``, ``exp_avg_sq`` and their blocks' scales, with
 ``seed`` for the roundings' random bits.  Its ``copies`` (one entry per parameter, None or a
 contiguous fp16 or bf16 tensor of its size) receive the stepped parameters, for a forward pass
-that reads 16-bit weights.  Token gradients are built densely there.
+that reads 16-bit weights; what they hold before a parameter's first step is the caller's.  Token
+gradients are built densely there.
 
 A Muon group's ``ns_mode`` (0 by default) selects the Newton-Schulz route: 1 runs the
 Gram-space iteration ("DMuon", section 2.2) on fp16 operands for the buckets whose long
