@@ -23,9 +23,9 @@
 // fp16 then keeps probabilities down to 2^-38.  Every sum has a fixed
 // order: the same inputs give the same bits.
 // fp32 operands: up to kSplitRows rows on the fp32 matrix instructions; above as three bf16 planes
-// each (x = x0 + x1 + x2 to 2^-24 of itself: three times 8 bits), whose six products of 2^-16 and more
-// run as one sum six times as long, the smallest first: the three that are left out are 2^-24 of the
-// product together.
+// each (x = x0 + x1 + x2 exactly: what two roundings to 8 bits leave of 24 fits the third), whose six
+// products of 2^-16 and more run as one sum six times as long, the smallest first: the three that are
+// left out are 2^-24 of the product together (2^-8 2^-17 twice, and less).
 #include "gemm_tile.h"
 #include "ma_act.h"
 #include "ma_internal.h"

@@ -11,9 +11,11 @@
  *                  (embeddings, LM head, normalisation gains, biases).
  *
  * ma_adamw_byte_step_multi is the AdamW step with both moments in 8 bits.  Beside them are the
- * training operators that produce the gradients of those AdamW parameters, or spare them: ma_embedding_forward / _backward, ma_adamw_step_embedding (AdamW on a table
- * straight from its tokens), ma_layer_norm_forward / _backward and ma_distill_forward /
- * _backward / _loss_grad.
+ * training operators that produce the gradients of those AdamW parameters, or spare them:
+ * ma_embedding_forward / _backward, ma_adamw_step_embedding (AdamW on a table straight from its
+ * tokens), ma_layer_norm_forward / _backward, ma_residual_norm_forward / _backward (the norms
+ * around a block), ma_distill_forward / _backward / _loss_grad and ma_head_loss_forward /
+ * _backward / _grad (the LM head with its cross entropy).
  *
  * Sources, by page title:
  *   [HB] "Optimizers: AdamW, Muon and the distributed optimizer" (AI infra handbook):
@@ -619,7 +621,7 @@ ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_
 
 /* The gradients of sum row_weight[r] loss[r] (row_weight, lse: n fp32):
  *   g = row_weight (exp(z - lse) - [v = label]),  dhidden = g W,  dweight (+)= g^T h
- * g is rounded once to the hidden type (2^-9 of each term of the sums for bf16, 2^-12 for fp16).
+ * g is rounded once to the hidden type (2^-8 of each term of the sums at most for bf16, 2^-11 for fp16).
  * Rows without a target or of weight 0 have gradient 0, whatever they hold.  dhidden has the hidden
  * type; dweight is (vocab, dim) of dweight_type, the hidden type or MA_F32, and is added to with
  * accumulate = 1 (MA_F32 only).  Either may be NULL. */

@@ -150,6 +150,24 @@ def test_many_tensors(sizes):
         first += -(-n // 64) * 64
 
 
+def test_elements_behind_2_32():
+    """Their addresses and their numbers pass 32 bits."""
+    n, seed, warm = (1 << 32) + 130, 21, 2
+    start = (1 << 32) - 128
+    p = torch.zeros(n, device=DEV)
+    grad = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    seg = (p, grad, *ma.adamw_byte_state(p), torch.zeros(n, dtype=torch.bfloat16, device=DEV))
+    tail = tuple(t[start // 64:] if i in (3, 5) else t[start:] for i, t in enumerate(seg))
+    g = torch.Generator(device=DEV).manual_seed(5)
+    tail[0].copy_(torch.randn(n - start, generator=g, device=DEV))
+    for t in range(1, warm + 2):
+        tail[1].copy_(torch.randn(n - start, generator=g, device=DEV))
+        before, = _clone([tail])
+        ma.adamw_byte_step_multi([seg], step=t, seed=seed, **HP)
+        _check(before, tail, t, start, seed)
+    assert not p[:start].any() and not seg[4].view(torch.uint8)[:start].any()
+
+
 @pytest.mark.parametrize("n", [65, 5003])
 def test_alignment_changes_nothing(n):
     runs = []

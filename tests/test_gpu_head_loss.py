@@ -153,6 +153,37 @@ def test_long_vocabularies(n, vocab, dim, dtype):
     _near(got[2], dw, bw)
 
 
+@pytest.mark.parametrize("dtype,n,vocab,dim", [(torch.float32, 4099, 30001, 72), (torch.float32, 100, 530003, 24),
+                                               (torch.bfloat16, 40, 1050003, 24)])
+def test_pieces_of_few_and_of_wide_rows(dtype, n, vocab, dim):
+    """Several pieces for fp32's planes, for fp32 tiles of few rows, and for a piece of 2^20 entries."""
+    h, w, labels, rw = _inputs(n, vocab, dim, dtype, n)
+    loss, _, dloss, _, dh, dw, bh, bw, _ = _reference(h, w, labels, rw)
+    got = ma.head_loss_grad(h, w, labels, rw)
+    _near(got[0], loss, dloss)
+    _near(got[1], dh, bh)
+    _near(got[2], dw, bw)
+
+
+@pytest.mark.parametrize("dtype,stride", [(torch.bfloat16, 1 << 22), (torch.float16, (1 << 22) + 8), (torch.float32, 1 << 21),
+                                          (torch.float32, (1 << 21) + 4)])
+@pytest.mark.parametrize("n", [50, 260])
+def test_rows_far_apart(dtype, stride, n):
+    """The weight's and its gradient's rows, on both sides of the stride from which they are copied;
+    offsets pass 32 bits."""
+    vocab, dim = 700, 72
+    h, w, labels, rw = _inputs(n, vocab, dim, dtype, n)
+    want = ma.head_loss_grad(h, w, labels, rw)
+    apart = lambda rows, cols: torch.empty(rows * stride, dtype=dtype, device=DEV).as_strided((rows, cols), (stride, 1))  # noqa: E731
+    far, out, hidden = apart(vocab, dim), apart(vocab, dim + 8), apart(n, dim)
+    far.copy_(w)
+    hidden.copy_(h)
+    out.fill_(3.0)
+    loss, dh, _ = ma.head_loss_grad(hidden, far, labels, rw, dweight=out[:, :dim])
+    assert torch.equal(loss, want[0]) and torch.equal(dh, want[1]) and torch.equal(out[:, :dim], want[2])
+    assert torch.equal(far, w) and (out[:, dim:] == 3).all()
+
+
 def test_matches_the_oracle():
     h, w, labels, rw = _inputs(30, 50, 24, torch.float32, 1)
     loss, lse = training.head_loss(h.cpu(), w.cpu(), labels.cpu())
@@ -320,6 +351,46 @@ def test_stream_and_graph(dtype):
         torch.cuda.synchronize()
         want = ma.head_loss_grad(h * scale, w, labels, rw)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_two_streams_and_graphs_of_one_workspace(dtype):
+    """Calls at once on two streams have workspaces of their own; graphs that share one are replayed
+    one after the other."""
+    calls = [_inputs(n, 1500, 136, dtype, n) for n in (90, 300)]
+    want = [ma.head_loss_grad(*c) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[ma.head_loss_grad(*c, stream=s) for c, s in zip(calls, streams)] for _ in range(4)]
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for turn in got:
+        assert all(torch.equal(a, b) for g, x in zip(turn, want) for a, b in zip(g, x))
+    need = max(ma.head_loss_workspace_bytes(c[0], c[1]) for c in calls)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(ma.head_loss_grad(*c, workspace=ws))
+    for _ in range(3):
+        for g, out, x in zip(graphs, outs, want):
+            for t in out:
+                t.fill_(9.0)
+            ws.fill_(255)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, x))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_gradient_wanted(dtype):
+    h, w, labels, rw = _inputs(70, 300, 72, dtype, 13)
+    loss, dh, dw = ma.head_loss_grad(h, w, labels, rw, hidden_grad=False, weight_grad=False)
+    assert dh is None and dw is None and torch.equal(loss, ma.head_loss_grad(h, w, labels, rw)[0])
+    lse = ma.head_loss_forward(h, w, labels)[1]
+    assert ma.head_loss_backward(h, w, labels, lse, rw, hidden_grad=False, weight_grad=False) == (None, None)
 
 
 @pytest.mark.parametrize("dtype", TYPES)

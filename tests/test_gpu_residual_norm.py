@@ -255,6 +255,29 @@ def test_stream_and_graph(dtype):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [200, 9000, 20000])
+def test_rows_far_apart(dtype, dim):
+    """Offsets pass 32 bits, and what lies between the rows stays."""
+    n, stride = 20, (1 << 27) + 13
+    (x, res, dy, dout), vec = _inputs(n, dim, dtype, 7, {}, "all")
+    want = ma.residual_norm_forward(x, res, **vec)
+    back = ma.residual_norm_backward(dout, dy, x, want[0], want[2], **vec)
+    wide = torch.empty(n * stride, dtype=dtype, device=DEV).as_strided((n, dim + 9), (stride, 1))
+    wide.fill_(5.0)
+    out = wide[:, :dim]
+    far = [torch.empty(n * stride, dtype=dtype, device=DEV).as_strided((n, dim), (stride, 1)) for _ in range(4)]
+    for a, t in zip(far, (x, res, dy, dout)):
+        a.copy_(t)
+    got = ma.residual_norm_forward(far[0], far[1], out=out, **vec)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and (wide[:, dim:] == 5).all()
+    got = ma.residual_norm_backward(far[3], far[2], far[0], out, got[2], **vec)
+    assert all(torch.equal(a, b) for a, b in zip(got, back))
+    # the residual in place
+    ma.residual_norm_forward(far[0], far[1], out=far[1], **vec)
+    assert torch.equal(far[1], want[0]) and torch.equal(far[0], x)
+
+
 def test_plain_norm_matches_layer_norm():
     """With a branch of nothing, y is the layer norm of the residual."""
     (x, res, _, _), vec = _inputs(50, 520, torch.float32, 6, {}, "weights")
