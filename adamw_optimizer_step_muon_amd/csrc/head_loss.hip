@@ -13,10 +13,13 @@
 // the price of not keeping them, makes it 8.  Both directions in one call keep the logits (fp32)
 // where those of all rows take no more than the piece's 512 MiB and the product costs more than
 // writing and reading them.
+// Each product may have few tiles: its sum (over the hidden size, the piece or the rows) is then split
+// over blocks, whose fp32 parts the next kernel adds in order.  Split logits are kept.
 //
 // Rows with a target (and, for gradients, a weight that is not zero) are gathered first into a
 // padded copy, so the others cost nothing and whatever they hold reaches no result, and tiles need
-// no checks along the rows.
+// no checks along the rows.  Both directions in one call number and gather the rows once where logits
+// are kept or one tile holds all rows; a row of weight 0 then goes on as zeros behind its loss.
 //
 // Rounding: products of 16-bit values are exact and summed in fp32.  g is rounded once to the
 // hidden type, as the matrix cores take it, after a scaling that makes the largest row weight 2^14:
@@ -119,8 +122,8 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
   for (int64_t first = 0; first < c.n; first += kRowThreads, turn ^= 1) {
     const int64_t r = first + t, label = r < c.n ? label_of(r) : -1;
     const float given = c.row_weight && r < c.n ? c.row_weight[r] : 1.0f;
-    // (kept logits are numbered by the labels alone)
-    const bool live = in_vocab(label) && (c.kept || given != 0.0f);
+    // (rows that are numbered once, for the loss too, by the labels alone)
+    const bool live = in_vocab(label) && (c.once || given != 0.0f);
     const unsigned long long mask = __ballot(live);
     if ((t & 63) == 0) counts[turn][wave] = __popcll(mask);
     __syncthreads();
@@ -139,16 +142,16 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     c.place[r] = at;
     c.row_of[at] = static_cast<int>(r);
     c.label[at] = static_cast<int>(label);
-    float w = given;
     if (c.row_weight) {
-      // exp(z - top) factor = weight exp(z - lse)
-      if (scaled) w = given / top * 0x1p14f;
+      const float w = scaled ? given / top * 0x1p14f : given;
       c.weight[at] = w;
-      c.top[at] = c.lse_in ? c.lse_in[r] : c.tops[r];
-      c.factor[at] = c.lse_in || w == 0.0f ? w : w / c.sums[r];
+      if (!c.once) {
+        // exp(z - top) factor = weight exp(z - lse)
+        c.top[at] = c.lse_in ? c.lse_in[r] : c.tops[r];
+        c.factor[at] = c.lse_in ? w : w / c.sums[r];
+      }
     }
-    // (kept logits: a row of weight 0 takes part as zeros)
-    if constexpr (kCopy) copied[at] = w == 0.0f ? -1 : static_cast<int>(r);
+    if constexpr (kCopy) copied[at] = static_cast<int>(r);
   }
   if (t == 0) {
     c.head->live = base;
@@ -185,9 +188,7 @@ __global__ __launch_bounds__(256) void head_gather_kernel(HeadCall c) {
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int live = c.head->live;
   if (at >= (live + c.row_tile - 1) / c.row_tile * static_cast<int64_t>(c.row_tile)) return;
-  // (kept logits: a row of weight 0 takes part as zeros)
-  const bool there = at < live && !(c.kept && c.row_weight && c.weight[at] == 0.0f);
-  const auto* in = there ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
+  const auto* in = at < live ? static_cast<const typename Act<T>::S*>(c.hidden) + c.row_of[at] * c.hidden_stride : nullptr;
   head_copy_row<T, kPlanes>(in, c.hidden_pad, at * c.dim_pad, c.hidden_plane, c.dim, c.dim_pad);
 }
 
@@ -213,6 +214,34 @@ __global__ __launch_bounds__(256) void head_clear_kernel(HeadCall c) {
   }
 }
 
+// A row's loss and lse, and what the backward pass takes from its largest logit and its sum: a wave,
+// whose lanes have the same values.
+__device__ __forceinline__ void head_row_done(const HeadCall& c, int64_t at, float top, float sum, float target) {
+  const int lane = threadIdx.x & 63, r = c.row_of[at];
+  const float log_sum = logf(sum);
+  if (lane == 0) {
+    if (c.loss) c.loss[r] = (top - target) + log_sum;
+    if (c.lse_out) c.lse_out[r] = top + log_sum;
+    if (c.tops) {
+      c.tops[r] = top;
+      c.sums[r] = sum;
+    }
+  }
+  if (!c.once) return;
+  const float w = c.weight[at];
+  if (lane == 0) {
+    c.top[at] = w == 0.0f ? 0.0f : top;
+    c.factor[at] = w == 0.0f ? 0.0f : w / sum;
+  }
+  if (w != 0.0f) return;
+  // a row without a gradient goes on as zeros, whatever it holds
+  const int size = c.type == kActF32 && !c.planes ? 4 : 2;
+  for (int plane = 0; plane < (c.planes ? 3 : 1); ++plane) {
+    char* out = static_cast<char*>(c.hidden_pad) + (plane * c.hidden_plane + at * c.dim_pad) * size;
+    for (int64_t i = lane * 4; i < c.dim_pad * size; i += 256) *reinterpret_cast<unsigned*>(out + i) = 0;
+  }
+}
+
 // Joins the tiles' maxima and sums of a row.  A wave per live row.
 __global__ __launch_bounds__(256) void head_join_kernel(HeadCall c) {
   const int lane = threadIdx.x & 63;
@@ -229,16 +258,49 @@ __global__ __launch_bounds__(256) void head_join_kernel(HeadCall c) {
     // a tile of -inf alone has no share
     sum += p.x == -INFINITY ? p.y : p.y * __builtin_amdgcn_exp2f((p.x - base) * kLog2e);
   }
-  sum = wave_sum(sum);
-  if (lane != 0) return;
-  const float log_sum = logf(sum);
-  const int r = c.row_of[at];
-  if (c.loss) c.loss[r] = (top - c.target[at]) + log_sum;
-  if (c.lse_out) c.lse_out[r] = top + log_sum;
-  if (c.tops) {
-    c.tops[r] = top;
-    c.sums[r] = sum;
+  head_row_done(c, at, top, wave_sum(sum), c.target[at]);
+}
+
+// The same from logits whose sums are split over blocks.  A block per live row.
+__global__ __launch_bounds__(256) void head_stats_kernel(HeadCall c) {
+  __shared__ float tops[4], sums[4], target;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t at = blockIdx.x;
+  if (at >= c.head->live) return;
+  const float* z = c.z + at * c.piece;
+  const int64_t label = c.label[at];
+  float top = -INFINITY, sum = 0.0f;
+  for (int64_t col = threadIdx.x * 4; col < c.vocab; col += 1024) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(z + col);
+#pragma unroll 4
+    for (int s = 1; s < c.logit_splits; ++s) v += *reinterpret_cast<const f32x4*>(z + s * c.z_plane + col);
+    float most = top;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < c.vocab) most = fmaxf(most, v[e]);
+    const float base = most == -INFINITY ? 0.0f : most;
+    if (top != -INFINITY) sum *= __builtin_amdgcn_exp2f((top - base) * kLog2e);
+    top = most;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (col + e < c.vocab) sum += __builtin_amdgcn_exp2f((v[e] - base) * kLog2e);
+      if (col + e == label) target = v[e];
+    }
   }
+  const float wave_top = wave_max(top), b = wave_top == -INFINITY ? 0.0f : wave_top;
+  // a thread of -inf alone has no share
+  sum = wave_sum(top == -INFINITY ? sum : sum * __builtin_amdgcn_exp2f((top - b) * kLog2e));
+  if (lane == 0) {
+    tops[wave] = wave_top;
+    sums[wave] = sum;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  const float base = top == -INFINITY ? 0.0f : top;
+  sum = 0.0f;
+  for (int w = 0; w < 4; ++w) sum += tops[w] == -INFINITY ? sums[w] : sums[w] * __builtin_amdgcn_exp2f((tops[w] - base) * kLog2e);
+  head_row_done(c, at, top, sum, target);
 }
 
 // g from kept logits, 8 values a thread; a block takes 2048 columns of a row.
@@ -254,7 +316,10 @@ __global__ __launch_bounds__(256) void head_convert_kernel(HeadCall c) {
   float g[8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const f32x4 z = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(in + 4 * h));
+    f32x4 z = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(in + 4 * h));
+#pragma unroll 4
+    for (int s = 1; s < c.logit_splits; ++s)
+      z += __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(in + s * c.z_plane + 4 * h));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t v = col + 4 * h + e;
@@ -368,16 +433,15 @@ __device__ __forceinline__ bool head_tile(int mode, int mt, int nt, int splits, 
   if ((b >> 3) >= per || t >= tiles) return false;
   // (integer divisions run on the vector unit: taken back to scalars, the operands' addresses are
   // made by scalar instructions)
-  split = 0;
+  split = splits > 1 ? t / (mt * nt) : 0;
+  const int here = t - split * mt * nt;
   if (mode == kStats || mode == kGrad) {
-    const int band = t / (4 * mt), rest = t - band * 4 * mt, left = nt - band * 4, width = left < 4 ? left : 4;
+    const int band = here / (4 * mt), rest = here - band * 4 * mt, left = nt - band * 4, width = left < 4 ? left : 4;
     m = rest / width;
     n = band * 4 + rest % width;
   } else {
-    split = t / (mt * nt);
-    const int rest = t - split * mt * nt;
-    n = rest % nt;
-    m = rest / nt;
+    n = here % nt;
+    m = here / nt;
   }
   m = __builtin_amdgcn_readfirstlane(m);
   n = __builtin_amdgcn_readfirstlane(n);
@@ -395,6 +459,18 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
   const int wm = wave / WN, wn = wave % WN, frow = lane & 31, half = lane >> 5;
   const int row0 = wm * (WTM * 32) + frow, col0 = wn * (WTN * 32) + 4 * half;
   if constexpr (kMode == kStats) {
+    if (c.logit_splits > 1) {
+      float* z = c.z + split * c.z_plane + static_cast<int64_t>(m0 + row0) * c.piece + n0 + col0;
+#pragma unroll
+      for (int i = 0; i < WTM; ++i)
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(z + i * 32 * c.piece + j * 32 + 8 * q) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      return;
+    }
     float2* shared = reinterpret_cast<float2*>(smem);  // [WN][BM]
     const int count = c.vocab - n0 < BN ? static_cast<int>(c.vocab - n0) : BN;
     __syncthreads();
@@ -670,6 +746,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     if constexpr (kMode == kStats || kMode == kGrad) {
       mt = row_tiles;
       nt = c.piece_tiles;
+      if constexpr (kMode == kStats) splits = c.logit_splits;
     } else if constexpr (kMode == kHidden) {
       mt = row_tiles;
       nt = dim_tiles;
@@ -690,12 +767,18 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   int lda, ldb, k_from = 0, steps;  // steps: stages along the summed index
   int64_t left_b;  // values of B behind gB
   if constexpr (kMode == kStats || kMode == kGrad) {
-    gA = static_cast<const unsigned short*>(c.hidden_pad) + static_cast<int64_t>(m0) * c.dim_pad;
-    lda = static_cast<int>(c.dim_pad);
-    gB = W + static_cast<int64_t>(n0) * c.weight_stride;
-    ldb = static_cast<int>(c.weight_stride);
-    left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use;
     steps = static_cast<int>(c.dim_pad / C::BK);
+    if (kMode == kStats && c.logit_splits > 1) {
+      const int per = __builtin_amdgcn_readfirstlane((steps + c.logit_splits - 1) / c.logit_splits);
+      k_from = split * per;
+      steps = steps - k_from < per ? steps - k_from : per;
+      steps = steps < 0 ? 0 : steps;
+    }
+    gA = static_cast<const unsigned short*>(c.hidden_pad) + static_cast<int64_t>(m0) * c.dim_pad + k_from * C::BK;
+    lda = static_cast<int>(c.dim_pad);
+    gB = W + static_cast<int64_t>(n0) * c.weight_stride + k_from * C::BK;
+    ldb = static_cast<int>(c.weight_stride);
+    left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use - k_from * C::BK;
   } else if constexpr (kMode == kHidden) {
     // stages that hold an entry of the vocabulary: none begins behind W's end
     const int64_t entries = w_left < c.piece_tiles * 256 ? w_left : c.piece_tiles * 256;
@@ -778,7 +861,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
       const int64_t left = left_b - step * C::BK;
       const int64_t most = static_cast<int64_t>(C::BN - 1) * ldb + C::BK;
       const int64_t values = left < most ? left : most;
-      const int off = step * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
+      const int off = (k_from + step) * C::BK + ch * 8 < c.dim_use ? (r * ldb + ch * 8) * 2 : 0x7ffffff0;
       dma16<C::kBT, 4>(base + step * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
     }
   };
@@ -890,7 +973,7 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
 // through registers into LDS rows of one index each, whatever the operand's order.  Few rows are
 // bound by memory and its latency: 32- and 64-row tiles, with longer stages.
 template <int BM, int kMode>
-__global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
+__global__ __launch_bounds__(256, BM == 128 ? 1 : 3) void head_gemm32_kernel(HeadCall c) {  // (waves per SIMD)
   constexpr int B = 128, BK = BM == 128 ? 16 : 32, LA = BM + (kMode == kWeight ? 4 : 2),
                 LB = B + (kMode == kHidden || kMode == kWeight ? 4 : 2);  // vectors along k are stored a value at a time
   constexpr int WM = BM == 32 ? 1 : 2, WN = 4 / WM, WTM = BM / (WM * 32), WTN = B / (WN * 32);
@@ -908,6 +991,7 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     if constexpr (kMode == kStats || kMode == kGrad) {
       mt = row_tiles;
       nt = c.piece_tiles;
+      if constexpr (kMode == kStats) splits = c.logit_splits;
     } else if constexpr (kMode == kHidden) {
       mt = row_tiles;
       nt = dim_tiles;
@@ -932,7 +1016,10 @@ __global__ __launch_bounds__(256) void head_gemm32_kernel(HeadCall c) {
     gB = W + static_cast<int64_t>(n0) * c.weight_stride;
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - n0 - 1) * c.weight_stride + c.dim_use;
-    k1 = static_cast<int>((c.dim + BK - 1) / BK * BK);  // no stage begins behind the row's end
+    // no stage begins behind the row's end
+    const int all = static_cast<int>((c.dim + BK - 1) / BK), per = kMode == kStats ? (all + c.logit_splits - 1) / c.logit_splits : all;
+    k0 = split * per * BK;
+    k1 = min(all, (split + 1) * per) * BK;
   } else if constexpr (kMode == kHidden) {
     const int64_t entries = w_left < c.piece_tiles * B ? w_left : c.piece_tiles * B;
     const int all = static_cast<int>((entries + BK - 1) / BK), per = (all + c.splits - 1) / c.splits;
@@ -1057,18 +1144,23 @@ int64_t head_row_tile(int type, int64_t n) {
 }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align_up(int64_t x, int64_t q) { return ceil_div(x, q) * q; }
-// Rounds of the chip (256 compute units, a block each) that a product's tiles take, in units of a
-// 256-row tile: smaller ones take 0.62 and 0.45 of it instead of a half and a quarter.
-double head_rounds(int64_t tiles, int64_t rows) {
-  return static_cast<double>(ceil_div(tiles, 256)) * (rows == 256 ? 1.0 : rows == 128 ? 0.62 : 0.45);
+// Seconds of a product of so many tiles and summed indices: rounds of the chip (256 compute units, a
+// block each) by what a tile takes for an index on the full chip.  A tile of half the rows takes more
+// than half of it (with few tiles in the chip 59 and 34 % instead of 62 and 45, fewer bytes in all).
+double head_time(int type, bool split, int64_t tiles, int64_t rows, int64_t length) {
+  double tile;
+  if (type == kActF32 && !split) tile = rows == 128 ? 80e-9 : rows == 64 ? 46e-9 : 25e-9;
+  else tile = (rows == 256 ? 27.9e-9 : rows == 128 ? 17.3e-9 : 12.5e-9) * (split ? 6 : 1);
+  return static_cast<double>(ceil_div(tiles, 256)) * length * tile;
 }
 // A tile's rows, in a product of `cols` tiles beside each other.
 int64_t head_best_rows(int type, int64_t n, int64_t cols) {
   const int64_t most = head_row_tile(type, n);
-  if (type == kActF32 && !head_split(type, n)) return most;
+  const bool split = head_split(type, n);
+  if (type == kActF32 && !split) return most;
   int64_t best = most;
   for (int64_t rows = most / 2; rows >= 64; rows /= 2)
-    if (head_rounds(ceil_div(n, rows) * cols, rows) < head_rounds(ceil_div(n, best) * cols, best)) best = rows;
+    if (head_time(type, split, ceil_div(n, rows) * cols, rows, 1) < head_time(type, split, ceil_div(n, best) * cols, best, 1)) best = rows;
   return best;
 }
 
@@ -1117,13 +1209,16 @@ hipError_t gather(const HeadCall& c, hipStream_t s) {
 template <int T, bool kSplit>
 hipError_t forward(const HeadCall& call, hipStream_t s) {
   HeadCall c = call;
-  c.row_weight = nullptr;
-  c.lse_in = nullptr;
+  if (!c.once) c.row_weight = nullptr;
   c.piece_start = 0;
   c.piece_tiles = static_cast<int>(ceil_div(c.vocab, head_tile_size(T, kSplit)));
   c.tiles = c.piece_tiles;
   if (const hipError_t e = gather<T, kSplit>(c, s)) return e;
-  if (const hipError_t e = launch_head_rows<T, kSplit, kStats>(c, c.stats_rows, c.piece_tiles, s)) return e;
+  if (const hipError_t e = launch_head_rows<T, kSplit, kStats>(c, c.stats_rows, c.piece_tiles * c.logit_splits, s)) return e;
+  if (c.logit_splits > 1) {
+    hipLaunchKernelGGL(head_stats_kernel, dim3(static_cast<unsigned>(c.n)), dim3(256), 0, s, c);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.n, 4))), dim3(256), 0, s, c);
   return hipGetLastError();
 }
@@ -1134,12 +1229,15 @@ hipError_t backward(const HeadCall& call, hipStream_t s) {
   c.loss = nullptr;
   c.lse_out = nullptr;
   const int64_t tile = head_tile_size(T, kSplit), dim_tiles = ceil_div(c.dim, tile);
-  if (const hipError_t e = gather<T, kSplit>(c, s)) return e;
+  if (!c.once)
+    if (const hipError_t e = gather<T, kSplit>(c, s)) return e;
   for (int64_t v = 0; v < c.vocab; v += c.piece) {
     c.piece_start = v;
     c.first = v == 0;
     const int64_t here = c.vocab - v < c.piece ? c.vocab - v : c.piece;
     c.piece_tiles = static_cast<int>(ceil_div(here, tile));
+    if (c.kept && c.lse_in)  // the backward pass alone
+      if (const hipError_t e = launch_head_rows<T, kSplit, kStats>(c, c.stats_rows, c.piece_tiles * c.logit_splits, s)) return e;
     if (c.kept) {
       const dim3 grid(static_cast<unsigned>(ceil_div(c.piece, 2048)), static_cast<unsigned>(align_up(c.n, c.row_tile)));
       hipLaunchKernelGGL((head_convert_kernel<T, kSplit>), grid, dim3(256), 0, s, c);
@@ -1184,7 +1282,7 @@ bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t strid
 
 int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p) {
   const int64_t tile = head_tile_size(type, p.split), dim_tiles = ceil_div(dim, tile);
-  int64_t tiles = ceil_div(n, p.stats_rows) * ceil_div(vocab, tile);
+  int64_t tiles = ceil_div(n, p.stats_rows) * ceil_div(vocab, tile) * p.logit_splits;
   const int64_t others[] = {ceil_div(n, p.hidden_rows) * dim_tiles * p.splits, ceil_div(n, p.grad_rows) * (p.piece / tile),
                             p.piece / tile * dim_tiles * p.weight_splits};
   for (const int64_t t : others) tiles = t > tiles ? t : tiles;
@@ -1220,34 +1318,55 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   p.hidden = take(p.rows_pad * p.dim_pad * size + tile * 4);
   p.weight_pad = copied || p.split ? take(vocab * p.dim_pad * size) : 0;
   // the statistics of the forward pass lie where the backward pass has g
-  const int64_t tiles = ceil_div(vocab, tile);
+  const int64_t tiles = ceil_div(vocab, tile), dim_tiles = ceil_div(dim, tile);
   int64_t piece = kHeadPieceBytes / (p.rows_pad * size) / tile;
   piece = piece < 1 ? 1 : piece;
   p.piece = ceil_div(tiles, ceil_div(tiles, piece)) * tile;
-  // kept logits: one product of the logits against 8 bytes of traffic each (1.2 PFLOP/s, 6 or 16
-  // times less in fp32, and 4.8 TB/s); in fp32 g takes their place
-  const int64_t logits = p.rows_pad * p.piece * 4, cost = dim * (p.split ? 6 : type == kActF32 ? 16 : 1);
-  p.kept = gradients && p.piece >= vocab && logits <= kHeadPieceBytes && cost >= 1024 && p.rows_pad <= 65535;
-  const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.piece * size : 0;
-  p.partial = take(stats > g ? stats : g);
-  p.logits = p.kept ? take(logits) : 0;
-  p.sum_stride = align_up(dim, 4);
+  const int64_t logits = p.rows_pad * p.piece * 4;
+  const bool fits = p.piece >= vocab && logits <= kHeadPieceBytes && p.rows_pad <= 65535;
   p.stats_rows = head_best_rows(type, n, tiles);
   p.grad_rows = head_best_rows(type, n, p.piece / tile);
   p.hidden_rows = head_row_tile(type, n);
-  p.splits = p.weight_splits = 1;
+  p.logit_splits = p.splits = p.weight_splits = 1;
+  // kept logits: the logits' second product, and where rows are numbered once two launches of 10 us,
+  // against 8 bytes of traffic each, 4.8 TB/s (fp32: g takes their place).  Rows that fill one tile at
+  // most are numbered once anyhow: leaving some out would save nothing.
+  const int64_t padded = align_up(n, head_row_tile(type, n));
+  p.kept = gradients && fits &&
+           8.0 * padded * p.piece / 4.8e12 < head_time(type, p.split, ceil_div(n, p.grad_rows) * (p.piece / tile), p.grad_rows, p.dim_pad) +
+                                          (n > head_row_tile(type, n) ? 10e-6 : 0.0);
+  // Products of few tiles: their sums are split over blocks where the fuller chip saves more than the
+  // sums' traffic (8 bytes a value, 4.8 TB/s) and another launch, if any, cost.
+  const int64_t most = head_row_tile(type, n), least = type == kActF32 && !p.split ? most : 64;
+  // the logits, over the hidden size (by 256 at least): they are kept then
+  if (fits) {
+    // (a tenth less does not count: 192 rows of fp32, 30758 x 1896, took 730 us in two parts, 687 whole;
+    // the backward pass alone has a launch more: 2 rows of bf16, 9756 x 1046, 68 us in parts, 63 whole.
+    // 89 rows of fp32, 1980 x 2421: 95 us in parts, 270 whole)
+    double best = 0.8 * head_time(type, p.split, ceil_div(n, p.stats_rows) * tiles, p.stats_rows, p.dim_pad);
+    for (int64_t rows = most; rows >= least; rows /= 2)
+      for (int64_t splits = 2; splits <= 32 && splits * 256 <= dim && splits * logits <= kHeadPieceBytes; ++splits) {
+        const double time = head_time(type, p.split, ceil_div(n, rows) * tiles * splits, rows, ceil_div(p.dim_pad, splits)) +
+                            8.0 * splits * padded * p.piece / 4.8e12 + (gradients ? 8e-6 : 2e-6);
+        if (time < best) {
+          best = time;
+          p.stats_rows = rows;
+          p.logit_splits = static_cast<int>(splits);
+        }
+      }
+    if (p.logit_splits > 1) p.kept = gradients;
+  }
+  const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.piece * size : 0;
+  p.partial = take(stats > g ? stats : g);
+  p.logits = p.kept || p.logit_splits > 1 ? take(p.logit_splits * logits) : 0;
+  p.sum_stride = align_up(dim, 4);
   if (gradients) {
-    // Both gradients may have few tiles: the sums over the piece, and over the rows, are split (by 256 vocabulary entries and 128 rows at least) where the fuller chip
-    // (4.7 TFLOP/s on each of 256 compute units) saves more than the sums' traffic (8 bytes each way a
-    // value, 4.8 TB/s) and a launch, 4 us, cost.
-    const int64_t dim_tiles = ceil_div(dim, tile), products = p.split ? 6 : type == kActF32 ? 16 : 1;
-    const double unit = 2.0 * 256 * tile * products / 4.7e12;  // seconds of a 256-row tile per summed index
+    // dh, over the piece (by 256 vocabulary entries at least)
     double best = 0.0;
-    const int64_t most = head_row_tile(type, n), least = type == kActF32 && !p.split ? most : 64;
     for (int64_t rows = most; rows >= least; rows /= 2) {
       const int64_t blocks = ceil_div(n, rows) * dim_tiles;
       for (int64_t splits = 1; splits <= 64 && (splits == 1 || splits * 256 <= p.piece); ++splits) {
-        const double time = unit * p.piece * head_rounds(blocks * splits, rows) / splits + 8.0 * splits * n * dim / 4.8e12;
+        const double time = head_time(type, p.split, blocks * splits, rows, ceil_div(p.piece, splits)) + 8.0 * splits * n * dim / 4.8e12;
         if (best == 0.0 || time < best) {
           best = time;
           p.hidden_rows = rows;
@@ -1256,11 +1375,12 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
       }
     }
     p.sum = take(p.splits * p.rows_pad * p.sum_stride * 4);
+    // dW, over the rows (by 128 at least)
     if (type != kActF32 || p.split) {
       const int64_t blocks = p.piece / tile * dim_tiles;
-      best = unit * n * head_rounds(blocks, 256);
+      best = head_time(type, p.split, blocks, 256, n);
       for (int64_t splits = 2; splits <= 64 && splits * 128 <= n; ++splits) {
-        const double time = unit * n * head_rounds(blocks * splits, 256) / splits + 8.0 * splits * p.piece * dim / 4.8e12 + 4e-6;
+        const double time = head_time(type, p.split, blocks * splits, 256, ceil_div(n, splits)) + 8.0 * splits * p.piece * dim / 4.8e12 + 4e-6;
         if (time < best) {
           best = time;
           p.weight_splits = static_cast<int>(splits);
@@ -1293,7 +1413,11 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.sums = work == kHeadBoth ? reinterpret_cast<float*>(ws + p.sums) : nullptr;
   c.hidden_pad = ws + p.hidden;
   c.partial = reinterpret_cast<float2*>(ws + p.partial);
-  c.kept = p.kept && work == kHeadBoth;
+  c.logit_splits = p.logit_splits;
+  c.z_plane = p.rows_pad * p.piece;
+  c.kept = p.kept && (work == kHeadBoth || p.logit_splits > 1);
+  c.once = work == kHeadBoth && (p.kept || c.n <= head_row_tile(c.type, c.n));
+  c.planes = p.split;
   c.z = reinterpret_cast<float*>(ws + p.logits);
   c.g = c.kept && c.type == kActF32 && !p.split ? ws + p.logits : ws + p.partial;
   c.sum = reinterpret_cast<float*>(ws + p.sum);

@@ -592,9 +592,9 @@ struct HeadPlan {
   int64_t head, place, row_of, label, target, weight, top, factor, tops, sums, hidden, weight_pad, partial, logits, sum, weight_sum, bytes;
   int64_t rows_pad, dim_pad, sum_stride, piece;
   int64_t stats_rows, grad_rows, hidden_rows;  // of the products' tiles
-  int splits, weight_splits;  // blocks that share a sum
+  int logit_splits, splits, weight_splits;  // blocks that share a sum: of the logits, dh and dW
   bool split;  // fp32 values as three bf16 planes
-  bool kept;   // both directions in one call keep the logits
+  bool kept;   // both directions in one call keep the logits (and the backward pass alone, where they are split)
 };
 // Whether the weight's rows must be copied to be aligned to 16 bytes.
 bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride);
@@ -635,14 +635,15 @@ struct HeadCall {
   const void* weight_use;
   float2* partial;  // per live row and tile
   void* g;          // rows_pad x piece
-  float* z;         // kept logits, rows_pad x piece
+  float* z;         // kept logits, logit_splits x rows_pad x piece
   float* sum;       // splits x rows_pad x sum_stride
   float* weight_sum;  // weight_splits x piece x sum_stride
   int64_t stats_rows, grad_rows, hidden_rows;
   int64_t rows_pad, dim_pad, dim_use, weight_stride, sum_stride, piece, tiles, piece_start;
-  int64_t hidden_plane, weight_plane, g_plane;  // values from one plane to the next
-  int piece_tiles, splits, weight_splits, row_tile;  // row_tile: the gathered rows are padded to it
-  bool first, kept, weight_lines;  // weight_lines: dW's rows start at multiples of 16 bytes
+  int64_t hidden_plane, weight_plane, g_plane, z_plane;  // values from one plane to the next
+  int piece_tiles, logit_splits, splits, weight_splits, row_tile;  // row_tile: the gathered rows are padded to it
+  bool first, kept, once;    // once: both directions number the rows, and gather them, once
+  bool planes, weight_lines;  // weight_lines: dW's rows start at multiples of 16 bytes
 };
 hipError_t launch_head_clear(const HeadCall& c, hipStream_t s);  // dweight = 0
 enum HeadWork { kHeadForward = 0, kHeadBackward = 1, kHeadBoth = 2 };

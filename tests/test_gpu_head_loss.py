@@ -27,7 +27,8 @@ E = 2.0 ** -24
 TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
 HALF = {torch.float32: 0.0, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
 SIZES = [(1, 1, 1), (1, 500, 64), (3, 257, 33), (5, 1000, 100), (20, 777, 130), (64, 300, 72), (65, 511, 40), (128, 640, 256), (130, 777, 128),
-         (257, 1025, 264), (300, 2500, 520), (511, 5000, 1001), (700, 3001, 768), (3001, 610, 200), (300, 900, 1100)]
+         (257, 1025, 264), (300, 2500, 520), (511, 5000, 1001), (700, 3001, 768), (3001, 610, 200), (300, 900, 1100),
+         (40, 700, 1300), (7, 2000, 2049), (128, 1500, 900), (2, 300, 4104)]
 
 
 def _strided(x, extra, offset):
@@ -206,7 +207,11 @@ def test_rows_without_a_target(dtype):
     loss, dh, dw = ma.head_loss_grad(bad, w, l2, rw2)
     assert torch.equal(loss[on], want[0]) and (loss[[0, 7]] == 0).all() and torch.isnan(loss[64])
     assert torch.equal(dh[on], want[1]) and (dh[~on] == 0).all()
-    assert torch.equal(dw, want[2])
+    # rows of weight 0 may keep their places in the sum over rows, as zeros: the matrix instructions
+    # then group the others' products differently, and both sums are within the bound of the exact one
+    _, _, _, _, _, exact, _, bound, _ = _reference(h[on], w, labels[on], rw[on])
+    _near(dw, exact, bound)
+    _near(want[2], exact, bound)
     none = torch.full_like(labels, -100)
     loss, dh, dw = ma.head_loss_grad(bad, w, none, rw)
     assert not loss.any() and not dh.any() and not dw.any()
