@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(HeadCall c) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t at = blockIdx.x;
   if (at >= c.head->live) return;
-  const float* z = c.z + at * c.piece;
+  const float* z = c.z + at * c.g_stride;
   const int64_t label = c.label[at];
   float top = -INFINITY, sum = 0.0f;
   for (int64_t col = threadIdx.x * 4; col < c.vocab; col += 1024) {
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(256) void head_convert_kernel(HeadCall c) {
   const bool on = at < live;
   const float top = on ? c.top[at] : 0.0f, factor = on ? c.factor[at] : 0.0f, weight = on ? c.weight[at] : 0.0f;
   const int64_t label = on ? c.label[at] : -1;
-  const float* in = c.z + at * c.piece + col;
+  const float* in = c.z + at * c.g_stride + col;
   float g[8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(256) void head_convert_kernel(HeadCall c) {
       if (v >= c.vocab || weight == 0.0f) g[4 * h + e] = 0.0f;
     }
   }
-  const int64_t out = at * c.piece + col;
+  const int64_t out = at * c.g_stride + col;
   if constexpr (T == kActF32 && !kPlanes) {
     // in place
     float* p = static_cast<float*>(c.g) + out;
@@ -460,14 +460,14 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
   const int row0 = wm * (WTM * 32) + frow, col0 = wn * (WTN * 32) + 4 * half;
   if constexpr (kMode == kStats) {
     if (c.logit_splits > 1) {
-      float* z = c.z + split * c.z_plane + static_cast<int64_t>(m0 + row0) * c.piece + n0 + col0;
+      float* z = c.z + split * c.z_plane + static_cast<int64_t>(m0 + row0) * c.g_stride + n0 + col0;
 #pragma unroll
       for (int i = 0; i < WTM; ++i)
 #pragma unroll
         for (int j = 0; j < WTN; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4*>(z + i * 32 * c.piece + j * 32 + 8 * q) =
+            *reinterpret_cast<f32x4*>(z + i * 32 * c.g_stride + j * 32 + 8 * q) =
                 f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       return;
     }
@@ -487,7 +487,7 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
             if (j * 32 + 4 * half + 8 * (k >> 2) + (k & 3) == label) c.target[m0 + row] = acc[i][j][k];
       }
       if (c.kept) {
-        float* z = c.z + static_cast<int64_t>(m0 + row) * c.piece + n0 + col0;
+        float* z = c.z + static_cast<int64_t>(m0 + row) * c.g_stride + n0 + col0;
 #pragma unroll
         for (int j = 0; j < WTN; ++j)
 #pragma unroll
@@ -571,7 +571,7 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
             if (col0 + j * 32 + 8 * (k >> 2) + (k & 3) >= count) g[j][k] = 0.0f;
       }
       if constexpr (!kStaged) {
-        float* out = static_cast<float*>(c.g) + static_cast<int64_t>(m0 + row) * c.piece + n0 + col0;
+        float* out = static_cast<float*>(c.g) + static_cast<int64_t>(m0 + row) * c.g_stride + n0 + col0;
 #pragma unroll
         for (int j = 0; j < WTN; ++j)
 #pragma unroll
@@ -609,7 +609,7 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
           for (int it = 0; it < 4; ++it) {
             const int r = it * 8 + (lane >> 3), ch = lane & 7;
             const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-            *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(m0 + wm * (WTM * 32) + i * 32 + r) * c.piece + ch * 8) = x;
+            *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(m0 + wm * (WTM * 32) + i * 32 + r) * c.g_stride + ch * 8) = x;
           }
         }
       }
@@ -787,8 +787,8 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     k_from = split * per;
     steps = all - k_from < per ? all - k_from : per;
     steps = steps < 0 ? 0 : steps;
-    gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(m0) * c.piece + k_from * C::BK;
-    lda = static_cast<int>(c.piece);
+    gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(m0) * c.g_stride + k_from * C::BK;
+    lda = static_cast<int>(c.g_stride);
     gB = W + static_cast<int64_t>(k_from) * C::BK * c.weight_stride + n0;
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - static_cast<int64_t>(k_from) * C::BK - 1) * c.weight_stride + c.dim_use - n0;
@@ -797,8 +797,8 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
     k_from = split * per;
     steps = all - k_from < per ? all - k_from : per;
     steps = steps < 0 ? 0 : steps;
-    gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(k_from) * C::BK * c.piece + m0;
-    lda = static_cast<int>(c.piece);
+    gA = static_cast<const unsigned short*>(c.g) + static_cast<int64_t>(k_from) * C::BK * c.g_stride + m0;
+    lda = static_cast<int>(c.g_stride);
     gB = static_cast<const unsigned short*>(c.hidden_pad) + static_cast<int64_t>(k_from) * C::BK * c.dim_pad + n0;
     ldb = static_cast<int>(c.dim_pad);
     left_b = static_cast<int64_t>(steps) * C::BK * c.dim_pad - n0;
@@ -1025,15 +1025,15 @@ __global__ __launch_bounds__(256, BM == 128 ? 1 : 3) void head_gemm32_kernel(Hea
     const int all = static_cast<int>((entries + BK - 1) / BK), per = (all + c.splits - 1) / c.splits;
     k0 = split * per * BK;
     k1 = min(all, (split + 1) * per) * BK;
-    gA = static_cast<const float*>(c.g) + static_cast<int64_t>(m0) * c.piece;
-    lda = static_cast<int>(c.piece);
+    gA = static_cast<const float*>(c.g) + static_cast<int64_t>(m0) * c.g_stride;
+    lda = static_cast<int>(c.g_stride);
     gB = W + n0;
     ldb = static_cast<int>(c.weight_stride);
     left_b = (w_left - 1) * c.weight_stride + c.dim_use - n0;
   } else {
     k1 = (live + BK - 1) / BK * BK;
     gA = static_cast<const float*>(c.g) + m0;
-    lda = static_cast<int>(c.piece);
+    lda = static_cast<int>(c.g_stride);
     gB = static_cast<const float*>(c.hidden_pad) + n0;
     ldb = static_cast<int>(c.dim_pad);
     left_b = static_cast<int64_t>(k1) * c.dim_pad - n0;
@@ -1322,8 +1322,11 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   int64_t piece = kHeadPieceBytes / (p.rows_pad * size) / tile;
   piece = piece < 1 ? 1 : piece;
   p.piece = ceil_div(tiles, ceil_div(tiles, piece)) * tile;
-  const int64_t logits = p.rows_pad * p.piece * 4;
-  const bool fits = p.piece >= vocab && logits <= kHeadPieceBytes && p.rows_pad <= 65535;
+  // rows a power of two apart would meet in the same memory channels (the gradients of 2048 rows, 65536 x
+  // 1280: 1042 us, 1020 with 64 values more)
+  p.g_stride = p.piece + 64;
+  const int64_t logits = p.rows_pad * p.g_stride * 4;
+  const bool fits = p.piece >= vocab && p.rows_pad * p.piece * 4 <= kHeadPieceBytes && p.rows_pad <= 65535;
   p.stats_rows = head_best_rows(type, n, tiles);
   p.grad_rows = head_best_rows(type, n, p.piece / tile);
   p.hidden_rows = head_row_tile(type, n);
@@ -1345,7 +1348,7 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
     // 89 rows of fp32, 1980 x 2421: 95 us in parts, 270 whole)
     double best = 0.8 * head_time(type, p.split, ceil_div(n, p.stats_rows) * tiles, p.stats_rows, p.dim_pad);
     for (int64_t rows = most; rows >= least; rows /= 2)
-      for (int64_t splits = 2; splits <= 32 && splits * 256 <= dim && splits * logits <= kHeadPieceBytes; ++splits) {
+      for (int64_t splits = 2; splits <= 32 && splits * 256 <= dim && splits * p.rows_pad * p.piece * 4 <= kHeadPieceBytes; ++splits) {
         const double time = head_time(type, p.split, ceil_div(n, rows) * tiles * splits, rows, ceil_div(p.dim_pad, splits)) +
                             8.0 * splits * padded * p.piece / 4.8e12 + (gradients ? 8e-6 : 2e-6);
         if (time < best) {
@@ -1356,7 +1359,7 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
       }
     if (p.logit_splits > 1) p.kept = gradients;
   }
-  const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.piece * size : 0;
+  const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.g_stride * size : 0;
   p.partial = take(stats > g ? stats : g);
   p.logits = p.kept || p.logit_splits > 1 ? take(p.logit_splits * logits) : 0;
   p.sum_stride = align_up(dim, 4);
@@ -1414,7 +1417,7 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.hidden_pad = ws + p.hidden;
   c.partial = reinterpret_cast<float2*>(ws + p.partial);
   c.logit_splits = p.logit_splits;
-  c.z_plane = p.rows_pad * p.piece;
+  c.z_plane = p.rows_pad * p.g_stride;
   c.kept = p.kept && (work == kHeadBoth || p.logit_splits > 1);
   c.once = work == kHeadBoth && (p.kept || c.n <= head_row_tile(c.type, c.n));
   c.planes = p.split;
@@ -1439,7 +1442,8 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.dim_use = c.dim;
   c.hidden_plane = p.rows_pad * p.dim_pad;
   c.weight_plane = c.vocab * p.dim_pad;
-  c.g_plane = p.rows_pad * p.piece;
+  c.g_plane = p.rows_pad * p.g_stride;
+  c.g_stride = p.g_stride;
   c.weight_pad = nullptr;
   if (p.weight_pad) {
     c.weight_pad = ws + p.weight_pad;

@@ -590,7 +590,7 @@ struct HeadInfo {
 // Workspace: byte offsets, and what its sizes settle.
 struct HeadPlan {
   int64_t head, place, row_of, label, target, weight, top, factor, tops, sums, hidden, weight_pad, partial, logits, sum, weight_sum, bytes;
-  int64_t rows_pad, dim_pad, sum_stride, piece;
+  int64_t rows_pad, dim_pad, sum_stride, piece, g_stride;
   int64_t stats_rows, grad_rows, hidden_rows;  // of the products' tiles
   int logit_splits, splits, weight_splits;  // blocks that share a sum: of the logits, dh and dW
   bool split;  // fp32 values as three bf16 planes
@@ -634,12 +634,13 @@ struct HeadCall {
   void* weight_pad;
   const void* weight_use;
   float2* partial;  // per live row and tile
-  void* g;          // rows_pad x piece
-  float* z;         // kept logits, logit_splits x rows_pad x piece
+  void* g;          // rows_pad x piece values, g_stride apart
+  float* z;         // kept logits, logit_splits times as many
   float* sum;       // splits x rows_pad x sum_stride
   float* weight_sum;  // weight_splits x piece x sum_stride
   int64_t stats_rows, grad_rows, hidden_rows;
   int64_t rows_pad, dim_pad, dim_use, weight_stride, sum_stride, piece, tiles, piece_start;
+  int64_t g_stride;  // from one row of g or of the logits to the next
   int64_t hidden_plane, weight_plane, g_plane, z_plane;  // values from one plane to the next
   int piece_tiles, logit_splits, splits, weight_splits, row_tile;  // row_tile: the gathered rows are padded to it
   bool first, kept, once;    // once: both directions number the rows, and gather them, once
