@@ -580,38 +580,40 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
       } else {
         // a wave stages its 32 rows of 64 columns, chunks of 16 bytes XOR-ed with the row, so that
         // whole 128-byte lines leave
-        static_assert(WTN == 2, "eight chunks a row");
+        static_assert(WTN % 2 == 0, "eight chunks a row");
         char* stage = smem + wave * (32 * 128);
 #pragma unroll
-        for (int plane = 0; plane < (kPlanes ? 3 : 1); ++plane) {
+        for (int plane = 0; plane < (kPlanes ? 3 : 1); ++plane)
 #pragma unroll
-          for (int j = 0; j < WTN; ++j)
+          for (int part = 0; part < WTN / 2; ++part) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              unsigned short x[4];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float& v = g[j][4 * q + e];
-                if constexpr (kPlanes) {
-                  x[e] = f2bf(v);
-                  v -= bf2f(x[e]);
-                } else {
-                  x[e] = Act<T>::down(v);
+              for (int q = 0; q < 4; ++q) {
+                unsigned short x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float& v = g[2 * part + j][4 * q + e];
+                  if constexpr (kPlanes) {
+                    x[e] = f2bf(v);
+                    v -= bf2f(x[e]);
+                  } else {
+                    x[e] = Act<T>::down(v);
+                  }
                 }
+                u32x2 w;
+                w[0] = x[0] | (static_cast<unsigned>(x[1]) << 16);
+                w[1] = x[2] | (static_cast<unsigned>(x[3]) << 16);
+                *reinterpret_cast<u32x2*>(stage + frow * 128 + (((j * 4 + q) ^ (frow & 7)) << 4) + half * 8) = w;
               }
-              u32x2 w;
-              w[0] = x[0] | (static_cast<unsigned>(x[1]) << 16);
-              w[1] = x[2] | (static_cast<unsigned>(x[3]) << 16);
-              *reinterpret_cast<u32x2*>(stage + frow * 128 + (((j * 4 + q) ^ (frow & 7)) << 4) + half * 8) = w;
-            }
-          unsigned short* out = static_cast<unsigned short*>(c.g) + plane * c.g_plane + n0 + wn * 64;
+            unsigned short* out = static_cast<unsigned short*>(c.g) + plane * c.g_plane + n0 + wn * (WTN * 32) + part * 64;
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int r = it * 8 + (lane >> 3), ch = lane & 7;
-            const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-            *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(m0 + wm * (WTM * 32) + i * 32 + r) * c.g_stride + ch * 8) = x;
+            for (int it = 0; it < 4; ++it) {
+              const int r = it * 8 + (lane >> 3), ch = lane & 7;
+              const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+              *reinterpret_cast<u32x4*>(out + static_cast<int64_t>(m0 + wm * (WTM * 32) + i * 32 + r) * c.g_stride + ch * 8) = x;
+            }
           }
-        }
       }
     }
   } else if constexpr (kMode == kHidden) {
@@ -649,27 +651,29 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
       char* stage = smem + wave * (32 * 128);
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < WTM; ++i) {
+      for (int i = 0; i < WTM; ++i)
 #pragma unroll
-        for (int j = 0; j < WTN; ++j)
+        for (int part = 0; part < WTN / 2; ++part) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            u32x2 w;
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              w[e] = Act<T>::down(acc[i][j][4 * q + 2 * e] * unscale) |
-                     (static_cast<unsigned>(Act<T>::down(acc[i][j][4 * q + 2 * e + 1] * unscale)) << 16);
-            *reinterpret_cast<u32x2*>(stage + frow * 128 + (((j * 4 + q) ^ (frow & 7)) << 4) + half * 8) = w;
+            for (int q = 0; q < 4; ++q) {
+              u32x2 w;
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                w[e] = Act<T>::down(acc[i][2 * part + j][4 * q + 2 * e] * unscale) |
+                       (static_cast<unsigned>(Act<T>::down(acc[i][2 * part + j][4 * q + 2 * e + 1] * unscale)) << 16);
+              *reinterpret_cast<u32x2*>(stage + frow * 128 + (((j * 4 + q) ^ (frow & 7)) << 4) + half * 8) = w;
+            }
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int r = it * 8 + (lane >> 3), ch = lane & 7, col = n0 + wn * (WTN * 32) + part * 64 + ch * 8;
+            const int64_t v = c.piece_start + m0 + wm * (WTM * 32) + i * 32 + r;
+            const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+            if (v < c.vocab && col < c.dim)
+              *reinterpret_cast<u32x4*>(static_cast<S*>(c.dweight) + v * c.dweight_stride + col) = x;
           }
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int r = it * 8 + (lane >> 3), ch = lane & 7, col = n0 + wn * 64 + ch * 8;
-          const int64_t v = c.piece_start + m0 + wm * (WTM * 32) + i * 32 + r;
-          const u32x4 x = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-          if (v < c.vocab && col < c.dim)
-            *reinterpret_cast<u32x4*>(static_cast<S*>(c.dweight) + v * c.dweight_stride + col) = x;
         }
-      }
     }
   } else {
     const float unscale = c.head->unscale;
@@ -715,7 +719,7 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
 template <int BM_, int kMode>
 struct HeadCfg {
   static constexpr int BM = BM_, BN = 256, BK = 64, WM = 2, WN = 4, kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int SA = BM == 64 ? 4 : 3, SB = BM == 256 ? 2 : SA, LA = SA - 1, LB = SB - 1;
+  static constexpr int SA = BM == 64 ? 4 : 3, SB = BM == 256 ? 2 : SA, LA = SA - 1;
   static constexpr int WTM = BM / (WM * 32), WTN = BN / (WN * 32);
   static constexpr bool kAT = kMode == kWeight, kBT = kMode == kHidden || kMode == kWeight;
   static constexpr int kDmaA = BM * BK / 512 / kWaves, kDmaB = BN * BK / 512 / kWaves, kDma = kDmaA + kDmaB;
@@ -731,7 +735,7 @@ __device__ __forceinline__ f32x16 head_mfma(bf16x8 a, bf16x8 b, f32x16 c) {
 }
 
 template <int T, int BM, int kMode>
-__global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
+__global__ __launch_bounds__((HeadCfg<BM, kMode>::kThreads)) void head_gemm_kernel(HeadCall c) {
   typedef HeadCfg<BM, kMode> C;
   __shared__ __attribute__((aligned(16))) unsigned short smem[C::kLds / 2];
   const int lane = threadIdx.x & 63;
@@ -865,14 +869,13 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
       dma16<C::kBT, 4>(base + step * C::BK, off, static_cast<unsigned>(values * 2), s + r0 * C::BK);
     }
   };
-  // group v of the loads: A of stage v + LA, B of stage v + LB (the shorter lead first)
-  const auto issue_group = [&](int v) {
+  const auto issue_stage_a = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < C::kDmaB; ++i)
-      if (v + C::LB >= 0 && v + C::LB < nk) issue_b(v + C::LB, i);
+    for (int i = 0; i < C::kDmaA; ++i) issue_a(st, i);
+  };
+  const auto issue_stage_b = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < C::kDmaA; ++i)
-      if (v + C::LA >= 0 && v + C::LA < nk) issue_a(v + C::LA, i);
+    for (int i = 0; i < C::kDmaB; ++i) issue_b(st, i);
   };
   // until stage st has landed: what was issued after it may stay in flight
   const auto wait_stage = [&](int st) {
@@ -925,21 +928,24 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
   if (nk > 0) {
     constexpr int KK = C::BK / 16;
 #pragma unroll
-    for (int v = -C::LA; v < 0; ++v) issue_group(v);
+    for (int st = 0; st < C::SB; ++st) {
+      if (st < C::LA && st < nk) issue_stage_a(st);
+      if (st < nk) issue_stage_b(st);
+    }
     bf16x8 fa[2][C::WTM], fb[2][C::WTN];
-    wait_stage(0);
+    if (nk >= C::SA) wait_vmcnt<(C::LA - 1) * C::kDmaA + (C::SB - 1) * C::kDmaB>();
+    else wait_vmcnt<0>();
     stage_barrier();
     load_frags(0, 0, fa[0], fb[0]);
+    // Stage kt loads A of stage kt + LA between its matrix instructions and, once its own slot of B has
+    // been read by all, B of stage kt + SB between the last of them.  (All loads ahead of the stage's
+    // first matrix instruction keep the matrix cores waiting: 8192 rows, 128000 x 2048, both directions:
+    // 14.0 ms, 13.4 in this order; the gradients of 2048 rows, 65536 x 1280: 1008 us, 932.  B spread over
+    // the stage comes too late: 1017.  Four waves of 128 x 128, whose fragments take two thirds of the
+    // LDS reads, but alone on their SIMD: 15.0 ms and 1048 us.)
     const auto run_stage = [&](int kt, auto steady) {
       constexpr bool kSteady = decltype(steady)::value;
-      if constexpr (kSteady) {
-#pragma unroll
-        for (int i = 0; i < C::kDmaB; ++i) issue_b(kt + C::LB, i);
-#pragma unroll
-        for (int i = 0; i < C::kDmaA; ++i) issue_a(kt + C::LA, i);
-      } else {
-        issue_group(kt);
-      }
+      constexpr int kSlots = (KK - 1) * C::WTM;
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         const int cur = kk & 1;
@@ -957,9 +963,19 @@ __global__ __launch_bounds__(512) void head_gemm_kernel(HeadCall c) {
           load_frags(kt + 1, 0, fa[cur ^ 1], fb[cur ^ 1]);
         }
 #pragma unroll
-        for (int i = 0; i < C::WTM; ++i)
+        for (int i = 0; i < C::WTM; ++i) {
+          if (kk + 1 < KK && (kSteady || kt + C::LA < nk)) {
+            const int slot = kk * C::WTM + i;
+#pragma unroll
+            for (int u = slot * C::kDmaA / kSlots; u < (slot + 1) * C::kDmaA / kSlots; ++u) issue_a(kt + C::LA, u);
+          }
+          if (kk + 1 == KK && (kSteady || kt + C::SB < nk)) {
+#pragma unroll
+            for (int u = i * C::kDmaB / C::WTM; u < (i + 1) * C::kDmaB / C::WTM; ++u) issue_b(kt + C::SB, u);
+          }
 #pragma unroll
           for (int j = 0; j < C::WTN; ++j) acc[i][j] = head_mfma<T>(fb[cur][j], fa[cur][i], acc[i][j]);
+        }
       }
     };
     int kt = 0;
@@ -1173,7 +1189,7 @@ hipError_t launch_head_gemm(const HeadCall& c, int64_t tiles, hipStream_t s) {
   if constexpr (T == kActF32 && !kSplit)
     hipLaunchKernelGGL((head_gemm32_kernel<BM, kMode>), head_grid(tiles), dim3(256), 0, s, c);
   else
-    hipLaunchKernelGGL((head_gemm_kernel<T, BM, kMode>), head_grid(tiles), dim3(512), 0, s, c);
+    hipLaunchKernelGGL((head_gemm_kernel<T, BM, kMode>), head_grid(tiles), dim3(HeadCfg<BM, kMode>::kThreads), 0, s, c);
   return hipGetLastError();
 }
 
