@@ -708,14 +708,18 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
   }
 }
 
-// 16-bit operands (or planes of them): BM x 256 tiles of 8 waves (2 x 4), v_mfma_f32_32x32x16, stages of 64 of the
-// summed index, loaded straight into LDS.  Operands are contiguous along that index (hidden rows and
+// 16-bit operands (or planes of them): BM x 256 tiles of 8 waves (2 x 4), v_mfma_f32_32x32x16, stages
+// of 64 of the summed index, loaded straight into LDS.  Operands are contiguous along that index (hidden rows and
 // W in the logits, g in dh) or across it (W in dh; g and the hidden rows in dW), which the
 // transposing LDS reads take, so nothing is stored twice.  The accumulators hold a row a lane
 // (operands passed to the matrix instruction the other way round), so a row's maximum and sum
 // need two lanes and four waves only.
 // LDS rings: 3 stages of A and 2 of B for 256 rows (160 KiB), 3 and 3 for 128, 4 and 4 for 64, whose
 // short stages are bound by the loads' latency.
+// Measured: the logits of 8192 rows, 128000 x 2048, bf16, 3.3 ms (1.26 PFLOP/s), of 2731 rows, 65536 x
+// 1280, fp16, 450 us (1.0; the epilogue's exponentials are some 60 us of it), of 8 rows, 65536 x 768, 20 us
+// (4.9 TB/s of W); a piece of 32000 entries of the 8192 rows: g 0.89 ms, dh 0.82 ms, dW 0.82 ms.  At
+// 1.7-1.9 GHz the large ones are held by power as much as by the matrix cores.
 template <int BM_, int kMode>
 struct HeadCfg {
   static constexpr int BM = BM_, BN = 256, BK = 64, WM = 2, WN = 4, kWaves = WM * WN, kThreads = 64 * kWaves;

@@ -16,7 +16,10 @@
 //
 // Memory-bound: four streams forward (x, residual in; out, y out), six backward.  Rows are held in
 // registers between their sums, as in layer norm, with the next row's loads issued before this
-// row's sums are joined; scale, gate, w1 and b1 enter as two vectors.
+// row's sums are joined; scale, gate, w1 and b1 enter as two vectors.  Measured, bf16: 32768 rows of
+// 2048 111 us (4.8 TB/s); gradients of 16384 rows of 8192 300 us (5.4 TB/s; 8 of them join the column
+// sums).  Calls of few rows are bound by their latency: gradients of 1023 rows of 1280, fp32, 13 us and 5
+// for the join, 8 rows of 768 forward 5 us.
 #include "ma_act.h"
 #include "ma_internal.h"
 #include "row_norm.h"
