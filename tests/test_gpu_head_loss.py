@@ -447,3 +447,45 @@ def test_training_step_with_an_8_bit_state_and_a_copy():
         opt.step()
         assert torch.equal(copy, head.detach().to(torch.bfloat16))
         opt.zero_grad()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_steps_of_all_three(dtype):
+    """Embedding, a block between two norms with its gate, the head on its copy and the 8-bit step:
+    autograd gives the gradients of the calls one by one, and the step what its call does."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    new = lambda *shape, scale=0.1: torch.nn.Parameter(torch.randn(*shape, generator=g, device=DEV) * scale)  # noqa: E731
+    table, head, post, gate, gain = new(300, 72), new(300, 72), new(72, scale=1), new(72, scale=1), new(72, scale=1)
+    params = [table, head, post, gate, gain]
+    copy = head.detach().to(dtype)
+    opt = ma.MuonAdamW([{"kind": "adamw", "params": params, "lr": 1e-2, "state_bits": 8, "seed": 3,
+                         "copies": [None, copy, None, None, None]}])
+    mine = [(p.detach().clone(), None, *ma.adamw_byte_state(p)) for p in params]
+    tokens = torch.randint(0, 300, (3, 41), generator=g, device=DEV)
+    labels = tokens[:, 1:].clone()
+    labels[1, 20:] = -100
+    how = dict(scale=0.5, center=False)
+    rw = torch.full((3, 40), 1 / 120, device=DEV)
+    for step in range(1, 4):
+        x = ma.embedding(tokens[:, :-1], table, out_dtype=dtype)
+        out, y = ma.residual_norm(torch.tanh(x), x, gain, post_weight=post, gate=gate, **how)
+        loss = ma.head_loss(y, head, labels, copy=copy)
+        loss.mean().backward()
+        # the same call by call
+        x = ma.embedding_forward(table.detach(), tokens[:, :-1], out_dtype=dtype)
+        block = torch.tanh(x)
+        out, y, stats = ma.residual_norm_forward(block, x, gain.detach(), post_weight=post.detach(), gate=gate.detach(), **how)
+        each, lse = ma.head_loss_forward(y, copy, labels)
+        dhead = torch.empty_like(head)
+        dy, _ = ma.head_loss_backward(y, copy, labels, lse, rw, dweight=dhead)
+        grads = ma.residual_norm_backward(None, dy, block, out, stats, gain.detach(), post_weight=post.detach(),
+                                          gate=gate.detach(), **how)
+        assert torch.equal(loss, each) and torch.equal(head.grad, dhead)
+        assert torch.equal(gain.grad, grads[2]) and torch.equal(post.grad, grads[4]) and torch.equal(gate.grad, grads[6])
+        assert all(torch.isfinite(p.grad).all() for p in params) and table.grad.any()
+        copied = torch.empty_like(copy)
+        ma.adamw_byte_step_multi([(m[0], p.grad, *m[2:], copied if p is head else None) for m, p in zip(mine, params)],
+                                 step=step, lr=1e-2, seed=3)
+        opt.step()
+        opt.zero_grad()
+        assert all(torch.equal(p.detach(), m[0]) for p, m in zip(params, mine)) and torch.equal(copy, copied)
