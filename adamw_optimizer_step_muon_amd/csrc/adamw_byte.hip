@@ -2,8 +2,8 @@
 //
 // A moment is a value of 8 bits per element and a power of two per block of 64 elements (in the
 // tensor's flattened order; the last block may be short):
-//   exp_avg     OCP e4m3, the block's largest magnitude scaled into [2^7, 2^8)
-//   exp_avg_sq  OCP e5m2, the block's largest value scaled into [2^14, 2^15)
+//   exp_avg     OCP e4m3, the block's largest finite magnitude scaled into [2^7, 2^8)
+//   exp_avg_sq  OCP e5m2, the block's largest finite value scaled into [2^14, 2^15)
 //   scale       e8m0: the byte b stands for 2^(b - 127)
 // The step widens them to fp32 (exact), runs the AdamW update on them, writes the parameter
 // from the moments before they are rounded, and rounds the moments back.
@@ -84,8 +84,16 @@ struct E5M2 {
 // lane of its row).  random: 16 bits per element.
 template <typename F>
 __device__ __forceinline__ int round8(const float (&x)[4], const uint32_t (&random)[4], unsigned& scale) {
-  float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+  float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));  // (NaN drops out)
   big = row16_reduce(big, 0.0f, Max());
+  // infinities leave the scale to the others, which they would take to zero (looked at when there is
+  // one: 444 and 715 us as without it, a select for every element takes 450 and 728)
+  if (__builtin_expect(__any(big == INFINITY), 0)) {
+    big = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) big = fmaxf(big, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.0f);
+    big = row16_reduce(big, 0.0f, Max());
+  }
   // the exponent of the largest magnitude (0 and subnormal numbers end at the lowest scale)
   const int top = static_cast<int>(__builtin_bit_cast(uint32_t, big) >> 23) - 127;
   int e = top - F::kTop;

@@ -284,14 +284,17 @@ typedef struct {
 /* ma_adamw_step over many tensors whose moments are held in 8 bits: 2 + 1/32 instead of 8 bytes
  * of state per element.  The moments are widened (exactly), updated as ma_adamw_step does, and
  * step the parameter before they are rounded back; grad may have 16 bits.  A block's scale is
- * 2^(E - 7) for exp_avg and 2^(E - 14) for exp_avg_sq, E the exponent of its largest magnitude
- * (at least 2^-126).  Each value goes up to the next one of its type with the probability of its
- * place between its two neighbours (16 bits of a hash of seed, step and the element's number,
+ * 2^(E - 7) for exp_avg and 2^(E - 14) for exp_avg_sq, E the exponent of its largest finite
+ * magnitude (at least 2^-126).  Each value goes up to the next one of its type with the probability
+ * of its place between its two neighbours (16 bits of a hash of seed, step and the element's number,
  * counted over the list with every segment starting at a multiple of 64), so that slow averages
- * keep moving; a positive exp_avg_sq stays positive.  The same inputs give the same bits on every
- * call; results do not depend on alignment (pointers need their element's).  One launch per 46
- * segments.  Segments with n == 0 are skipped.  No written range (all but grad) may overlap any
- * other range of any segment.  NaN and Inf in a gradient make their element's state NaN or Inf.
+ * keep moving; a positive exp_avg_sq stays positive.  (So beside a magnitude of 2^E an exp_avg below
+ * 2^(E - 16) becomes that or 0, and an exp_avg_sq below 2^(E - 30) becomes that.)  The same inputs
+ * give the same bits on every call; results do not depend on alignment (pointers need their
+ * element's).  One launch per 46 segments.  Segments with n == 0 are skipped.  No written range (all
+ * but grad) may overlap any other range of any segment.  A gradient of NaN or Inf, or one whose
+ * (1 - beta2) grad^2 passes fp32, makes its element's state NaN or Inf and leaves the rest of the
+ * block alone.
  * Errors: as ma_adamw_step_multi. */
 ma_status ma_adamw_byte_step_multi(const ma_adamw_byte_segment* segs, int32_t n_segs,
                                const ma_adamw_byte_hparams* hp, uint64_t seed, void* stream);

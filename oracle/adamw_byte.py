@@ -50,7 +50,8 @@ def widen(values, scale_bytes):
 
 def exponents(x, kind):
     """The scale's exponent of each block of a moment x."""
-    big = np.abs(blocks(x)).max(1)
+    big = np.abs(blocks(x))
+    big = np.where(np.isfinite(big), big, 0.0).max(1)
     e = np.frexp(big)[1] - 1 - kind[2]
     return np.clip(np.where(big > 0, e, -126), -126, 127)
 
