@@ -22,9 +22,9 @@
 // are kept or one tile holds all rows; a row of weight 0 then goes on as zeros behind its loss.
 //
 // Rounding: products of 16-bit values are exact and summed in fp32.  g is rounded once to the
-// hidden type, as the matrix cores take it, after a scaling that makes the largest row weight 2^14:
-// fp16 then keeps probabilities down to 2^-38.  Every sum has a fixed
-// order: the same inputs give the same bits.
+// hidden type, as the matrix cores take it, after a scaling by a power of two that takes the largest
+// finite row weight to 2^14 or more: fp16 then keeps what is 2^-39 of that weight or more.  Every sum has
+// a fixed order: the same inputs give the same bits.
 // fp32 operands: up to kSplitRows rows on the fp32 matrix instructions; above as three bf16 planes
 // each (x = x0 + x1 + x2 exactly: what two roundings to 8 bits leave of 24 fits the third), whose six
 // products of 2^-16 and more run as one sum six times as long, the smallest first: the three that are
@@ -104,20 +104,25 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     return c.label_bits == 64 ? static_cast<const int64_t*>(c.labels)[r] : static_cast<const int32_t*>(c.labels)[r];
   };
   const auto in_vocab = [&](int64_t l) { return l >= 0 && l < c.vocab; };
-  // the largest weight of a row with a target
+  // the largest finite weight of a row with a target
   float top = 0.0f;
   if (c.row_weight) {
 #pragma unroll 4
     for (int64_t r = t; r < c.n; r += kRowThreads)
-      if (in_vocab(label_of(r))) top = fmaxf(top, fabsf(c.row_weight[r]));
+      if (in_vocab(label_of(r))) {
+        const float w = fabsf(c.row_weight[r]);
+        top = fmaxf(top, w < INFINITY ? w : 0.0f);
+      }
     top = wave_max(top);
     if ((t & 63) == 0) tops[wave] = top;
     __syncthreads();
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w]);
   }
-  // weights are scaled so that the largest becomes 2^14 (exactly: then g of an unlikely label, nearly
-  // the weight itself, hardly rounds); fp32 needs no scaling
-  const bool scaled = T != kActF32 && top > 0.0f && top <= 3.4028234663852886e38f;
+  // weights are scaled by the power of two that takes the largest into [2^14, 2^15) (then g of an
+  // unlikely label, nearly the weight itself, stays within fp16), or by 2^126, whose inverse is a normal
+  // number; fp32 needs no scaling
+  const int exponent = static_cast<int>(__builtin_bit_cast(uint32_t, top) >> 23) - 127;
+  const int shift = T != kActF32 && top > 0.0f ? (exponent < -112 ? 126 : 14 - exponent) : 0;
   int base = 0, turn = 0;
   for (int64_t first = 0; first < c.n; first += kRowThreads, turn ^= 1) {
     const int64_t r = first + t, label = r < c.n ? label_of(r) : -1;
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
     c.row_of[at] = static_cast<int>(r);
     c.label[at] = static_cast<int>(label);
     if (c.row_weight) {
-      const float w = scaled ? given / top * 0x1p14f : given;
+      const float w = __builtin_ldexpf(given, shift);
       c.weight[at] = w;
       if (!c.once) {
         // exp(z - top) factor = weight exp(z - lse)
@@ -155,7 +160,7 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadCall c) {
   }
   if (t == 0) {
     c.head->live = base;
-    c.head->unscale = scaled ? top * 0x1p-14f : 1.0f;
+    c.head->unscale = __builtin_ldexpf(1.0f, -shift);
   }
   if constexpr (kCopy) {
     typedef typename Act<T>::S S;

@@ -624,7 +624,8 @@ ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_
 
 /* The gradients of sum row_weight[r] loss[r] (row_weight, lse: n fp32):
  *   g = row_weight (exp(z - lse) - [v = label]),  dhidden = g W,  dweight (+)= g^T h
- * g is rounded once to the hidden type (2^-8 of each term of the sums at most for bf16, 2^-11 for fp16).
+ * g is rounded once to the hidden type (2^-8 of each term of the sums at most for bf16, 2^-11 for fp16
+ * or 2^-39 of the largest finite weight of a row with a target).
  * Rows without a target or of weight 0 have gradient 0, whatever they hold.  dhidden has the hidden
  * type; dweight is (vocab, dim) of dweight_type, the hidden type or MA_F32, and is added to with
  * accumulate = 1 (MA_F32 only).  Either may be NULL. */
