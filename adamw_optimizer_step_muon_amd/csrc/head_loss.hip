@@ -377,7 +377,7 @@ __global__ __launch_bounds__(256) void head_out_kernel(HeadCall c) {
   if (i >= c.dim) return;
   const int cnt = c.dim - i < 4 ? static_cast<int>(c.dim - i) : 4;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (at >= 0) {
+  if (at >= 0 && c.weight[at] != 0.0f) {
 #pragma unroll 8
     for (int s = 0; s < c.splits; ++s) {
       const f32x4 x = *reinterpret_cast<const f32x4*>(c.sum + (s * c.rows_pad + at) * c.sum_stride + i);
@@ -574,6 +574,14 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (col0 + j * 32 + 8 * (k >> 2) + (k & 3) >= count) g[j][k] = 0.0f;
+      }
+      // nothing comes of a row without a gradient, also where its zeros meet an infinity of W
+      const bool none = !on || (factor == 0.0f && c.weight[m0 + row] == 0.0f);
+      if (__any(none)) {
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) g[j][k] = none ? 0.0f : g[j][k];
       }
       if constexpr (!kStaged) {
         float* out = static_cast<float*>(c.g) + static_cast<int64_t>(m0 + row) * c.g_stride + n0 + col0;

@@ -52,3 +52,29 @@ def test_an_infinite_weight_leaves_other_rows_their_bounds(dtype, weight, size, 
                               (ma.head_loss_backward(h, w, labels, lse, rw)[0], (ref_lse[4], ref_lse[6]))):
         assert not torch.isfinite(dh[17]).any()
         _near(dh[on], want[on], bound[on])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,dim", [(1, 136), (40, 136), (40, 1100), (100, 136), (300, 136), (300, 1100)])
+def test_an_infinity_in_the_weight_beside_rows_of_weight_zero(dtype, n, dim):
+    """An entry of the vocabulary whose logits are all -inf has probability 0: it takes part in nothing,
+    its own gradient is 0, and so is dh of a row of weight 0.  (The others' dh has 0 x inf in one
+    column.)  fp32 above 128 rows takes no infinities."""
+    if dtype == torch.float32 and n > 128:
+        pytest.skip("magnitudes up to 2^127")
+    h, w, labels, rw = _inputs(n, 700, dim, dtype, 4, ignored=0)
+    h[:, 3] = -h[:, 3].abs() - 0.125
+    labels[labels == 5] = 6
+    rw[n // 2] = 0.0
+    ref = _reference(h, torch.cat([w[:5], w[6:]]), labels - (labels > 5).long(), rw)
+    w[5, 3] = float("inf")
+    cols = torch.arange(dim, device=DEV) != 3
+    entries = torch.arange(700, device=DEV) != 5
+    loss, dh, dw = ma.head_loss_grad(h, w, labels, rw)
+    _near(loss, ref[0], ref[2])
+    lse = ma.head_loss_forward(h, w, labels)[1]
+    ref_lse = _reference(h, torch.cat([w[:5], w[6:]]), labels - (labels > 5).long(), rw, lse)
+    for got, want in (((dh, dw), ref), (ma.head_loss_backward(h, w, labels, lse, rw), ref_lse)):
+        assert not got[0][n // 2].any() and not got[1][5].any()
+        _near(got[0][:, cols], want[4][:, cols], want[6][:, cols])
+        _near(got[1][entries], want[5], want[7])
