@@ -2045,7 +2045,10 @@ size_t ma_head_loss_workspace_bytes(int32_t type, int64_t n, int64_t dim, int64_
   if (type < MA_F32 || type > MA_BF16 || n < 1 || dim < 1 || vocab < 1 || n > kMaxThreadsPerLaunch / 1024 ||
       dim > kMaxDim || vocab > kMaxVocab)
     return 0;
-  return static_cast<size_t>(plan_head(type, n, dim, vocab, head_weight_copied(type, dim, weight, weight_stride), gradients != 0).bytes);
+  const bool copied = head_weight_copied(type, dim, weight, weight_stride);
+  // (a forward call may split its logits where one with gradients keeps them whole, and need more)
+  const int64_t forward = plan_head(type, n, dim, vocab, copied, false).bytes;
+  return static_cast<size_t>(gradients ? std::max(forward, plan_head(type, n, dim, vocab, copied, true).bytes) : forward);
 }
 
 ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,

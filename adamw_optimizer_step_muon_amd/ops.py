@@ -537,7 +537,7 @@ def _head_workspace(dtype: int, n: int, dim: int, vocab: int, aligned: int, stri
 
 
 def head_loss_workspace_bytes(hidden, weight, *, gradients: bool = True) -> int:
-    """Workspace of the head loss calls on these tensors; gradients False: of the forward call."""
+    """Workspace for any of the head loss calls on these tensors; gradients False: for the forward call."""
     n, dim, _ = _rows("hidden", hidden, anywhere=True)
     vocab, _, stride = _rows("weight", weight, anywhere=True)
     return _head_workspace(_type("hidden", hidden.dtype), n, dim, vocab, weight.data_ptr() % 16, stride, bool(gradients))

@@ -606,7 +606,7 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
  * row's hidden states makes that row's loss NaN (or its loss infinite), one in W may make all of them NaN.
  * n < 2^22, dim <= 2^20, vocab <= 2^30.  n = 0 is a no-op, but for a dweight that is not added to.
  *
- * Host only: workspace bytes of the calls (gradients = 1 for _backward and _grad).  Of `weight`
+ * Host only: workspace bytes of the calls (gradients = 1: of any of them, 0: of _forward).  Of `weight`
  * only the alignment counts: rows that do not start at multiples of 16 bytes (or of a dim that is no
  * multiple of 8) are copied there, and in fp32 with more than 128 rows all of it, in 6 bytes a value.
  * Otherwise some 2 dim bytes a row (6 in fp32), and for the gradients at most 512 MiB of the logits'
