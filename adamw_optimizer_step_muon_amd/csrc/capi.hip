@@ -757,7 +757,7 @@ ma_status run_head(HeadCall& c, HeadWork work, const Range* out, int outs, void*
   if (const ma_status st = check_bits(c.label_bits, "label")) return st;
   if (const ma_status st = check_rows(c.weight_in, c.type, c.vocab, c.dim, c.weight_in_stride, "weight", &in[2])) return st;
   const bool gradients = work != kHeadForward;
-  const HeadPlan p = plan_head(c.type, c.n, c.dim, c.vocab, head_weight_copied(c.type, c.dim, c.weight_in, c.weight_in_stride), gradients);
+  const HeadPlan p = plan_head(c.type, c.n, c.dim, c.vocab, head_weight_copied(c.type, c.dim, c.weight_in, c.weight_in_stride), work);
   if (head_threads(c.type, c.n, c.dim, c.vocab, p) > kMaxThreadsPerLaunch)
     return fail(MA_ERR_UNSUPPORTED, "%lld rows with a vocabulary of %lld exceed one launch", (long long)c.n, (long long)c.vocab);
   if (const ma_status st = check_rows(c.hidden, c.type, c.n, c.dim, c.hidden_stride, "hidden", &in[1])) return st;
@@ -2041,14 +2041,17 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
 }
 
 size_t ma_head_loss_workspace_bytes(int32_t type, int64_t n, int64_t dim, int64_t vocab, const void* weight,
-                                    int64_t weight_stride, int32_t gradients) {
+                                    int64_t weight_stride, int32_t calls) {
   if (type < MA_F32 || type > MA_BF16 || n < 1 || dim < 1 || vocab < 1 || n > kMaxThreadsPerLaunch / 1024 ||
       dim > kMaxDim || vocab > kMaxVocab)
     return 0;
   const bool copied = head_weight_copied(type, dim, weight, weight_stride);
+  const auto bytes = [&](HeadWork work) { return static_cast<size_t>(plan_head(type, n, dim, vocab, copied, work).bytes); };
+  if (calls == 0) return bytes(kHeadForward);
+  if (calls == 2) return bytes(kHeadBackward);
+  if (calls == 3) return bytes(kHeadBoth);
   // (a forward call may split its logits where one with gradients keeps them whole, and need more)
-  const int64_t forward = plan_head(type, n, dim, vocab, copied, false).bytes;
-  return static_cast<size_t>(gradients ? std::max(forward, plan_head(type, n, dim, vocab, copied, true).bytes) : forward);
+  return std::max(std::max(bytes(kHeadForward), bytes(kHeadBackward)), bytes(kHeadBoth));
 }
 
 ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,

@@ -4,9 +4,9 @@
 //   g = w_r (exp(z - lse) - [v = label]),  dh = g W,  dW = g^T h
 //
 // h: n hidden rows of D values, W: vocab x D, both of one type; labels outside the vocabulary mark
-// rows without a target.  The logits of the forward pass live in registers only: every tile of
-// 256 rows x 256 vocabulary entries leaves its rows' maxima and sums of exponentials, which a
-// second kernel joins.  The backward pass works through pieces of the vocabulary: a piece's logits
+// rows without a target.  The logits of the forward pass live in registers, but where their sums are
+// split (below): every tile of 256 rows x 256 vocabulary entries leaves its rows' maxima and sums of
+// exponentials, which a second kernel joins.  The backward pass works through pieces of the vocabulary: a piece's logits
 // are computed again, its g is written to the workspace in the hidden type (n x piece values), and
 // two products take it to dh (a sum over pieces, fp32) and to the piece's rows of dW.
 // Arithmetic: 2 n vocab D FLOP forward, 6 n vocab D with the gradients; the logits' second product,
@@ -14,7 +14,8 @@
 // where those of all rows take no more than the piece's 512 MiB and the product costs more than
 // writing and reading them.
 // Each product may have few tiles: its sum (over the hidden size, the piece or the rows) is then split
-// over blocks, whose fp32 parts the next kernel adds in order.  Split logits are kept.
+// over blocks, whose fp32 parts the next kernel adds in order.  Split logits are kept, in the forward pass
+// too.
 //
 // Rows with a target (and, for gradients, a weight that is not zero) are gathered first into a
 // padded copy, so the others cost nothing and whatever they hold reaches no result, and tiles need
@@ -1324,12 +1325,16 @@ int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const Head
   return (tiles + 8) * 512 > waves ? (tiles + 8) * 512 : waves;
 }
 
-HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, bool gradients) {
+HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, HeadWork work) {
   HeadPlan p{};
+  const bool gradients = work != kHeadForward;
   p.split = head_split(type, n);
   // bytes of a value of the gathered rows, g and a copied W
   const int64_t size = p.split ? 6 : type == kActF32 ? 4 : 2, tile = head_tile_size(type, p.split);
-  p.rows_pad = align_up(n, kHeadTile);
+  // memory is taken for the rows of whole tiles; pieces and splits are chosen for rows padded to
+  // kHeadTile
+  p.rows_pad = align_up(n, head_row_tile(type, n));
+  const int64_t full_rows = align_up(n, kHeadTile);
   p.dim_pad = align_up(dim, 64);
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
@@ -1352,14 +1357,14 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   p.weight_pad = copied || p.split ? take(vocab * p.dim_pad * size) : 0;
   // the statistics of the forward pass lie where the backward pass has g
   const int64_t tiles = ceil_div(vocab, tile), dim_tiles = ceil_div(dim, tile);
-  int64_t piece = kHeadPieceBytes / (p.rows_pad * size) / tile;
+  int64_t piece = kHeadPieceBytes / (full_rows * size) / tile;
   piece = piece < 1 ? 1 : piece;
   p.piece = ceil_div(tiles, ceil_div(tiles, piece)) * tile;
   // rows a power of two apart would meet in the same memory channels (the gradients of 2048 rows, 65536 x
   // 1280: 1042 us, 1020 with 64 values more)
   p.g_stride = p.piece + 64;
   const int64_t logits = p.rows_pad * p.g_stride * 4;
-  const bool fits = p.piece >= vocab && p.rows_pad * p.piece * 4 <= kHeadPieceBytes && p.rows_pad <= 65535;
+  const bool fits = p.piece >= vocab && full_rows * p.piece * 4 <= kHeadPieceBytes && full_rows <= 65535;
   p.stats_rows = head_best_rows(type, n, tiles);
   p.grad_rows = head_best_rows(type, n, p.piece / tile);
   p.hidden_rows = head_row_tile(type, n);
@@ -1368,7 +1373,7 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   // against 8 bytes of traffic each, 4.8 TB/s (fp32: g takes their place).  Rows that fill one tile at
   // most are numbered once anyhow: leaving some out would save nothing.
   const int64_t padded = align_up(n, head_row_tile(type, n));
-  p.kept = gradients && fits &&
+  p.kept = work == kHeadBoth && fits &&
            8.0 * padded * p.piece / 4.8e12 < head_time(type, p.split, ceil_div(n, p.grad_rows) * (p.piece / tile), p.grad_rows, p.dim_pad) +
                                           (n > head_row_tile(type, n) ? 10e-6 : 0.0);
   // Products of few tiles: their sums are split over blocks where the fuller chip saves more than the
@@ -1381,7 +1386,7 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
     // 89 rows of fp32, 1980 x 2421: 95 us in parts, 270 whole)
     double best = 0.8 * head_time(type, p.split, ceil_div(n, p.stats_rows) * tiles, p.stats_rows, p.dim_pad);
     for (int64_t rows = most; rows >= least; rows /= 2)
-      for (int64_t splits = 2; splits <= 32 && splits * 256 <= dim && splits * p.rows_pad * p.piece * 4 <= kHeadPieceBytes; ++splits) {
+      for (int64_t splits = 2; splits <= 32 && splits * 256 <= dim && splits * full_rows * p.piece * 4 <= kHeadPieceBytes; ++splits) {
         const double time = head_time(type, p.split, ceil_div(n, rows) * tiles * splits, rows, ceil_div(p.dim_pad, splits)) +
                             8.0 * splits * padded * p.piece / 4.8e12 + (gradients ? 8e-6 : 2e-6);
         if (time < best) {
@@ -1392,7 +1397,9 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
       }
     if (p.logit_splits > 1) p.kept = gradients;
   }
-  const int64_t stats = n * tiles * 8, g = gradients ? p.rows_pad * p.g_stride * size : 0;
+  // (fp32's g takes the place of kept logits)
+  const bool in_place = p.kept && type == kActF32 && !p.split;
+  const int64_t stats = n * tiles * 8, g = gradients && !in_place ? p.rows_pad * p.g_stride * size : 0;
   p.partial = take(stats > g ? stats : g);
   p.logits = p.kept || p.logit_splits > 1 ? take(p.logit_splits * logits) : 0;
   p.sum_stride = align_up(dim, 4);
@@ -1451,7 +1458,7 @@ hipError_t launch_head(const HeadCall& call, const HeadPlan& p, void* workspace,
   c.partial = reinterpret_cast<float2*>(ws + p.partial);
   c.logit_splits = p.logit_splits;
   c.z_plane = p.rows_pad * p.g_stride;
-  c.kept = p.kept && (work == kHeadBoth || p.logit_splits > 1);
+  c.kept = p.kept;
   c.once = work == kHeadBoth && (p.kept || c.n <= head_row_tile(c.type, c.n));
   c.planes = p.split;
   c.z = reinterpret_cast<float*>(ws + p.logits);

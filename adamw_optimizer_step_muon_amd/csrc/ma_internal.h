@@ -580,7 +580,7 @@ size_t residual_workspace_bytes(int64_t n, int64_t dim);
 hipError_t launch_residual_backward(const ResidualGradCall& c, hipStream_t s);
 
 // The LM head's cross entropy (head_loss.hip).
-constexpr int kHeadTile = 256;  // gathered rows are padded to a multiple of this
+constexpr int kHeadTile = 256;  // rows of the largest tile
 constexpr int64_t kHeadPieceBytes = int64_t{512} << 20;  // of g, for up to 2^20 rows
 // fp32 calls of more rows run on bf16 planes: loss and gradients of 130, 256 and 512 rows, 65536 x 768,
 // take 570, 621 and 990 us, on the fp32 matrix instructions 678, 768 and 1397.  (Fewer rows need one
@@ -601,7 +601,8 @@ struct HeadPlan {
 };
 // Whether the weight's rows must be copied to be aligned to 16 bytes.
 bool head_weight_copied(int type, int64_t dim, const void* weight, int64_t stride);
-HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, bool gradients);
+enum HeadWork { kHeadForward = 0, kHeadBackward = 1, kHeadBoth = 2 };
+HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied, HeadWork work);
 // Threads of the call's largest launch, at most.
 int64_t head_threads(int type, int64_t n, int64_t dim, int64_t vocab, const HeadPlan& p);
 struct HeadCall {
@@ -650,7 +651,6 @@ struct HeadCall {
   bool planes, weight_lines;  // weight_lines: dW's rows start at multiples of 16 bytes
 };
 hipError_t launch_head_clear(const HeadCall& c, hipStream_t s);  // dweight = 0
-enum HeadWork { kHeadForward = 0, kHeadBackward = 1, kHeadBoth = 2 };
 hipError_t launch_head(const HeadCall& c, const HeadPlan& p, void* workspace, HeadWork work, hipStream_t s);
 
 }  // namespace ma

@@ -530,20 +530,27 @@ def distill_loss_grad(logits, teacher, ids, row_weight, *, temperature: float = 
 # --------------------------------------------------------------------------
 # the LM head's cross entropy
 # --------------------------------------------------------------------------
+_HEAD_CALLS = {"forward": 0, "backward": 2, "grad": 3}
+
+
 @functools.lru_cache(maxsize=256)
-def _head_workspace(dtype: int, n: int, dim: int, vocab: int, aligned: int, stride: int, gradients: bool) -> int:
+def _head_workspace(dtype: int, n: int, dim: int, vocab: int, aligned: int, stride: int, calls: int) -> int:
     # of the weight's address only its alignment counts
-    return int(load().ma_head_loss_workspace_bytes(dtype, n, dim, vocab, 256 + aligned, stride, gradients))
+    return int(load().ma_head_loss_workspace_bytes(dtype, n, dim, vocab, 256 + aligned, stride, calls))
 
 
-def head_loss_workspace_bytes(hidden, weight, *, gradients: bool = True) -> int:
-    """Workspace for any of the head loss calls on these tensors; gradients False: for the forward call."""
+def head_loss_workspace_bytes(hidden, weight, *, gradients: bool = True, call=None) -> int:
+    """Workspace for any of the head loss calls on these tensors; gradients False: for the forward call;
+    call "forward", "backward" or "grad": for that one alone."""
+    if call is not None and call not in _HEAD_CALLS:
+        raise ValueError(f"call must be one of {sorted(_HEAD_CALLS)} (got {call!r})")
     n, dim, _ = _rows("hidden", hidden, anywhere=True)
     vocab, _, stride = _rows("weight", weight, anywhere=True)
-    return _head_workspace(_type("hidden", hidden.dtype), n, dim, vocab, weight.data_ptr() % 16, stride, bool(gradients))
+    return _head_workspace(_type("hidden", hidden.dtype), n, dim, vocab, weight.data_ptr() % 16, stride,
+                           int(bool(gradients)) if call is None else _HEAD_CALLS[call])
 
 
-def _head(hidden, weight, labels, gradients, workspace, stream):
+def _head(hidden, weight, labels, call, workspace, stream):
     """The leading arguments shared by the three calls, the number of rows, the workspace, and
     what the arguments' addresses need alive."""
     n, dim, hidden_stride = _rows("hidden", hidden)
@@ -555,7 +562,8 @@ def _head(hidden, weight, labels, gradients, workspace, stream):
     if labels.shape != hidden.shape[:-1]:
         raise ValueError("labels must have the hidden states' leading dimensions")
     at = labels if labels.is_contiguous() else _contiguous(labels, stream)
-    need = _head_workspace(dtype, n, dim, vocab, weight.data_ptr() % 16, weight_stride, gradients)
+    need = _head_workspace(dtype, n, dim, vocab, weight.data_ptr() % 16, weight_stride,
+                           _HEAD_CALLS[call])
     keep, ws, size = _workspace(workspace, need, hidden, stream)
     return (hidden.data_ptr(), dtype, hidden_stride, n, dim, weight.data_ptr(), weight_stride, vocab, at.data_ptr(),
             bits), n, (ws, size), (keep, at)
@@ -587,7 +595,7 @@ def head_loss_forward(hidden, weight, labels, *, workspace=None, stream=None):
     which are not kept.  hidden and weight have one type; weight is the head in that type (see
     adamw_byte_step_multi's copies).  A label outside the vocabulary marks a row without a target:
     loss and lse 0.  lse, the logarithm of the sum of exponentials, is the backward pass's input."""
-    args, _, space, _keep = _head(hidden, weight, labels, False, workspace, stream)
+    args, _, space, _keep = _head(hidden, weight, labels, "forward", workspace, stream)
     loss = _empty(hidden, hidden.shape[:-1], torch.float32, stream)
     lse = _like(loss, stream)
     _call("ma_head_loss_forward", hidden.device, stream, *args, loss.data_ptr(), lse.data_ptr(), *space)
@@ -602,7 +610,7 @@ def head_loss_backward(hidden, weight, labels, lse, row_weight, *, hidden_grad: 
     """(dhidden, dweight) of ma_head_loss_backward: the gradients of sum row_weight * loss.  Either
     can be left out (None).  dweight has the weight's type, or is given: of that type, or float32
     and with accumulate added to.  The logits' gradients are rounded to the hidden type once."""
-    args, n, space, _keep = _head(hidden, weight, labels, True, workspace, stream)
+    args, n, space, _keep = _head(hidden, weight, labels, "backward", workspace, stream)
     device, given = hidden.device, dweight
     rows = _floats("lse", lse, n, device), _floats("row_weight", row_weight, n, device)
     dhidden, dweight, outs = _head_gradients(hidden, weight, hidden_grad, weight_grad, dweight, accumulate, stream)
@@ -617,7 +625,7 @@ def head_loss_backward(hidden, weight, labels, lse, row_weight, *, hidden_grad: 
 def head_loss_grad(hidden, weight, labels, row_weight, *, hidden_grad: bool = True, weight_grad: bool = True,
                    dweight=None, accumulate: bool = False, workspace=None, stream=None):
     """(loss, dhidden, dweight) in one call (ma_head_loss_grad), for a row_weight known beforehand."""
-    args, n, space, _keep = _head(hidden, weight, labels, True, workspace, stream)
+    args, n, space, _keep = _head(hidden, weight, labels, "grad", workspace, stream)
     device, given = hidden.device, dweight
     row = _floats("row_weight", row_weight, n, device)
     loss = _empty(hidden, hidden.shape[:-1], torch.float32, stream)

@@ -606,15 +606,20 @@ ma_status ma_distill_loss_grad(const void* logits, int32_t type, int64_t stride,
  * row's hidden states makes that row's loss NaN (or its loss infinite), one in W may make all of them NaN.
  * n < 2^22, dim <= 2^20, vocab <= 2^30.  n = 0 is a no-op, but for a dweight that is not added to.
  *
- * Host only: workspace bytes of the calls (gradients = 1: of any of them, 0: of _forward).  Of `weight`
- * only the alignment counts: rows that do not start at multiples of 16 bytes (or of a dim that is no
- * multiple of 8) are copied there, and in fp32 with more than 128 rows all of it, in 6 bytes a value.
- * Otherwise some 2 dim bytes a row (6 in fp32), and for the gradients at most 512 MiB of the logits'
- * (up to 2^20 rows), as much for logits that are few enough to be kept from one direction to the
- * other, and 4 dim bytes a row once or several times.  0 for invalid sizes, which the calls then
- * report. */
+ * Host only: workspace bytes of `calls`: 1 of any of the three, 0 of _forward, 2 of _backward, 3 of
+ * _grad.  Of `weight` only the alignment counts: rows that do not start at multiples of 16 bytes (or of
+ * a dim that is no multiple of 8) are copied there, and in fp32 with more than 128 rows all of it, in
+ * 6 bytes a value.  Otherwise, with the rows padded to whole tiles (of 64, 128 or 256 rows, or 32 in
+ * fp32), these are taken:
+ *   the rows that take part, 2 dim bytes each (fp32: 4, and 6 from 129 rows on);
+ *   8 bytes a row and 256 vocabulary entries (128 in fp32), or in the same place, for gradients, g: the
+ *   hidden type's bytes (6 in fp32 from 129 rows on) of a row and entry, at most 512 MiB (up to 2^20 rows);
+ *   4 bytes of a row and entry for logits that _grad keeps from one direction to the other, at most 512 MiB;
+ *   where few rows fill few tiles and a product's sum is split, 4 bytes of each result and part: logits (at
+ *   most 512 MiB), and for gradients dhidden (once at least) and dweight.
+ * 0 for invalid sizes, which the calls then report. */
 size_t ma_head_loss_workspace_bytes(int32_t type, int64_t n, int64_t dim, int64_t vocab, const void* weight,
-                                    int64_t weight_stride, int32_t gradients);
+                                    int64_t weight_stride, int32_t calls);
 
 /* loss, lse: n fp32 each. */
 ma_status ma_head_loss_forward(const void* hidden, int32_t type, int64_t hidden_stride, int64_t n, int64_t dim,
