@@ -31,7 +31,8 @@ An AdamW group's ``state_bits=8`` holds its moments in 8 bits instead (2 + 1/32 
 parameter, see adamw_byte_step_multi): ``exp_avg``, ``exp_avg_sq`` and their blocks' scales, with
 ``seed`` for the roundings' random bits.  Its ``copies`` (one entry per parameter, None or a
 contiguous fp16 or bf16 tensor of its size) receive the stepped parameters, for a forward pass
-that reads 16-bit weights; what they hold before a parameter's first step is the caller's.  Token
+that reads 16-bit weights; what they hold before a parameter's first step is the caller's, but
+load_state_dict writes them from the parameters (which are to be restored before it).  Token
 gradients are built densely there.
 
 A Muon group's ``ns_mode`` (0 by default) selects the Newton-Schulz route: 1 runs the
@@ -401,6 +402,8 @@ class MuonAdamW:
         return {"state": state, "param_groups": groups}
 
     def load_state_dict(self, sd: Dict) -> None:
+        import torch
+
         flat = [p for g in self.param_groups for p in g["params"]]
         for (idx, st) in sd["state"].items():
             # 8-bit moments mean nothing without their scales, and a cast would lose most values
@@ -411,3 +414,8 @@ class MuonAdamW:
                 self.state[id(flat[int(idx)])][k].copy_(v)
         for g, sg in zip(self.param_groups, sd["param_groups"]):
             g["step"] = sg["step"]
+            # a forward pass before the next step reads what the parameters are now
+            with torch.no_grad():
+                for p, c in zip(g["params"], g.get("copies") or ()):
+                    if c is not None:
+                        c.copy_(p.view(c.shape))
