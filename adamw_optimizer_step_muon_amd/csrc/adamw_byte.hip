@@ -21,9 +21,9 @@
 // moment: the same inputs give the same bits on every call, and no state is kept.
 //
 // Bound by memory: 16 bytes per element with a 16-bit gradient and a 16-bit copy of the parameter,
-// and 1/16 byte of scales (28 bytes with moments in 32 bits).  Measured: 168 M elements with fp32
-// gradients 434-442 us, 262 M with bf16 gradients and copies 705-716 us, 5.9-6.2 TB/s.  Four elements a
-// lane make a scale's block one row of 16 lanes, whose maximum needs no shared memory; four groups of
+// and 1/16 byte of scales (28 bytes with moments in 32 bits).  Measured, card to card: 168 M elements with
+// fp32 gradients 434-460 us, 262 M with bf16 gradients and copies 705-745 us, 5.7-6.2 TB/s.  Four elements
+// a lane make a scale's block one row of 16 lanes, whose maximum needs no shared memory; four groups of
 // loads in flight a thread.  With library root and division, and a hash a moment, it was bound by
 // arithmetic (501 and 811 us).
 #include "adamw_elem.h"

@@ -6,9 +6,10 @@
 // h: n hidden rows of D values, W: vocab x D, both of one type; labels outside the vocabulary mark
 // rows without a target.  The logits of the forward pass live in registers, but where their sums are
 // split (below): every tile of 256 rows x 256 vocabulary entries leaves its rows' maxima and sums of
-// exponentials, which a second kernel joins.  The backward pass works through pieces of the vocabulary: a piece's logits
-// are computed again, its g is written to the workspace in the hidden type (n x piece values), and
-// two products take it to dh (a sum over pieces, fp32) and to the piece's rows of dW.
+// exponentials, which a second kernel joins.  The backward pass works through pieces of the
+// vocabulary: a piece's logits are computed again, its g is written to the workspace in the hidden type
+// (n x piece values), and two products take it to dh (a sum over pieces, fp32) and to the piece's rows
+// of dW.
 // Arithmetic: 2 n vocab D FLOP forward, 6 n vocab D with the gradients; the logits' second product,
 // the price of not keeping them, makes it 8.  Both directions in one call keep the logits (fp32)
 // where those of all rows take no more than the piece's 512 MiB and the product costs more than
@@ -730,10 +731,12 @@ __device__ __forceinline__ void head_epilogue(const HeadCall& c, const f32x16 (&
 // need two lanes and four waves only.
 // LDS rings: 3 stages of A and 2 of B for 256 rows (160 KiB), 3 and 3 for 128, 4 and 4 for 64, whose
 // short stages are bound by the loads' latency.
-// Measured: the logits of 8192 rows, 128000 x 2048, bf16, 3.3 ms (1.26 PFLOP/s), of 2731 rows, 65536 x
-// 1280, fp16, 450 us (1.0; the epilogue's exponentials are some 60 us of it), of 8 rows, 65536 x 768, 20 us
-// (4.9 TB/s of W); a piece of 32000 entries of the 8192 rows: g 0.89 ms, dh 0.82 ms, dW 0.82 ms.  At
-// 1.7-1.9 GHz the large ones are held by power as much as by the matrix cores.
+// Measured: the logits of 8192 rows, 128000 x 2048, bf16, 3.3-3.5 ms (1.2-1.3 PFLOP/s), of 2730 rows,
+// 65536 x 1280, fp16, 446-482 us (1.0; the epilogue's exponentials are some 60 us of it), of 8 rows, 65536 x
+// 768, 20 us (4.9 TB/s of W); a piece of 32000 entries of the 8192 rows: g 0.89-0.91 ms, dh 0.80-0.83, dW
+// 0.82-0.85.  Power holds the clock at 1.7-1.9 GHz under the large ones; the matrix cores are busy in
+// 63-70 % of those cycles in the 8192-row call, in 53-63 % in the shorter ones.  A compute unit has room
+// for one block, so that nothing runs beside a tile's epilogue, nor beside its first loads.
 template <int BM_, int kMode>
 struct HeadCfg {
   static constexpr int BM = BM_, BN = 256, BK = 64, WM = 2, WN = 4, kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -957,10 +960,11 @@ __global__ __launch_bounds__((HeadCfg<BM, kMode>::kThreads)) void head_gemm_kern
     load_frags(0, 0, fa[0], fb[0]);
     // Stage kt loads A of stage kt + LA between its matrix instructions and, once its own slot of B has
     // been read by all, B of stage kt + SB between the last of them.  (All loads ahead of the stage's
-    // first matrix instruction keep the matrix cores waiting: 8192 rows, 128000 x 2048, both directions:
-    // 14.0 ms, 13.4 in this order; the gradients of 2048 rows, 65536 x 1280: 1008 us, 932.  B spread over
-    // the stage comes too late: 1017.  Four waves of 128 x 128, whose fragments take two thirds of the
-    // LDS reads, but alone on their SIMD: 15.0 ms and 1048 us.)
+    // first matrix instruction keep the matrix cores waiting.  In turn on one card, that way and this: 8192
+    // rows, 128000 x 2048, both directions, 14.55 and 13.95 ms; the gradients of 2048 rows, 65536 x 1280, 1002
+    // and 947 us; the forward pass of 4095, 476 and 460.  B spread over the stage comes too late: 9 % slower.
+    // Four waves of 128 x 128, whose fragments take two thirds of the LDS reads, but alone on their SIMD:
+    // 12 % slower.)
     const auto run_stage = [&](int kt, auto steady) {
       constexpr bool kSteady = decltype(steady)::value;
       constexpr int kSlots = (KK - 1) * C::WTM;
@@ -1180,7 +1184,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align_up(int64_t x, int64_t q) { return ceil_div(x, q) * q; }
 // Seconds of a product of so many tiles and summed indices: rounds of the chip (256 compute units, a
 // block each) by what a tile takes for an index on the full chip.  A tile of half the rows takes more
-// than half of it (with few tiles in the chip 59 and 34 % instead of 62 and 45, fewer bytes in all).
+// than half of it.  Measured, a round of 256 tiles of logits over 256 to 1024 indices, the slope: tiles of
+// 256, 128 and 64 rows 27, 17 and 18 ns an index (the last by the rate at which W is read, which the model
+// leaves out: 12.5), on the fp32 instructions 75, 47 and 27 for 128, 64 and 32; and 3 to 8 us whatever the
+// length, which all choices have.
 double head_time(int type, bool split, int64_t tiles, int64_t rows, int64_t length) {
   double tile;
   if (type == kActF32 && !split) tile = rows == 128 ? 80e-9 : rows == 64 ? 46e-9 : 25e-9;
@@ -1370,8 +1377,8 @@ HeadPlan plan_head(int type, int64_t n, int64_t dim, int64_t vocab, bool copied,
   p.hidden_rows = head_row_tile(type, n);
   p.logit_splits = p.splits = p.weight_splits = 1;
   // kept logits: the logits' second product, and where rows are numbered once two launches of 10 us,
-  // against 8 bytes of traffic each, 4.8 TB/s (fp32: g takes their place).  Rows that fill one tile at
-  // most are numbered once anyhow: leaving some out would save nothing.
+  // against 8 bytes of traffic each, at a large copy's 4.8 TB/s (fp32: g takes their place).  Rows that
+  // fill one tile at most are numbered once anyhow: leaving some out would save nothing.
   const int64_t padded = align_up(n, head_row_tile(type, n));
   p.kept = work == kHeadBoth && fits &&
            8.0 * padded * p.piece / 4.8e12 < head_time(type, p.split, ceil_div(n, p.grad_rows) * (p.piece / tile), p.grad_rows, p.dim_pad) +

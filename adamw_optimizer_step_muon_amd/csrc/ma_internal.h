@@ -583,7 +583,7 @@ hipError_t launch_residual_backward(const ResidualGradCall& c, hipStream_t s);
 constexpr int kHeadTile = 256;  // rows of the largest tile
 constexpr int64_t kHeadPieceBytes = int64_t{512} << 20;  // of g, for up to 2^20 rows
 // fp32 calls of more rows run on bf16 planes: loss and gradients of 130, 256 and 512 rows, 65536 x 768,
-// take 570, 621 and 990 us, on the fp32 matrix instructions 678, 768 and 1397.  (Fewer rows need one
+// take 562, 625 and 995 us, on the fp32 matrix instructions 677, 766 and 1396.  (Fewer rows need one
 // tile of those.)
 constexpr int64_t kSplitRows = 128;
 struct HeadInfo {
